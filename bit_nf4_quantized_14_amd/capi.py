@@ -9,6 +9,7 @@ exception is raised.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -35,7 +36,11 @@ EXPORTS = ("nf4_codebook", "nf4_quantize", "nf4_dequantize",
            "qlora_linear_fwd_dropout", "qlora_linear_bwd_dropout",
            "qlora_workspace_bytes", "qlora_linear_fwd", "qlora_linear_bwd",
            "qn_strerror", "qn_profile_kernel", "qlora_linear_fwd_noalloc",
-           "qlora_fwd_batch_workspace_bytes", "qlora_linear_fwd_batch")
+           "qlora_fwd_batch_workspace_bytes", "qlora_linear_fwd_batch",
+           "qn_act8_encode", "qn_act8_decode", "qlora_linear_bwd_act8",
+           "qlora_bwd_act8_workspace_bytes",
+           "qn_seq_workspace_bytes", "qn_seq_logprob", "qn_seq_logprob_bwd",
+           "qn_pref_loss_fwd", "qn_pref_loss_bwd")
 QN_FWD_BATCH_MAX = 8
 QN_DEQUANT_BATCH_MAX = 16
 QN_CODE_NF4, QN_CODE_FP4, QN_CODE_INT4 = 0, 1, 2
@@ -79,6 +84,22 @@ class _FwdJob(ctypes.Structure):
 
 class _Dropout(ctypes.Structure):
     _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64)]
+
+
+class _Act8Struct(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
+
+
+class _SeqBatch(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("rows", ctypes.c_int64), ("vocab", ctypes.c_int64),
+                ("ld", ctypes.c_int64), ("labels", ctypes.c_void_p),
+                ("offsets", ctypes.c_void_p), ("nseq", ctypes.c_int64)]
+
+
+class _PrefHP(ctypes.Structure):
+    _fields_ = [("beta", ctypes.c_double), ("label_smoothing", ctypes.c_double)]
 
 
 _lib = None
@@ -167,6 +188,29 @@ def lib() -> ctypes.CDLL:
     L.qlora_linear_fwd_noalloc.argtypes = [vp, i64, sp, vp, vp, i32, f32, vp,
                                            i32, vp, vp]
     L.qlora_linear_fwd_noalloc.restype = ctypes.c_int
+    ap = ctypes.POINTER(_Act8Struct)
+    L.qn_act8_encode.argtypes = [vp, i32, ap, vp]
+    L.qn_act8_encode.restype = ctypes.c_int
+    L.qn_act8_decode.argtypes = [ap, vp, i32, vp]
+    L.qn_act8_decode.restype = ctypes.c_int
+    L.qlora_bwd_act8_workspace_bytes.argtypes = [i64, i64, i64, i32]
+    L.qlora_bwd_act8_workspace_bytes.restype = ctypes.c_size_t
+    L.qlora_linear_bwd_act8.argtypes = [vp, ap, i64, sp, vp, vp, i32, f32, vp,
+                                        vp, i32, vp, vp, dp, vp,
+                                        ctypes.c_size_t, vp]
+    L.qlora_linear_bwd_act8.restype = ctypes.c_int
+    bp, pp = ctypes.POINTER(_SeqBatch), ctypes.POINTER(_PrefHP)
+    L.qn_seq_workspace_bytes.argtypes = [i64, i64, i64]
+    L.qn_seq_workspace_bytes.restype = ctypes.c_size_t
+    L.qn_seq_logprob.argtypes = [bp, vp, vp, vp, vp, ctypes.c_size_t, vp]
+    L.qn_seq_logprob.restype = ctypes.c_int
+    L.qn_seq_logprob_bwd.argtypes = [bp, vp, vp, vp, i32, i64, i64, vp]
+    L.qn_seq_logprob_bwd.restype = ctypes.c_int
+    L.qn_pref_loss_fwd.argtypes = [bp, vp, pp, vp, vp, vp, vp, vp, vp,
+                                   ctypes.c_size_t, vp]
+    L.qn_pref_loss_fwd.restype = ctypes.c_int
+    L.qn_pref_loss_bwd.argtypes = [bp, vp, vp, vp, vp, i32, i64, i64, vp]
+    L.qn_pref_loss_bwd.restype = ctypes.c_int
     L.qn_profile_kernel.argtypes = [ctypes.c_char_p, vp, vp, i32]
     L.qn_profile_kernel.restype = ctypes.c_int
     L.qn_strerror.argtypes = [ctypes.c_int]
@@ -180,8 +224,9 @@ def qn_strerror(code: int) -> str:
 
 
 class QNError(RuntimeError):
-    def __init__(self, fn: str, code: int):
-        super().__init__(f"{fn}: {qn_strerror(code)} ({code})")
+    def __init__(self, fn: str, code: int, detail: str = ""):
+        super().__init__(f"{fn}: {qn_strerror(code)} ({code})" +
+                         (f": {detail}" if detail else ""))
         self.code = code
 
 
@@ -598,6 +643,306 @@ def qlora_linear_bwd_dropout(dy, x, w: NF4Tensor, A, B, r: int, alpha: float,
         ctypes.byref(d), _ptr(ws), ws.numel() * ws.element_size(),
         _stream(stream)))
     return dx, dA, dB
+
+
+# ---------------------------------------------------------------------------
+# 8-bit activation checkpoints and the preference loss.  Tensors are checked
+# here (device, type, shape, layout) before their addresses are passed on;
+# calls run on the device of their tensors, and what they allocate belongs to
+# the stream they run on.
+# ---------------------------------------------------------------------------
+
+def _need(fn: str, ok: bool, what: str) -> None:
+    if not ok:
+        raise QNError(fn, QN_EINVAL, what)
+
+
+def _dtype_code(fn: str, name: str, t) -> int:
+    import torch
+    _need(fn, t.dtype in (torch.float32, torch.bfloat16),
+          f"{name} must be float32 or bfloat16, not {t.dtype}")
+    return QN_F32 if t.dtype == torch.float32 else QN_BF16
+
+
+def _torch_dtype(fn: str, code: int):
+    import torch
+    _need(fn, code in (QN_F32, QN_BF16), f"unknown dtype {code}")
+    return torch.float32 if code == QN_F32 else torch.bfloat16
+
+
+def _tensor(fn: str, name: str, t, shape, dtype, device) -> None:
+    """`t` must be a dense tensor of that shape and type on that device."""
+    _need(fn, t.device == device, f"{name} is on {t.device}, not {device}")
+    _need(fn, dtype is None or t.dtype == dtype, f"{name} must be {dtype}, not {t.dtype}")
+    _need(fn, tuple(t.shape) == tuple(shape),
+          f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    _need(fn, t.is_contiguous(), f"{name} must be contiguous")
+
+
+@contextlib.contextmanager
+def _on(device, stream):
+    """The handle of the stream a call runs on (the device's current one when
+    `stream` is None), with that stream and device current inside."""
+    import torch
+    if stream is None:
+        with torch.cuda.device(device):
+            yield torch.cuda.current_stream(device).cuda_stream
+        return
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        yield stream.cuda_stream
+
+
+def _gpu(fn: str, name: str, t):
+    _need(fn, t.is_cuda, f"{name} must be on a GPU")
+    return t.device
+
+
+@dataclass
+class Act8Tensor:
+    """Device buffers of an 8-bit activation checkpoint (see qn_act8 in the
+    header): int8 codes [rows, cols], fp32 scales [rows, ceil(cols / 64)]."""
+    codes: "object"
+    scale: "object"
+    rows: int
+    cols: int
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, device="cuda"):
+        import torch
+        return cls(torch.empty((rows, cols), dtype=torch.int8, device=device),
+                   torch.empty((rows, -(-cols // QN_BLOCK)), dtype=torch.float32,
+                               device=device), rows, cols)
+
+    def as_struct(self) -> _Act8Struct:
+        return _Act8Struct(self.codes.data_ptr(), self.scale.data_ptr(),
+                           self.rows, self.cols)
+
+    def check(self, fn: str, device) -> None:
+        import torch
+        _need(fn, self.cols >= 1, "a checkpoint has at least one column")
+        _tensor(fn, "codes", self.codes, (self.rows, self.cols), torch.int8, device)
+        _tensor(fn, "scale", self.scale, (self.rows, -(-self.cols // QN_BLOCK)),
+                torch.float32, device)
+
+
+def qn_act8_encode(x, out: Act8Tensor | None = None, stream=None):
+    """8-bit checkpoint of a device activation [rows, cols] (fp32 or bf16,
+    contiguous); returns the Act8Tensor."""
+    fn = "qn_act8_encode"
+    dev = _gpu(fn, "x", x)
+    code = _dtype_code(fn, "x", x)
+    _need(fn, x.dim() == 2 and x.shape[1] >= 1, "x must be [rows, cols]")
+    _tensor(fn, "x", x, x.shape, None, dev)
+    with _on(dev, stream) as st:
+        if out is None:
+            out = Act8Tensor.empty(x.shape[0], x.shape[1], device=dev)
+        _need(fn, (out.rows, out.cols) == tuple(x.shape), "out has another shape than x")
+        out.check(fn, dev)
+        s = out.as_struct()
+        _check(fn, lib().qn_act8_encode(_ptr(x), code, ctypes.byref(s), st))
+    return out
+
+
+def qn_act8_decode(x8: Act8Tensor, out=None, dtype: int = QN_BF16, stream=None):
+    """The restored activation [rows, cols] in bf16 or fp32 (`out`'s type
+    when it is given)."""
+    import torch
+    fn = "qn_act8_decode"
+    dev = _gpu(fn, "codes", x8.codes)
+    x8.check(fn, dev)
+    with _on(dev, stream) as st:
+        if out is None:
+            out = torch.empty((x8.rows, x8.cols), dtype=_torch_dtype(fn, dtype), device=dev)
+        _tensor(fn, "out", out, (x8.rows, x8.cols), None, dev)
+        s = x8.as_struct()
+        _check(fn, lib().qn_act8_decode(ctypes.byref(s), _ptr(out),
+                                        _dtype_code(fn, "out", out), st))
+    return out
+
+
+def qlora_bwd_act8_workspace_bytes(M: int, N: int, K: int, r: int) -> int:
+    return int(lib().qlora_bwd_act8_workspace_bytes(M, N, K, r))
+
+
+def qlora_linear_bwd_act8(dy, x8: Act8Tensor, w: NF4Tensor, A, B, r: int,
+                          alpha: float, t_saved, p: float = 0.0, seed: int = 0,
+                          dx=None, dx_dtype: int = QN_F32, need_dx: bool = True,
+                          dA=None, dB=None, ws=None, stream=None):
+    """Fused backward from an 8-bit checkpoint of the layer's input, with LoRA
+    dropout (probability p, 64-bit seed) if p > 0; returns (dx, dA, dB), dx
+    None where need_dx is False."""
+    import torch
+    fn = "qlora_linear_bwd_act8"
+    dev = _gpu(fn, "dy", dy)
+    M, N, K = x8.rows, w.rows, w.cols
+    bf, f32 = torch.bfloat16, torch.float32
+    x8.check(fn, dev)
+    _need(fn, x8.cols == K, f"the checkpoint has {x8.cols} columns, the weight {K}")
+    _need(fn, M >= 1 and 1 <= r <= QN_MAX_RANK, "M or r out of range")
+    _tensor(fn, "dy", dy, (M, N), bf, dev)
+    _tensor(fn, "A", A, (r, K), bf, dev)
+    _tensor(fn, "B", B, (N, r), bf, dev)
+    _tensor(fn, "t_saved", t_saved, (M, r), f32, dev)
+    with _on(dev, stream) as st:
+        if not need_dx:
+            _need(fn, dx is None, "dx given with need_dx=False")
+        else:
+            if dx is None:
+                dx = torch.empty((M, K), device=dev, dtype=_torch_dtype(fn, dx_dtype))
+            _tensor(fn, "dx", dx, (M, K), None, dev)
+            dx_dtype = _dtype_code(fn, "dx", dx)
+        if dA is None:
+            dA = torch.empty((r, K), device=dev, dtype=f32)
+        if dB is None:
+            dB = torch.empty((N, r), device=dev, dtype=f32)
+        _tensor(fn, "dA", dA, (r, K), f32, dev)
+        _tensor(fn, "dB", dB, (N, r), f32, dev)
+        if ws is None:
+            ws = torch.empty(max(1, qlora_bwd_act8_workspace_bytes(M, N, K, r)),
+                             dtype=torch.uint8, device=dev)
+        _need(fn, ws.device == dev and ws.is_contiguous(), "ws must be contiguous, on dy's device")
+        wt, xt = w.as_struct(), x8.as_struct()
+        d = _Dropout(float(p), int(seed) & 0xFFFFFFFFFFFFFFFF)
+        _check(fn, lib().qlora_linear_bwd_act8(
+            _ptr(dy), ctypes.byref(xt), M, ctypes.byref(wt), _ptr(A), _ptr(B), r,
+            float(alpha), _ptr(t_saved), _ptr(dx), dx_dtype, _ptr(dA), _ptr(dB),
+            ctypes.byref(d), _ptr(ws), ws.numel() * ws.element_size(), st))
+    return dx, dA, dB
+
+
+def qn_seq_workspace_bytes(rows: int, vocab: int, nseq: int) -> int:
+    return int(lib().qn_seq_workspace_bytes(rows, vocab, nseq))
+
+
+def _seq_batch(fn: str, logits, labels, offsets):
+    """(device, qn_seq_batch) of logits [rows, vocab] whose rows may be apart
+    (stride(0) >= vocab), labels [rows] and offsets [nseq + 1]."""
+    import torch
+    dev = _gpu(fn, "logits", logits)
+    code = _dtype_code(fn, "logits", logits)
+    _need(fn, logits.dim() == 2 and logits.shape[1] >= 1, "logits must be [rows, vocab]")
+    rows, vocab = logits.shape
+    _need(fn, vocab == 1 or logits.stride(1) == 1, "a row of logits must be contiguous")
+    ld = logits.stride(0) if rows > 1 else vocab
+    _need(fn, ld >= vocab, "rows of logits overlap")
+    _tensor(fn, "labels", labels, (rows,), torch.int64, dev)
+    _need(fn, offsets.dim() == 1 and offsets.numel() >= 2, "offsets must be [nseq + 1]")
+    _tensor(fn, "offsets", offsets, offsets.shape, torch.int64, dev)
+    return dev, _SeqBatch(_ptr(logits), code, rows, vocab, ld, _ptr(labels),
+                          _ptr(offsets), offsets.numel() - 1)
+
+
+def _seq_outputs(fn, b, dev, lse, logp, status, ws):
+    import torch
+    if lse is None:
+        lse = torch.empty(b.rows, dtype=torch.float32, device=dev)
+    if logp is None:
+        logp = torch.empty(b.nseq, dtype=torch.float32, device=dev)
+    if ws is None:
+        ws = torch.empty(max(1, qn_seq_workspace_bytes(b.rows, b.vocab, b.nseq)),
+                         dtype=torch.uint8, device=dev)
+    _tensor(fn, "lse", lse, (b.rows,), torch.float32, dev)
+    _tensor(fn, "logp", logp, (b.nseq,), torch.float32, dev)
+    _need(fn, ws.device == dev and ws.is_contiguous(), "ws must be contiguous, on the logits' device")
+    if status is not None:
+        _tensor(fn, "status", status, (1,), torch.int32, dev)
+    return lse, logp, ws
+
+
+def qn_seq_logprob(logits, labels, offsets, lse=None, logp=None, status=None,
+                   ws=None, stream=None):
+    """Log-probability of each packed sequence and log-sum-exp of each row;
+    returns (logp [nseq], lse [rows])."""
+    fn = "qn_seq_logprob"
+    dev, b = _seq_batch(fn, logits, labels, offsets)
+    with _on(dev, stream) as st:
+        lse, logp, ws = _seq_outputs(fn, b, dev, lse, logp, status, ws)
+        _check(fn, lib().qn_seq_logprob(
+            ctypes.byref(b), _ptr(lse), _ptr(logp), _ptr(status), _ptr(ws),
+            ws.numel() * ws.element_size(), st))
+    return logp, lse
+
+
+@dataclass
+class PrefLoss:
+    """Outputs of qn_pref_loss_fwd: loss [P], logp [2P], dlogp [2P] (the
+    derivative of a pair's loss by its sequences' logp) and lse [rows]."""
+    loss: "object"
+    logp: "object"
+    dlogp: "object"
+    lse: "object"
+
+
+def qn_pref_loss_fwd(logits, labels, offsets, ref_logp, beta: float,
+                     label_smoothing: float = 0.0, out: PrefLoss | None = None,
+                     status=None, ws=None, stream=None):
+    """Paired log-ratio loss of sequences p (chosen) and P + p (rejected);
+    ref_logp [2P] or None for zeros; returns a PrefLoss."""
+    import torch
+    fn = "qn_pref_loss_fwd"
+    dev, b = _seq_batch(fn, logits, labels, offsets)
+    _need(fn, b.nseq % 2 == 0, "sequences must come in pairs")
+    if ref_logp is not None:
+        _tensor(fn, "ref_logp", ref_logp, (b.nseq,), torch.float32, dev)
+    with _on(dev, stream) as st:
+        lse, logp, ws = _seq_outputs(fn, b, dev, out and out.lse, out and out.logp, status, ws)
+        if out is None:
+            out = PrefLoss(torch.empty(b.nseq // 2, dtype=torch.float32, device=dev), logp,
+                           torch.empty(b.nseq, dtype=torch.float32, device=dev), lse)
+        _tensor(fn, "loss", out.loss, (b.nseq // 2,), torch.float32, dev)
+        _tensor(fn, "dlogp", out.dlogp, (b.nseq,), torch.float32, dev)
+        hp = _PrefHP(float(beta), float(label_smoothing))
+        _check(fn, lib().qn_pref_loss_fwd(
+            ctypes.byref(b), _ptr(ref_logp), ctypes.byref(hp), _ptr(lse), _ptr(logp),
+            _ptr(out.loss), _ptr(out.dlogp), _ptr(status), _ptr(ws),
+            ws.numel() * ws.element_size(), st))
+    return out
+
+
+def _seq_bwd(fn, logits, labels, offsets, lse, dlogp, dloss, dlogits, dl_dtype, stream):
+    import torch
+    dev, b = _seq_batch(fn, logits, labels, offsets)
+    _tensor(fn, "lse", lse, (b.rows,), torch.float32, dev)
+    _tensor(fn, "dlogp", dlogp, (b.nseq,), torch.float32, dev)
+    if dloss is not None:
+        _need(fn, b.nseq % 2 == 0, "sequences must come in pairs")
+        _tensor(fn, "dloss", dloss, (b.nseq // 2,), torch.float32, dev)
+    with _on(dev, stream) as st:
+        if dlogits is None:
+            dt = logits.dtype if dl_dtype is None else _torch_dtype(fn, dl_dtype)
+            dlogits = torch.empty((b.rows, b.vocab), dtype=dt, device=dev)
+        _need(fn, dlogits.device == dev, f"dlogits is on {dlogits.device}, not {dev}")
+        _need(fn, dlogits.dim() == 2 and dlogits.shape[0] == b.rows and
+              dlogits.shape[1] >= b.vocab, "dlogits must be [rows, cols], cols >= vocab")
+        cols = dlogits.shape[1]
+        _need(fn, cols == 1 or dlogits.stride(1) == 1, "a row of dlogits must be contiguous")
+        ld = dlogits.stride(0) if b.rows > 1 else max(cols, b.ld)
+        args = [ctypes.byref(b), _ptr(lse), _ptr(dlogp)]
+        if fn == "qn_pref_loss_bwd":
+            args.append(_ptr(dloss))
+        _check(fn, getattr(lib(), fn)(*args, _ptr(dlogits), _dtype_code(fn, "dlogits", dlogits),
+                                      cols, ld, st))
+    return dlogits
+
+
+def qn_seq_logprob_bwd(logits, labels, offsets, lse, dlogp, dlogits=None,
+                       dl_dtype: int | None = None, stream=None):
+    """Gradient of sum(dlogp * logp) by the logits.  dlogits may have more
+    columns than the logits (written as zeros) and may be the logits
+    themselves; it is allocated in dl_dtype (the logits' type) when None."""
+    return _seq_bwd("qn_seq_logprob_bwd", logits, labels, offsets, lse, dlogp, None,
+                    dlogits, dl_dtype, stream)
+
+
+def qn_pref_loss_bwd(logits, labels, offsets, fwd: PrefLoss, dloss=None,
+                     dlogits=None, dl_dtype: int | None = None, stream=None):
+    """Gradient of sum(dloss * loss) by the logits (dloss None: the mean
+    loss), from what qn_pref_loss_fwd returned; dlogits as in
+    qn_seq_logprob_bwd."""
+    return _seq_bwd("qn_pref_loss_bwd", logits, labels, offsets, fwd.lse, fwd.dlogp, dloss,
+                    dlogits, dl_dtype, stream)
 
 
 def qn_profile_kernel(name: str | None, starts=None, stops=None) -> int:

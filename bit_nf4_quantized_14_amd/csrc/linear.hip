@@ -87,6 +87,12 @@ size_t qlora_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t r,
   return 0;
 }
 
+size_t qlora_bwd_act8_workspace_bytes(int64_t M, int64_t N, int64_t K,
+                                      int32_t r) {
+  if (M <= 0 || N <= 0 || K <= 0 || r < 1 || r > QN_MAX_RANK) return 0;
+  return qn::bwd_workspace_layout(M, N, K, r, true).total;
+}
+
 }  // extern "C"
 
 namespace {
@@ -171,23 +177,30 @@ int linear_fwd(const uint16_t* x, int64_t M, const nf4_tensor* w,
   return check_launch();
 }
 
-int linear_bwd(const uint16_t* dy, const uint16_t* x, int64_t M,
-               const nf4_tensor* w, const uint16_t* A, const uint16_t* B,
-               int32_t r, float alpha, const float* t_saved, void* dx,
-               int32_t dx_dtype, float* dA, float* dB, const qn_dropout* drop,
-               void* ws, size_t ws_bytes, void* stream) {
-  if (dy == nullptr || x == nullptr || A == nullptr || B == nullptr ||
-      t_saved == nullptr || dx == nullptr || dA == nullptr || dB == nullptr)
+// X is either x (bf16) or the checkpoint x8.  With x8, dx may be null: the
+// gradient of X is then not formed.
+int linear_bwd(const uint16_t* dy, const uint16_t* x, const qn_act8* x8,
+               int64_t M, const nf4_tensor* w, const uint16_t* A,
+               const uint16_t* B, int32_t r, float alpha, const float* t_saved,
+               void* dx, int32_t dx_dtype, float* dA, float* dB,
+               const qn_dropout* drop, void* ws, size_t ws_bytes, void* stream) {
+  const bool act8 = x8 != nullptr, want_dx = !act8 || dx != nullptr;
+  if (dy == nullptr || (x == nullptr && !act8) || A == nullptr || B == nullptr ||
+      t_saved == nullptr || (want_dx && dx == nullptr) || dA == nullptr ||
+      dB == nullptr)
     return QN_EINVAL;
   if (!valid_linear(M, w, r)) return QN_EINVAL;
-  if (dx_dtype != QN_F32 && dx_dtype != QN_BF16) return QN_EINVAL;
+  if (want_dx && dx_dtype != QN_F32 && dx_dtype != QN_BF16) return QN_EINVAL;
   if (!aligned16(dy) || !aligned16(x) || !aligned16(A) || !aligned16(dx))
+    return QN_EINVAL;
+  if (act8 && (!valid_act8(x8) || x8->rows != M || x8->cols != w->cols ||
+               !aligned16(x8->codes)))
     return QN_EINVAL;
   qn::DropArgs da{};
   bool use_drop = false;
   if (!drop_args(drop, &da, &use_drop)) return QN_EINVAL;
   const int64_t N = w->rows, K = w->cols;
-  const qn::BwdWorkspace L = qn::bwd_workspace_layout(M, N, K, r);
+  const qn::BwdWorkspace L = qn::bwd_workspace_layout(M, N, K, r, act8);
   if (ws == nullptr || ws_bytes < L.total || !aligned16(ws))
     return QN_EWORKSPACE;
   uint16_t* Bt = ws_at<uint16_t>(ws, L.bt);
@@ -226,9 +239,15 @@ int linear_bwd(const uint16_t* dy, const uint16_t* x, int64_t M,
   zero_split_counters(f1.P1, split_ws, gemm_split_plan(M, K, N, use_drop));
   launch_finish(st, f1);
   // dX = dY W' + (s G) A
-  launch_gemm<true>(st, dy, w, Gh, Gl, Atp, Mi, L.rpad, dx,
-                    (int)(dx_dtype == QN_BF16), use_drop ? &da : nullptr,
-                    split_ws);
+  if (want_dx)
+    launch_gemm<true>(st, dy, w, Gh, Gl, Atp, Mi, L.rpad, dx,
+                      (int)(dx_dtype == QN_BF16), use_drop ? &da : nullptr,
+                      split_ws);
+  if (act8) {
+    uint16_t* xr = ws_at<uint16_t>(ws, L.xr);
+    launch_act8_decode(st, *x8, xr, QN_BF16);
+    x = xr;
+  }
   // dA = (s G)^T X: row-block partials of out[k][j] -> dA[j][k]
   const StreamPlan Pa = stream_plan(RS_COLS, M, K, jt, use_drop);
   launch_rank_stream<RS_COLS>(st, "k_rank_stream_da", Pa, x, Mi, Ki, nullptr,
@@ -269,8 +288,19 @@ int qlora_linear_bwd(const uint16_t* dy, const uint16_t* x, int64_t M,
                      const float* t_saved, void* dx, int32_t dx_dtype,
                      float* dA, float* dB, void* ws, size_t ws_bytes,
                      void* stream) {
-  return linear_bwd(dy, x, M, w, A, B, r, alpha, t_saved, dx, dx_dtype, dA,
-                    dB, nullptr, ws, ws_bytes, stream);
+  return linear_bwd(dy, x, nullptr, M, w, A, B, r, alpha, t_saved, dx,
+                    dx_dtype, dA, dB, nullptr, ws, ws_bytes, stream);
+}
+
+int qlora_linear_bwd_act8(const uint16_t* dy, const qn_act8* x8, int64_t M,
+                          const nf4_tensor* w, const uint16_t* A,
+                          const uint16_t* B, int32_t r, float alpha,
+                          const float* t_saved, void* dx, int32_t dx_dtype,
+                          float* dA, float* dB, const qn_dropout* drop,
+                          void* ws, size_t ws_bytes, void* stream) {
+  if (x8 == nullptr) return QN_EINVAL;
+  return linear_bwd(dy, nullptr, x8, M, w, A, B, r, alpha, t_saved, dx,
+                    dx_dtype, dA, dB, drop, ws, ws_bytes, stream);
 }
 
 int qlora_linear_bwd_dropout(const uint16_t* dy, const uint16_t* x,
@@ -281,8 +311,8 @@ int qlora_linear_bwd_dropout(const uint16_t* dy, const uint16_t* x,
                              const qn_dropout* drop, void* ws,
                              size_t ws_bytes, void* stream) {
   if (drop == nullptr) return QN_EINVAL;
-  return linear_bwd(dy, x, M, w, A, B, r, alpha, t_saved, dx, dx_dtype, dA,
-                    dB, drop, ws, ws_bytes, stream);
+  return linear_bwd(dy, x, nullptr, M, w, A, B, r, alpha, t_saved, dx,
+                    dx_dtype, dA, dB, drop, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -176,7 +176,7 @@ FwdWorkspace fwd_workspace_layout(int64_t M, int64_t N, int64_t K,
 }
 
 BwdWorkspace bwd_workspace_layout(int64_t M, int64_t N, int64_t K,
-                                  int32_t r) {
+                                  int32_t r, bool act8) {
   BwdWorkspace L{};
   const int jt = rank_tiles(r);
   L.rpad = 16 * jt;
@@ -208,6 +208,8 @@ BwdWorkspace bwd_workspace_layout(int64_t M, int64_t N, int64_t K,
   off += align256(size_t(Pg.nb) * M * L.rpad * 4);
   L.pcol = off;
   off += align256(pcol * L.rpad * 4);
+  L.xr = off;
+  if (act8) off += align256(size_t(M) * K * 2);
   L.total = off;
   return L;
 }

@@ -1,0 +1,437 @@
+// Log-probabilities of packed sequences under given logits, the paired
+// log-ratio loss of preference tuning, and their gradients.
+//
+//   lse_t  = log sum_v exp l_tv         logp_s = sum_t (l_{t,label_t} - lse_t)
+//   h_p    = beta ((logp_p - ref_p) - (logp_{P+p} - ref_{P+p}))
+//   loss_p = -(1 - e) log sigmoid(h_p) - e log sigmoid(-h_p)
+//   dl_tv  = c_s (1[v = label_t] - exp(l_tv - lse_t))
+//
+// The forward reads the logits once and the backward reads them once and
+// writes the gradient once; both are bound by memory.  The loss of a pair
+// needs every row of both of its sequences before the first gradient, so
+// the two passes cannot be one.
+#include <cmath>
+
+#include "qn_host.h"
+
+namespace {
+
+using namespace qn;
+
+constexpr int SQ_THREADS = 256;                // 4 waves
+constexpr int SQ_STEP = SQ_THREADS * 8;        // elements a workgroup takes at once
+constexpr float SQ_LOG2E = 1.4426950408889634f;
+constexpr float SQ_NEG_INF = -__builtin_inff();
+
+// Eight consecutive logits from element c of a row; elements from `vocab`
+// on read as -infinity.  16-byte loads at any alignment.
+template <bool F32>
+__device__ __forceinline__ void sq_load(const char* row, int64_t c, int64_t vocab,
+                                        float (&v)[8]) {
+  typedef uint32_t v4 __attribute__((ext_vector_type(4), aligned(2)));
+  if (c + 8 <= vocab) {
+    if constexpr (F32) {
+      const v4 p = *reinterpret_cast<const v4*>(row + 4 * c);
+      const v4 q = *reinterpret_cast<const v4*>(row + 4 * c + 16);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = __uint_as_float(p[i]);
+        v[4 + i] = __uint_as_float(q[i]);
+      }
+    } else {
+      const v4 p = *reinterpret_cast<const v4*>(row + 2 * c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(p[i] << 16);
+        v[2 * i + 1] = __uint_as_float(p[i] & 0xFFFF0000u);
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] = SQ_NEG_INF;
+    if (c + i < vocab) {
+      if constexpr (F32)
+        v[i] = reinterpret_cast<const float*>(row)[c + i];
+      else
+        v[i] = bf16_to_f32(reinterpret_cast<const uint16_t*>(row)[c + i]);
+    }
+  }
+}
+
+// A running maximum m and s = sum exp(x - m).  m starts at -infinity, where
+// the shift is taken as 0 so that no infinity meets its own.
+struct MaxSum {
+  float m, s;
+};
+
+__device__ __forceinline__ float sq_shift(float m) { return m == SQ_NEG_INF ? 0.0f : m; }
+
+__device__ __forceinline__ float sq_exp(float x) {
+  return __builtin_amdgcn_exp2f(x * SQ_LOG2E);
+}
+
+__device__ __forceinline__ MaxSum sq_join(const MaxSum& a, const MaxSum& b) {
+  const float m = fmaxf(a.m, b.m), z = sq_shift(m);
+  return MaxSum{m, a.s * sq_exp(a.m - z) + b.s * sq_exp(b.m - z)};
+}
+
+struct SeqArgs {
+  const char* logits;
+  const int64_t* labels;
+  const int64_t* offsets;
+  int64_t vocab, ld, chunk;
+  int32_t rows, nseq, nchunk;
+};
+
+// Maximum and sum of one chunk of one row.  Rows that are not counted are
+// not read.
+template <bool F32>
+__global__ __launch_bounds__(SQ_THREADS) void k_seq_rows(SeqArgs a, MaxSum* __restrict__ part,
+                                                         float* __restrict__ lse) {
+  __shared__ MaxSum red[SQ_THREADS / 64];
+  const int row = (int)(blockIdx.x / (unsigned)a.nchunk);
+  const int ch = (int)(blockIdx.x - (unsigned)row * (unsigned)a.nchunk);
+  const int64_t label = a.labels[row];
+  const bool counted = label >= 0 && label < a.vocab && row >= a.offsets[0] &&
+                       row < a.offsets[a.nseq];
+  if (!counted) {
+    if (ch == 0 && threadIdx.x == 0) lse[row] = 0.0f;
+    return;
+  }
+  const char* p = a.logits + (int64_t)row * a.ld * (F32 ? 4 : 2);
+  const int64_t begin = ch * a.chunk, end = min(a.vocab, begin + a.chunk);
+  MaxSum r{SQ_NEG_INF, 0.0f};
+  for (int64_t c = begin + 8 * threadIdx.x; c < end; c += SQ_STEP) {
+    float v[8];
+    sq_load<F32>(p, c, end, v);
+    float m = r.m;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, v[i]);
+    const float z = sq_shift(m);
+    float s = r.s * sq_exp(r.m - z);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += sq_exp(v[i] - z);
+    r = MaxSum{m, s};
+  }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1)
+    r = sq_join(r, MaxSum{__shfl_xor(r.m, off), __shfl_xor(r.s, off)});
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = r;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < SQ_THREADS / 64; ++w) r = sq_join(r, red[w]);
+    part[(int64_t)row * a.nchunk + ch] = r;
+  }
+}
+
+__device__ __forceinline__ double sq_logit(const SeqArgs& a, bool f32, int64_t row, int64_t c) {
+  const int64_t i = row * a.ld + c;
+  return f32 ? (double)reinterpret_cast<const float*>(a.logits)[i]
+             : (double)bf16_to_f32(reinterpret_cast<const uint16_t*>(a.logits)[i]);
+}
+
+// log(1 + exp(-x)) = -log sigmoid(x)
+__device__ __forceinline__ double sq_softplus_neg(double x) {
+  return log1p(exp(-fabs(x))) + (x < 0.0 ? -x : 0.0);
+}
+
+struct PrefArgs {
+  const float* ref;
+  float *loss, *dlogp;
+  double beta, smooth;
+  int32_t pairs;     // 0: log-probabilities only
+};
+
+constexpr int SQ_FIN = 1024;
+
+// Sum over the rows of sequence s, in a fixed order; writes lse of its rows
+// and (thread 0) logp[s].  Every thread gets the sum.
+__device__ double sq_sequence(const SeqArgs& a, bool f32, const MaxSum* __restrict__ part,
+                              float* __restrict__ lse, float* __restrict__ logp,
+                              int32_t* status, int s, double* red) {
+  const int64_t lo = a.offsets[s], hi = a.offsets[s + 1];
+  const int64_t begin = min(max(lo, (int64_t)0), (int64_t)a.rows);
+  const int64_t end = min(max(hi, begin), (int64_t)a.rows);
+  bool bad = begin != lo || end != hi;
+  double sum = 0.0;
+  for (int64_t t = begin + threadIdx.x; t < end; t += SQ_FIN) {
+    const int64_t label = a.labels[t];
+    if (label >= a.vocab) bad = true;
+    if (label < 0 || label >= a.vocab) continue;
+    const double hit = sq_logit(a, f32, t, label);
+    const MaxSum* q = part + t * a.nchunk;
+    MaxSum r = q[0];
+    for (int c = 1; c < a.nchunk; ++c) r = sq_join(r, q[c]);
+    const double l = (double)r.m + log((double)r.s);
+    lse[t] = (float)l;
+    sum += hit - l;
+  }
+  if (bad && status != nullptr) *status = QN_EINVAL;
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off);
+  __syncthreads();                       // red is free again
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  sum = 0.0;
+  for (int w = 0; w < SQ_FIN / 64; ++w) sum += red[w];
+  if (threadIdx.x == 0) logp[s] = (float)sum;
+  return sum;
+}
+
+// One workgroup per sequence, or per pair of sequences and their loss.
+__global__ __launch_bounds__(SQ_FIN) void k_seq_finish(SeqArgs a, int f32,
+                                                       const MaxSum* __restrict__ part,
+                                                       float* __restrict__ lse,
+                                                       float* __restrict__ logp,
+                                                       int32_t* status, PrefArgs pa) {
+  __shared__ double red[SQ_FIN / 64];
+  const int b = blockIdx.x;
+  const double c = sq_sequence(a, f32 != 0, part, lse, logp, status, b, red);
+  if (pa.pairs == 0) return;
+  const double r = sq_sequence(a, f32 != 0, part, lse, logp, status, pa.pairs + b, red);
+  if (threadIdx.x != 0) return;
+  const double rc = pa.ref != nullptr ? (double)pa.ref[b] : 0.0;
+  const double rr = pa.ref != nullptr ? (double)pa.ref[pa.pairs + b] : 0.0;
+  const double h = pa.beta * ((c - rc) - (r - rr)), e = pa.smooth;
+  pa.loss[b] = (float)((1.0 - e) * sq_softplus_neg(h) + (e > 0.0 ? e * sq_softplus_neg(-h) : 0.0));
+  // sigmoid(-h) = 1 / (1 + exp(h)): an exp that overflows gives 0
+  const double g = pa.beta * (e / (1.0 + exp(-h)) - (1.0 - e) / (1.0 + exp(h)));
+  pa.dlogp[b] = (float)g;
+  pa.dlogp[pa.pairs + b] = (float)-g;
+}
+
+struct SeqBwdArgs {
+  const float *lse, *dlogp, *dloss;
+  char* out;
+  int64_t cols, ld_out;
+  int32_t pairs;      // 0: dlogp alone
+  float mean;         // dloss of every pair where dloss is null
+};
+
+template <bool F32>
+__device__ __forceinline__ void sq_store(char* row, int64_t c, int64_t cols, const float (&v)[8]) {
+  typedef uint32_t v4 __attribute__((ext_vector_type(4), aligned(2)));
+  if (c + 8 <= cols) {
+    if constexpr (F32) {
+      *reinterpret_cast<v4*>(row + 4 * c) =
+          v4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+      *reinterpret_cast<v4*>(row + 4 * c + 16) =
+          v4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])};
+    } else {
+      *reinterpret_cast<v4*>(row + 2 * c) = v4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                               pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c + i < cols) {
+      if constexpr (F32)
+        reinterpret_cast<float*>(row)[c + i] = v[i];
+      else
+        reinterpret_cast<uint16_t*>(row)[c + i] = (uint16_t)(pack_bf16x2(v[i], 0.0f) & 0xFFFFu);
+    }
+}
+
+// Gradient of one chunk of one row.  Its sequence is the number of
+// offsets[1..nseq] that are not behind the row, counted by every wave for
+// itself (64 offsets at a time).
+template <bool FIN, bool FOUT>
+__global__ __launch_bounds__(SQ_THREADS) void k_seq_bwd(SeqArgs a, SeqBwdArgs g) {
+  const int row = (int)(blockIdx.x / (unsigned)a.nchunk);
+  const int ch = (int)(blockIdx.x - (unsigned)row * (unsigned)a.nchunk);
+  const int lane = threadIdx.x & 63;
+  const int64_t label = a.labels[row];
+  int seq = 0;
+  for (int base = 0; base < a.nseq; base += 64) {
+    const bool before = base + lane < a.nseq && a.offsets[1 + base + lane] <= row;
+    seq += __popcll(__ballot(before));
+  }
+  const bool counted = label >= 0 && label < a.vocab && row >= a.offsets[0] && seq < a.nseq;
+  char* out = g.out + (int64_t)row * g.ld_out * (FOUT ? 4 : 2);
+  const int64_t begin = ch * a.chunk, end = min(g.cols, begin + a.chunk);
+  if (!counted) {
+    const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int64_t c = begin + 8 * threadIdx.x; c < end; c += SQ_STEP)
+      sq_store<FOUT>(out, c, end, zero);
+    return;
+  }
+  float coef = g.dlogp[seq];
+  if (g.pairs > 0)
+    coef *= g.dloss != nullptr ? g.dloss[seq < g.pairs ? seq : seq - g.pairs] : g.mean;
+  const float lse = g.lse[row];
+  const char* p = a.logits + (int64_t)row * a.ld * (FIN ? 4 : 2);
+  for (int64_t c = begin + 8 * threadIdx.x; c < end; c += SQ_STEP) {
+    float v[8];
+    sq_load<FIN>(p, c, a.vocab, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = -coef * sq_exp(v[i] - lse);
+    if (label >= c && label < c + 8) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += c + i == label ? coef : 0.0f;
+    }
+    if (c + 8 > a.vocab) {     // padding columns: zero whatever coef is
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = c + i < a.vocab ? v[i] : 0.0f;
+    }
+    sq_store<FOUT>(out, c, end, v);
+  }
+}
+
+bool sized_ptr(const void* p, int32_t dtype) {
+  return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (dtype == QN_F32 ? 3u : 1u)) == 0;
+}
+
+// A launch holds less than 2^32 threads: rows in workgroups of SQ_THREADS
+// (SQ_FILL and more rows are not split), sequences in ones of SQ_FIN.
+bool valid_sizes(int64_t rows, int64_t vocab, int64_t nseq) {
+  return rows >= 0 && rows < (1LL << 24) && nseq >= 1 && nseq < (1LL << 22) &&
+         vocab >= 1 && vocab <= (1LL << 30);
+}
+
+bool valid_batch(const qn_seq_batch* b) {
+  if (b == nullptr || !valid_sizes(b->rows, b->vocab, b->nseq)) return false;
+  if (b->dtype != QN_F32 && b->dtype != QN_BF16) return false;
+  if (b->ld < b->vocab || b->ld > (1LL << 31) || b->offsets == nullptr) return false;
+  return b->rows == 0 || (sized_ptr(b->logits, b->dtype) && b->labels != nullptr);
+}
+
+// Workgroups per row and the columns of each: one where the rows fill the
+// GPU, else about SQ_FILL workgroups in all, of at least one step each.
+constexpr int64_t SQ_FILL = 8 * G_CUS;
+void split_rows(int64_t rows, int64_t cols, int64_t* chunk, int32_t* nchunk) {
+  const int64_t steps = cdiv(cols, SQ_STEP);
+  const int64_t want = rows > 0 ? std::min(steps, cdiv(SQ_FILL, rows)) : 1;
+  const int64_t per = cdiv(steps, want);
+  *chunk = per * SQ_STEP;
+  *nchunk = (int32_t)cdiv(steps, per);
+}
+
+SeqArgs seq_args(const qn_seq_batch* b, int64_t cols) {
+  SeqArgs a;
+  a.logits = static_cast<const char*>(b->logits);
+  a.labels = b->labels;
+  a.offsets = b->offsets;
+  a.vocab = b->vocab;
+  a.ld = b->ld;
+  a.rows = (int32_t)b->rows;
+  a.nseq = (int32_t)b->nseq;
+  split_rows(b->rows, cols, &a.chunk, &a.nchunk);
+  return a;
+}
+
+int seq_forward(const qn_seq_batch* b, float* lse, float* logp, int32_t* status,
+                void* ws, size_t ws_bytes, void* stream, const PrefArgs& pa) {
+  if (logp == nullptr || (b->rows > 0 && lse == nullptr)) return QN_EINVAL;
+  const SeqArgs a = seq_args(b, b->vocab);
+  if (ws == nullptr || !aligned16(ws) ||
+      ws_bytes < qn_seq_workspace_bytes(b->rows, b->vocab, b->nseq))
+    return QN_EWORKSPACE;
+  MaxSum* part = static_cast<MaxSum*>(ws);
+  hipStream_t st = (hipStream_t)stream;
+  const bool f32 = b->dtype == QN_F32;
+  if (b->rows > 0) {
+    const dim3 grid((unsigned)(b->rows * a.nchunk));
+    if (f32)
+      QN_LAUNCH("k_seq_rows", k_seq_rows<true>, grid, dim3(SQ_THREADS), st, a, part, lse);
+    else
+      QN_LAUNCH("k_seq_rows", k_seq_rows<false>, grid, dim3(SQ_THREADS), st, a, part, lse);
+  }
+  QN_LAUNCH("k_seq_finish", k_seq_finish,
+            dim3((unsigned)(pa.pairs > 0 ? pa.pairs : b->nseq)), dim3(SQ_FIN), st, a,
+            (int)f32, part, lse, logp, status, pa);
+  return check_launch();
+}
+
+int seq_backward(const qn_seq_batch* b, const float* lse, const float* dlogp,
+                 const float* dloss, int32_t pairs, void* dl, int32_t dl_dtype,
+                 int64_t cols, int64_t ld_dl, void* stream) {
+  if (!valid_batch(b) || dlogp == nullptr) return QN_EINVAL;
+  if (dl_dtype != QN_F32 && dl_dtype != QN_BF16) return QN_EINVAL;
+  if (cols < b->vocab || cols > (1LL << 30) || ld_dl < cols || ld_dl > (1LL << 31))
+    return QN_EINVAL;
+  if (b->rows == 0) return QN_OK;
+  if (lse == nullptr || !sized_ptr(dl, dl_dtype)) return QN_EINVAL;
+  // in place means element for element
+  if (dl == b->logits && (dl_dtype != b->dtype || ld_dl != b->ld)) return QN_EINVAL;
+  const SeqArgs a = seq_args(b, cols);
+  SeqBwdArgs g;
+  g.lse = lse;
+  g.dlogp = dlogp;
+  g.dloss = dloss;
+  g.out = static_cast<char*>(dl);
+  g.cols = cols;
+  g.ld_out = ld_dl;
+  g.pairs = pairs;
+  g.mean = pairs > 0 ? (float)(1.0 / pairs) : 0.0f;
+  hipStream_t st = (hipStream_t)stream;
+  const dim3 grid((unsigned)(b->rows * a.nchunk)), wg(SQ_THREADS);
+  const bool fi = b->dtype == QN_F32, fo = dl_dtype == QN_F32;
+  if (fi && fo)
+    QN_LAUNCH("k_seq_bwd", (k_seq_bwd<true, true>), grid, wg, st, a, g);
+  else if (fi)
+    QN_LAUNCH("k_seq_bwd", (k_seq_bwd<true, false>), grid, wg, st, a, g);
+  else if (fo)
+    QN_LAUNCH("k_seq_bwd", (k_seq_bwd<false, true>), grid, wg, st, a, g);
+  else
+    QN_LAUNCH("k_seq_bwd", (k_seq_bwd<false, false>), grid, wg, st, a, g);
+  return check_launch();
+}
+
+}  // namespace
+
+extern "C" size_t qn_seq_workspace_bytes(int64_t rows, int64_t vocab, int64_t nseq) {
+  if (!valid_sizes(rows, vocab, nseq)) return 0;
+  int64_t chunk;
+  int32_t nchunk;
+  split_rows(rows, vocab, &chunk, &nchunk);
+  return align256(std::max<size_t>(1, size_t(rows) * nchunk * sizeof(MaxSum)));
+}
+
+extern "C" int qn_seq_logprob(const qn_seq_batch* b, float* lse, float* logp,
+                              int32_t* status_dev, void* ws, size_t ws_bytes,
+                              void* stream) {
+  if (!valid_batch(b)) return QN_EINVAL;
+  const PrefArgs none{};
+  return seq_forward(b, lse, logp, status_dev, ws, ws_bytes, stream, none);
+}
+
+extern "C" int qn_pref_loss_fwd(const qn_seq_batch* b, const float* ref_logp,
+                                const qn_pref_hparams* hp, float* lse,
+                                float* logp, float* loss, float* dlogp,
+                                int32_t* status_dev, void* ws, size_t ws_bytes,
+                                void* stream) {
+  if (!valid_batch(b)) return QN_EINVAL;
+  if (b->nseq % 2 != 0 || hp == nullptr || loss == nullptr || dlogp == nullptr)
+    return QN_EINVAL;
+  if (!(std::isfinite(hp->beta) && hp->beta > 0.0 && hp->label_smoothing >= 0.0 &&
+        hp->label_smoothing <= 0.5))
+    return QN_EINVAL;
+  PrefArgs pa;
+  pa.ref = ref_logp;
+  pa.loss = loss;
+  pa.dlogp = dlogp;
+  pa.beta = hp->beta;
+  pa.smooth = hp->label_smoothing;
+  pa.pairs = (int32_t)(b->nseq / 2);
+  return seq_forward(b, lse, logp, status_dev, ws, ws_bytes, stream, pa);
+}
+
+extern "C" int qn_seq_logprob_bwd(const qn_seq_batch* b, const float* lse,
+                                  const float* dlogp, void* dlogits,
+                                  int32_t dl_dtype, int64_t cols, int64_t ld_dl,
+                                  void* stream) {
+  return seq_backward(b, lse, dlogp, nullptr, 0, dlogits, dl_dtype, cols, ld_dl,
+                      stream);
+}
+
+extern "C" int qn_pref_loss_bwd(const qn_seq_batch* b, const float* lse,
+                                const float* dlogp, const float* dloss,
+                                void* dlogits, int32_t dl_dtype, int64_t cols,
+                                int64_t ld_dl, void* stream) {
+  if (b == nullptr || b->nseq % 2 != 0) return QN_EINVAL;
+  return seq_backward(b, lse, dlogp, dloss, (int32_t)(b->nseq / 2), dlogits,
+                      dl_dtype, cols, ld_dl, stream);
+}

@@ -131,6 +131,10 @@ struct FinishArgs {
 FinishArgs finish_args();
 void launch_finish(hipStream_t st, FinishArgs& a);
 
+// ---- act8.hip: 8-bit activation checkpoints.
+bool valid_act8(const qn_act8* t);
+void launch_act8_decode(hipStream_t st, const qn_act8& t, void* y, int32_t y_dtype);
+
 // ---- skinny.hip: forward for M <= 16 tokens, a batch of up to
 // QN_FWD_BATCH_MAX projections in one launch pair; ws holds each
 // projection's partial sums (skinny_part_bytes, 256-byte aligned, in order).

@@ -185,6 +185,8 @@ struct BwdWorkspace {
   size_t ugh, ugl;  // bf16 [r, Mp]    hi/lo parts of s*G, transposed
   size_t prow;      // fp32 [nb, M, rpad] column-block partials of G
   size_t pcol;      // fp32 [mb, max(N, K), rpad] row-block partials of dB, dA
+  size_t xr;        // bf16 [M, K]     X restored from its 8-bit checkpoint
+                    // (qlora_linear_bwd_act8 only)
   size_t total;
   int64_t mp;       // M rounded up to a multiple of 8
   int32_t rpad;
@@ -196,6 +198,7 @@ struct BwdWorkspace {
 // the split area holds only the status word).
 FwdWorkspace fwd_workspace_layout(int64_t M, int64_t N, int64_t K, int32_t r,
                                   bool general, bool split = true);
-BwdWorkspace bwd_workspace_layout(int64_t M, int64_t N, int64_t K, int32_t r);
+BwdWorkspace bwd_workspace_layout(int64_t M, int64_t N, int64_t K, int32_t r,
+                                  bool act8 = false);
 
 }  // namespace qn

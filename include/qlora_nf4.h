@@ -13,8 +13,10 @@
  *      on the adapter input;
  * and around it: dequantize-and-merge of an adapter into a dense bf16
  * weight, codec variants (FP4 / INT4 tables, fp32 or centered 8-bit block
- * constants) for quantization-error comparisons, and an 8-bit AdamW step on
- * the adapters with its state in device memory or paged through host memory.
+ * constants) for quantization-error comparisons, an 8-bit AdamW step on
+ * the adapters with its state in device memory or paged through host memory,
+ * 8-bit checkpoints of activations with the layer's backward from such a
+ * checkpoint, and the paired log-ratio loss of preference tuning.
  *
  * Sources for what each call computes are the pages "Qlora Expert" (Core
  * Concept), "QLoRA: The 4-bit Revolution" (sections 1 and 2), "QLoRA Guide"
@@ -443,6 +445,192 @@ int qlora_linear_bwd_dropout(const uint16_t* dy, const uint16_t* x,
                              int32_t dx_dtype, float* dA, float* dB,
                              const qn_dropout* drop, void* ws,
                              size_t ws_bytes, void* stream);
+
+/*
+ * 8-bit activation checkpoints.
+ *
+ * "Qlora Expert", Core Concept and "QLoRA Guide", Example train with
+ * gradient checkpointing, because the activations kept for the backward
+ * dominate once the weights are 4 bit wide (Memory Math).  Here a layer's
+ * input X is kept in about half the memory of bf16 instead of being
+ * recomputed.  The pages give no format; the one used:
+ *   - blocks of QN_BLOCK consecutive columns of one row (the last block of a
+ *     row may be shorter), one fp32 scale per block, one int8 code per
+ *     element;
+ *   - a = max|x| of the block;  scale = fp32(a / 127);
+ *     code = rint_half_even(fp32(fp32(x * (127/256)) / (a/256))), one
+ *     correctly rounded fp32 quotient (for bf16 inputs exactly the nearest
+ *     integer to 127 x / a, ties to even); -127 <= code <= 127;
+ *   - a < 2^-100: scale 0 and codes 0;
+ *   - a block with an infinity or a NaN: scale NaN and codes 0, so the whole
+ *     block comes back as NaN and the fault stays visible.
+ * Restored value: fp32(code * scale), or that rounded to bf16 (RNE).
+ */
+typedef struct {
+  int8_t* codes;    /* device, [rows][cols] row-major */
+  float* scale;     /* device, [rows][ceil(cols / QN_BLOCK)] row-major */
+  int64_t rows, cols;
+} qn_act8;
+
+/*
+ * qn_act8_encode -- x (device, [rows][cols] row-major of x_dtype, aligned to
+ * its element) into `out` (device buffers, 4-byte aligned scales).
+ * rows >= 0 (0 does nothing), cols >= 1, and rows * ceil(cols / QN_BLOCK)
+ * <= 2^28.  The checkpoint must not overlap x.
+ * Errors: QN_EINVAL, QN_EHIP.
+ */
+int qn_act8_encode(const void* x, int32_t x_dtype, const qn_act8* out,
+                   void* stream);
+
+/*
+ * qn_act8_decode -- the restored activation, [rows][cols] row-major of
+ * y_dtype (device, aligned to its element).  Limits and errors as
+ * qn_act8_encode.
+ */
+int qn_act8_decode(const qn_act8* x8, void* y, int32_t y_dtype, void* stream);
+
+/*
+ * qlora_linear_bwd_act8 -- qlora_linear_bwd / qlora_linear_bwd_dropout with
+ * X given as an 8-bit checkpoint (device).
+ *
+ * The same gradients ("QLoRA Guide", Forward pass: only A and B receive
+ * them) with X replaced by its restored bf16 value
+ *   Xr = bf16_rne(fp32(code * scale)),
+ * which is never written to memory:
+ *   dX = dY W' + s G A;  dA = s G^T Xr;  dB = s dY^T T;  G = dY B
+ * with drop != NULL: Xr is masked as X is in qlora_linear_bwd_dropout, and
+ * so is the adapter term of dX.  T is the forward's (formed from the exact
+ * X), so dX and dB do not depend on the checkpoint at all.
+ * x8   : checkpoint of [M][K] (x8->rows == M, x8->cols == K), its codes
+ *        16-byte aligned.
+ * dx   : as qlora_linear_bwd, or NULL where the layer's input needs no
+ *        gradient (dx_dtype is then ignored; the GEMM is not run).
+ * drop : NULL or p == 0 for no dropout.
+ * ws   : ws_bytes >= qlora_bwd_act8_workspace_bytes(M, N, K, r), 16-byte
+ *        aligned, with its status word as in qlora_linear_bwd.
+ * Other arguments, shape rules and errors as qlora_linear_bwd.
+ */
+size_t qlora_bwd_act8_workspace_bytes(int64_t M, int64_t N, int64_t K,
+                                      int32_t r);   /* 0: invalid sizes */
+
+int qlora_linear_bwd_act8(const uint16_t* dy, const qn_act8* x8, int64_t M,
+                          const nf4_tensor* w, const uint16_t* A,
+                          const uint16_t* B, int32_t r, float alpha,
+                          const float* t_saved, void* dx, int32_t dx_dtype,
+                          float* dA, float* dB, const qn_dropout* drop,
+                          void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Log-probabilities of sequences and the preference loss.
+ *
+ * Adapters are also tuned on preferences: pairs of a chosen and a rejected
+ * answer, scored by the policy (base and adapter) and by a reference, which
+ * for adapter tuning is the frozen base itself.  The pages name no loss; the
+ * paired log-ratio loss (Rafailov et al., "Direct Preference Optimization",
+ * 2023, equation 7) with label smoothing is the one here.  Rows t of the
+ * logits are the tokens of all sequences, packed one after another:
+ *   lse_t  = log sum_{v < vocab} exp(l[t][v])
+ *   logp_s = sum over the counted rows of sequence s of l[t][label_t] - lse_t
+ * A row is counted when it lies in a sequence and 0 <= label_t < vocab.
+ *   logits  : device, rows x vocab of `dtype` (QN_F32 or QN_BF16), row t at
+ *             element t * ld (ld >= vocab), aligned to its element;
+ *   labels  : device int64 [rows]; negative (for instance -100): the row is
+ *             not counted;
+ *   offsets : device int64 [nseq + 1]: sequence s holds rows
+ *             [offsets[s], offsets[s + 1]).  0 <= offsets[0] and offsets do
+ *             not decrease or pass `rows`; empty sequences are allowed
+ *             (logp 0).  Rows before the first or behind the last sequence
+ *             are not counted.
+ * 0 <= rows < 2^24 (logits and labels may be NULL when it is 0),
+ * 1 <= nseq < 2^22, 1 <= vocab <= 2^30, ld <= 2^31.
+ * A row whose logits hold a NaN or +infinity, or nothing above -infinity,
+ * has no log-probability: its sequence's logp, the loss and the gradient of
+ * that row are NaN (or infinite where only the label's logit is -infinity).
+ */
+typedef struct {
+  const void* logits;
+  int32_t dtype;
+  int64_t rows, vocab, ld;
+  const int64_t* labels;
+  const int64_t* offsets;
+  int64_t nseq;
+} qn_seq_batch;
+
+/* Workspace of qn_seq_logprob and qn_pref_loss_fwd (host): the partial
+ * maxima and sums of rows that are split over workgroups.  0 for invalid
+ * sizes. */
+size_t qn_seq_workspace_bytes(int64_t rows, int64_t vocab, int64_t nseq);
+
+/*
+ * qn_seq_logprob -- lse_t and logp_s of a batch (device).
+ * lse  : device float [rows]; 0 for rows that are not counted.
+ * logp : device float [nseq] (summed in double, rounded once).
+ * status_dev : device int32 or NULL.  QN_EINVAL is stored there if a label
+ *        is not below vocab (that row is not counted) or if the offsets
+ *        break their rule (lse and logp are then undefined; nothing outside
+ *        the buffers is touched); otherwise it is left as it was.
+ * ws   : ws_bytes >= qn_seq_workspace_bytes(rows, vocab, nseq), 16-byte
+ *        aligned; calls that run at the same time need workspaces of their
+ *        own.
+ * Errors: QN_EINVAL, QN_EWORKSPACE, QN_EHIP.
+ */
+int qn_seq_logprob(const qn_seq_batch* b, float* lse, float* logp,
+                   int32_t* status_dev, void* ws, size_t ws_bytes,
+                   void* stream);
+
+/*
+ * qn_seq_logprob_bwd -- gradient of sum_s dlogp_s logp_s (device):
+ *   dl[t][v] = dlogp_s (1[v == label_t] - exp(l[t][v] - lse_t))
+ * for counted rows, and 0 for all others.
+ * lse     : as written by the forward for this batch.
+ * dlogp   : device float [nseq].
+ * dlogits : device, [rows][cols] of dl_dtype (QN_F32 or QN_BF16), row t at
+ *           element t * ld_dl (cols >= vocab, ld_dl >= cols); columns from
+ *           vocab to cols (a head padded to a multiple of 8 words) are
+ *           written as zeros.  It may be the logits' own memory (same
+ *           pointer, type and pitch); any other overlap is not allowed.
+ * Errors: QN_EINVAL, QN_EHIP.
+ */
+int qn_seq_logprob_bwd(const qn_seq_batch* b, const float* lse,
+                       const float* dlogp, void* dlogits, int32_t dl_dtype,
+                       int64_t cols, int64_t ld_dl, void* stream);
+
+/*
+ * qn_pref_loss_fwd -- the paired log-ratio loss (device).  With P = nseq / 2
+ * pairs, sequence p chosen and sequence P + p rejected, and e =
+ * label_smoothing:
+ *   h_p    = beta ((logp_p - ref_p) - (logp_{P+p} - ref_{P+p}))
+ *   loss_p = -(1 - e) log sigmoid(h_p) - e log sigmoid(-h_p)
+ * ref_logp : device float [nseq], the reference's logp (qn_seq_logprob on
+ *            its logits), or NULL for zeros.
+ * hp       : host; beta > 0, 0 <= label_smoothing <= 0.5, both finite.
+ * lse, logp, status_dev, ws: as qn_seq_logprob (h is formed from the double
+ *            sums, before logp is rounded).
+ * loss     : device float [P].
+ * dlogp    : device float [nseq]: d loss_p / d logp of its two sequences.
+ * nseq must be even.  Errors: QN_EINVAL, QN_EWORKSPACE, QN_EHIP.
+ */
+typedef struct {
+  double beta, label_smoothing;
+} qn_pref_hparams;
+
+int qn_pref_loss_fwd(const qn_seq_batch* b, const float* ref_logp,
+                     const qn_pref_hparams* hp, float* lse, float* logp,
+                     float* loss, float* dlogp, int32_t* status_dev, void* ws,
+                     size_t ws_bytes, void* stream);
+
+/*
+ * qn_pref_loss_bwd -- gradient of sum_p dloss_p loss_p with respect to the
+ * logits (device): qn_seq_logprob_bwd with dloss_p dlogp_s in dlogp_s's
+ * place.
+ * dlogp : as written by qn_pref_loss_fwd.
+ * dloss : device float [P], or NULL for 1 / P each (the mean loss).
+ * Other arguments and errors as qn_seq_logprob_bwd.
+ */
+int qn_pref_loss_bwd(const qn_seq_batch* b, const float* lse,
+                     const float* dlogp, const float* dloss, void* dlogits,
+                     int32_t dl_dtype, int64_t cols, int64_t ld_dl,
+                     void* stream);
 
 /*
  * qlora_linear_fwd_batch -- qlora_linear_fwd for up to QN_FWD_BATCH_MAX
