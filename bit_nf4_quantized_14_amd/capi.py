@@ -9,7 +9,6 @@ exception is raised.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -649,54 +648,81 @@ def qlora_linear_bwd_dropout(dy, x, w: NF4Tensor, A, B, r: int, alpha: float,
 # 8-bit activation checkpoints and the preference loss.  Tensors are checked
 # here (device, type, shape, layout) before their addresses are passed on;
 # calls run on the device of their tensors, and what they allocate belongs to
-# the stream they run on.
+# the stream they run on.  Small calls take a few microseconds on the GPU, so
+# the checks build no text unless they fail and the plain case (the current
+# device's current stream) enters no context.
 # ---------------------------------------------------------------------------
 
-def _need(fn: str, ok: bool, what: str) -> None:
-    if not ok:
-        raise QNError(fn, QN_EINVAL, what)
+def _bad(fn: str, what: str):
+    return QNError(fn, QN_EINVAL, what)
+
+
+def _raw_stream(index: int) -> int:
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw else torch.cuda.current_stream(index).cuda_stream
+
+
+def _run_on(index: int, stream, body):
+    """body(handle) on the stream given, or on device `index`'s current one;
+    that stream and device are current inside."""
+    import torch
+    if stream is None:
+        if index == torch.cuda.current_device():
+            return body(_raw_stream(index))
+        with torch.cuda.device(index):
+            return body(_raw_stream(index))
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=index)
+    if stream.device_index != index:
+        raise _bad("stream", f"the stream is on device {stream.device_index}, the tensors on {index}")
+    with torch.cuda.stream(stream):
+        return body(stream.cuda_stream)
+
+
+def _gpu(fn: str, name: str, t) -> int:
+    if not t.is_cuda:
+        raise _bad(fn, f"{name} must be on a GPU")
+    return t.get_device()
 
 
 def _dtype_code(fn: str, name: str, t) -> int:
     import torch
-    _need(fn, t.dtype in (torch.float32, torch.bfloat16),
-          f"{name} must be float32 or bfloat16, not {t.dtype}")
-    return QN_F32 if t.dtype == torch.float32 else QN_BF16
+    dt = t.dtype
+    if dt is torch.bfloat16:
+        return QN_BF16
+    if dt is torch.float32:
+        return QN_F32
+    raise _bad(fn, f"{name} must be float32 or bfloat16, not {dt}")
 
 
 def _torch_dtype(fn: str, code: int):
     import torch
-    _need(fn, code in (QN_F32, QN_BF16), f"unknown dtype {code}")
+    if code not in (QN_F32, QN_BF16):
+        raise _bad(fn, f"unknown dtype {code}")
     return torch.float32 if code == QN_F32 else torch.bfloat16
 
 
-def _tensor(fn: str, name: str, t, shape, dtype, device) -> None:
-    """`t` must be a dense tensor of that shape and type on that device."""
-    _need(fn, t.device == device, f"{name} is on {t.device}, not {device}")
-    _need(fn, dtype is None or t.dtype == dtype, f"{name} must be {dtype}, not {t.dtype}")
-    _need(fn, tuple(t.shape) == tuple(shape),
-          f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    _need(fn, t.is_contiguous(), f"{name} must be contiguous")
+def _tensor(fn: str, name: str, t, shape: tuple, dtype, index: int) -> int:
+    """The address of `t`, a dense tensor of that shape and type (None: any)
+    on device `index`."""
+    if (t.shape == shape and (dtype is None or t.dtype is dtype) and t.is_contiguous()
+            and t.is_cuda and t.get_device() == index):
+        return t.data_ptr()
+    if not t.is_cuda or t.get_device() != index:
+        raise _bad(fn, f"{name} is on {t.device}, not on GPU {index}")
+    if dtype is not None and t.dtype is not dtype:
+        raise _bad(fn, f"{name} must be {dtype}, not {t.dtype}")
+    if t.shape != shape:
+        raise _bad(fn, f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    raise _bad(fn, f"{name} must be contiguous")
 
 
-@contextlib.contextmanager
-def _on(device, stream):
-    """The handle of the stream a call runs on (the device's current one when
-    `stream` is None), with that stream and device current inside."""
-    import torch
-    if stream is None:
-        with torch.cuda.device(device):
-            yield torch.cuda.current_stream(device).cuda_stream
-        return
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    with torch.cuda.stream(stream):
-        yield stream.cuda_stream
-
-
-def _gpu(fn: str, name: str, t):
-    _need(fn, t.is_cuda, f"{name} must be on a GPU")
-    return t.device
+def _workspace(fn: str, ws, index: int) -> tuple[int, int]:
+    """(address, bytes) of a caller's workspace."""
+    if not ws.is_cuda or ws.get_device() != index or not ws.is_contiguous():
+        raise _bad(fn, f"ws must be contiguous and on GPU {index}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 @dataclass
@@ -719,47 +745,54 @@ class Act8Tensor:
         return _Act8Struct(self.codes.data_ptr(), self.scale.data_ptr(),
                            self.rows, self.cols)
 
-    def check(self, fn: str, device) -> None:
+    def checked_struct(self, fn: str, index: int) -> _Act8Struct:
         import torch
-        _need(fn, self.cols >= 1, "a checkpoint has at least one column")
-        _tensor(fn, "codes", self.codes, (self.rows, self.cols), torch.int8, device)
-        _tensor(fn, "scale", self.scale, (self.rows, -(-self.cols // QN_BLOCK)),
-                torch.float32, device)
+        rows, cols = self.rows, self.cols
+        if cols < 1:
+            raise _bad(fn, "a checkpoint has at least one column")
+        return _Act8Struct(
+            _tensor(fn, "codes", self.codes, (rows, cols), torch.int8, index),
+            _tensor(fn, "scale", self.scale, (rows, -(-cols // QN_BLOCK)), torch.float32, index),
+            rows, cols)
 
 
 def qn_act8_encode(x, out: Act8Tensor | None = None, stream=None):
     """8-bit checkpoint of a device activation [rows, cols] (fp32 or bf16,
     contiguous); returns the Act8Tensor."""
     fn = "qn_act8_encode"
-    dev = _gpu(fn, "x", x)
+    index = _gpu(fn, "x", x)
     code = _dtype_code(fn, "x", x)
-    _need(fn, x.dim() == 2 and x.shape[1] >= 1, "x must be [rows, cols]")
-    _tensor(fn, "x", x, x.shape, None, dev)
-    with _on(dev, stream) as st:
-        if out is None:
-            out = Act8Tensor.empty(x.shape[0], x.shape[1], device=dev)
-        _need(fn, (out.rows, out.cols) == tuple(x.shape), "out has another shape than x")
-        out.check(fn, dev)
-        s = out.as_struct()
-        _check(fn, lib().qn_act8_encode(_ptr(x), code, ctypes.byref(s), st))
-    return out
+    shape = x.shape
+    if len(shape) != 2 or shape[1] < 1:
+        raise _bad(fn, "x must be [rows, cols]")
+    px = _tensor(fn, "x", x, shape, None, index)
+    if out is not None and (out.rows, out.cols) != shape:
+        raise _bad(fn, "out has another shape than x")
+
+    def body(st):
+        t = out if out is not None else Act8Tensor.empty(shape[0], shape[1], device=x.device)
+        s = t.checked_struct(fn, index)
+        _check(fn, lib().qn_act8_encode(px, code, s, st))
+        return t
+    return _run_on(index, stream, body)
 
 
 def qn_act8_decode(x8: Act8Tensor, out=None, dtype: int = QN_BF16, stream=None):
     """The restored activation [rows, cols] in bf16 or fp32 (`out`'s type
     when it is given)."""
-    import torch
     fn = "qn_act8_decode"
-    dev = _gpu(fn, "codes", x8.codes)
-    x8.check(fn, dev)
-    with _on(dev, stream) as st:
-        if out is None:
-            out = torch.empty((x8.rows, x8.cols), dtype=_torch_dtype(fn, dtype), device=dev)
-        _tensor(fn, "out", out, (x8.rows, x8.cols), None, dev)
-        s = x8.as_struct()
-        _check(fn, lib().qn_act8_decode(ctypes.byref(s), _ptr(out),
-                                        _dtype_code(fn, "out", out), st))
-    return out
+    index = _gpu(fn, "codes", x8.codes)
+    s = x8.checked_struct(fn, index)
+    shape = (x8.rows, x8.cols)
+
+    def body(st):
+        y = out
+        if y is None:
+            y = x8.codes.new_empty(shape, dtype=_torch_dtype(fn, dtype))
+        py = _tensor(fn, "out", y, shape, None, index)
+        _check(fn, lib().qn_act8_decode(s, py, _dtype_code(fn, "out", y), st))
+        return y
+    return _run_on(index, stream, body)
 
 
 def qlora_bwd_act8_workspace_bytes(M: int, N: int, K: int, r: int) -> int:
@@ -775,41 +808,45 @@ def qlora_linear_bwd_act8(dy, x8: Act8Tensor, w: NF4Tensor, A, B, r: int,
     None where need_dx is False."""
     import torch
     fn = "qlora_linear_bwd_act8"
-    dev = _gpu(fn, "dy", dy)
+    index = _gpu(fn, "dy", dy)
     M, N, K = x8.rows, w.rows, w.cols
     bf, f32 = torch.bfloat16, torch.float32
-    x8.check(fn, dev)
-    _need(fn, x8.cols == K, f"the checkpoint has {x8.cols} columns, the weight {K}")
-    _need(fn, M >= 1 and 1 <= r <= QN_MAX_RANK, "M or r out of range")
-    _tensor(fn, "dy", dy, (M, N), bf, dev)
-    _tensor(fn, "A", A, (r, K), bf, dev)
-    _tensor(fn, "B", B, (N, r), bf, dev)
-    _tensor(fn, "t_saved", t_saved, (M, r), f32, dev)
-    with _on(dev, stream) as st:
-        if not need_dx:
-            _need(fn, dx is None, "dx given with need_dx=False")
-        else:
-            if dx is None:
-                dx = torch.empty((M, K), device=dev, dtype=_torch_dtype(fn, dx_dtype))
-            _tensor(fn, "dx", dx, (M, K), None, dev)
-            dx_dtype = _dtype_code(fn, "dx", dx)
-        if dA is None:
-            dA = torch.empty((r, K), device=dev, dtype=f32)
-        if dB is None:
-            dB = torch.empty((N, r), device=dev, dtype=f32)
-        _tensor(fn, "dA", dA, (r, K), f32, dev)
-        _tensor(fn, "dB", dB, (N, r), f32, dev)
-        if ws is None:
-            ws = torch.empty(max(1, qlora_bwd_act8_workspace_bytes(M, N, K, r)),
-                             dtype=torch.uint8, device=dev)
-        _need(fn, ws.device == dev and ws.is_contiguous(), "ws must be contiguous, on dy's device")
-        wt, xt = w.as_struct(), x8.as_struct()
-        d = _Dropout(float(p), int(seed) & 0xFFFFFFFFFFFFFFFF)
+    xt = x8.checked_struct(fn, index)
+    if x8.cols != K:
+        raise _bad(fn, f"the checkpoint has {x8.cols} columns, the weight {K}")
+    if M < 1 or not 1 <= r <= QN_MAX_RANK:
+        raise _bad(fn, "M or r out of range")
+    if dx is not None and not need_dx:
+        raise _bad(fn, "dx given with need_dx=False")
+    pdy = _tensor(fn, "dy", dy, (M, N), bf, index)
+    pA = _tensor(fn, "A", A, (r, K), bf, index)
+    pB = _tensor(fn, "B", B, (N, r), bf, index)
+    pt = _tensor(fn, "t_saved", t_saved, (M, r), f32, index)
+
+    def body(st):
+        gx, gA, gB = dx, dA, dB
+        if need_dx and gx is None:
+            gx = dy.new_empty((M, K), dtype=_torch_dtype(fn, dx_dtype))
+        if gA is None:
+            gA = dy.new_empty((r, K), dtype=f32)
+        if gB is None:
+            gB = dy.new_empty((N, r), dtype=f32)
+        wk = ws
+        if wk is None:
+            wk = dy.new_empty(max(1, qlora_bwd_act8_workspace_bytes(M, N, K, r)),
+                              dtype=torch.uint8)
+        pw, nw = _workspace(fn, wk, index)
+        pdx, code = None, QN_F32
+        if need_dx:
+            pdx = _tensor(fn, "dx", gx, (M, K), None, index)
+            code = _dtype_code(fn, "dx", gx)
+        d = _Dropout(p, seed & 0xFFFFFFFFFFFFFFFF)
         _check(fn, lib().qlora_linear_bwd_act8(
-            _ptr(dy), ctypes.byref(xt), M, ctypes.byref(wt), _ptr(A), _ptr(B), r,
-            float(alpha), _ptr(t_saved), _ptr(dx), dx_dtype, _ptr(dA), _ptr(dB),
-            ctypes.byref(d), _ptr(ws), ws.numel() * ws.element_size(), st))
-    return dx, dA, dB
+            pdy, xt, M, w.as_struct(), pA, pB, r, alpha, pt, pdx, code,
+            _tensor(fn, "dA", gA, (r, K), f32, index),
+            _tensor(fn, "dB", gB, (N, r), f32, index), d, pw, nw, st))
+        return gx, gA, gB
+    return _run_on(index, stream, body)
 
 
 def qn_seq_workspace_bytes(rows: int, vocab: int, nseq: int) -> int:
@@ -817,52 +854,67 @@ def qn_seq_workspace_bytes(rows: int, vocab: int, nseq: int) -> int:
 
 
 def _seq_batch(fn: str, logits, labels, offsets):
-    """(device, qn_seq_batch) of logits [rows, vocab] whose rows may be apart
-    (stride(0) >= vocab), labels [rows] and offsets [nseq + 1]."""
+    """(device index, qn_seq_batch) of logits [rows, vocab] whose rows may be
+    apart (stride(0) >= vocab), labels [rows] and offsets [nseq + 1]."""
     import torch
-    dev = _gpu(fn, "logits", logits)
+    index = _gpu(fn, "logits", logits)
     code = _dtype_code(fn, "logits", logits)
-    _need(fn, logits.dim() == 2 and logits.shape[1] >= 1, "logits must be [rows, vocab]")
-    rows, vocab = logits.shape
-    _need(fn, vocab == 1 or logits.stride(1) == 1, "a row of logits must be contiguous")
-    ld = logits.stride(0) if rows > 1 else vocab
-    _need(fn, ld >= vocab, "rows of logits overlap")
-    _tensor(fn, "labels", labels, (rows,), torch.int64, dev)
-    _need(fn, offsets.dim() == 1 and offsets.numel() >= 2, "offsets must be [nseq + 1]")
-    _tensor(fn, "offsets", offsets, offsets.shape, torch.int64, dev)
-    return dev, _SeqBatch(_ptr(logits), code, rows, vocab, ld, _ptr(labels),
-                          _ptr(offsets), offsets.numel() - 1)
+    shape = logits.shape
+    if len(shape) != 2 or shape[1] < 1:
+        raise _bad(fn, "logits must be [rows, vocab]")
+    rows, vocab = shape
+    ld, step = logits.stride()
+    if step != 1 and vocab > 1:
+        raise _bad(fn, "a row of logits must be contiguous")
+    if rows <= 1:
+        ld = vocab
+    if ld < vocab:
+        raise _bad(fn, "rows of logits overlap")
+    n = offsets.shape
+    if len(n) != 1 or n[0] < 2:
+        raise _bad(fn, "offsets must be [nseq + 1]")
+    return index, _SeqBatch(
+        logits.data_ptr(), code, rows, vocab, ld,
+        _tensor(fn, "labels", labels, (rows,), torch.int64, index),
+        _tensor(fn, "offsets", offsets, n, torch.int64, index), n[0] - 1)
 
 
-def _seq_outputs(fn, b, dev, lse, logp, status, ws):
+def _seq_workspace(fn, b, like, ws, index):
+    """(address, bytes, tensor) of the caller's workspace or a new one."""
     import torch
-    if lse is None:
-        lse = torch.empty(b.rows, dtype=torch.float32, device=dev)
-    if logp is None:
-        logp = torch.empty(b.nseq, dtype=torch.float32, device=dev)
     if ws is None:
-        ws = torch.empty(max(1, qn_seq_workspace_bytes(b.rows, b.vocab, b.nseq)),
-                         dtype=torch.uint8, device=dev)
-    _tensor(fn, "lse", lse, (b.rows,), torch.float32, dev)
-    _tensor(fn, "logp", logp, (b.nseq,), torch.float32, dev)
-    _need(fn, ws.device == dev and ws.is_contiguous(), "ws must be contiguous, on the logits' device")
-    if status is not None:
-        _tensor(fn, "status", status, (1,), torch.int32, dev)
-    return lse, logp, ws
+        ws = like.new_empty(max(1, qn_seq_workspace_bytes(b.rows, b.vocab, b.nseq)),
+                            dtype=torch.uint8)
+    return (*_workspace(fn, ws, index), ws)
+
+
+def _status_ptr(fn, status, index):
+    import torch
+    return None if status is None else _tensor(fn, "status", status, (1,), torch.int32, index)
 
 
 def qn_seq_logprob(logits, labels, offsets, lse=None, logp=None, status=None,
                    ws=None, stream=None):
     """Log-probability of each packed sequence and log-sum-exp of each row;
     returns (logp [nseq], lse [rows])."""
+    import torch
     fn = "qn_seq_logprob"
-    dev, b = _seq_batch(fn, logits, labels, offsets)
-    with _on(dev, stream) as st:
-        lse, logp, ws = _seq_outputs(fn, b, dev, lse, logp, status, ws)
+    index, b = _seq_batch(fn, logits, labels, offsets)
+    f32 = torch.float32
+
+    def body(st):
+        e, g = lse, logp
+        if e is None:
+            e = logits.new_empty(b.rows, dtype=f32)
+        if g is None:
+            g = logits.new_empty(b.nseq, dtype=f32)
+        pw, nw, _w = _seq_workspace(fn, b, logits, ws, index)
         _check(fn, lib().qn_seq_logprob(
-            ctypes.byref(b), _ptr(lse), _ptr(logp), _ptr(status), _ptr(ws),
-            ws.numel() * ws.element_size(), st))
-    return logp, lse
+            b, _tensor(fn, "lse", e, (b.rows,), f32, index),
+            _tensor(fn, "logp", g, (b.nseq,), f32, index),
+            _status_ptr(fn, status, index), pw, nw, st))
+        return g, e
+    return _run_on(index, stream, body)
 
 
 @dataclass
@@ -882,49 +934,63 @@ def qn_pref_loss_fwd(logits, labels, offsets, ref_logp, beta: float,
     ref_logp [2P] or None for zeros; returns a PrefLoss."""
     import torch
     fn = "qn_pref_loss_fwd"
-    dev, b = _seq_batch(fn, logits, labels, offsets)
-    _need(fn, b.nseq % 2 == 0, "sequences must come in pairs")
-    if ref_logp is not None:
-        _tensor(fn, "ref_logp", ref_logp, (b.nseq,), torch.float32, dev)
-    with _on(dev, stream) as st:
-        lse, logp, ws = _seq_outputs(fn, b, dev, out and out.lse, out and out.logp, status, ws)
-        if out is None:
-            out = PrefLoss(torch.empty(b.nseq // 2, dtype=torch.float32, device=dev), logp,
-                           torch.empty(b.nseq, dtype=torch.float32, device=dev), lse)
-        _tensor(fn, "loss", out.loss, (b.nseq // 2,), torch.float32, dev)
-        _tensor(fn, "dlogp", out.dlogp, (b.nseq,), torch.float32, dev)
-        hp = _PrefHP(float(beta), float(label_smoothing))
+    index, b = _seq_batch(fn, logits, labels, offsets)
+    f32, rows, nseq = torch.float32, b.rows, b.nseq
+    pairs = nseq // 2
+    if nseq != 2 * pairs:
+        raise _bad(fn, "sequences must come in pairs")
+    pr = None if ref_logp is None else _tensor(fn, "ref_logp", ref_logp, (nseq,), f32, index)
+
+    def body(st):
+        o = out
+        if o is None:
+            o = PrefLoss(logits.new_empty(pairs, dtype=f32), logits.new_empty(nseq, dtype=f32),
+                         logits.new_empty(nseq, dtype=f32), logits.new_empty(rows, dtype=f32))
+        pw, nw, _w = _seq_workspace(fn, b, logits, ws, index)
         _check(fn, lib().qn_pref_loss_fwd(
-            ctypes.byref(b), _ptr(ref_logp), ctypes.byref(hp), _ptr(lse), _ptr(logp),
-            _ptr(out.loss), _ptr(out.dlogp), _ptr(status), _ptr(ws),
-            ws.numel() * ws.element_size(), st))
-    return out
+            b, pr, _PrefHP(beta, label_smoothing),
+            _tensor(fn, "lse", o.lse, (rows,), f32, index),
+            _tensor(fn, "logp", o.logp, (nseq,), f32, index),
+            _tensor(fn, "loss", o.loss, (pairs,), f32, index),
+            _tensor(fn, "dlogp", o.dlogp, (nseq,), f32, index),
+            _status_ptr(fn, status, index), pw, nw, st))
+        return o
+    return _run_on(index, stream, body)
 
 
 def _seq_bwd(fn, logits, labels, offsets, lse, dlogp, dloss, dlogits, dl_dtype, stream):
     import torch
-    dev, b = _seq_batch(fn, logits, labels, offsets)
-    _tensor(fn, "lse", lse, (b.rows,), torch.float32, dev)
-    _tensor(fn, "dlogp", dlogp, (b.nseq,), torch.float32, dev)
-    if dloss is not None:
-        _need(fn, b.nseq % 2 == 0, "sequences must come in pairs")
-        _tensor(fn, "dloss", dloss, (b.nseq // 2,), torch.float32, dev)
-    with _on(dev, stream) as st:
-        if dlogits is None:
-            dt = logits.dtype if dl_dtype is None else _torch_dtype(fn, dl_dtype)
-            dlogits = torch.empty((b.rows, b.vocab), dtype=dt, device=dev)
-        _need(fn, dlogits.device == dev, f"dlogits is on {dlogits.device}, not {dev}")
-        _need(fn, dlogits.dim() == 2 and dlogits.shape[0] == b.rows and
-              dlogits.shape[1] >= b.vocab, "dlogits must be [rows, cols], cols >= vocab")
-        cols = dlogits.shape[1]
-        _need(fn, cols == 1 or dlogits.stride(1) == 1, "a row of dlogits must be contiguous")
-        ld = dlogits.stride(0) if b.rows > 1 else max(cols, b.ld)
-        args = [ctypes.byref(b), _ptr(lse), _ptr(dlogp)]
-        if fn == "qn_pref_loss_bwd":
-            args.append(_ptr(dloss))
-        _check(fn, getattr(lib(), fn)(*args, _ptr(dlogits), _dtype_code(fn, "dlogits", dlogits),
-                                      cols, ld, st))
-    return dlogits
+    index, b = _seq_batch(fn, logits, labels, offsets)
+    f32, rows, vocab, nseq = torch.float32, b.rows, b.vocab, b.nseq
+    args = [b, _tensor(fn, "lse", lse, (rows,), f32, index),
+            _tensor(fn, "dlogp", dlogp, (nseq,), f32, index)]
+    if fn == "qn_pref_loss_bwd":
+        if nseq % 2:
+            raise _bad(fn, "sequences must come in pairs")
+        args.append(None if dloss is None
+                    else _tensor(fn, "dloss", dloss, (nseq // 2,), f32, index))
+    call = getattr(lib(), fn)
+
+    def body(st):
+        dl = dlogits
+        if dl is None:
+            dl = logits.new_empty((rows, vocab), dtype=logits.dtype if dl_dtype is None
+                                  else _torch_dtype(fn, dl_dtype))
+        code = _dtype_code(fn, "dlogits", dl)
+        shape = dl.shape
+        if not dl.is_cuda or dl.get_device() != index:
+            raise _bad(fn, f"dlogits is on {dl.device}, not on GPU {index}")
+        if len(shape) != 2 or shape[0] != rows or shape[1] < vocab:
+            raise _bad(fn, "dlogits must be [rows, cols], cols >= vocab")
+        cols = shape[1]
+        ld, step = dl.stride()
+        if step != 1 and cols > 1:
+            raise _bad(fn, "a row of dlogits must be contiguous")
+        if rows <= 1:
+            ld = max(cols, b.ld)
+        _check(fn, call(*args, dl.data_ptr(), code, cols, ld, st))
+        return dl
+    return _run_on(index, stream, body)
 
 
 def qn_seq_logprob_bwd(logits, labels, offsets, lse, dlogp, dlogits=None,

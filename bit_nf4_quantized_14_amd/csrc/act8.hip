@@ -176,17 +176,6 @@ bool valid_act8(const qn_act8* t) {
          (t->codes != nullptr && t->scale != nullptr && aligned_to(t->scale, 4));
 }
 
-void launch_act8_decode(hipStream_t st, const qn_act8& t, void* y, int32_t y_dtype) {
-  const int nb = (int)cdiv(t.cols, QN_BLOCK), nblocks = (int)t.rows * nb;
-  const dim3 grid((unsigned)cdiv((int64_t)nblocks * 8, A8_THREADS)), wg(A8_THREADS);
-  if (y_dtype == QN_F32)
-    QN_LAUNCH("k_act8_decode", k_act8_decode<true>, grid, wg, st, t.codes, t.scale,
-              static_cast<char*>(y), nblocks, nb, (int)t.cols);
-  else
-    QN_LAUNCH("k_act8_decode", k_act8_decode<false>, grid, wg, st, t.codes, t.scale,
-              static_cast<char*>(y), nblocks, nb, (int)t.cols);
-}
-
 }  // namespace qn
 
 using namespace qn;
@@ -214,6 +203,15 @@ extern "C" int qn_act8_decode(const qn_act8* x8, void* y, int32_t y_dtype,
   if (!valid_act8(x8)) return QN_EINVAL;
   if (x8->rows == 0) return y_dtype == QN_F32 || y_dtype == QN_BF16 ? QN_OK : QN_EINVAL;
   if (!valid_dense(y, y_dtype)) return QN_EINVAL;
-  launch_act8_decode((hipStream_t)stream, *x8, y, y_dtype);
+  hipStream_t st = (hipStream_t)stream;
+  const int nb = (int)cdiv(x8->cols, QN_BLOCK), nblocks = (int)x8->rows * nb;
+  const dim3 grid((unsigned)cdiv((int64_t)nblocks * 8, A8_THREADS)), wg(A8_THREADS);
+  char* p = static_cast<char*>(y);
+  if (y_dtype == QN_F32)
+    QN_LAUNCH("k_act8_decode", k_act8_decode<true>, grid, wg, st, x8->codes, x8->scale, p,
+              nblocks, nb, (int)x8->cols);
+  else
+    QN_LAUNCH("k_act8_decode", k_act8_decode<false>, grid, wg, st, x8->codes, x8->scale, p,
+              nblocks, nb, (int)x8->cols);
   return check_launch();
 }

@@ -90,7 +90,7 @@ size_t qlora_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t r,
 size_t qlora_bwd_act8_workspace_bytes(int64_t M, int64_t N, int64_t K,
                                       int32_t r) {
   if (M <= 0 || N <= 0 || K <= 0 || r < 1 || r > QN_MAX_RANK) return 0;
-  return qn::bwd_workspace_layout(M, N, K, r, true).total;
+  return qn::act8_bwd_workspace_layout(M, N, K, r).total;
 }
 
 }  // extern "C"
@@ -177,30 +177,23 @@ int linear_fwd(const uint16_t* x, int64_t M, const nf4_tensor* w,
   return check_launch();
 }
 
-// X is either x (bf16) or the checkpoint x8.  With x8, dx may be null: the
-// gradient of X is then not formed.
-int linear_bwd(const uint16_t* dy, const uint16_t* x, const qn_act8* x8,
-               int64_t M, const nf4_tensor* w, const uint16_t* A,
-               const uint16_t* B, int32_t r, float alpha, const float* t_saved,
-               void* dx, int32_t dx_dtype, float* dA, float* dB,
-               const qn_dropout* drop, void* ws, size_t ws_bytes, void* stream) {
-  const bool act8 = x8 != nullptr, want_dx = !act8 || dx != nullptr;
-  if (dy == nullptr || (x == nullptr && !act8) || A == nullptr || B == nullptr ||
-      t_saved == nullptr || (want_dx && dx == nullptr) || dA == nullptr ||
-      dB == nullptr)
+int linear_bwd(const uint16_t* dy, const uint16_t* x, int64_t M,
+               const nf4_tensor* w, const uint16_t* A, const uint16_t* B,
+               int32_t r, float alpha, const float* t_saved, void* dx,
+               int32_t dx_dtype, float* dA, float* dB, const qn_dropout* drop,
+               void* ws, size_t ws_bytes, void* stream) {
+  if (dy == nullptr || x == nullptr || A == nullptr || B == nullptr ||
+      t_saved == nullptr || dx == nullptr || dA == nullptr || dB == nullptr)
     return QN_EINVAL;
   if (!valid_linear(M, w, r)) return QN_EINVAL;
-  if (want_dx && dx_dtype != QN_F32 && dx_dtype != QN_BF16) return QN_EINVAL;
+  if (dx_dtype != QN_F32 && dx_dtype != QN_BF16) return QN_EINVAL;
   if (!aligned16(dy) || !aligned16(x) || !aligned16(A) || !aligned16(dx))
-    return QN_EINVAL;
-  if (act8 && (!valid_act8(x8) || x8->rows != M || x8->cols != w->cols ||
-               !aligned16(x8->codes)))
     return QN_EINVAL;
   qn::DropArgs da{};
   bool use_drop = false;
   if (!drop_args(drop, &da, &use_drop)) return QN_EINVAL;
   const int64_t N = w->rows, K = w->cols;
-  const qn::BwdWorkspace L = qn::bwd_workspace_layout(M, N, K, r, act8);
+  const qn::BwdWorkspace L = qn::bwd_workspace_layout(M, N, K, r);
   if (ws == nullptr || ws_bytes < L.total || !aligned16(ws))
     return QN_EWORKSPACE;
   uint16_t* Bt = ws_at<uint16_t>(ws, L.bt);
@@ -239,15 +232,9 @@ int linear_bwd(const uint16_t* dy, const uint16_t* x, const qn_act8* x8,
   zero_split_counters(f1.P1, split_ws, gemm_split_plan(M, K, N, use_drop));
   launch_finish(st, f1);
   // dX = dY W' + (s G) A
-  if (want_dx)
-    launch_gemm<true>(st, dy, w, Gh, Gl, Atp, Mi, L.rpad, dx,
-                      (int)(dx_dtype == QN_BF16), use_drop ? &da : nullptr,
-                      split_ws);
-  if (act8) {
-    uint16_t* xr = ws_at<uint16_t>(ws, L.xr);
-    launch_act8_decode(st, *x8, xr, QN_BF16);
-    x = xr;
-  }
+  launch_gemm<true>(st, dy, w, Gh, Gl, Atp, Mi, L.rpad, dx,
+                    (int)(dx_dtype == QN_BF16), use_drop ? &da : nullptr,
+                    split_ws);
   // dA = (s G)^T X: row-block partials of out[k][j] -> dA[j][k]
   const StreamPlan Pa = stream_plan(RS_COLS, M, K, jt, use_drop);
   launch_rank_stream<RS_COLS>(st, "k_rank_stream_da", Pa, x, Mi, Ki, nullptr,
@@ -259,9 +246,94 @@ int linear_bwd(const uint16_t* dy, const uint16_t* x, const qn_act8* x8,
   return check_launch();
 }
 
+// The backward with X as an 8-bit checkpoint; dx may be null.  Five launches
+// and the dX GEMM: operands, G, split of G, [dX,] both column sums, slices.
+int linear_bwd_act8(const uint16_t* dy, const qn_act8* x8, int64_t M,
+                    const nf4_tensor* w, const uint16_t* A, const uint16_t* B,
+                    int32_t r, float alpha, const float* t_saved, void* dx,
+                    int32_t dx_dtype, float* dA, float* dB,
+                    const qn_dropout* drop, void* ws, size_t ws_bytes,
+                    void* stream) {
+  if (dy == nullptr || x8 == nullptr || A == nullptr || B == nullptr ||
+      t_saved == nullptr || dA == nullptr || dB == nullptr)
+    return QN_EINVAL;
+  if (!valid_linear(M, w, r)) return QN_EINVAL;
+  if (dx != nullptr && dx_dtype != QN_F32 && dx_dtype != QN_BF16) return QN_EINVAL;
+  if (!aligned16(dy) || !aligned16(A) || !aligned16(dx)) return QN_EINVAL;
+  if (!valid_act8(x8) || x8->rows != M || x8->cols != w->cols ||
+      !aligned16(x8->codes))
+    return QN_EINVAL;
+  qn::DropArgs da{};
+  bool use_drop = false;
+  if (!drop_args(drop, &da, &use_drop)) return QN_EINVAL;
+  const int64_t N = w->rows, K = w->cols;
+  const qn::Act8BwdWorkspace L = qn::act8_bwd_workspace_layout(M, N, K, r);
+  if (ws == nullptr || ws_bytes < L.total || !aligned16(ws))
+    return QN_EWORKSPACE;
+  uint16_t* Bt = ws_at<uint16_t>(ws, L.bt);
+  uint16_t* Atp = ws_at<uint16_t>(ws, L.atp);
+  uint16_t* Gh = ws_at<uint16_t>(ws, L.gh);
+  uint16_t* Gl = ws_at<uint16_t>(ws, L.gl);
+  uint16_t* UT = ws_at<uint16_t>(ws, L.ut);
+  uint16_t* UG = ws_at<uint16_t>(ws, L.ug);
+  float* prow = ws_at<float>(ws, L.prow);
+  char* split_ws = ws_at<char>(ws, L.split);
+  const float s = alpha / (float)r;
+  const int Mi = (int)M, Ni = (int)N, Ki = (int)K, jt = rank_tiles(r);
+  hipStream_t st = (hipStream_t)stream;
+
+  // B^T for the G pass, A^T padded to [K][rpad] for dX, s T in three terms
+  FinishArgs f0 = finish_args();
+  if (dx != nullptr) f0.P1 = FinishPad{A, Atp, Ki, L.rpad, (int)r, (int64_t)1, K};
+  f0.P2 = FinishPad{B, Bt, (int)r, Ni, Ni, (int)1, (int64_t)r};
+  launch_finish(st, f0);
+  AdapterSplit pt{t_saved, 0, (int)r, 1, M, (int)r, jt, s, UT, nullptr, nullptr,
+                  nullptr, 0, 0};
+  launch_adapter_split(st, pt);
+  // G = dY B: partials over column blocks of dY
+  const StreamPlan Pg = stream_plan(RS_ROWS, M, N, jt);
+  launch_rank_stream<RS_ROWS>(st, "k_rank_stream_g", Pg, dy, Mi, Ni, Bt, (int)r,
+                              nullptr, nullptr, 0, prow, nullptr, nullptr);
+  // s G in three terms (and two for the GEMM); the status word and the
+  // counters of the GEMM's split tiles cleared
+  const GemmSplit sp = gemm_split_plan(M, K, N, use_drop);
+  AdapterSplit pg{prow, (int64_t)M * L.rpad, L.rpad, Pg.nb, M, (int)r, jt, s, UG,
+                  dx != nullptr ? Gh : nullptr, Gl,
+                  reinterpret_cast<uint32_t*>(split_ws),
+                  (int64_t)(G_SPLIT_HDR / 4) + 2 * sp.rem, 0};
+  launch_adapter_split(st, pg);
+  if (dx != nullptr)
+    launch_gemm<true>(st, dy, w, Gh, Gl, Atp, Mi, L.rpad, dx,
+                      (int)(dx_dtype == QN_BF16), use_drop ? &da : nullptr,
+                      split_ws);
+  // dB = dY^T (s T), dA = (s G)^T Xr
+  const ColsPlan Pb = cols_plan(M, N, jt), Pa = cols_plan(M, K, jt);
+  float* outB = Pb.slices > 1 ? ws_at<float>(ws, L.pb) : dB;
+  float* outA = Pa.slices > 1 ? ws_at<float>(ws, L.pa) : dA;
+  const ColsJob jb{dy, nullptr, (uint32_t)(M * N * 2), Mi, Ni, (int)r, UT, outB, 0,
+                   Pb.cb, Pb.slices, Pb.steps, Pb.steps_per};
+  const ColsJob ja{x8->codes, x8->scale, (uint32_t)(M * K), Mi, Ki, (int)r, UG, outA, 1,
+                   Pa.cb, Pa.slices, Pa.steps, Pa.steps_per};
+  launch_adapter_cols(st, jb, ja, (int)r, use_drop ? &da : nullptr);
+  launch_adapter_reduce(
+      st, ColsReduce{outB, dB, Pb.slices > 1 ? N * r : 0, Pb.slices},
+      ColsReduce{outA, dA, Pa.slices > 1 ? K * r : 0, Pa.slices});
+  return check_launch();
+}
+
 }  // namespace
 
 extern "C" {
+
+int qlora_linear_bwd_act8(const uint16_t* dy, const qn_act8* x8, int64_t M,
+                          const nf4_tensor* w, const uint16_t* A,
+                          const uint16_t* B, int32_t r, float alpha,
+                          const float* t_saved, void* dx, int32_t dx_dtype,
+                          float* dA, float* dB, const qn_dropout* drop,
+                          void* ws, size_t ws_bytes, void* stream) {
+  return linear_bwd_act8(dy, x8, M, w, A, B, r, alpha, t_saved, dx, dx_dtype,
+                         dA, dB, drop, ws, ws_bytes, stream);
+}
 
 int qlora_linear_fwd(const uint16_t* x, int64_t M, const nf4_tensor* w,
                      const uint16_t* A, const uint16_t* B, int32_t r,
@@ -288,19 +360,8 @@ int qlora_linear_bwd(const uint16_t* dy, const uint16_t* x, int64_t M,
                      const float* t_saved, void* dx, int32_t dx_dtype,
                      float* dA, float* dB, void* ws, size_t ws_bytes,
                      void* stream) {
-  return linear_bwd(dy, x, nullptr, M, w, A, B, r, alpha, t_saved, dx,
-                    dx_dtype, dA, dB, nullptr, ws, ws_bytes, stream);
-}
-
-int qlora_linear_bwd_act8(const uint16_t* dy, const qn_act8* x8, int64_t M,
-                          const nf4_tensor* w, const uint16_t* A,
-                          const uint16_t* B, int32_t r, float alpha,
-                          const float* t_saved, void* dx, int32_t dx_dtype,
-                          float* dA, float* dB, const qn_dropout* drop,
-                          void* ws, size_t ws_bytes, void* stream) {
-  if (x8 == nullptr) return QN_EINVAL;
-  return linear_bwd(dy, nullptr, x8, M, w, A, B, r, alpha, t_saved, dx,
-                    dx_dtype, dA, dB, drop, ws, ws_bytes, stream);
+  return linear_bwd(dy, x, M, w, A, B, r, alpha, t_saved, dx, dx_dtype, dA,
+                    dB, nullptr, ws, ws_bytes, stream);
 }
 
 int qlora_linear_bwd_dropout(const uint16_t* dy, const uint16_t* x,
@@ -311,8 +372,8 @@ int qlora_linear_bwd_dropout(const uint16_t* dy, const uint16_t* x,
                              const qn_dropout* drop, void* ws,
                              size_t ws_bytes, void* stream) {
   if (drop == nullptr) return QN_EINVAL;
-  return linear_bwd(dy, x, nullptr, M, w, A, B, r, alpha, t_saved, dx,
-                    dx_dtype, dA, dB, drop, ws, ws_bytes, stream);
+  return linear_bwd(dy, x, M, w, A, B, r, alpha, t_saved, dx, dx_dtype, dA,
+                    dB, drop, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -176,7 +176,7 @@ FwdWorkspace fwd_workspace_layout(int64_t M, int64_t N, int64_t K,
 }
 
 BwdWorkspace bwd_workspace_layout(int64_t M, int64_t N, int64_t K,
-                                  int32_t r, bool act8) {
+                                  int32_t r) {
   BwdWorkspace L{};
   const int jt = rank_tiles(r);
   L.rpad = 16 * jt;
@@ -208,8 +208,44 @@ BwdWorkspace bwd_workspace_layout(int64_t M, int64_t N, int64_t K,
   off += align256(size_t(Pg.nb) * M * L.rpad * 4);
   L.pcol = off;
   off += align256(pcol * L.rpad * 4);
-  L.xr = off;
-  if (act8) off += align256(size_t(M) * K * 2);
+  L.total = off;
+  return L;
+}
+
+ColsPlan cols_plan(int64_t M, int64_t C, int jt) {
+  ColsPlan P;
+  P.cb = (int)cdiv(C, 64);
+  P.steps = (int)cdiv(M, 32);
+  const int64_t want = std::min(cdiv(2 * G_CUS, P.cb), cdiv(P.steps, cols_waves(jt)));
+  P.steps_per = (int)cdiv(P.steps, want);
+  P.slices = (int)cdiv(P.steps, P.steps_per);
+  return P;
+}
+
+Act8BwdWorkspace act8_bwd_workspace_layout(int64_t M, int64_t N, int64_t K,
+                                           int32_t r) {
+  Act8BwdWorkspace L{};
+  const int jt = rank_tiles(r);
+  L.rpad = 16 * jt;
+  const StreamPlan Pg = stream_plan(RS_ROWS, M, N, jt);
+  const ColsPlan Pb = cols_plan(M, N, jt), Pa = cols_plan(M, K, jt);
+  const size_t frag = size_t(Pb.steps) * jt * 3 * 64 * 16;
+  size_t off = 0;
+  const auto take = [&off](size_t bytes) {
+    const size_t at = off;
+    off += align256(bytes);
+    return at;
+  };
+  L.split = take(gemm_split_bytes(gemm_split_plan(M, K, N, false)));
+  L.bt = take(size_t(r) * N * 2);
+  L.atp = take(size_t(K) * L.rpad * 2);
+  L.gh = take(size_t(M) * L.rpad * 2);
+  L.gl = take(size_t(M) * L.rpad * 2);
+  L.prow = take(size_t(Pg.nb) * M * L.rpad * 4);
+  L.ut = take(frag);
+  L.ug = take(frag);
+  L.pb = take(Pb.slices > 1 ? size_t(Pb.slices) * N * r * 4 : 0);
+  L.pa = take(Pa.slices > 1 ? size_t(Pa.slices) * K * r * 4 : 0);
   L.total = off;
   return L;
 }

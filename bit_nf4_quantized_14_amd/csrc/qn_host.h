@@ -133,7 +133,39 @@ void launch_finish(hipStream_t st, FinishArgs& a);
 
 // ---- act8.hip: 8-bit activation checkpoints.
 bool valid_act8(const qn_act8* t);
-void launch_act8_decode(hipStream_t st, const qn_act8& t, void* y, int32_t y_dtype);
+
+// ---- adapter8.hip: adapter gradients from an 8-bit checkpoint.
+struct AdapterSplit {           // U = scale sum_b src[b] as three bf16 terms
+  const float* src;             // [nb][M][ld], blocks bstride apart
+  int64_t bstride;
+  int ld, nb;
+  int64_t M;
+  int r, jt;
+  float scale;
+  uint16_t* frag;               // [ceil(M / 32)][jt][3][64][8]
+  uint16_t *hi, *lo;            // [M][16 jt] terms 0 and 1, or null
+  uint32_t* zero;               // zero_words words to clear on the way
+  int64_t zero_words, total;
+};
+struct ColsJob {                // column sums of S against U
+  const void* S;                // bf16 or int8 [M][C]
+  const float* scale;           // int8: [M][C / 64]
+  uint32_t s_bytes;
+  int M, C, r;
+  const uint16_t* U;            // an AdapterSplit's frag
+  float* out;                   // slices of [C][r], or of [r][C] with by_j
+  int by_j, cb, slices, steps, steps_per;
+};
+struct ColsReduce {             // out[i] = sum of slices of part[slice][i]
+  const float* part;
+  float* out;
+  int64_t n;                    // 0: nothing to do
+  int slices;
+};
+void launch_adapter_split(hipStream_t st, AdapterSplit& p);
+void launch_adapter_cols(hipStream_t st, const ColsJob& B, const ColsJob& A, int r,
+                         const DropArgs* drop);
+void launch_adapter_reduce(hipStream_t st, const ColsReduce& p0, const ColsReduce& p1);
 
 // ---- skinny.hip: forward for M <= 16 tokens, a batch of up to
 // QN_FWD_BATCH_MAX projections in one launch pair; ws holds each

@@ -185,8 +185,6 @@ struct BwdWorkspace {
   size_t ugh, ugl;  // bf16 [r, Mp]    hi/lo parts of s*G, transposed
   size_t prow;      // fp32 [nb, M, rpad] column-block partials of G
   size_t pcol;      // fp32 [mb, max(N, K), rpad] row-block partials of dB, dA
-  size_t xr;        // bf16 [M, K]     X restored from its 8-bit checkpoint
-                    // (qlora_linear_bwd_act8 only)
   size_t total;
   int64_t mp;       // M rounded up to a multiple of 8
   int32_t rpad;
@@ -198,7 +196,33 @@ struct BwdWorkspace {
 // the split area holds only the status word).
 FwdWorkspace fwd_workspace_layout(int64_t M, int64_t N, int64_t K, int32_t r,
                                   bool general, bool split = true);
-BwdWorkspace bwd_workspace_layout(int64_t M, int64_t N, int64_t K, int32_t r,
-                                  bool act8 = false);
+BwdWorkspace bwd_workspace_layout(int64_t M, int64_t N, int64_t K, int32_t r);
+
+// ---- adapter gradients from an 8-bit checkpoint (adapter8.hip).
+// Waves of a workgroup of the column sums: their LDS slots (half of the
+// waves, 16 jt x 68 floats each) stay within 140 KB.
+constexpr int cols_waves(int jt) { return jt <= 4 ? 8 : 4; }
+// Column blocks of 64 and slices of the rows (steps of 32): about two
+// workgroups per CU, each wave with a step at least.
+struct ColsPlan {
+  int cb, slices, steps, steps_per;
+};
+ColsPlan cols_plan(int64_t M, int64_t C, int jt);
+
+struct Act8BwdWorkspace {
+  size_t split;       // as BwdWorkspace (offset 0)
+  size_t bt;          // bf16 [r, N]     B transposed
+  size_t atp;         // bf16 [K, rpad]  A transposed, zero-padded
+  size_t gh, gl;      // bf16 [M, rpad]  two terms of s*G for the dX GEMM
+  size_t prow;        // fp32 [nb, M, rpad] column-block partials of G
+  size_t ut, ug;      // bf16 [ceil(M / 32), jt, 3, 64, 8]  s*T, s*G as three
+                      // terms in operand order
+  size_t pb, pa;      // fp32 [slices, N r], [slices, K r] partial dB, dA
+                      // (with one slice the gradients are written directly)
+  size_t total;
+  int32_t rpad;
+};
+Act8BwdWorkspace act8_bwd_workspace_layout(int64_t M, int64_t N, int64_t K,
+                                           int32_t r);
 
 }  // namespace qn
