@@ -879,13 +879,38 @@ def _seq_batch(fn: str, logits, labels, offsets):
         _tensor(fn, "offsets", offsets, n, torch.int64, index), n[0] - 1)
 
 
-def _seq_workspace(fn, b, like, ws, index):
-    """(address, bytes, tensor) of the caller's workspace or a new one."""
+def _seq_buffers(fn, b, like, given: dict, ws, index):
+    """({name: tensor}, {name: address}, workspace address, bytes, what keeps
+    the workspace alive) of a forward's fp32 outputs; `given` maps a name to
+    (tensor or None, length).  What the caller does not bring comes from one
+    allocation."""
     import torch
+    f32 = torch.float32
+    outs, ptrs, sizes, names = {}, {}, [], []
+    nw = 0
     if ws is None:
-        ws = like.new_empty(max(1, qn_seq_workspace_bytes(b.rows, b.vocab, b.nseq)),
-                            dtype=torch.uint8)
-    return (*_workspace(fn, ws, index), ws)
+        nw = qn_seq_workspace_bytes(b.rows, b.vocab, b.nseq)
+        sizes.append(nw // 4)
+    for name, (t, n) in given.items():
+        if t is None:
+            names.append(name)
+            sizes.append(n)
+        else:
+            outs[name], ptrs[name] = t, _tensor(fn, name, t, (n,), f32, index)
+    buf = None
+    if sizes:
+        buf = like.new_empty(sum(sizes), dtype=f32)
+        base = at = buf.data_ptr()
+        views = torch.split_with_sizes(buf, sizes)
+        at += nw
+        for name, v, n in zip(names, views[1:] if ws is None else views,
+                              sizes[1:] if ws is None else sizes):
+            outs[name], ptrs[name] = v, at
+            at += 4 * n
+    if ws is None:
+        return outs, ptrs, base, nw, buf
+    pw, nw = _workspace(fn, ws, index)
+    return outs, ptrs, pw, nw, ws
 
 
 def _status_ptr(fn, status, index):
@@ -897,23 +922,15 @@ def qn_seq_logprob(logits, labels, offsets, lse=None, logp=None, status=None,
                    ws=None, stream=None):
     """Log-probability of each packed sequence and log-sum-exp of each row;
     returns (logp [nseq], lse [rows])."""
-    import torch
     fn = "qn_seq_logprob"
     index, b = _seq_batch(fn, logits, labels, offsets)
-    f32 = torch.float32
 
     def body(st):
-        e, g = lse, logp
-        if e is None:
-            e = logits.new_empty(b.rows, dtype=f32)
-        if g is None:
-            g = logits.new_empty(b.nseq, dtype=f32)
-        pw, nw, _w = _seq_workspace(fn, b, logits, ws, index)
-        _check(fn, lib().qn_seq_logprob(
-            b, _tensor(fn, "lse", e, (b.rows,), f32, index),
-            _tensor(fn, "logp", g, (b.nseq,), f32, index),
-            _status_ptr(fn, status, index), pw, nw, st))
-        return g, e
+        o, p, pw, nw, _keep = _seq_buffers(
+            fn, b, logits, {"logp": (logp, b.nseq), "lse": (lse, b.rows)}, ws, index)
+        _check(fn, lib().qn_seq_logprob(b, p["lse"], p["logp"], _status_ptr(fn, status, index),
+                                        pw, nw, st))
+        return o["logp"], o["lse"]
     return _run_on(index, stream, body)
 
 
@@ -942,19 +959,14 @@ def qn_pref_loss_fwd(logits, labels, offsets, ref_logp, beta: float,
     pr = None if ref_logp is None else _tensor(fn, "ref_logp", ref_logp, (nseq,), f32, index)
 
     def body(st):
-        o = out
-        if o is None:
-            o = PrefLoss(logits.new_empty(pairs, dtype=f32), logits.new_empty(nseq, dtype=f32),
-                         logits.new_empty(nseq, dtype=f32), logits.new_empty(rows, dtype=f32))
-        pw, nw, _w = _seq_workspace(fn, b, logits, ws, index)
+        g = out or PrefLoss(None, None, None, None)
+        o, p, pw, nw, _keep = _seq_buffers(
+            fn, b, logits, {"loss": (g.loss, pairs), "logp": (g.logp, nseq),
+                            "dlogp": (g.dlogp, nseq), "lse": (g.lse, rows)}, ws, index)
         _check(fn, lib().qn_pref_loss_fwd(
-            b, pr, _PrefHP(beta, label_smoothing),
-            _tensor(fn, "lse", o.lse, (rows,), f32, index),
-            _tensor(fn, "logp", o.logp, (nseq,), f32, index),
-            _tensor(fn, "loss", o.loss, (pairs,), f32, index),
-            _tensor(fn, "dlogp", o.dlogp, (nseq,), f32, index),
+            b, pr, _PrefHP(beta, label_smoothing), p["lse"], p["logp"], p["loss"], p["dlogp"],
             _status_ptr(fn, status, index), pw, nw, st))
-        return o
+        return PrefLoss(**o) if out is None else out
     return _run_on(index, stream, body)
 
 

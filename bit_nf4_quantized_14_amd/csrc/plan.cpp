@@ -212,11 +212,25 @@ BwdWorkspace bwd_workspace_layout(int64_t M, int64_t N, int64_t K,
   return L;
 }
 
-ColsPlan cols_plan(int64_t M, int64_t C, int jt) {
+ColsPlan cols_plan(int64_t M, int64_t C, int64_t other, int jt) {
   ColsPlan P;
-  P.cb = (int)cdiv(C, 64);
+  const int64_t width = 16 * cols_lane(jt);
+  P.cb = (int)cdiv(C, width);
+  P.parts = jt > COLS_JT ? jt / COLS_JT : 1;
   P.steps = (int)cdiv(M, 32);
-  const int64_t want = std::min(cdiv(2 * G_CUS, P.cb), cdiv(P.steps, cols_waves(jt)));
+  const int64_t want = std::max<int64_t>(
+      1, std::min(COLS_WGS / (P.parts * (P.cb + cdiv(other, width))),
+                  cdiv(P.steps, cols_waves(jt))));
+  P.steps_per = (int)cdiv(P.steps, want);
+  P.slices = (int)cdiv(P.steps, P.steps_per);
+  return P;
+}
+
+DxPlan dx_plan(int64_t N, int64_t K) {
+  DxPlan P;
+  P.cb = (int)cdiv(K, 128);
+  P.steps = (int)cdiv(N, 32);
+  const int64_t want = std::min(cdiv(G_CUS, P.cb), cdiv(P.steps, 8));
   P.steps_per = (int)cdiv(P.steps, want);
   P.slices = (int)cdiv(P.steps, P.steps_per);
   return P;
@@ -228,7 +242,7 @@ Act8BwdWorkspace act8_bwd_workspace_layout(int64_t M, int64_t N, int64_t K,
   const int jt = rank_tiles(r);
   L.rpad = 16 * jt;
   const StreamPlan Pg = stream_plan(RS_ROWS, M, N, jt);
-  const ColsPlan Pb = cols_plan(M, N, jt), Pa = cols_plan(M, K, jt);
+  const ColsPlan Pb = cols_plan(M, N, K, jt), Pa = cols_plan(M, K, N, jt);
   const size_t frag = size_t(Pb.steps) * jt * 3 * 64 * 16;
   size_t off = 0;
   const auto take = [&off](size_t bytes) {
@@ -246,6 +260,7 @@ Act8BwdWorkspace act8_bwd_workspace_layout(int64_t M, int64_t N, int64_t K,
   L.ug = take(frag);
   L.pb = take(Pb.slices > 1 ? size_t(Pb.slices) * N * r * 4 : 0);
   L.pa = take(Pa.slices > 1 ? size_t(Pa.slices) * K * r * 4 : 0);
+  L.px = take(M <= DX_SKINNY_M ? size_t(dx_plan(N, K).slices) * M * K * 4 : 0);
   L.total = off;
   return L;
 }

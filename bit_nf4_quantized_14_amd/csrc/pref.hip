@@ -20,32 +20,43 @@ using namespace qn;
 
 constexpr int SQ_THREADS = 256;                // 4 waves
 constexpr int SQ_STEP = SQ_THREADS * 8;        // elements a workgroup takes at once
+#ifndef SQ_G
+#define SQ_G 4
+#endif
+constexpr int SQ_GROUPS = SQ_G;                // 16-byte loads of a thread in flight
 constexpr float SQ_LOG2E = 1.4426950408889634f;
 constexpr float SQ_NEG_INF = -__builtin_inff();
 
-// Eight consecutive logits from element c of a row; elements from `vocab`
-// on read as -infinity.  16-byte loads at any alignment.
+// Eight consecutive logits from element c of a row, all of them inside it.
+// 16-byte loads, which this hardware does at any alignment (rows of an odd
+// pitch start anywhere).
 template <bool F32>
-__device__ __forceinline__ void sq_load(const char* row, int64_t c, int64_t vocab,
-                                        float (&v)[8]) {
+__device__ __forceinline__ void sq_load8(const char* row, int c, float* v) {
   typedef uint32_t v4 __attribute__((ext_vector_type(4), aligned(2)));
-  if (c + 8 <= vocab) {
-    if constexpr (F32) {
-      const v4 p = *reinterpret_cast<const v4*>(row + 4 * c);
-      const v4 q = *reinterpret_cast<const v4*>(row + 4 * c + 16);
+  if constexpr (F32) {
+    const v4 p = *reinterpret_cast<const v4*>(row + 4 * (int64_t)c);
+    const v4 q = *reinterpret_cast<const v4*>(row + 4 * (int64_t)c + 16);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] = __uint_as_float(p[i]);
-        v[4 + i] = __uint_as_float(q[i]);
-      }
-    } else {
-      const v4 p = *reinterpret_cast<const v4*>(row + 2 * c);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(p[i] << 16);
-        v[2 * i + 1] = __uint_as_float(p[i] & 0xFFFF0000u);
-      }
+    for (int i = 0; i < 4; ++i) {
+      v[i] = __uint_as_float(p[i]);
+      v[4 + i] = __uint_as_float(q[i]);
     }
+  } else {
+    const v4 p = *reinterpret_cast<const v4*>(row + 2 * (int64_t)c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(p[i] << 16);
+      v[2 * i + 1] = __uint_as_float(p[i] & 0xFFFF0000u);
+    }
+  }
+}
+
+// The same where the group may pass `vocab`: elements from there on read as
+// -infinity.
+template <bool F32>
+__device__ __forceinline__ void sq_load(const char* row, int c, int vocab, float (&v)[8]) {
+  if (c + 8 <= vocab) {
+    sq_load8<F32>(row, c, v);
     return;
   }
 #pragma unroll
@@ -81,15 +92,49 @@ struct SeqArgs {
   const char* logits;
   const int64_t* labels;
   const int64_t* offsets;
-  int64_t vocab, ld, chunk;
-  int32_t rows, nseq, nchunk;
+  int64_t ld;
+  int32_t vocab, chunk, rows, nseq, nchunk;
 };
 
-// Maximum and sum of one chunk of one row.  Rows that are not counted are
-// not read.
+// The workspace of the forward: a row's partial sums, or, where one
+// workgroup takes the whole row, its token's log-probability.
+union SeqPart {
+  MaxSum part;     // [rows][nchunk]
+  double token;    // [rows], nchunk == 1
+};
+static_assert(sizeof(SeqPart) == 8, "one slot for each row and workgroup");
+
+// Adds logits to a running maximum and sum.
+template <int N>
+__device__ __forceinline__ void sq_add(MaxSum& r, const float (&v)[N]) {
+  float m = r.m;
+#pragma unroll
+  for (int i = 0; i < N; ++i) m = fmaxf(m, v[i]);
+  const float z = sq_shift(m);
+  float s = r.s * sq_exp(r.m - z), s2 = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    s += sq_exp(v[i] - z);
+    s2 += sq_exp(v[i + 1] - z);
+  }
+  r = MaxSum{m, s + s2};
+}
+
 template <bool F32>
-__global__ __launch_bounds__(SQ_THREADS) void k_seq_rows(SeqArgs a, MaxSum* __restrict__ part,
+__device__ __forceinline__ double sq_logit(const char* row, int64_t c) {
+  return F32 ? (double)reinterpret_cast<const float*>(row)[c]
+             : (double)bf16_to_f32(reinterpret_cast<const uint16_t*>(row)[c]);
+}
+
+// Maximum and sum of one chunk of one row.  Rows that are not counted are
+// not read.  Each thread keeps SQ_GROUPS 16-byte loads in flight; the last
+// round (one group at a time where at most half of the groups are left)
+// reads a group from the end of the chunk where it would pass it, and drops
+// what another thread has.
+template <bool F32>
+__global__ __launch_bounds__(SQ_THREADS) void k_seq_rows(SeqArgs a, SeqPart* __restrict__ ws,
                                                          float* __restrict__ lse) {
+  constexpr int G = F32 ? SQ_GROUPS / 2 : SQ_GROUPS;
   __shared__ MaxSum red[SQ_THREADS / 64];
   const int row = (int)(blockIdx.x / (unsigned)a.nchunk);
   const int ch = (int)(blockIdx.x - (unsigned)row * (unsigned)a.nchunk);
@@ -101,19 +146,42 @@ __global__ __launch_bounds__(SQ_THREADS) void k_seq_rows(SeqArgs a, MaxSum* __re
     return;
   }
   const char* p = a.logits + (int64_t)row * a.ld * (F32 ? 4 : 2);
-  const int64_t begin = ch * a.chunk, end = min(a.vocab, begin + a.chunk);
+  const int begin = ch * a.chunk, end = min(a.vocab, begin + a.chunk);
   MaxSum r{SQ_NEG_INF, 0.0f};
-  for (int64_t c = begin + 8 * threadIdx.x; c < end; c += SQ_STEP) {
+  int c = begin + 8 * threadIdx.x;
+  int at = begin;
+  for (; at + G * SQ_STEP <= end; at += G * SQ_STEP, c += G * SQ_STEP) {
+    float v[8 * G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) sq_load8<F32>(p, c + g * SQ_STEP, v + 8 * g);
+    sq_add(r, v);
+  }
+  if (end - begin >= 8) {
+    for (; at < end && end - at <= SQ_STEP * (G / 2); at += SQ_STEP, c += SQ_STEP) {
+      float v[8];
+      sq_load8<F32>(p, min(c, end - 8), v);
+      const int skip = c - (end - 8);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = i >= skip ? v[i] : SQ_NEG_INF;
+      sq_add(r, v);
+    }
+    if (at < end) {
+      float v[8 * G];
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        sq_load8<F32>(p, min(c + g * SQ_STEP, end - 8), v + 8 * g);
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const int skip = c + g * SQ_STEP - (end - 8);   // of this group, if any
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[8 * g + i] = i >= skip ? v[8 * g + i] : SQ_NEG_INF;
+      }
+      sq_add(r, v);
+    }
+  } else {                             // a vocabulary of fewer than 8 words
     float v[8];
     sq_load<F32>(p, c, end, v);
-    float m = r.m;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, v[i]);
-    const float z = sq_shift(m);
-    float s = r.s * sq_exp(r.m - z);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s += sq_exp(v[i] - z);
-    r = MaxSum{m, s};
+    sq_add(r, v);
   }
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1)
@@ -122,19 +190,14 @@ __global__ __launch_bounds__(SQ_THREADS) void k_seq_rows(SeqArgs a, MaxSum* __re
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int w = 1; w < SQ_THREADS / 64; ++w) r = sq_join(r, red[w]);
-    part[(int64_t)row * a.nchunk + ch] = r;
+    if (a.nchunk > 1) {
+      ws[(int64_t)row * a.nchunk + ch].part = r;
+    } else {
+      const double l = (double)r.m + log((double)r.s);
+      lse[row] = (float)l;
+      ws[row].token = sq_logit<F32>(p, label) - l;
+    }
   }
-}
-
-__device__ __forceinline__ double sq_logit(const SeqArgs& a, bool f32, int64_t row, int64_t c) {
-  const int64_t i = row * a.ld + c;
-  return f32 ? (double)reinterpret_cast<const float*>(a.logits)[i]
-             : (double)bf16_to_f32(reinterpret_cast<const uint16_t*>(a.logits)[i]);
-}
-
-// log(1 + exp(-x)) = -log sigmoid(x)
-__device__ __forceinline__ double sq_softplus_neg(double x) {
-  return log1p(exp(-fabs(x))) + (x < 0.0 ? -x : 0.0);
 }
 
 struct PrefArgs {
@@ -146,58 +209,83 @@ struct PrefArgs {
 
 constexpr int SQ_FIN = 1024;
 
-// Sum over the rows of sequence s, in a fixed order; writes lse of its rows
-// and (thread 0) logp[s].  Every thread gets the sum.
-__device__ double sq_sequence(const SeqArgs& a, bool f32, const MaxSum* __restrict__ part,
-                              float* __restrict__ lse, float* __restrict__ logp,
-                              int32_t* status, int s, double* red) {
+// Sum over the rows of sequence s that the calling wave takes (wave `w` of
+// `nw`); writes lse of rows that were split, which a wave joins with a
+// partial sum in each lane.
+template <bool F32>
+__device__ __forceinline__ double sq_rows_sum(const SeqArgs& a, const SeqPart* __restrict__ ws,
+                                              float* __restrict__ lse, int32_t* status, int s,
+                                              int w, int nw) {
+  const int lane = threadIdx.x & 63;
   const int64_t lo = a.offsets[s], hi = a.offsets[s + 1];
   const int64_t begin = min(max(lo, (int64_t)0), (int64_t)a.rows);
   const int64_t end = min(max(hi, begin), (int64_t)a.rows);
   bool bad = begin != lo || end != hi;
   double sum = 0.0;
-  for (int64_t t = begin + threadIdx.x; t < end; t += SQ_FIN) {
-    const int64_t label = a.labels[t];
-    if (label >= a.vocab) bad = true;
-    if (label < 0 || label >= a.vocab) continue;
-    const double hit = sq_logit(a, f32, t, label);
-    const MaxSum* q = part + t * a.nchunk;
-    MaxSum r = q[0];
-    for (int c = 1; c < a.nchunk; ++c) r = sq_join(r, q[c]);
-    const double l = (double)r.m + log((double)r.s);
-    lse[t] = (float)l;
-    sum += hit - l;
+  if (a.nchunk == 1) {
+    for (int64_t t = begin + 64 * w + lane; t < end; t += 64 * nw) {
+      const int64_t label = a.labels[t];
+      const double tok = ws[t].token;
+      bad = bad || label >= a.vocab;
+      sum += label >= 0 && label < a.vocab ? tok : 0.0;
+    }
+  } else {
+    for (int64_t t = begin + w; t < end; t += nw) {
+      const int64_t label = a.labels[t];
+      bad = bad || label >= a.vocab;
+      if (label < 0 || label >= a.vocab) continue;
+      const double hit = sq_logit<F32>(a.logits + t * a.ld * (F32 ? 4 : 2), label);
+      MaxSum r{SQ_NEG_INF, 0.0f};
+      for (int c = lane; c < a.nchunk; c += 64) r = sq_join(r, ws[t * a.nchunk + c].part);
+#pragma unroll
+      for (int off = 32; off >= 1; off >>= 1)
+        r = sq_join(r, MaxSum{__shfl_xor(r.m, off), __shfl_xor(r.s, off)});
+      const double l = (double)r.m + log((double)r.s);
+      if (lane == 0) {
+        lse[t] = (float)l;
+        sum += hit - l;
+      }
+    }
   }
   if (bad && status != nullptr) *status = QN_EINVAL;
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off);
-  __syncthreads();                       // red is free again
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
-  __syncthreads();
-  sum = 0.0;
-  for (int w = 0; w < SQ_FIN / 64; ++w) sum += red[w];
-  if (threadIdx.x == 0) logp[s] = (float)sum;
   return sum;
 }
 
-// One workgroup per sequence, or per pair of sequences and their loss.
-__global__ __launch_bounds__(SQ_FIN) void k_seq_finish(SeqArgs a, int f32,
-                                                       const MaxSum* __restrict__ part,
+// One workgroup per sequence, or per pair of sequences (half of the waves
+// each) and their loss.
+template <bool F32>
+__global__ __launch_bounds__(SQ_FIN) void k_seq_finish(SeqArgs a, const SeqPart* __restrict__ ws,
                                                        float* __restrict__ lse,
                                                        float* __restrict__ logp,
                                                        int32_t* status, PrefArgs pa) {
-  __shared__ double red[SQ_FIN / 64];
-  const int b = blockIdx.x;
-  const double c = sq_sequence(a, f32 != 0, part, lse, logp, status, b, red);
-  if (pa.pairs == 0) return;
-  const double r = sq_sequence(a, f32 != 0, part, lse, logp, status, pa.pairs + b, red);
+  constexpr int W = SQ_FIN / 64;
+  __shared__ double red[W];
+  const int b = blockIdx.x, wave = threadIdx.x >> 6;
+  const int nw = pa.pairs > 0 ? W / 2 : W;          // waves of a sequence
+  const int second = wave >= nw;
+  const double part = sq_rows_sum<F32>(a, ws, lse, status, b + second * pa.pairs,
+                                       wave - second * nw, nw);
+  if ((threadIdx.x & 63) == 0) red[wave] = part;
+  __syncthreads();
   if (threadIdx.x != 0) return;
+  double c = 0.0, r = 0.0;
+  for (int w = 0; w < W; ++w) (w < nw ? c : r) += red[w];
+  logp[b] = (float)c;
+  if (pa.pairs == 0) return;
+  logp[pa.pairs + b] = (float)r;
   const double rc = pa.ref != nullptr ? (double)pa.ref[b] : 0.0;
   const double rr = pa.ref != nullptr ? (double)pa.ref[pa.pairs + b] : 0.0;
   const double h = pa.beta * ((c - rc) - (r - rr)), e = pa.smooth;
-  pa.loss[b] = (float)((1.0 - e) * sq_softplus_neg(h) + (e > 0.0 ? e * sq_softplus_neg(-h) : 0.0));
-  // sigmoid(-h) = 1 / (1 + exp(h)): an exp that overflows gives 0
-  const double g = pa.beta * (e / (1.0 + exp(-h)) - (1.0 - e) / (1.0 + exp(h)));
+  // with t = exp(-|h|): -log sigmoid(h) = log(1 + t) + max(-h, 0) and
+  // sigmoid(|h|) = 1 / (1 + t), so nothing overflows
+  const double t = exp(-fabs(h)), l = log1p(t), q = 1.0 / (1.0 + t);
+  const double up = h >= 0.0 ? q : t * q, down = h >= 0.0 ? t * q : q;
+  double loss = (1.0 - e) * (l + (h < 0.0 ? -h : 0.0));
+  if (e > 0.0) loss += e * (l + (h > 0.0 ? h : 0.0));
+  const double g = pa.beta * (e * up - (1.0 - e) * down);
+  pa.loss[b] = (float)loss;
   pa.dlogp[b] = (float)g;
   pa.dlogp[pa.pairs + b] = (float)-g;
 }
@@ -205,15 +293,19 @@ __global__ __launch_bounds__(SQ_FIN) void k_seq_finish(SeqArgs a, int f32,
 struct SeqBwdArgs {
   const float *lse, *dlogp, *dloss;
   char* out;
-  int64_t cols, ld_out;
+  int64_t ld_out;
+  int32_t cols;
   int32_t pairs;      // 0: dlogp alone
   float mean;         // dloss of every pair where dloss is null
 };
 
 template <bool F32>
-__device__ __forceinline__ void sq_store(char* row, int64_t c, int64_t cols, const float (&v)[8]) {
+__device__ __forceinline__ void sq_store(char* base, int at, int cols, const float (&v)[8]) {
   typedef uint32_t v4 __attribute__((ext_vector_type(4), aligned(2)));
-  if (c + 8 <= cols) {
+  char* row = base + (int64_t)at * (F32 ? 4 : 2);
+  constexpr int c = 0;
+  cols -= at;
+  if (8 <= cols) {
     if constexpr (F32) {
       *reinterpret_cast<v4*>(row + 4 * c) =
           v4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
@@ -251,10 +343,10 @@ __global__ __launch_bounds__(SQ_THREADS) void k_seq_bwd(SeqArgs a, SeqBwdArgs g)
   }
   const bool counted = label >= 0 && label < a.vocab && row >= a.offsets[0] && seq < a.nseq;
   char* out = g.out + (int64_t)row * g.ld_out * (FOUT ? 4 : 2);
-  const int64_t begin = ch * a.chunk, end = min(g.cols, begin + a.chunk);
+  const int begin = ch * a.chunk, end = min(g.cols, begin + a.chunk);
   if (!counted) {
     const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int64_t c = begin + 8 * threadIdx.x; c < end; c += SQ_STEP)
+    for (int c = begin + 8 * threadIdx.x; c < end; c += SQ_STEP)
       sq_store<FOUT>(out, c, end, zero);
     return;
   }
@@ -263,14 +355,15 @@ __global__ __launch_bounds__(SQ_THREADS) void k_seq_bwd(SeqArgs a, SeqBwdArgs g)
     coef *= g.dloss != nullptr ? g.dloss[seq < g.pairs ? seq : seq - g.pairs] : g.mean;
   const float lse = g.lse[row];
   const char* p = a.logits + (int64_t)row * a.ld * (FIN ? 4 : 2);
-  for (int64_t c = begin + 8 * threadIdx.x; c < end; c += SQ_STEP) {
+  const int hit = (int)label;
+  for (int c = begin + 8 * threadIdx.x; c < end; c += SQ_STEP) {
     float v[8];
     sq_load<FIN>(p, c, a.vocab, v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = -coef * sq_exp(v[i] - lse);
-    if (label >= c && label < c + 8) {
+    if (hit >= c && hit < c + 8) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += c + i == label ? coef : 0.0f;
+      for (int i = 0; i < 8; ++i) v[i] += c + i == hit ? coef : 0.0f;
     }
     if (c + 8 > a.vocab) {     // padding columns: zero whatever coef is
 #pragma unroll
@@ -301,11 +394,11 @@ bool valid_batch(const qn_seq_batch* b) {
 // Workgroups per row and the columns of each: one where the rows fill the
 // GPU, else about SQ_FILL workgroups in all, of at least one step each.
 constexpr int64_t SQ_FILL = 8 * G_CUS;
-void split_rows(int64_t rows, int64_t cols, int64_t* chunk, int32_t* nchunk) {
+void split_rows(int64_t rows, int64_t cols, int32_t* chunk, int32_t* nchunk) {
   const int64_t steps = cdiv(cols, SQ_STEP);
   const int64_t want = rows > 0 ? std::min(steps, cdiv(SQ_FILL, rows)) : 1;
   const int64_t per = cdiv(steps, want);
-  *chunk = per * SQ_STEP;
+  *chunk = (int32_t)(per * SQ_STEP);
   *nchunk = (int32_t)cdiv(steps, per);
 }
 
@@ -314,7 +407,7 @@ SeqArgs seq_args(const qn_seq_batch* b, int64_t cols) {
   a.logits = static_cast<const char*>(b->logits);
   a.labels = b->labels;
   a.offsets = b->offsets;
-  a.vocab = b->vocab;
+  a.vocab = (int32_t)b->vocab;
   a.ld = b->ld;
   a.rows = (int32_t)b->rows;
   a.nseq = (int32_t)b->nseq;
@@ -329,7 +422,7 @@ int seq_forward(const qn_seq_batch* b, float* lse, float* logp, int32_t* status,
   if (ws == nullptr || !aligned16(ws) ||
       ws_bytes < qn_seq_workspace_bytes(b->rows, b->vocab, b->nseq))
     return QN_EWORKSPACE;
-  MaxSum* part = static_cast<MaxSum*>(ws);
+  SeqPart* part = static_cast<SeqPart*>(ws);
   hipStream_t st = (hipStream_t)stream;
   const bool f32 = b->dtype == QN_F32;
   if (b->rows > 0) {
@@ -339,9 +432,13 @@ int seq_forward(const qn_seq_batch* b, float* lse, float* logp, int32_t* status,
     else
       QN_LAUNCH("k_seq_rows", k_seq_rows<false>, grid, dim3(SQ_THREADS), st, a, part, lse);
   }
-  QN_LAUNCH("k_seq_finish", k_seq_finish,
-            dim3((unsigned)(pa.pairs > 0 ? pa.pairs : b->nseq)), dim3(SQ_FIN), st, a,
-            (int)f32, part, lse, logp, status, pa);
+  const dim3 grid((unsigned)(pa.pairs > 0 ? pa.pairs : b->nseq));
+  if (f32)
+    QN_LAUNCH("k_seq_finish", k_seq_finish<true>, grid, dim3(SQ_FIN), st, a, part, lse, logp,
+              status, pa);
+  else
+    QN_LAUNCH("k_seq_finish", k_seq_finish<false>, grid, dim3(SQ_FIN), st, a, part, lse, logp,
+              status, pa);
   return check_launch();
 }
 
@@ -362,7 +459,7 @@ int seq_backward(const qn_seq_batch* b, const float* lse, const float* dlogp,
   g.dlogp = dlogp;
   g.dloss = dloss;
   g.out = static_cast<char*>(dl);
-  g.cols = cols;
+  g.cols = (int32_t)cols;
   g.ld_out = ld_dl;
   g.pairs = pairs;
   g.mean = pairs > 0 ? (float)(1.0 / pairs) : 0.0f;
@@ -384,10 +481,9 @@ int seq_backward(const qn_seq_batch* b, const float* lse, const float* dlogp,
 
 extern "C" size_t qn_seq_workspace_bytes(int64_t rows, int64_t vocab, int64_t nseq) {
   if (!valid_sizes(rows, vocab, nseq)) return 0;
-  int64_t chunk;
-  int32_t nchunk;
+  int32_t chunk, nchunk;
   split_rows(rows, vocab, &chunk, &nchunk);
-  return align256(std::max<size_t>(1, size_t(rows) * nchunk * sizeof(MaxSum)));
+  return align256(std::max<size_t>(1, size_t(rows) * nchunk * sizeof(SeqPart)));
 }
 
 extern "C" int qn_seq_logprob(const qn_seq_batch* b, float* lse, float* logp,

@@ -134,6 +134,23 @@ void launch_finish(hipStream_t st, FinishArgs& a);
 // ---- act8.hip: 8-bit activation checkpoints.
 bool valid_act8(const qn_act8* t);
 
+// ---- skinny_dx.hip: dX for few tokens.
+struct DxSkinny {
+  const uint16_t* dy;
+  const uint8_t *packed, *qabs;
+  const float* gscale;
+  int M, N, K;
+  int cb, slices, steps, steps_per;   // as DxPlan
+  float* part;                        // [slices][M][K]
+  const float* G;                     // s G, fp32 [M][ldg]
+  int ldg;
+  const uint16_t* A;                  // bf16 [r][K]
+  int r;
+  void* dx;
+  int dx_bf16;
+};
+void launch_dx_skinny(hipStream_t st, const DxSkinny& p);   // the slices
+
 // ---- adapter8.hip: adapter gradients from an 8-bit checkpoint.
 struct AdapterSplit {           // U = scale sum_b src[b] as three bf16 terms
   const float* src;             // [nb][M][ld], blocks bstride apart
@@ -144,6 +161,7 @@ struct AdapterSplit {           // U = scale sum_b src[b] as three bf16 terms
   float scale;
   uint16_t* frag;               // [ceil(M / 32)][jt][3][64][8]
   uint16_t *hi, *lo;            // [M][16 jt] terms 0 and 1, or null
+  float* full;                  // [M][16 jt] U itself, or null
   uint32_t* zero;               // zero_words words to clear on the way
   int64_t zero_words, total;
 };
@@ -154,7 +172,7 @@ struct ColsJob {                // column sums of S against U
   int M, C, r;
   const uint16_t* U;            // an AdapterSplit's frag
   float* out;                   // slices of [C][r], or of [r][C] with by_j
-  int by_j, cb, slices, steps, steps_per;
+  int by_j, cb, parts, slices, steps, steps_per;   // as ColsPlan
 };
 struct ColsReduce {             // out[i] = sum of slices of part[slice][i]
   const float* part;
@@ -162,9 +180,16 @@ struct ColsReduce {             // out[i] = sum of slices of part[slice][i]
   int64_t n;                    // 0: nothing to do
   int slices;
 };
-void launch_adapter_split(hipStream_t st, AdapterSplit& p);
-void launch_adapter_cols(hipStream_t st, const ColsJob& B, const ColsJob& A, int r,
-                         const DropArgs* drop);
+struct AdapterTranspose {       // dst [n][8 chunks] = src [valid][n]^T, bf16,
+  const uint16_t* src;          // zero past `valid`; chunks 0: nothing to do
+  uint16_t* dst;
+  int valid, n, chunks;
+};
+void launch_adapter_split(hipStream_t st, AdapterSplit p, const AdapterTranspose& t0,
+                          const AdapterTranspose& t1);
+// X: few tokens, the slices of dX to be added up in the same launch (or null)
+void launch_adapter_cols(hipStream_t st, const ColsJob& B, const ColsJob& A, const DxSkinny* X,
+                         int r, const DropArgs* drop);
 void launch_adapter_reduce(hipStream_t st, const ColsReduce& p0, const ColsReduce& p1);
 
 // ---- skinny.hip: forward for M <= 16 tokens, a batch of up to

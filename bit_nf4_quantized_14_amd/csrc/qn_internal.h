@@ -199,26 +199,48 @@ FwdWorkspace fwd_workspace_layout(int64_t M, int64_t N, int64_t K, int32_t r,
 BwdWorkspace bwd_workspace_layout(int64_t M, int64_t N, int64_t K, int32_t r);
 
 // ---- adapter gradients from an 8-bit checkpoint (adapter8.hip).
-// Waves of a workgroup of the column sums: their LDS slots (half of the
-// waves, 16 jt x 68 floats each) stay within 140 KB.
+// A workgroup of the column sums takes up to COLS_JT tiles of 16 ranks: 8
+// fill the registers of one wave per SIMD (with 16 the sums spilled).  Its
+// waves' LDS slots (half of the waves' sums) are 70 KB at most.
+constexpr int COLS_JT = 8;
 constexpr int cols_waves(int jt) { return jt <= 4 ? 8 : 4; }
-// Column blocks of 64 and slices of the rows (steps of 32): about two
-// workgroups per CU, each wave with a step at least.
+// Columns of a lane; 16 lanes stand side by side.  8 read whole 256-byte
+// pieces of dY's rows (7B gate backward, r = 16: 24.7 us and 4.8 us for the
+// slices' sum, with 4 columns 29.8 us); from r = 17 on the wider workgroup
+// needs slices where the narrow one does not (1003 x 1024 x 8192, r = 24:
+// 9.4 and 4.0 us, with 4 columns 9.9 us).
+constexpr int cols_lane(int jt) { return jt == 1 ? 8 : 4; }
+// Column blocks and slices of the rows (steps of 32) of one of the two jobs
+// of a launch (`other`: the other one's columns): at most COLS_WGS
+// workgroups in all where one slice does not give more, each wave with a
+// step at least.  One workgroup per CU: with two (512) the 70B adapters'
+// launch took 29.5 us and 5.2 us for the sum, with one 23 us and no sum.
+constexpr int64_t COLS_WGS = G_CUS;
 struct ColsPlan {
+  int cb, parts, slices, steps, steps_per;   // parts: of the rank
+};
+ColsPlan cols_plan(int64_t M, int64_t C, int64_t other, int jt);
+
+// dX for few tokens (skinny_dx.hip): blocks of 128 columns, slices of the
+// weight's rows (steps of 32), about one workgroup per CU.
+constexpr int64_t DX_SKINNY_M = 64;
+struct DxPlan {
   int cb, slices, steps, steps_per;
 };
-ColsPlan cols_plan(int64_t M, int64_t C, int jt);
+DxPlan dx_plan(int64_t N, int64_t K);
 
 struct Act8BwdWorkspace {
   size_t split;       // as BwdWorkspace (offset 0)
   size_t bt;          // bf16 [r, N]     B transposed
   size_t atp;         // bf16 [K, rpad]  A transposed, zero-padded
-  size_t gh, gl;      // bf16 [M, rpad]  two terms of s*G for the dX GEMM
+  size_t gh, gl;      // bf16 [M, rpad]  two terms of s*G for the dX GEMM, or
+                      // (M <= DX_SKINNY_M, at gh) fp32 s*G
   size_t prow;        // fp32 [nb, M, rpad] column-block partials of G
   size_t ut, ug;      // bf16 [ceil(M / 32), jt, 3, 64, 8]  s*T, s*G as three
                       // terms in operand order
   size_t pb, pa;      // fp32 [slices, N r], [slices, K r] partial dB, dA
                       // (with one slice the gradients are written directly)
+  size_t px;          // fp32 [slices, M, K] partial dX (M <= DX_SKINNY_M)
   size_t total;
   int32_t rpad;
 };

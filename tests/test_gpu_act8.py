@@ -170,6 +170,13 @@ def _check_bwd(m, n, k, r, alpha, p=0.0, seed=0, dx_dtype=capi.QN_F32, need_dx=T
     (1, 8, 64, 1, 1.0), (37, 200, 192, 5, 7.0), (16, 64, 4160, 33, 64.0),
     (130, 136, 320, 64, 16.0), (64, 128, 256, 256, 512.0), (300, 264, 1024, 16, 32.0),
     (257, 1024, 576, 16, 32.0), (520, 256, 640, 100, 100.0), (1003, 64, 128, 8, 16.0),
+    # few tokens: one, two and four tiles of 16, a half block of columns, one
+    # and many slices of the weight's rows; and the first M of the GEMM
+    (16, 4096, 1088, 16, 32.0), (17, 1032, 192, 12, 12.0), (33, 1032, 1216, 12, 24.0),
+    (64, 520, 4160, 40, 40.0), (65, 520, 320, 16, 16.0),
+    # ranks in two parts, and row slices of each width of workgroup
+    (200, 136, 192, 160, 160.0), (1500, 72, 64, 200, 200.0), (2100, 64, 64, 64, 64.0),
+    (2100, 136, 64, 16, 16.0), (2100, 64, 128, 24, 24.0),
 ])
 def test_backward_from_a_checkpoint(m, n, k, r, alpha):
     _check_bwd(m, n, k, r, alpha)
@@ -177,7 +184,8 @@ def test_backward_from_a_checkpoint(m, n, k, r, alpha):
 
 @pytest.mark.parametrize("m,n,k,r,p", [
     (1, 8, 64, 1, 0.5), (37, 200, 192, 5, 0.1), (130, 136, 320, 64, 0.3),
-    (64, 128, 256, 256, 0.1), (258, 264, 576, 16, 0.05),
+    (64, 128, 256, 256, 0.1), (258, 264, 576, 16, 0.05), (33, 1032, 192, 12, 0.2),
+    (700, 72, 64, 160, 0.1), (1100, 64, 64, 24, 0.3),
 ])
 def test_backward_with_dropout(m, n, k, r, p):
     _check_bwd(m, n, k, r, 2.0 * r, p=p, seed=(m * 1000003 + k) | (1 << 40))
