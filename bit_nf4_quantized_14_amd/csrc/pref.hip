@@ -20,10 +20,7 @@ using namespace qn;
 
 constexpr int SQ_THREADS = 256;                // 4 waves
 constexpr int SQ_STEP = SQ_THREADS * 8;        // elements a workgroup takes at once
-#ifndef SQ_G
-#define SQ_G 4
-#endif
-constexpr int SQ_GROUPS = SQ_G;                // 16-byte loads of a thread in flight
+constexpr int SQ_GROUPS = 4;                   // 16-byte loads of a thread in flight
 constexpr float SQ_LOG2E = 1.4426950408889634f;
 constexpr float SQ_NEG_INF = -__builtin_inff();
 
@@ -210,8 +207,10 @@ struct PrefArgs {
 constexpr int SQ_FIN = 1024;
 
 // Sum over the rows of sequence s that the calling wave takes (wave `w` of
-// `nw`); writes lse of rows that were split, which a wave joins with a
-// partial sum in each lane.
+// `nw`); writes lse of rows that were split.  A row's partial sums are
+// joined by one lane where there are at most 8 of them (then there are many
+// rows), else by 8 neighbouring lanes; with a whole wave to a row, 1024 rows
+// of one pair took 130 us here.
 template <bool F32>
 __device__ __forceinline__ double sq_rows_sum(const SeqArgs& a, const SeqPart* __restrict__ ws,
                                               float* __restrict__ lse, int32_t* status, int s,
@@ -230,18 +229,29 @@ __device__ __forceinline__ double sq_rows_sum(const SeqArgs& a, const SeqPart* _
       sum += label >= 0 && label < a.vocab ? tok : 0.0;
     }
   } else {
-    for (int64_t t = begin + w; t < end; t += nw) {
+    const int team = a.nchunk <= 8 ? 1 : 8, sub = lane & (team - 1);
+    for (int64_t t = begin + (64 * w + lane) / team; t < end; t += 64 * nw / team) {
       const int64_t label = a.labels[t];
       bad = bad || label >= a.vocab;
-      if (label < 0 || label >= a.vocab) continue;
+      if (label < 0 || label >= a.vocab) continue;      // the whole team's
       const double hit = sq_logit<F32>(a.logits + t * a.ld * (F32 ? 4 : 2), label);
+      const SeqPart* q = ws + t * a.nchunk;
       MaxSum r{SQ_NEG_INF, 0.0f};
-      for (int c = lane; c < a.nchunk; c += 64) r = sq_join(r, ws[t * a.nchunk + c].part);
+      for (int c0 = sub; c0 < a.nchunk; c0 += 8 * team) {
+        MaxSum x[8];
 #pragma unroll
-      for (int off = 32; off >= 1; off >>= 1)
-        r = sq_join(r, MaxSum{__shfl_xor(r.m, off), __shfl_xor(r.s, off)});
+        for (int u = 0; u < 8; ++u)
+          x[u] = c0 + u * team < a.nchunk ? q[c0 + u * team].part : MaxSum{SQ_NEG_INF, 0.0f};
+#pragma unroll
+        for (int u = 0; u < 8; ++u) r = sq_join(r, x[u]);
+      }
+      if (team == 8) {
+#pragma unroll
+        for (int off = 4; off >= 1; off >>= 1)
+          r = sq_join(r, MaxSum{__shfl_xor(r.m, off), __shfl_xor(r.s, off)});
+      }
       const double l = (double)r.m + log((double)r.s);
-      if (lane == 0) {
+      if (sub == 0) {
         lse[t] = (float)l;
         sum += hit - l;
       }
@@ -299,38 +309,52 @@ struct SeqBwdArgs {
   float mean;         // dloss of every pair where dloss is null
 };
 
-template <bool F32>
+// Non-temporal (NT) stores leave the caches to others.  A gradient of 64 MB
+// and more does not stay in them until it is read: 8 pairs of 256 tokens and
+// 32000 words (250 MB) took 167 us forward and backward with plain stores,
+// 137 us with these, and with a pass that reads the gradient behind it 253
+// and 236 us; 125 MB: 130 and 124 us; 31 MB: 93 and 96 us, so smaller ones
+// are stored plainly.
+constexpr int64_t SQ_NT_BYTES = 64 << 20;
+
+template <bool NT, typename V>
+__device__ __forceinline__ void sq_put(char* p, V v) {
+  if constexpr (NT)
+    __builtin_nontemporal_store(v, reinterpret_cast<V*>(p));
+  else
+    *reinterpret_cast<V*>(p) = v;
+}
+
+template <bool F32, bool NT>
 __device__ __forceinline__ void sq_store(char* base, int at, int cols, const float (&v)[8]) {
   typedef uint32_t v4 __attribute__((ext_vector_type(4), aligned(2)));
-  char* row = base + (int64_t)at * (F32 ? 4 : 2);
-  constexpr int c = 0;
-  cols -= at;
-  if (8 <= cols) {
+  char* p = base + (int64_t)at * (F32 ? 4 : 2);
+  if (at + 8 <= cols) {
     if constexpr (F32) {
-      *reinterpret_cast<v4*>(row + 4 * c) =
-          v4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
-      *reinterpret_cast<v4*>(row + 4 * c + 16) =
-          v4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])};
+      sq_put<NT>(p, v4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                       __float_as_uint(v[3])});
+      sq_put<NT>(p + 16, v4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]),
+                            __float_as_uint(v[7])});
     } else {
-      *reinterpret_cast<v4*>(row + 2 * c) = v4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                               pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+      sq_put<NT>(p, v4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                       pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])});
     }
     return;
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    if (c + i < cols) {
+    if (at + i < cols) {
       if constexpr (F32)
-        reinterpret_cast<float*>(row)[c + i] = v[i];
+        reinterpret_cast<float*>(p)[i] = v[i];
       else
-        reinterpret_cast<uint16_t*>(row)[c + i] = (uint16_t)(pack_bf16x2(v[i], 0.0f) & 0xFFFFu);
+        reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)(pack_bf16x2(v[i], 0.0f) & 0xFFFFu);
     }
 }
 
 // Gradient of one chunk of one row.  Its sequence is the number of
 // offsets[1..nseq] that are not behind the row, counted by every wave for
 // itself (64 offsets at a time).
-template <bool FIN, bool FOUT>
+template <bool FIN, bool FOUT, bool NT>
 __global__ __launch_bounds__(SQ_THREADS) void k_seq_bwd(SeqArgs a, SeqBwdArgs g) {
   const int row = (int)(blockIdx.x / (unsigned)a.nchunk);
   const int ch = (int)(blockIdx.x - (unsigned)row * (unsigned)a.nchunk);
@@ -347,7 +371,7 @@ __global__ __launch_bounds__(SQ_THREADS) void k_seq_bwd(SeqArgs a, SeqBwdArgs g)
   if (!counted) {
     const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (int c = begin + 8 * threadIdx.x; c < end; c += SQ_STEP)
-      sq_store<FOUT>(out, c, end, zero);
+      sq_store<FOUT, NT>(out, c, end, zero);
     return;
   }
   float coef = g.dlogp[seq];
@@ -369,7 +393,7 @@ __global__ __launch_bounds__(SQ_THREADS) void k_seq_bwd(SeqArgs a, SeqBwdArgs g)
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = c + i < a.vocab ? v[i] : 0.0f;
     }
-    sq_store<FOUT>(out, c, end, v);
+    sq_store<FOUT, NT>(out, c, end, v);
   }
 }
 
@@ -466,14 +490,20 @@ int seq_backward(const qn_seq_batch* b, const float* lse, const float* dlogp,
   hipStream_t st = (hipStream_t)stream;
   const dim3 grid((unsigned)(b->rows * a.nchunk)), wg(SQ_THREADS);
   const bool fi = b->dtype == QN_F32, fo = dl_dtype == QN_F32;
-  if (fi && fo)
-    QN_LAUNCH("k_seq_bwd", (k_seq_bwd<true, true>), grid, wg, st, a, g);
-  else if (fi)
-    QN_LAUNCH("k_seq_bwd", (k_seq_bwd<true, false>), grid, wg, st, a, g);
-  else if (fo)
-    QN_LAUNCH("k_seq_bwd", (k_seq_bwd<false, true>), grid, wg, st, a, g);
-  else
-    QN_LAUNCH("k_seq_bwd", (k_seq_bwd<false, false>), grid, wg, st, a, g);
+  const bool nt = b->rows * cols * (fo ? 4 : 2) >= SQ_NT_BYTES;
+#define SQ_BWD(FI, FO, NT) \
+  QN_LAUNCH("k_seq_bwd", (k_seq_bwd<FI, FO, NT>), grid, wg, st, a, g)
+  switch (4 * fi + 2 * fo + nt) {
+    case 0: SQ_BWD(false, false, false); break;
+    case 1: SQ_BWD(false, false, true); break;
+    case 2: SQ_BWD(false, true, false); break;
+    case 3: SQ_BWD(false, true, true); break;
+    case 4: SQ_BWD(true, false, false); break;
+    case 5: SQ_BWD(true, false, true); break;
+    case 6: SQ_BWD(true, true, false); break;
+    default: SQ_BWD(true, true, true); break;
+  }
+#undef SQ_BWD
   return check_launch();
 }
 
