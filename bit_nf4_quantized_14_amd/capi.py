@@ -657,10 +657,17 @@ def _bad(fn: str, what: str):
     return QNError(fn, QN_EINVAL, what)
 
 
+_raw = None
+
+
 def _raw_stream(index: int) -> int:
-    import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(index) if raw else torch.cuda.current_stream(index).cuda_stream
+    """Handle of device `index`'s current stream."""
+    global _raw
+    if _raw is None:
+        import torch
+        _raw = getattr(torch._C, "_cuda_getCurrentRawStream",
+                       lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return _raw(index)
 
 
 def _run_on(index: int, stream, body):
@@ -770,8 +777,12 @@ def qn_act8_encode(x, out: Act8Tensor | None = None, stream=None):
         raise _bad(fn, "out has another shape than x")
 
     def body(st):
-        t = out if out is not None else Act8Tensor.empty(shape[0], shape[1], device=x.device)
-        s = t.checked_struct(fn, index)
+        t = out
+        if t is None:
+            t = Act8Tensor.empty(shape[0], shape[1], device=x.device)
+            s = t.as_struct()
+        else:
+            s = t.checked_struct(fn, index)
         _check(fn, lib().qn_act8_encode(px, code, s, st))
         return t
     return _run_on(index, stream, body)
@@ -786,11 +797,13 @@ def qn_act8_decode(x8: Act8Tensor, out=None, dtype: int = QN_BF16, stream=None):
     shape = (x8.rows, x8.cols)
 
     def body(st):
-        y = out
+        y, code = out, dtype
         if y is None:
             y = x8.codes.new_empty(shape, dtype=_torch_dtype(fn, dtype))
-        py = _tensor(fn, "out", y, shape, None, index)
-        _check(fn, lib().qn_act8_decode(s, py, _dtype_code(fn, "out", y), st))
+            py = y.data_ptr()
+        else:
+            py, code = _tensor(fn, "out", y, shape, None, index), _dtype_code(fn, "out", y)
+        _check(fn, lib().qn_act8_decode(s, py, code, st))
         return y
     return _run_on(index, stream, body)
 
@@ -825,26 +838,29 @@ def qlora_linear_bwd_act8(dy, x8: Act8Tensor, w: NF4Tensor, A, B, r: int,
 
     def body(st):
         gx, gA, gB = dx, dA, dB
-        if need_dx and gx is None:
+        pdx, code = None, dx_dtype
+        if gx is not None:
+            pdx, code = _tensor(fn, "dx", gx, (M, K), None, index), _dtype_code(fn, "dx", gx)
+        elif need_dx:
             gx = dy.new_empty((M, K), dtype=_torch_dtype(fn, dx_dtype))
+            pdx = gx.data_ptr()
         if gA is None:
             gA = dy.new_empty((r, K), dtype=f32)
+        else:
+            _tensor(fn, "dA", gA, (r, K), f32, index)
         if gB is None:
             gB = dy.new_empty((N, r), dtype=f32)
-        wk = ws
-        if wk is None:
-            wk = dy.new_empty(max(1, qlora_bwd_act8_workspace_bytes(M, N, K, r)),
-                              dtype=torch.uint8)
-        pw, nw = _workspace(fn, wk, index)
-        pdx, code = None, QN_F32
-        if need_dx:
-            pdx = _tensor(fn, "dx", gx, (M, K), None, index)
-            code = _dtype_code(fn, "dx", gx)
-        d = _Dropout(p, seed & 0xFFFFFFFFFFFFFFFF)
+        else:
+            _tensor(fn, "dB", gB, (N, r), f32, index)
+        if ws is None:
+            nw = qlora_bwd_act8_workspace_bytes(M, N, K, r)
+            wk = dy.new_empty(nw, dtype=torch.uint8)
+            pw = wk.data_ptr()
+        else:
+            pw, nw = _workspace(fn, ws, index)
         _check(fn, lib().qlora_linear_bwd_act8(
-            pdy, xt, M, w.as_struct(), pA, pB, r, alpha, pt, pdx, code,
-            _tensor(fn, "dA", gA, (r, K), f32, index),
-            _tensor(fn, "dB", gB, (N, r), f32, index), d, pw, nw, st))
+            pdy, xt, M, w.as_struct(), pA, pB, r, alpha, pt, pdx, code, gA.data_ptr(),
+            gB.data_ptr(), _Dropout(p, seed & 0xFFFFFFFFFFFFFFFF), pw, nw, st))
         return gx, gA, gB
     return _run_on(index, stream, body)
 

@@ -8,6 +8,8 @@ namespace {
 
 using namespace qn;
 
+constexpr int AD_W = 8;     // waves of the kernels for G and between
+
 // ---------------------------------------------------------------------------
 // Operand U [M][r] (s T or s G, fp32) as three bf16 terms u0 + u1 + u2: the
 // matrix cores take bf16, and two terms (2^-17 of a value lost) would be the
@@ -68,16 +70,337 @@ __device__ __forceinline__ void transpose_thread(const AdapterTranspose& p, int6
   reinterpret_cast<u32x4*>(p.dst)[(int64_t)col * p.chunks + ch] = w;
 }
 
-// One launch: the split, then (by block) up to two transposes.
-__global__ __launch_bounds__(256) void k_adapter_split(AdapterSplit p, AdapterTranspose t0,
-                                                       AdapterTranspose t1, int nb0, int nb1) {
+// ---------------------------------------------------------------------------
+// G = dY B, partial sums over slices of dY's columns n.
+//
+// A workgroup owns 16 TR tokens; its waves take the slice's steps of 32 H
+// columns in turn and add through LDS at the end, in a fixed order.  dY is
+// the first MFMA operand as it lies in memory (lane l: token l % 16, columns
+// 8 (l / 16) .. + 7, 16 bytes).  B [N][r] is the second one through
+// registers, without a transposed copy: the lane loads L adjacent ranks of
+// its 8 rows n, and a byte shuffle makes the operands of L MFMAs, number c
+// for ranks L i + c, i = 0 .. 15.  VEC: B's rows allow loads of L ranks
+// (r a multiple of L, B aligned to them); else one rank at a time.
+// ---------------------------------------------------------------------------
+template <int JT>
+struct RowsCfg {
+  static constexpr int TR = rows_tiles(JT), H = rows_halves(JT);
+  static constexpr int L = JT < 8 ? JT : 8, PARTS = JT / L;
+  static constexpr int LW = L > 1 ? L / 2 : 1;          // dwords of L ranks
+  static constexpr int P = 16 * JT + 4;                 // LDS pitch of a token
+  static constexpr int SLOT = 16 * TR * P;
+};
+
+template <int JT>
+struct RowsRegs {
+  u32x4 y[RowsCfg<JT>::H][RowsCfg<JT>::TR];
+  uint32_t b[RowsCfg<JT>::H][RowsCfg<JT>::PARTS][8][RowsCfg<JT>::LW];
+};
+
+template <int JT, bool VEC>
+__device__ __forceinline__ void rows_load(RowsRegs<JT>& R, rsrc_t ry, rsrc_t rb, int m0, int n0,
+                                          const RowsJob& p, int lane) {
+  using G = RowsCfg<JT>;
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+  for (int h = 0; h < G::H; ++h) {
+    const int n = n0 + 32 * h + 8 * (lane >> 4);
+#pragma unroll
+    for (int t = 0; t < G::TR; ++t) {
+      const int m = m0 + 16 * t + (lane & 15);
+      const uint32_t off =
+          m < p.M && n < p.N ? ((uint32_t)m * (uint32_t)p.N + (uint32_t)n) * 2u : G_OOB;
+      R.y[h][t] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ry, off, 0, 0));
+    }
+#pragma unroll
+    for (int q = 0; q < G::PARTS; ++q)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int j = 16 * G::L * q + G::L * (lane & 15);
+        const uint32_t at = ((uint32_t)(n + i) * (uint32_t)p.r + (uint32_t)j) * 2u;
+        const bool row = n + i < p.N;
+        if constexpr (VEC && G::L > 1) {
+          const uint32_t off = row && j < p.r ? at : G_OOB;
+          if constexpr (G::L == 2) {
+            R.b[h][q][i][0] = __builtin_amdgcn_raw_buffer_load_b32(rb, off, 0, 0);
+          } else if constexpr (G::L == 4) {
+            const u32x2 v = __builtin_bit_cast(
+                u32x2, __builtin_amdgcn_raw_buffer_load_b64(rb, off, 0, 0));
+            R.b[h][q][i][0] = v.x;
+            R.b[h][q][i][1] = v.y;
+          } else {
+            const u32x4 v = __builtin_bit_cast(
+                u32x4, __builtin_amdgcn_raw_buffer_load_b128(rb, off, 0, 0));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) R.b[h][q][i][k] = v[k];
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < G::LW; ++k) {
+            const uint32_t lo = row && j + 2 * k < p.r ? at + 4u * k : G_OOB;
+            uint32_t w = __builtin_amdgcn_raw_buffer_load_b16(rb, lo, 0, 0);
+            if constexpr (G::L > 1) {
+              const uint32_t hi = row && j + 2 * k + 1 < p.r ? at + 4u * k + 2u : G_OOB;
+              w |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(rb, hi, 0, 0) << 16;
+            }
+            R.b[h][q][i][k] = w;
+          }
+        }
+      }
+  }
+}
+
+template <int JT, bool VEC>
+__global__ __launch_bounds__(64 * AD_W) void k_adapter_rows(RowsJob p) {
+  using G = RowsCfg<JT>;
+  __shared__ __attribute__((aligned(16))) float red[(AD_W / 2) * G::SLOT];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int m0 = 16 * G::TR * (int)(blockIdx.x % p.mt), slice = blockIdx.x / p.mt;
+  const int s0 = slice * p.steps_per, s1 = min(p.steps, s0 + p.steps_per);
+  const rsrc_t ry = make_rsrc(p.dy, (uint32_t)p.M * (uint32_t)p.N * 2u);
+  const rsrc_t rb = make_rsrc(p.B, (uint32_t)p.N * (uint32_t)p.r * 2u);
+  f32x4 acc[G::TR][JT];
+#pragma unroll
+  for (int t = 0; t < G::TR; ++t)
+#pragma unroll
+    for (int j = 0; j < JT; ++j) acc[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  RowsRegs<JT> R;
+  if (s0 + wave < s1) rows_load<JT, VEC>(R, ry, rb, m0, 32 * G::H * (s0 + wave), p, lane);
+  for (int s = s0 + wave; s < s1; s += AD_W) {
+    const RowsRegs<JT> X = R;
+    if (s + AD_W < s1) rows_load<JT, VEC>(R, ry, rb, m0, 32 * G::H * (s + AD_W), p, lane);
+#pragma unroll
+    for (int h = 0; h < G::H; ++h)
+#pragma unroll
+      for (int q = 0; q < G::PARTS; ++q)
+#pragma unroll
+        for (int c = 0; c < G::L; ++c) {
+          u32x4 b;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            b[k] = perm(X.b[h][q][2 * k + 1][c / 2], X.b[h][q][2 * k][c / 2],
+                        c % 2 ? 0x07060302u : 0x05040100u);
+#pragma unroll
+          for (int t = 0; t < G::TR; ++t)
+            acc[t][G::L * q + c] = mfma16(X.y[h][t], b, acc[t][G::L * q + c]);
+        }
+  }
+
+  // acc[t][L q + c][v] of lane l: token 16 t + 4 (l / 16) + v, rank
+  // 16 L q + L (l % 16) + c
+  const auto at = [&](float* slot, int t, int q, int v) {
+    return slot + (16 * t + 4 * (lane >> 4) + v) * G::P + 16 * G::L * q + G::L * (lane & 15);
+  };
+#pragma unroll
+  for (int half = AD_W / 2; half >= 1; half /= 2) {
+    if (wave >= half && wave < 2 * half) {
+#pragma unroll
+      for (int t = 0; t < G::TR; ++t)
+#pragma unroll
+        for (int q = 0; q < G::PARTS; ++q)
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+#pragma unroll
+            for (int c = 0; c < G::L; ++c)
+              at(red + (wave - half) * G::SLOT, t, q, v)[c] = acc[t][G::L * q + c][v];
+    }
+    __syncthreads();
+    if (wave < half) {
+#pragma unroll
+      for (int t = 0; t < G::TR; ++t)
+#pragma unroll
+        for (int q = 0; q < G::PARTS; ++q)
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+#pragma unroll
+            for (int c = 0; c < G::L; ++c)
+              acc[t][G::L * q + c][v] += at(red + wave * G::SLOT, t, q, v)[c];
+    }
+    __syncthreads();
+  }
+  if (wave == 0) {
+#pragma unroll
+    for (int t = 0; t < G::TR; ++t)
+#pragma unroll
+      for (int q = 0; q < G::PARTS; ++q)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+#pragma unroll
+          for (int c = 0; c < G::L; ++c) at(red, t, q, v)[c] = acc[t][G::L * q + c][v];
+  }
+  __syncthreads();
+  float* out = p.out + ((int64_t)slice * p.M + m0) * (16 * JT);
+  const int n = min(16 * G::TR, p.M - m0) * 16 * JT;
+  for (int i = tid; i < n; i += 64 * AD_W) out[i] = red[(i / (16 * JT)) * G::P + i % (16 * JT)];
+}
+
+// ---------------------------------------------------------------------------
+// dX of few tokens (M <= DX_SKINNY_M): dY W', the reduction over the weight's
+// rows n, bound by streaming the
+// 4-bit weight (the 128 x 128 tiles of the GEMM spend 32 us on a 4096 x 4096
+// weight for any M up to 128: 64 workgroups, 32 dependent steps each).
+//
+// A workgroup owns 128 columns k and a slice of the rows n; its 8 waves take
+// the slice's steps of 32 rows in turn.  Lane l loads the packed dword of
+// columns 8 (l % 16) .. + 7 of rows 8 (l / 16) .. + 7: nibble c of the eight
+// dwords is the transposed operand (8 rows of one column) of MFMA number c,
+// whose columns are 8 i + c, i = 0 .. 15.  A code's level comes from a
+// 16-entry LDS table (16 banks, so no conflicts), is multiplied by the
+// block's constant of its row in fp32 and rounded to bf16, which is W'
+// exactly.  The waves add through LDS in a fixed order; slices are added,
+// with the adapter term, by blocks of k_adapter_cols.
+// ---------------------------------------------------------------------------
+constexpr int DX_P = 132;            // LDS pitch of a token's 128 columns
+
+template <int MT>
+struct DxRegs {
+  uint32_t w[8];                     // packed codes
+  uint32_t q, d;                     // constant of row lane % 32, block lane / 32
+  u32x4 y[MT];                       // dY of token l % 16, rows 8 (l / 16) .. + 7
+};
+
+template <int MT>
+__device__ __forceinline__ void dx_load(DxRegs<MT>& R, rsrc_t rw, rsrc_t rq, rsrc_t rd, rsrc_t ry,
+                                        int n0, int c0, int M, int N, int K, int lane) {
+  const int col = c0 + 8 * (lane & 15), g = lane >> 4;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int n = n0 + 8 * g + i;
+    const uint32_t off = n < N && col < K
+                             ? (uint32_t)(((int64_t)n * K + col) >> 1) : G_OOB;
+    R.w[i] = __builtin_amdgcn_raw_buffer_load_b32(rw, off, 0, 0);
+  }
+  const int n = n0 + (lane & 31), kb = c0 + 64 * (lane >> 5);
+  const bool in = n < N && kb < K;
+  const int64_t blk = ((int64_t)n * K + kb) >> 6;
+  R.q = __builtin_amdgcn_raw_buffer_load_b8(rq, in ? (uint32_t)blk : G_OOB, 0, 0);
+  R.d = __builtin_amdgcn_raw_buffer_load_b32(rd, in ? (uint32_t)(blk >> 8) * 4u : G_OOB, 0, 0);
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const int m = 16 * t + (lane & 15), nn = n0 + 8 * g;
+    const uint32_t off = m < M && nn < N ? (uint32_t)(((int64_t)m * N + nn) * 2) : G_OOB;
+    R.y[t] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ry, off, 0, 0));
+  }
+}
+
+template <int MT>
+__device__ __forceinline__ void dx_body(const DxSkinny& p, const Codebook& cb, int block,
+                                        float* red, float* level) {
+  constexpr int SLOT = 16 * MT * DX_P;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  if (tid < 16) {
+    float v = cb.L[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) v = tid == i ? cb.L[i] : v;
+    level[tid] = v;
+  }
+  __syncthreads();
+  const int c0 = 128 * (block % p.cb), slice = block / p.cb;
+  const int s0 = slice * p.steps_per, s1 = min(p.steps, s0 + p.steps_per);
+  const int64_t nk = (int64_t)p.N * p.K;
+  const rsrc_t rw = make_rsrc(p.packed, (uint32_t)(nk >> 1));
+  const rsrc_t rq = make_rsrc(p.qabs, (uint32_t)(nk >> 6));
+  const rsrc_t rd = make_rsrc(p.gscale, (uint32_t)((nk + 16383) >> 14) * 4u);
+  const rsrc_t ry = make_rsrc(p.dy, (uint32_t)((int64_t)p.M * p.N * 2));
+  f32x4 acc[MT][8];
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int c = 0; c < 8; ++c) acc[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  DxRegs<MT> R;
+  if (s0 + wave < s1)
+    dx_load<MT>(R, rw, rq, rd, ry, 32 * (s0 + wave), c0, p.M, p.N, p.K, lane);
+  for (int s = s0 + wave; s < s1; s += AD_W) {
+    const DxRegs<MT> X = R;
+    if (s + AD_W < s1)
+      dx_load<MT>(R, rw, rq, rd, ry, 32 * (s + AD_W), c0, p.M, p.N, p.K, lane);
+    // c' of the lane's eight rows, of the block its columns are in
+    const float cp = (float)X.q * __uint_as_float(X.d);
+    const int from = 8 * (lane >> 4) + 32 * ((lane >> 3) & 1);
+    float sc[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sc[i] = __shfl(cp, from + i);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      u32x4 b;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float x = level[(X.w[2 * q] >> (4 * c)) & 15u] * sc[2 * q];
+        const float y = level[(X.w[2 * q + 1] >> (4 * c)) & 15u] * sc[2 * q + 1];
+        b[q] = pack_bf16x2(x, y);
+      }
+#pragma unroll
+      for (int t = 0; t < MT; ++t) acc[t][c] = mfma16(X.y[t], b, acc[t][c]);
+    }
+  }
+
+  // acc[t][c][v] of lane l: token 16 t + 4 (l / 16) + v, column 8 (l % 16) + c
+  const auto at = [&](float* slot, int t, int v, int h) {
+    return reinterpret_cast<f32x4*>(slot + (16 * t + 4 * (lane >> 4) + v) * DX_P +
+                                    8 * (lane & 15) + 4 * h);
+  };
+  const auto put = [&](float* slot) {
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          *at(slot, t, v, h) = f32x4{acc[t][4 * h][v], acc[t][4 * h + 1][v],
+                                     acc[t][4 * h + 2][v], acc[t][4 * h + 3][v]};
+  };
+#pragma unroll
+  for (int half = AD_W / 2; half >= 1; half /= 2) {
+    if (wave >= half && wave < 2 * half) put(red + (wave - half) * SLOT);
+    __syncthreads();
+    if (wave < half) {
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const f32x4 x = *at(red + wave * SLOT, t, v, h);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[t][4 * h + c][v] += x[c];
+          }
+    }
+    __syncthreads();
+  }
+  if (wave == 0) put(red);
+  __syncthreads();
+  float* out = p.part + (int64_t)slice * p.M * p.K;
+  for (int i = tid; i < 32 * p.M; i += 64 * AD_W) {     // four columns each
+    const int m = i >> 5, c = 4 * (i & 31);
+    if (c0 + c < p.K)
+      *reinterpret_cast<f32x4*>(out + (int64_t)m * p.K + c0 + c) =
+          *reinterpret_cast<const f32x4*>(red + m * DX_P + c);
+  }
+}
+
+// The launch between G's partial sums and the column sums: (by block) the
+// slices of dX for few tokens (MT tiles of 16 of them), the split of s G, the
+// split of s T, and A transposed for the dX GEMM.
+template <int MT>
+__global__ __launch_bounds__(64 * AD_W) void k_adapter_mid(AdapterMid p, Codebook cb) {
+  __shared__ __attribute__((aligned(16))) float red[MT > 0 ? (AD_W / 2) * 16 * MT * DX_P : 4];
+  __shared__ float level[16];
   const int b = blockIdx.x;
-  if (b < nb0)
-    split_thread(p, (int64_t)b * 256 + threadIdx.x);
-  else if (b < nb1)
-    transpose_thread(t0, (int64_t)(b - nb0) * 256 + threadIdx.x);
+  if (MT > 0 && b < p.end[0]) {
+    dx_body<MT < 1 ? 1 : MT>(p.dx, cb, b, red, level);
+    return;
+  }
+  const auto thread = [&](int first) { return (int64_t)(b - first) * (64 * AD_W) + threadIdx.x; };
+  if (b < p.end[1])
+    split_thread(p.g, thread(p.end[0]));
+  else if (b < p.end[2])
+    split_thread(p.t, thread(p.end[1]));
   else
-    transpose_thread(t1, (int64_t)(b - nb1) * 256 + threadIdx.x);
+    transpose_thread(p.a, thread(p.end[2]));
 }
 
 // ---------------------------------------------------------------------------
@@ -384,14 +707,33 @@ namespace qn {
     default: { constexpr int JT = COLS_JT; CALL; break; } \
   }
 
-void launch_adapter_split(hipStream_t st, AdapterSplit p, const AdapterTranspose& t0,
-                          const AdapterTranspose& t1) {
-  p.total = cdiv(p.M, 32) * p.jt * 512;
-  const int nb0 = (int)cdiv(std::max<int64_t>(p.total, p.zero_words), 256);
-  const int nb1 = nb0 + (int)cdiv((int64_t)t0.chunks * t0.n, 256);
-  const int nb2 = nb1 + (int)cdiv((int64_t)t1.chunks * t1.n, 256);
-  QN_LAUNCH("k_adapter_split", k_adapter_split, dim3((unsigned)nb2), dim3(256), st, p, t0, t1,
-            nb0, nb1);
+void launch_adapter_rows(hipStream_t st, const RowsJob& p) {
+  const dim3 grid((unsigned)(p.mt * p.slices)), wg(64 * AD_W);
+  QN_RANK_DISPATCH(p.r, {
+    constexpr int L = RowsCfg<JT>::L;
+    if (p.r % L == 0 && (reinterpret_cast<uintptr_t>(p.B) & (2 * L - 1)) == 0)
+      QN_LAUNCH("k_adapter_rows", (k_adapter_rows<JT, true>), grid, wg, st, p);
+    else
+      QN_LAUNCH("k_adapter_rows", (k_adapter_rows<JT, false>), grid, wg, st, p);
+  });
+}
+
+void launch_adapter_mid(hipStream_t st, AdapterMid p) {
+  const auto blocks = [](int64_t threads) { return (int)cdiv(threads, 64 * AD_W); };
+  for (AdapterSplit* q : {&p.g, &p.t}) q->total = cdiv(q->M, 32) * q->jt * 512;
+  p.end[0] = p.dx.cb * p.dx.slices;
+  p.end[1] = p.end[0] + blocks(std::max<int64_t>(p.g.total, p.g.zero_words));
+  p.end[2] = p.end[1] + blocks(p.t.total);
+  const dim3 grid((unsigned)(p.end[2] + blocks((int64_t)p.a.chunks * p.a.n))), wg(64 * AD_W);
+  const Codebook cb = codebook();
+  if (p.end[0] == 0)
+    QN_LAUNCH("k_adapter_mid", k_adapter_mid<0>, grid, wg, st, p, cb);
+  else if (p.dx.M <= 16)
+    QN_LAUNCH("k_adapter_mid", k_adapter_mid<1>, grid, wg, st, p, cb);
+  else if (p.dx.M <= 32)
+    QN_LAUNCH("k_adapter_mid", k_adapter_mid<2>, grid, wg, st, p, cb);
+  else
+    QN_LAUNCH("k_adapter_mid", k_adapter_mid<4>, grid, wg, st, p, cb);
 }
 
 void launch_adapter_cols(hipStream_t st, const ColsJob& B, const ColsJob& A, const DxSkinny* X,

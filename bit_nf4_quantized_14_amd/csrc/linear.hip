@@ -247,8 +247,8 @@ int linear_bwd(const uint16_t* dy, const uint16_t* x, int64_t M,
 }
 
 // The backward with X as an 8-bit checkpoint; dx may be null.  Launches:
-// operands, G, split of G, dX (the GEMM, or its slices for few tokens), both
-// column sums, their slices (where there are any).
+// G, its split (and all that needs no G), the dX GEMM, both column sums (and
+// dX for few tokens), their slices (where there are any).
 int linear_bwd_act8(const uint16_t* dy, const qn_act8* x8, int64_t M,
                     const nf4_tensor* w, const uint16_t* A, const uint16_t* B,
                     int32_t r, float alpha, const float* t_saved, void* dx,
@@ -271,7 +271,6 @@ int linear_bwd_act8(const uint16_t* dy, const qn_act8* x8, int64_t M,
   const qn::Act8BwdWorkspace L = qn::act8_bwd_workspace_layout(M, N, K, r);
   if (ws == nullptr || ws_bytes < L.total || !aligned16(ws))
     return QN_EWORKSPACE;
-  uint16_t* Bt = ws_at<uint16_t>(ws, L.bt);
   uint16_t* Atp = ws_at<uint16_t>(ws, L.atp);
   uint16_t* Gh = ws_at<uint16_t>(ws, L.gh);
   uint16_t* Gl = ws_at<uint16_t>(ws, L.gl);
@@ -286,40 +285,34 @@ int linear_bwd_act8(const uint16_t* dy, const qn_act8* x8, int64_t M,
   // few tokens: dX by its own kernels, from A as it is
   const bool gemm = dx != nullptr && M > DX_SKINNY_M;
   const bool skinny = dx != nullptr && !gemm;
-  // B^T for the G pass, A^T padded to [K][rpad] for the GEMM, s T in three
-  // terms
-  const AdapterTranspose none{nullptr, nullptr, 0, 0, 0};
-  const AdapterTranspose tb{B, Bt, Ni, (int)r, Ni / 8};
-  const AdapterTranspose ta{A, Atp, (int)r, Ki, L.rpad / 8};
-  launch_adapter_split(st, AdapterSplit{t_saved, 0, (int)r, 1, M, (int)r, jt, s, UT,
-                                        nullptr, nullptr, nullptr, nullptr, 0, 0},
-                       tb, gemm ? ta : none);
-  // G = dY B: partials over column blocks of dY
-  const StreamPlan Pg = stream_plan(RS_ROWS, M, N, jt);
-  launch_rank_stream<RS_ROWS>(st, "k_rank_stream_g", Pg, dy, Mi, Ni, Bt, (int)r,
-                              nullptr, nullptr, 0, prow, nullptr, nullptr);
-  // s G in three terms (and as dX needs it); the status word and the
-  // counters of the GEMM's split tiles cleared
+  // G = dY B: partial sums over slices of dY's columns
+  const RowsPlan Pg = rows_plan(M, N, jt);
+  launch_adapter_rows(st, RowsJob{dy, B, Mi, Ni, (int)r, Pg.mt, Pg.slices, Pg.steps,
+                                  Pg.steps_per, prow});
+  // s T and s G in three terms (s G also as dX needs it), A^T padded to
+  // [K][rpad] for the GEMM, the slices of dX for few tokens; the status word
+  // and the counters of the GEMM's split tiles cleared
   const GemmSplit sp = gemm_split_plan(M, K, N, use_drop);
   float* Gf = reinterpret_cast<float*>(Gh);
-  launch_adapter_split(st, AdapterSplit{prow, (int64_t)M * L.rpad, L.rpad, Pg.nb, M, (int)r,
-                                        jt, s, UG, gemm ? Gh : nullptr, Gl,
-                                        skinny ? Gf : nullptr,
-                                        reinterpret_cast<uint32_t*>(split_ws),
-                                        (int64_t)(G_SPLIT_HDR / 4) + 2 * sp.rem, 0},
-                       none, none);
+  AdapterMid mid{};
+  mid.t = AdapterSplit{t_saved, 0, (int)r, 1, M, (int)r, jt, s, UT, nullptr, nullptr,
+                       nullptr, nullptr, 0, 0};
+  mid.g = AdapterSplit{prow, (int64_t)M * L.rpad, L.rpad, Pg.slices, M, (int)r, jt, s, UG,
+                       gemm ? Gh : nullptr, Gl, skinny ? Gf : nullptr,
+                       reinterpret_cast<uint32_t*>(split_ws),
+                       (int64_t)(G_SPLIT_HDR / 4) + 2 * sp.rem, 0};
+  if (gemm) mid.a = AdapterTranspose{A, Atp, (int)r, Ki, L.rpad / 8};
+  if (skinny) {
+    const DxPlan Px = dx_plan(N, K);
+    mid.dx = DxSkinny{dy, w->packed, w->qabs, w->gscale, Mi, Ni, Ki, Px.cb, Px.slices,
+                      Px.steps, Px.steps_per, ws_at<float>(ws, L.px), Gf, L.rpad, A,
+                      (int)r, dx, (int)(dx_dtype == QN_BF16)};
+  }
+  launch_adapter_mid(st, mid);
   const DropArgs* dp = use_drop ? &da : nullptr;
   if (gemm)
     launch_gemm<true>(st, dy, w, Gh, Gl, Atp, Mi, L.rpad, dx,
                       (int)(dx_dtype == QN_BF16), dp, split_ws);
-  DxSkinny px{};
-  if (skinny) {
-    const DxPlan Px = dx_plan(N, K);
-    px = DxSkinny{dy, w->packed, w->qabs, w->gscale, Mi, Ni, Ki, Px.cb, Px.slices,
-                      Px.steps, Px.steps_per, ws_at<float>(ws, L.px), Gf, L.rpad, A,
-                      (int)r, dx, (int)(dx_dtype == QN_BF16)};
-    launch_dx_skinny(st, px);
-  }
   // dB = dY^T (s T), dA = (s G)^T Xr
   const ColsPlan Pb = cols_plan(M, N, K, jt), Pa = cols_plan(M, K, N, jt);
   float* outB = Pb.slices > 1 ? ws_at<float>(ws, L.pb) : dB;
@@ -328,7 +321,7 @@ int linear_bwd_act8(const uint16_t* dy, const qn_act8* x8, int64_t M,
                    Pb.cb, Pb.parts, Pb.slices, Pb.steps, Pb.steps_per};
   const ColsJob ja{x8->codes, x8->scale, (uint32_t)(M * K), Mi, Ki, (int)r, UG, outA, 1,
                    Pa.cb, Pa.parts, Pa.slices, Pa.steps, Pa.steps_per};
-  launch_adapter_cols(st, jb, ja, skinny ? &px : nullptr, (int)r, dp);
+  launch_adapter_cols(st, jb, ja, skinny ? &mid.dx : nullptr, (int)r, dp);
   launch_adapter_reduce(
       st, ColsReduce{outB, dB, Pb.slices > 1 ? N * r : 0, Pb.slices},
       ColsReduce{outA, dA, Pa.slices > 1 ? K * r : 0, Pa.slices});

@@ -226,6 +226,17 @@ ColsPlan cols_plan(int64_t M, int64_t C, int64_t other, int jt) {
   return P;
 }
 
+RowsPlan rows_plan(int64_t M, int64_t N, int jt) {
+  RowsPlan P;
+  P.mt = (int)cdiv(M, 16 * rows_tiles(jt));
+  P.steps = (int)cdiv(N, 32 * rows_halves(jt));
+  const int64_t want =
+      std::max<int64_t>(1, std::min<int64_t>(rows_wgs(jt) / P.mt, cdiv(P.steps, 8)));
+  P.steps_per = (int)cdiv(P.steps, want);
+  P.slices = (int)cdiv(P.steps, P.steps_per);
+  return P;
+}
+
 DxPlan dx_plan(int64_t N, int64_t K) {
   DxPlan P;
   P.cb = (int)cdiv(K, 128);
@@ -241,7 +252,7 @@ Act8BwdWorkspace act8_bwd_workspace_layout(int64_t M, int64_t N, int64_t K,
   Act8BwdWorkspace L{};
   const int jt = rank_tiles(r);
   L.rpad = 16 * jt;
-  const StreamPlan Pg = stream_plan(RS_ROWS, M, N, jt);
+  const RowsPlan Pg = rows_plan(M, N, jt);
   const ColsPlan Pb = cols_plan(M, N, K, jt), Pa = cols_plan(M, K, N, jt);
   const size_t frag = size_t(Pb.steps) * jt * 3 * 64 * 16;
   size_t off = 0;
@@ -251,11 +262,10 @@ Act8BwdWorkspace act8_bwd_workspace_layout(int64_t M, int64_t N, int64_t K,
     return at;
   };
   L.split = take(gemm_split_bytes(gemm_split_plan(M, K, N, false)));
-  L.bt = take(size_t(r) * N * 2);
-  L.atp = take(size_t(K) * L.rpad * 2);
+  L.atp = take(M > DX_SKINNY_M ? size_t(K) * L.rpad * 2 : 0);
   L.gh = take(size_t(M) * L.rpad * 2);
   L.gl = take(size_t(M) * L.rpad * 2);
-  L.prow = take(size_t(Pg.nb) * M * L.rpad * 4);
+  L.prow = take(size_t(Pg.slices) * M * L.rpad * 4);
   L.ut = take(frag);
   L.ug = take(frag);
   L.pb = take(Pb.slices > 1 ? size_t(Pb.slices) * N * r * 4 : 0);

@@ -134,8 +134,8 @@ void launch_finish(hipStream_t st, FinishArgs& a);
 // ---- act8.hip: 8-bit activation checkpoints.
 bool valid_act8(const qn_act8* t);
 
-// ---- skinny_dx.hip: dX for few tokens.
-struct DxSkinny {
+// ---- adapter8.hip: the backward from an 8-bit checkpoint.
+struct DxSkinny {                     // dX of few tokens; cb 0: none
   const uint16_t* dy;
   const uint8_t *packed, *qabs;
   const float* gscale;
@@ -149,9 +149,6 @@ struct DxSkinny {
   void* dx;
   int dx_bf16;
 };
-void launch_dx_skinny(hipStream_t st, const DxSkinny& p);   // the slices
-
-// ---- adapter8.hip: adapter gradients from an 8-bit checkpoint.
 struct AdapterSplit {           // U = scale sum_b src[b] as three bf16 terms
   const float* src;             // [nb][M][ld], blocks bstride apart
   int64_t bstride;
@@ -185,8 +182,20 @@ struct AdapterTranspose {       // dst [n][8 chunks] = src [valid][n]^T, bf16,
   uint16_t* dst;
   int valid, n, chunks;
 };
-void launch_adapter_split(hipStream_t st, AdapterSplit p, const AdapterTranspose& t0,
-                          const AdapterTranspose& t1);
+struct RowsJob {                // partial G = dY B over slices of N
+  const uint16_t *dy, *B;
+  int M, N, r;
+  int mt, slices, steps, steps_per;   // as RowsPlan
+  float* out;                   // [slices][M][16 jt]
+};
+struct AdapterMid {
+  DxSkinny dx;
+  AdapterSplit g, t;
+  AdapterTranspose a;
+  int end[3];                   // first block behind dx, g and t
+};
+void launch_adapter_rows(hipStream_t st, const RowsJob& p);
+void launch_adapter_mid(hipStream_t st, AdapterMid p);
 // X: few tokens, the slices of dX to be added up in the same launch (or null)
 void launch_adapter_cols(hipStream_t st, const ColsJob& B, const ColsJob& A, const DxSkinny* X,
                          int r, const DropArgs* drop);

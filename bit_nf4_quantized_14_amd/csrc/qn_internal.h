@@ -221,7 +221,21 @@ struct ColsPlan {
 };
 ColsPlan cols_plan(int64_t M, int64_t C, int64_t other, int jt);
 
-// dX for few tokens (skinny_dx.hip): blocks of 128 columns, slices of the
+// G = dY B: blocks of 16 rows_tiles(jt) tokens, slices of the columns in steps
+// of 32 rows_halves(jt), at most rows_wgs(jt) workgroups where one slice does
+// not give more.  Up to 16 ranks B is a small part of what is read and two
+// workgroups per CU stream dY faster (7B gate, 4096 tokens: 23.1 us, one per
+// CU 25.2 us); above, the sums of many slices cost more (2048 x 8192, r = 64:
+// 17.8 us with two, 13.9 us with one, 12.3 us in steps of 32 instead of 64).
+constexpr int64_t rows_wgs(int jt) { return jt == 1 ? 2 * G_CUS : G_CUS; }
+constexpr int rows_tiles(int jt) { return jt <= 8 ? 2 : 1; }
+constexpr int rows_halves(int jt) { return jt == 1 ? 2 : 1; }
+struct RowsPlan {
+  int mt, slices, steps, steps_per;
+};
+RowsPlan rows_plan(int64_t M, int64_t N, int jt);
+
+// dX for few tokens: blocks of 128 columns, slices of the
 // weight's rows (steps of 32), about one workgroup per CU.
 constexpr int64_t DX_SKINNY_M = 64;
 struct DxPlan {
@@ -231,11 +245,10 @@ DxPlan dx_plan(int64_t N, int64_t K);
 
 struct Act8BwdWorkspace {
   size_t split;       // as BwdWorkspace (offset 0)
-  size_t bt;          // bf16 [r, N]     B transposed
-  size_t atp;         // bf16 [K, rpad]  A transposed, zero-padded
+  size_t atp;         // bf16 [K, rpad]  A transposed, zero-padded (GEMM)
   size_t gh, gl;      // bf16 [M, rpad]  two terms of s*G for the dX GEMM, or
                       // (M <= DX_SKINNY_M, at gh) fp32 s*G
-  size_t prow;        // fp32 [nb, M, rpad] column-block partials of G
+  size_t prow;        // fp32 [slices, M, rpad] partial G
   size_t ut, ug;      // bf16 [ceil(M / 32), jt, 3, 64, 8]  s*T, s*G as three
                       // terms in operand order
   size_t pb, pa;      // fp32 [slices, N r], [slices, K r] partial dB, dA
