@@ -237,12 +237,13 @@ __global__ __launch_bounds__(64 * AD_W) void k_adapter_rows(RowsJob p) {
 }
 
 // ---------------------------------------------------------------------------
-// dX of few tokens (M <= DX_SKINNY_M): dY W', the reduction over the weight's
+// dX of small outputs (dx_skinny): dY W', the reduction over the weight's
 // rows n, bound by streaming the
 // 4-bit weight (the 128 x 128 tiles of the GEMM spend 32 us on a 4096 x 4096
 // weight for any M up to 128: 64 workgroups, 32 dependent steps each).
 //
-// A workgroup owns 128 columns k and a slice of the rows n; its 8 waves take
+// A workgroup owns 128 columns k, 16 MT tokens and a slice of the rows n; its
+// 8 waves take
 // the slice's steps of 32 rows in turn.  Lane l loads the packed dword of
 // columns 8 (l % 16) .. + 7 of rows 8 (l / 16) .. + 7: nibble c of the eight
 // dwords is the transposed operand (8 rows of one column) of MFMA number c,
@@ -263,7 +264,7 @@ struct DxRegs {
 
 template <int MT>
 __device__ __forceinline__ void dx_load(DxRegs<MT>& R, rsrc_t rw, rsrc_t rq, rsrc_t rd, rsrc_t ry,
-                                        int n0, int c0, int M, int N, int K, int lane) {
+                                        int n0, int c0, int m0, int M, int N, int K, int lane) {
   const int col = c0 + 8 * (lane & 15), g = lane >> 4;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -279,7 +280,7 @@ __device__ __forceinline__ void dx_load(DxRegs<MT>& R, rsrc_t rw, rsrc_t rq, rsr
   R.d = __builtin_amdgcn_raw_buffer_load_b32(rd, in ? (uint32_t)(blk >> 8) * 4u : G_OOB, 0, 0);
 #pragma unroll
   for (int t = 0; t < MT; ++t) {
-    const int m = 16 * t + (lane & 15), nn = n0 + 8 * g;
+    const int m = m0 + 16 * t + (lane & 15), nn = n0 + 8 * g;
     const uint32_t off = m < M && nn < N ? (uint32_t)(((int64_t)m * N + nn) * 2) : G_OOB;
     R.y[t] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ry, off, 0, 0));
   }
@@ -298,7 +299,8 @@ __device__ __forceinline__ void dx_body(const DxSkinny& p, const Codebook& cb, i
     level[tid] = v;
   }
   __syncthreads();
-  const int c0 = 128 * (block % p.cb), slice = block / p.cb;
+  const int c0 = 128 * (block % p.cb), slice = (block / p.cb) % p.slices;
+  const int m0 = 16 * MT * (block / (p.cb * p.slices));
   const int s0 = slice * p.steps_per, s1 = min(p.steps, s0 + p.steps_per);
   const int64_t nk = (int64_t)p.N * p.K;
   const rsrc_t rw = make_rsrc(p.packed, (uint32_t)(nk >> 1));
@@ -313,11 +315,11 @@ __device__ __forceinline__ void dx_body(const DxSkinny& p, const Codebook& cb, i
 
   DxRegs<MT> R;
   if (s0 + wave < s1)
-    dx_load<MT>(R, rw, rq, rd, ry, 32 * (s0 + wave), c0, p.M, p.N, p.K, lane);
+    dx_load<MT>(R, rw, rq, rd, ry, 32 * (s0 + wave), c0, m0, p.M, p.N, p.K, lane);
   for (int s = s0 + wave; s < s1; s += AD_W) {
     const DxRegs<MT> X = R;
     if (s + AD_W < s1)
-      dx_load<MT>(R, rw, rq, rd, ry, 32 * (s + AD_W), c0, p.M, p.N, p.K, lane);
+      dx_load<MT>(R, rw, rq, rd, ry, 32 * (s + AD_W), c0, m0, p.M, p.N, p.K, lane);
     // c' of the lane's eight rows, of the block its columns are in
     const float cp = (float)X.q * __uint_as_float(X.d);
     const int from = 8 * (lane >> 4) + 32 * ((lane >> 3) & 1);
@@ -373,8 +375,9 @@ __device__ __forceinline__ void dx_body(const DxSkinny& p, const Codebook& cb, i
   }
   if (wave == 0) put(red);
   __syncthreads();
-  float* out = p.part + (int64_t)slice * p.M * p.K;
-  for (int i = tid; i < 32 * p.M; i += 64 * AD_W) {     // four columns each
+  float* out = p.part + ((int64_t)slice * p.M + m0) * p.K;
+  const int n = 32 * min(16 * MT, p.M - m0);
+  for (int i = tid; i < n; i += 64 * AD_W) {            // four columns each
     const int m = i >> 5, c = 4 * (i & 31);
     if (c0 + c < p.K)
       *reinterpret_cast<f32x4*>(out + (int64_t)m * p.K + c0 + c) =
@@ -721,16 +724,17 @@ void launch_adapter_rows(hipStream_t st, const RowsJob& p) {
 void launch_adapter_mid(hipStream_t st, AdapterMid p) {
   const auto blocks = [](int64_t threads) { return (int)cdiv(threads, 64 * AD_W); };
   for (AdapterSplit* q : {&p.g, &p.t}) q->total = cdiv(q->M, 32) * q->jt * 512;
-  p.end[0] = p.dx.cb * p.dx.slices;
+  const int mt = p.dx.M <= 16 ? 1 : (p.dx.M <= 32 ? 2 : 4);
+  p.end[0] = p.dx.cb * p.dx.slices * (int)cdiv(p.dx.M, 16 * mt);
   p.end[1] = p.end[0] + blocks(std::max<int64_t>(p.g.total, p.g.zero_words));
   p.end[2] = p.end[1] + blocks(p.t.total);
   const dim3 grid((unsigned)(p.end[2] + blocks((int64_t)p.a.chunks * p.a.n))), wg(64 * AD_W);
   const Codebook cb = codebook();
   if (p.end[0] == 0)
     QN_LAUNCH("k_adapter_mid", k_adapter_mid<0>, grid, wg, st, p, cb);
-  else if (p.dx.M <= 16)
+  else if (mt == 1)
     QN_LAUNCH("k_adapter_mid", k_adapter_mid<1>, grid, wg, st, p, cb);
-  else if (p.dx.M <= 32)
+  else if (mt == 2)
     QN_LAUNCH("k_adapter_mid", k_adapter_mid<2>, grid, wg, st, p, cb);
   else
     QN_LAUNCH("k_adapter_mid", k_adapter_mid<4>, grid, wg, st, p, cb);

@@ -283,7 +283,7 @@ int linear_bwd_act8(const uint16_t* dy, const qn_act8* x8, int64_t M,
   hipStream_t st = (hipStream_t)stream;
 
   // few tokens: dX by its own kernels, from A as it is
-  const bool gemm = dx != nullptr && M > DX_SKINNY_M;
+  const bool gemm = dx != nullptr && !dx_skinny(M, N, K);
   const bool skinny = dx != nullptr && !gemm;
   // G = dY B: partial sums over slices of dY's columns
   const RowsPlan Pg = rows_plan(M, N, jt);
@@ -303,7 +303,7 @@ int linear_bwd_act8(const uint16_t* dy, const qn_act8* x8, int64_t M,
                        (int64_t)(G_SPLIT_HDR / 4) + 2 * sp.rem, 0};
   if (gemm) mid.a = AdapterTranspose{A, Atp, (int)r, Ki, L.rpad / 8};
   if (skinny) {
-    const DxPlan Px = dx_plan(N, K);
+    const DxPlan Px = dx_plan(M, N, K);
     mid.dx = DxSkinny{dy, w->packed, w->qabs, w->gscale, Mi, Ni, Ki, Px.cb, Px.slices,
                       Px.steps, Px.steps_per, ws_at<float>(ws, L.px), Gf, L.rpad, A,
                       (int)r, dx, (int)(dx_dtype == QN_BF16)};

@@ -237,11 +237,16 @@ RowsPlan rows_plan(int64_t M, int64_t N, int jt) {
   return P;
 }
 
-DxPlan dx_plan(int64_t N, int64_t K) {
+bool dx_skinny(int64_t M, int64_t N, int64_t K) {
+  const int64_t tiles = cdiv(M, 128) * cdiv(K, 128);
+  return M <= DX_SKINNY_M || tiles <= 32 || (tiles <= 64 && N >= 4096);
+}
+
+DxPlan dx_plan(int64_t M, int64_t N, int64_t K) {
   DxPlan P;
   P.cb = (int)cdiv(K, 128);
   P.steps = (int)cdiv(N, 32);
-  const int64_t want = std::min(cdiv(G_CUS, P.cb), cdiv(P.steps, 8));
+  const int64_t want = std::max<int64_t>(1, std::min(cdiv(G_CUS, P.cb * cdiv(M, 64)), cdiv(P.steps, 8)));
   P.steps_per = (int)cdiv(P.steps, want);
   P.slices = (int)cdiv(P.steps, P.steps_per);
   return P;
@@ -262,7 +267,7 @@ Act8BwdWorkspace act8_bwd_workspace_layout(int64_t M, int64_t N, int64_t K,
     return at;
   };
   L.split = take(gemm_split_bytes(gemm_split_plan(M, K, N, false)));
-  L.atp = take(M > DX_SKINNY_M ? size_t(K) * L.rpad * 2 : 0);
+  L.atp = take(dx_skinny(M, N, K) ? 0 : size_t(K) * L.rpad * 2);
   L.gh = take(size_t(M) * L.rpad * 2);
   L.gl = take(size_t(M) * L.rpad * 2);
   L.prow = take(size_t(Pg.slices) * M * L.rpad * 4);
@@ -270,7 +275,7 @@ Act8BwdWorkspace act8_bwd_workspace_layout(int64_t M, int64_t N, int64_t K,
   L.ug = take(frag);
   L.pb = take(Pb.slices > 1 ? size_t(Pb.slices) * N * r * 4 : 0);
   L.pa = take(Pa.slices > 1 ? size_t(Pa.slices) * K * r * 4 : 0);
-  L.px = take(M <= DX_SKINNY_M ? size_t(dx_plan(N, K).slices) * M * K * 4 : 0);
+  L.px = take(dx_skinny(M, N, K) ? size_t(dx_plan(M, N, K).slices) * M * K * 4 : 0);
   L.total = off;
   return L;
 }

@@ -235,25 +235,33 @@ struct RowsPlan {
 };
 RowsPlan rows_plan(int64_t M, int64_t N, int jt);
 
-// dX for few tokens: blocks of 128 columns, slices of the
-// weight's rows (steps of 32), about one workgroup per CU.
+// dX of small outputs without the GEMM: blocks of 128 columns and 64 tokens,
+// slices of the weight's rows (steps of 32), about one workgroup per CU.  The
+// GEMM's time for few tiles is that of one tile's reduction over N, so this
+// one wins for up to 32 of its 128 x 128 tiles (whole backward, r = 16, this
+// and the GEMM: 128 x 4096 x 4096 tokens x N x K 35.7 and 46.2 us; 128 x 1024
+// x 1024 25.6 and 29.6 us; 4096 x 4096 x 128 48.2 and 59.8 us) and, where N
+// is long, 64 (2048 x 8192 x 512 72.2 and 82.1 us, 256 x 4096 x 4096 45.7 and
+// 48.3 us, but 256 x 1024 x 4096 35.9 and 31.1 us); at 128 tiles it loses
+// (512 x 4096 x 4096 68.8 and 56.0 us).
 constexpr int64_t DX_SKINNY_M = 64;
+bool dx_skinny(int64_t M, int64_t N, int64_t K);
 struct DxPlan {
   int cb, slices, steps, steps_per;
 };
-DxPlan dx_plan(int64_t N, int64_t K);
+DxPlan dx_plan(int64_t M, int64_t N, int64_t K);
 
 struct Act8BwdWorkspace {
   size_t split;       // as BwdWorkspace (offset 0)
   size_t atp;         // bf16 [K, rpad]  A transposed, zero-padded (GEMM)
   size_t gh, gl;      // bf16 [M, rpad]  two terms of s*G for the dX GEMM, or
-                      // (M <= DX_SKINNY_M, at gh) fp32 s*G
+                      // (dx_skinny, at gh) fp32 s*G
   size_t prow;        // fp32 [slices, M, rpad] partial G
   size_t ut, ug;      // bf16 [ceil(M / 32), jt, 3, 64, 8]  s*T, s*G as three
                       // terms in operand order
   size_t pb, pa;      // fp32 [slices, N r], [slices, K r] partial dB, dA
                       // (with one slice the gradients are written directly)
-  size_t px;          // fp32 [slices, M, K] partial dX (M <= DX_SKINNY_M)
+  size_t px;          // fp32 [slices, M, K] partial dX (dx_skinny)
   size_t total;
   int32_t rpad;
 };

@@ -177,6 +177,9 @@ def _check_bwd(m, n, k, r, alpha, p=0.0, seed=0, dx_dtype=capi.QN_F32, need_dx=T
     # ranks in two parts, and row slices of each width of workgroup
     (200, 136, 192, 160, 160.0), (1500, 72, 64, 200, 200.0), (2100, 64, 64, 64, 64.0),
     (2100, 136, 64, 16, 16.0), (2100, 64, 128, 24, 24.0),
+    # several blocks of 64 tokens; the GEMM with 128- and with 256-wide tiles
+    (100, 4104, 192, 8, 8.0), (1003, 64, 1024, 8, 16.0), (257, 1024, 2112, 16, 32.0),
+    (2050, 264, 6208, 16, 16.0),
 ])
 def test_backward_from_a_checkpoint(m, n, k, r, alpha):
     _check_bwd(m, n, k, r, alpha)
@@ -185,7 +188,7 @@ def test_backward_from_a_checkpoint(m, n, k, r, alpha):
 @pytest.mark.parametrize("m,n,k,r,p", [
     (1, 8, 64, 1, 0.5), (37, 200, 192, 5, 0.1), (130, 136, 320, 64, 0.3),
     (64, 128, 256, 256, 0.1), (258, 264, 576, 16, 0.05), (33, 1032, 192, 12, 0.2),
-    (700, 72, 64, 160, 0.1), (1100, 64, 64, 24, 0.3),
+    (700, 72, 64, 160, 0.1), (1100, 64, 64, 24, 0.3), (257, 136, 2112, 16, 0.1),
 ])
 def test_backward_with_dropout(m, n, k, r, p):
     _check_bwd(m, n, k, r, 2.0 * r, p=p, seed=(m * 1000003 + k) | (1 << 40))
