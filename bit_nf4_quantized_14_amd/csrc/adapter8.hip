@@ -617,52 +617,62 @@ __device__ __forceinline__ void cols_body(const ColsJob& p, int block, float* re
   }
 }
 
-// dX for few tokens, four of them and one column a thread: the slices'
+// dX of small outputs, four columns of one token a thread: the slices'
 // partial sums in order, then the adapter term s G A (masked under dropout).
 __device__ __forceinline__ void dx_finish_thread(const DxSkinny& p, int64_t idx, bool drop,
                                                  const DropArgs& dp) {
-  const int quads = (p.M + 3) / 4;
-  if (idx >= (int64_t)quads * p.K) return;
-  const int quad = (int)(idx / p.K), k = (int)(idx - (int64_t)quad * p.K), m0 = 4 * quad;
-  int row[4];                          // tokens past M read the last one
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  const int k4 = p.K / 4;
+  if (idx >= (int64_t)p.M * k4) return;
+  const int m = (int)(idx / k4), k = 4 * (int)(idx - (int64_t)m * k4);
+  f32x4 v = {0.f, 0.f, 0.f, 0.f}, a = {0.f, 0.f, 0.f, 0.f};
+  const float* src = p.part + (int64_t)m * p.K + k;
+  for (int s0 = 0; s0 < p.slices; s0 += 4) {
+    f32x4 x[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) row[i] = min(m0 + i, p.M - 1);
-  float v[4] = {0.f, 0.f, 0.f, 0.f}, a[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int s0 = 0; s0 < p.slices; s0 += 4) {         // 16 loads in flight
-    float x[4][4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        x[u][i] = s0 + u < p.slices ? p.part[((int64_t)(s0 + u) * p.M + row[i]) * p.K + k] : 0.0f;
+    for (int u = 0; u < 4; ++u)       // past the last slice: read it again
+      x[u] = *reinterpret_cast<const f32x4*>(
+          src + (int64_t)min(s0 + u, p.slices - 1) * p.M * p.K);
 #pragma unroll
     for (int u = 0; u < 4; ++u)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += x[u][i];
+      for (int i = 0; i < 4; ++i) v[i] += s0 + u < p.slices ? x[u][i] : 0.0f;
   }
-  // G's rows are 16 jt wide and zero past r, so whole groups of 4 are safe
-  for (int j0 = 0; j0 < p.r; j0 += 4) {
-    float w[4];
-    f32x4 g[4];
+  // G's rows are 16 jt wide and zero past r, so whole groups of 8 are safe
+  const float* g = p.G + (int64_t)m * p.ldg;
+  for (int j0 = 0; j0 < p.r; j0 += 8) {
+    u32x2 w[8];
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      w[u] = j0 + u < p.r ? bf16_to_f32(p.A[(int64_t)(j0 + u) * p.K + k]) : 0.0f;
+    for (int u = 0; u < 8; ++u)
+      w[u] = *reinterpret_cast<const u32x2*>(p.A + (int64_t)min(j0 + u, p.r - 1) * p.K + k);
+    const f32x4 g0 = *reinterpret_cast<const f32x4*>(g + j0);
+    const f32x4 g1 = *reinterpret_cast<const f32x4*>(g + j0 + 4);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      g[i] = *reinterpret_cast<const f32x4*>(p.G + (int64_t)row[i] * p.ldg + j0);
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) a[i] = fmaf(g[i][u], w[u], a[i]);
+    for (int u = 0; u < 8; ++u) {
+      const float c = u < 4 ? g0[u % 4] : g1[u % 4];
+      if (j0 + u < p.r) {
+        a[0] = fmaf(c, __uint_as_float(w[u].x << 16), a[0]);
+        a[1] = fmaf(c, __uint_as_float(w[u].x & 0xFFFF0000u), a[1]);
+        a[2] = fmaf(c, __uint_as_float(w[u].y << 16), a[2]);
+        a[3] = fmaf(c, __uint_as_float(w[u].y & 0xFFFF0000u), a[3]);
+      }
+    }
   }
   if (drop) {
-    const u32x4 w = philox4x32_10((uint32_t)k, (uint32_t)quad, dp.key0, dp.key1);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = w[i] >= dp.thresh ? a[i] * dp.scale : 0.0f;
+    for (int i = 0; i < 4; ++i) {
+      const u32x4 w = philox4x32_10((uint32_t)(k + i), (uint32_t)m >> 2, dp.key0, dp.key1);
+      a[i] = pick4(w, m & 3) >= dp.thresh ? a[i] * dp.scale : 0.0f;
+    }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (m0 + i < p.M) store_out(p.dx, p.dx_bf16, (int64_t)(m0 + i) * p.K + k, v[i] + a[i]);
+  for (int i = 0; i < 4; ++i) a[i] += v[i];
+  const int64_t at = (int64_t)m * p.K + k;
+  if (p.dx_bf16)
+    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p.dx) + at) =
+        u32x2{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3])};
+  else
+    *reinterpret_cast<f32x4*>(static_cast<float*>(p.dx) + at) = a;
 }
 
 template <int JT, bool DROP>
@@ -746,7 +756,7 @@ void launch_adapter_cols(hipStream_t st, const ColsJob& B, const ColsJob& A, con
   // ranks above 128: two workgroups of 128 each
   const int rank = std::min(r, 16 * COLS_JT);
   const DxSkinny x = X != nullptr ? *X : DxSkinny{};
-  const int64_t dx_threads = cdiv(x.M, 4) * (int64_t)x.K;
+  const int64_t dx_threads = (int64_t)x.M * (x.K / 4);
   const int threads = 64 * cols_waves(rank_tiles(rank));
   const dim3 grid((unsigned)(nA + cdiv(dx_threads, threads))), wg(threads);
   const DropArgs dp = drop != nullptr ? *drop : DropArgs{};

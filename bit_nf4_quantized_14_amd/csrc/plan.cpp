@@ -246,7 +246,8 @@ DxPlan dx_plan(int64_t M, int64_t N, int64_t K) {
   DxPlan P;
   P.cb = (int)cdiv(K, 128);
   P.steps = (int)cdiv(N, 32);
-  const int64_t want = std::max<int64_t>(1, std::min(cdiv(G_CUS, P.cb * cdiv(M, 64)), cdiv(P.steps, 8)));
+  const int64_t want = std::max<int64_t>(
+      1, std::min(DX_WGS / (P.cb * cdiv(M, 64)), cdiv(P.steps, 8)));
   P.steps_per = (int)cdiv(P.steps, want);
   P.slices = (int)cdiv(P.steps, P.steps_per);
   return P;

@@ -236,7 +236,9 @@ struct RowsPlan {
 RowsPlan rows_plan(int64_t M, int64_t N, int jt);
 
 // dX of small outputs without the GEMM: blocks of 128 columns and 64 tokens,
-// slices of the weight's rows (steps of 32), about one workgroup per CU.  The
+// slices of the weight's rows (steps of 32), at most DX_WGS workgroups (one per
+// CU: with 64 tokens no second one fits) where one slice does not give more.
+// The
 // GEMM's time for few tiles is that of one tile's reduction over N, so this
 // one wins for up to 32 of its 128 x 128 tiles (whole backward, r = 16, this
 // and the GEMM: 128 x 4096 x 4096 tokens x N x K 35.7 and 46.2 us; 128 x 1024
@@ -246,6 +248,7 @@ RowsPlan rows_plan(int64_t M, int64_t N, int jt);
 // (512 x 4096 x 4096 68.8 and 56.0 us).
 constexpr int64_t DX_SKINNY_M = 64;
 bool dx_skinny(int64_t M, int64_t N, int64_t K);
+constexpr int64_t DX_WGS = G_CUS;
 struct DxPlan {
   int cb, slices, steps, steps_per;
 };
