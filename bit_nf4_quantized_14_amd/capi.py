@@ -859,8 +859,9 @@ def qlora_linear_bwd_act8(dy, x8: Act8Tensor, w: NF4Tensor, A, B, r: int,
         else:
             pw, nw = _workspace(fn, ws, index)
         _check(fn, lib().qlora_linear_bwd_act8(
-            pdy, xt, M, w.as_struct(), pA, pB, r, alpha, pt, pdx, code, gA.data_ptr(),
-            gB.data_ptr(), _Dropout(p, seed & 0xFFFFFFFFFFFFFFFF), pw, nw, st))
+            pdy, xt, M, w.as_struct(), pA, pB, int(r), float(alpha), pt, pdx, code,
+            gA.data_ptr(), gB.data_ptr(),
+            _Dropout(float(p), int(seed) & 0xFFFFFFFFFFFFFFFF), pw, nw, st))
         return gx, gA, gB
     return _run_on(index, stream, body)
 
@@ -980,7 +981,7 @@ def qn_pref_loss_fwd(logits, labels, offsets, ref_logp, beta: float,
             fn, b, logits, {"loss": (g.loss, pairs), "logp": (g.logp, nseq),
                             "dlogp": (g.dlogp, nseq), "lse": (g.lse, rows)}, ws, index)
         _check(fn, lib().qn_pref_loss_fwd(
-            b, pr, _PrefHP(beta, label_smoothing), p["lse"], p["logp"], p["loss"], p["dlogp"],
+            b, pr, _PrefHP(float(beta), float(label_smoothing)), p["lse"], p["logp"], p["loss"], p["dlogp"],
             _status_ptr(fn, status, index), pw, nw, st))
         return PrefLoss(**o) if out is None else out
     return _run_on(index, stream, body)

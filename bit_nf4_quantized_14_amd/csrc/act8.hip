@@ -6,7 +6,14 @@
 //   restored: fp32(code * scale), or that rounded to bf16
 //
 // Both directions are one pass over memory and bound by it: 2 (or 4) + 1 +
-// 1/16 bytes per element in total.
+// 1/16 bytes per element in total.  Eight lanes share a block, so its maximum
+// takes three cross-lane moves and no LDS, and a wave reads 1 KB and writes
+// 512 B of codes without gaps.  Measured (MI355X; a 256 MB copy moves 5.4
+// TB/s): 4096 x 4096 bf16 encode 10.8 us (4.8 TB/s; its arithmetic, 14
+// operations per element with the two divisions of each lane, runs beside the
+// loads for most of that), decode 9.4 us (5.5 TB/s); 2048 x 28672 fp32 encode
+// 54.8 us (5.4 TB/s).  Two and four blocks per eight lanes, loaded together,
+// took 12.2 and 17.1 us for the first.
 #include "qn_host.h"
 
 namespace {

@@ -90,6 +90,7 @@ size_t qlora_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t r,
 size_t qlora_bwd_act8_workspace_bytes(int64_t M, int64_t N, int64_t K,
                                       int32_t r) {
   if (M <= 0 || N <= 0 || K <= 0 || r < 1 || r > QN_MAX_RANK) return 0;
+  if (!qn::act8_bwd_fits(M, r)) return 0;
   return qn::act8_bwd_workspace_layout(M, N, K, r).total;
 }
 
@@ -248,7 +249,7 @@ int linear_bwd(const uint16_t* dy, const uint16_t* x, int64_t M,
 
 // The backward with X as an 8-bit checkpoint; dx may be null.  Launches:
 // G, its split (and all that needs no G), the dX GEMM, both column sums (and
-// dX for few tokens), their slices (where there are any).
+// dX of small outputs), their slices (where there are any).
 int linear_bwd_act8(const uint16_t* dy, const qn_act8* x8, int64_t M,
                     const nf4_tensor* w, const uint16_t* A, const uint16_t* B,
                     int32_t r, float alpha, const float* t_saved, void* dx,
@@ -258,7 +259,7 @@ int linear_bwd_act8(const uint16_t* dy, const qn_act8* x8, int64_t M,
   if (dy == nullptr || x8 == nullptr || A == nullptr || B == nullptr ||
       t_saved == nullptr || dA == nullptr || dB == nullptr)
     return QN_EINVAL;
-  if (!valid_linear(M, w, r)) return QN_EINVAL;
+  if (!valid_linear(M, w, r) || !act8_bwd_fits(M, r)) return QN_EINVAL;
   if (dx != nullptr && dx_dtype != QN_F32 && dx_dtype != QN_BF16) return QN_EINVAL;
   if (!aligned16(dy) || !aligned16(A) || !aligned16(dx)) return QN_EINVAL;
   if (!valid_act8(x8) || x8->rows != M || x8->cols != w->cols ||
@@ -282,7 +283,7 @@ int linear_bwd_act8(const uint16_t* dy, const qn_act8* x8, int64_t M,
   const int Mi = (int)M, Ni = (int)N, Ki = (int)K, jt = rank_tiles(r);
   hipStream_t st = (hipStream_t)stream;
 
-  // few tokens: dX by its own kernels, from A as it is
+  // small outputs: dX by its own kernels, from A as it is
   const bool gemm = dx != nullptr && !dx_skinny(M, N, K);
   const bool skinny = dx != nullptr && !gemm;
   // G = dY B: partial sums over slices of dY's columns
@@ -290,7 +291,7 @@ int linear_bwd_act8(const uint16_t* dy, const qn_act8* x8, int64_t M,
   launch_adapter_rows(st, RowsJob{dy, B, Mi, Ni, (int)r, Pg.mt, Pg.slices, Pg.steps,
                                   Pg.steps_per, prow});
   // s T and s G in three terms (s G also as dX needs it), A^T padded to
-  // [K][rpad] for the GEMM, the slices of dX for few tokens; the status word
+  // [K][rpad] for the GEMM, the slices of a small dX; the status word
   // and the counters of the GEMM's split tiles cleared
   const GemmSplit sp = gemm_split_plan(M, K, N, use_drop);
   float* Gf = reinterpret_cast<float*>(Gh);

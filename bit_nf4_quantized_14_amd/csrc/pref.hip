@@ -10,6 +10,13 @@
 // writes the gradient once; both are bound by memory.  The loss of a pair
 // needs every row of both of its sequences before the first gradient, so
 // the two passes cannot be one.
+//
+// Measured (MI355X; a 256 MB copy moves 5.4 TB/s), 8 pairs, 4109 tokens of
+// which 2745 count, 32000 words, bf16: maximum and sum 36 us (176 MB, 4.8
+// TB/s), sequences and loss 4.6 us, gradient 75 us (176 MB read, 263 MB
+// written, 5.8 TB/s); fp32 logits of 128256 words, 2508 tokens: 153 us (5.6
+// TB/s) and, with a bf16 gradient, 310 us (4.9 TB/s).  Below some MB the
+// three launches' own time is what is left: 3.5 + 3.5 us for 24 tokens.
 #include <cmath>
 
 #include "qn_host.h"
@@ -20,7 +27,9 @@ using namespace qn;
 
 constexpr int SQ_THREADS = 256;                // 4 waves
 constexpr int SQ_STEP = SQ_THREADS * 8;        // elements a workgroup takes at once
-constexpr int SQ_GROUPS = 4;                   // 16-byte loads of a thread in flight
+// 16-byte loads of a thread in flight: with 2 the fp32 case above took 5% and
+// the bf16 case 1% longer, with 8 nothing less
+constexpr int SQ_GROUPS = 4;
 constexpr float SQ_LOG2E = 1.4426950408889634f;
 constexpr float SQ_NEG_INF = -__builtin_inff();
 
@@ -310,11 +319,12 @@ struct SeqBwdArgs {
 };
 
 // Non-temporal (NT) stores leave the caches to others.  A gradient of 64 MB
-// and more does not stay in them until it is read: 8 pairs of 256 tokens and
-// 32000 words (250 MB) took 167 us forward and backward with plain stores,
-// 137 us with these, and with a pass that reads the gradient behind it 253
-// and 236 us; 125 MB: 130 and 124 us; 31 MB: 93 and 96 us, so smaller ones
-// are stored plainly.
+// and more does not stay in them until it is read.  Forward and backward with
+// plain and with these stores, 32000 words, alone and with a pass behind them
+// that reads the gradient: 250 MB 167 and 137 us, 253 and 236 us; 125 MB 89
+// and 74 us, 130 and 124 us; 500 MB 320 and 306 us, 486 and 492 us.  At 31 MB
+// they gained nothing alone and lost 2 us with the pass behind, so smaller
+// gradients are stored plainly.
 constexpr int64_t SQ_NT_BYTES = 64 << 20;
 
 template <bool NT, typename V>
@@ -351,20 +361,31 @@ __device__ __forceinline__ void sq_store(char* base, int at, int cols, const flo
     }
 }
 
-// Gradient of one chunk of one row.  Its sequence is the number of
-// offsets[1..nseq] that are not behind the row, counted by every wave for
-// itself (64 offsets at a time).
+// The number of offsets[1 .. nseq] that are not behind the row, found by a
+// wave: its lanes look at the last offset of 64 equal parts and go on with the
+// part where the row lies (two rounds for 4096 sequences).  Between 0 and nseq
+// whatever the offsets hold.
+__device__ __forceinline__ int sq_sequence_of(const int64_t* __restrict__ offsets, int nseq,
+                                              int row, int lane) {
+  int lo = 0, n = nseq;
+  while (n > 64) {
+    const int step = (n + 63) / 64;
+    const int i = lo + min((lane + 1) * step, n) - 1;
+    const int skip = min(__popcll(__ballot(offsets[1 + i] <= row)) * step, n);
+    lo += skip;
+    n = min(step, n - skip);
+  }
+  return lo + __popcll(__ballot(lane < n && offsets[1 + lo + min(lane, max(n - 1, 0))] <= row));
+}
+
+// Gradient of one chunk of one row.
 template <bool FIN, bool FOUT, bool NT>
 __global__ __launch_bounds__(SQ_THREADS) void k_seq_bwd(SeqArgs a, SeqBwdArgs g) {
   const int row = (int)(blockIdx.x / (unsigned)a.nchunk);
   const int ch = (int)(blockIdx.x - (unsigned)row * (unsigned)a.nchunk);
   const int lane = threadIdx.x & 63;
   const int64_t label = a.labels[row];
-  int seq = 0;
-  for (int base = 0; base < a.nseq; base += 64) {
-    const bool before = base + lane < a.nseq && a.offsets[1 + base + lane] <= row;
-    seq += __popcll(__ballot(before));
-  }
+  const int seq = sq_sequence_of(a.offsets, a.nseq, row, lane);
   const bool counted = label >= 0 && label < a.vocab && row >= a.offsets[0] && seq < a.nseq;
   char* out = g.out + (int64_t)row * g.ld_out * (FOUT ? 4 : 2);
   const int begin = ch * a.chunk, end = min(g.cols, begin + a.chunk);
@@ -415,8 +436,9 @@ bool valid_batch(const qn_seq_batch* b) {
   return b->rows == 0 || (sized_ptr(b->logits, b->dtype) && b->labels != nullptr);
 }
 
-// Workgroups per row and the columns of each: one where the rows fill the
-// GPU, else about SQ_FILL workgroups in all, of at least one step each.
+// Workgroups per row and the columns of each: one where the rows fill the GPU
+// (8 workgroups a CU), else about SQ_FILL workgroups in all, of at least one
+// step each, so that few rows are read by the whole GPU too.
 constexpr int64_t SQ_FILL = 8 * G_CUS;
 void split_rows(int64_t rows, int64_t cols, int32_t* chunk, int32_t* nchunk) {
   const int64_t steps = cdiv(cols, SQ_STEP);

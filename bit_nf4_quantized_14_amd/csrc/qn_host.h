@@ -135,7 +135,7 @@ void launch_finish(hipStream_t st, FinishArgs& a);
 bool valid_act8(const qn_act8* t);
 
 // ---- adapter8.hip: the backward from an 8-bit checkpoint.
-struct DxSkinny {                     // dX of few tokens; cb 0: none
+struct DxSkinny {                     // dX of small outputs; cb 0: none
   const uint16_t* dy;
   const uint8_t *packed, *qabs;
   const float* gscale;
@@ -196,7 +196,7 @@ struct AdapterMid {
 };
 void launch_adapter_rows(hipStream_t st, const RowsJob& p);
 void launch_adapter_mid(hipStream_t st, AdapterMid p);
-// X: few tokens, the slices of dX to be added up in the same launch (or null)
+// X: slices of dX to be added up in the same launch (or null)
 void launch_adapter_cols(hipStream_t st, const ColsJob& B, const ColsJob& A, const DxSkinny* X,
                          int r, const DropArgs* drop);
 void launch_adapter_reduce(hipStream_t st, const ColsReduce& p0, const ColsReduce& p1);

@@ -254,6 +254,12 @@ struct DxPlan {
 };
 DxPlan dx_plan(int64_t M, int64_t N, int64_t K);
 
+// The splits of s T and s G take a thread per padded element, and a launch
+// holds less than 2^32 threads.
+inline bool act8_bwd_fits(int64_t M, int r) {
+  return M < (1LL << 30) / (16 * rank_tiles(r));
+}
+
 struct Act8BwdWorkspace {
   size_t split;       // as BwdWorkspace (offset 0)
   size_t atp;         // bf16 [K, rpad]  A transposed, zero-padded (GEMM)

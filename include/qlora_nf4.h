@@ -508,6 +508,7 @@ int qn_act8_decode(const qn_act8* x8, void* y, int32_t y_dtype, void* stream);
  * drop : NULL or p == 0 for no dropout.
  * ws   : ws_bytes >= qlora_bwd_act8_workspace_bytes(M, N, K, r), 16-byte
  *        aligned, with its status word as in qlora_linear_bwd.
+ * M times r (rounded up to 16, 32, 64, 128 or 256) must be below 2^30.
  * Other arguments, shape rules and errors as qlora_linear_bwd.
  */
 size_t qlora_bwd_act8_workspace_bytes(int64_t M, int64_t N, int64_t K,

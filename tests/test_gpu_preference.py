@@ -102,6 +102,7 @@ CASES = [
     ([1, 1], 128256, 0, 0, 0),
     ([1100, 600, 500, 300], 300, 4, 5, 20),     # rows not split
     ([2] * 140, 64, 0, 1, 1),                   # more sequences than lanes
+    ([0, 1, 0, 0, 2, 0, 1, 0] * 600, 9, 0, 2, 3),   # and than their square
 ]
 
 
@@ -342,6 +343,17 @@ def test_other_streams_and_two_calls_at_once():
     for g, dl in zip(got, dls):
         assert torch.equal(g.loss, f.loss) and torch.equal(g.logp, f.logp)
         assert torch.equal(dl, want)
+
+
+def test_default_stream_by_handle_and_by_object():
+    prob = _problem([5, 4], 100, torch.float32)
+    logits, lab, off = prob[:3]
+    want = capi.qn_seq_logprob(logits, lab, off)
+    torch.cuda.synchronize()
+    for s in (0, torch.cuda.default_stream(), torch.cuda.Stream().cuda_stream):
+        got = capi.qn_seq_logprob(logits, lab, off, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 def test_graph_replays_follow_new_logits():
