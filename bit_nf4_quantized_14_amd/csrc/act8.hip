@@ -14,7 +14,7 @@
 // loads for most of that), decode 9.4 us (5.5 TB/s); 2048 x 28672 fp32 encode
 // 54.8 us (5.4 TB/s).  Two and four blocks per eight lanes, loaded together,
 // took 12.2 and 17.1 us for the first.
-#include "qn_host.h"
+#include "act8_host.h"
 
 namespace {
 

@@ -9,7 +9,7 @@
 // dX), [the dX GEMM], k_adapter_cols (dB, dA, the rest of dX), and
 // k_adapter_reduce where the column sums were sliced.  Nothing is added by
 // atomics: every sum has one order.
-#include "qn_host.h"
+#include "act8_host.h"
 
 namespace {
 

@@ -48,7 +48,8 @@ KERNEL_SOURCES = (("k_gemm", "gemm.hip"), ("k_fwd_gemm", "gemm.hip"),
                   ("k_bwd_dx_gemm", "gemm.hip"), ("k_rank", "rank.hip"),
                   ("k_dequant", "codec.hip"), ("k_quantize", "codec.hip"),
                   ("k_skinny", "skinny.hip"), ("k_merge", "merge.hip"),
-                  ("k_adamw8", "adamw.hip"))
+                  ("k_adamw8", "adamw.hip"), ("k_act8", "act8.hip"),
+                  ("k_adapter", "adapter8.hip"), ("k_seq", "pref.hip"))
 
 COPY_BYTES = 256 << 20   # bench.py --calibrate-copy: one 256 MiB copy
 

@@ -8,7 +8,8 @@
 #include <cstdlib>
 #include <random>
 
-#include "qn_internal.h"
+#include "act8_plan.h"
+#include "plan.cpp"   // the layer's own plans, which these build on
 
 using namespace qn;
 
