@@ -27,6 +27,13 @@ using namespace qn;
 
 constexpr int SQ_THREADS = 256;                // 4 waves
 constexpr int SQ_STEP = SQ_THREADS * 8;        // elements a workgroup takes at once
+// Many short rows: a wave to a row (TEAM = 64 threads) instead of a workgroup,
+// whose barrier and last sums are most of its time there.  Forward and
+// backward, with a workgroup and with a wave to a row: 12000 rows of 500 bf16
+// words 36 and 24 us, of 2113 51 and 40 us, 8192 rows of 6000 60 and 56 us, of
+// 8000 71 and 73 us; fp32, 12000 rows of 2113 71 and 65 us, 8192 rows of 4000
+// 76 and 79 us.
+constexpr int64_t SQ_WAVE_BYTES = 12 << 10;
 // 16-byte loads of a thread in flight: with 2 the fp32 case above took 5% and
 // the bf16 case 1% longer, with 8 nothing less
 constexpr int SQ_GROUPS = 4;
@@ -132,38 +139,41 @@ __device__ __forceinline__ double sq_logit(const char* row, int64_t c) {
              : (double)bf16_to_f32(reinterpret_cast<const uint16_t*>(row)[c]);
 }
 
-// Maximum and sum of one chunk of one row.  Rows that are not counted are
+// Maximum and sum of one chunk of one row by TEAM threads.  Rows that are not counted are
 // not read.  Each thread keeps SQ_GROUPS 16-byte loads in flight; the last
 // round (one group at a time where at most half of the groups are left)
 // reads a group from the end of the chunk where it would pass it, and drops
 // what another thread has.
-template <bool F32>
+template <bool F32, int TEAM>
 __global__ __launch_bounds__(SQ_THREADS) void k_seq_rows(SeqArgs a, SeqPart* __restrict__ ws,
                                                          float* __restrict__ lse) {
-  constexpr int G = F32 ? SQ_GROUPS / 2 : SQ_GROUPS;
+  constexpr int G = F32 ? SQ_GROUPS / 2 : SQ_GROUPS, STEP = 8 * TEAM;
   __shared__ MaxSum red[SQ_THREADS / 64];
-  const int row = (int)(blockIdx.x / (unsigned)a.nchunk);
-  const int ch = (int)(blockIdx.x - (unsigned)row * (unsigned)a.nchunk);
+  const unsigned team = blockIdx.x * (SQ_THREADS / TEAM) + threadIdx.x / TEAM;
+  const int tid = threadIdx.x % TEAM;
+  const int row = (int)(team / (unsigned)a.nchunk);
+  const int ch = (int)(team - (unsigned)row * (unsigned)a.nchunk);
+  if (TEAM < SQ_THREADS && row >= a.rows) return;
   const int64_t label = a.labels[row];
   const bool counted = label >= 0 && label < a.vocab && row >= a.offsets[0] &&
                        row < a.offsets[a.nseq];
   if (!counted) {
-    if (ch == 0 && threadIdx.x == 0) lse[row] = 0.0f;
+    if (ch == 0 && tid == 0) lse[row] = 0.0f;
     return;
   }
   const char* p = a.logits + (int64_t)row * a.ld * (F32 ? 4 : 2);
   const int begin = ch * a.chunk, end = min(a.vocab, begin + a.chunk);
   MaxSum r{SQ_NEG_INF, 0.0f};
-  int c = begin + 8 * threadIdx.x;
+  int c = begin + 8 * tid;
   int at = begin;
-  for (; at + G * SQ_STEP <= end; at += G * SQ_STEP, c += G * SQ_STEP) {
+  for (; at + G * STEP <= end; at += G * STEP, c += G * STEP) {
     float v[8 * G];
 #pragma unroll
-    for (int g = 0; g < G; ++g) sq_load8<F32>(p, c + g * SQ_STEP, v + 8 * g);
+    for (int g = 0; g < G; ++g) sq_load8<F32>(p, c + g * STEP, v + 8 * g);
     sq_add(r, v);
   }
   if (end - begin >= 8) {
-    for (; at < end && end - at <= SQ_STEP * (G / 2); at += SQ_STEP, c += SQ_STEP) {
+    for (; at < end && end - at <= STEP * (G / 2); at += STEP, c += STEP) {
       float v[8];
       sq_load8<F32>(p, min(c, end - 8), v);
       const int skip = c - (end - 8);
@@ -175,10 +185,10 @@ __global__ __launch_bounds__(SQ_THREADS) void k_seq_rows(SeqArgs a, SeqPart* __r
       float v[8 * G];
 #pragma unroll
       for (int g = 0; g < G; ++g)
-        sq_load8<F32>(p, min(c + g * SQ_STEP, end - 8), v + 8 * g);
+        sq_load8<F32>(p, min(c + g * STEP, end - 8), v + 8 * g);
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        const int skip = c + g * SQ_STEP - (end - 8);   // of this group, if any
+        const int skip = c + g * STEP - (end - 8);   // of this group, if any
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[8 * g + i] = i >= skip ? v[8 * g + i] : SQ_NEG_INF;
       }
@@ -192,10 +202,13 @@ __global__ __launch_bounds__(SQ_THREADS) void k_seq_rows(SeqArgs a, SeqPart* __r
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1)
     r = sq_join(r, MaxSum{__shfl_xor(r.m, off), __shfl_xor(r.s, off)});
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = r;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < SQ_THREADS / 64; ++w) r = sq_join(r, red[w]);
+  if constexpr (TEAM == SQ_THREADS) {
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = r;
+    __syncthreads();
+    if (tid == 0)
+      for (int w = 1; w < SQ_THREADS / 64; ++w) r = sq_join(r, red[w]);
+  }
+  if (tid == 0) {
     if (a.nchunk > 1) {
       ws[(int64_t)row * a.nchunk + ch].part = r;
     } else {
@@ -378,12 +391,15 @@ __device__ __forceinline__ int sq_sequence_of(const int64_t* __restrict__ offset
   return lo + __popcll(__ballot(lane < n && offsets[1 + lo + min(lane, max(n - 1, 0))] <= row));
 }
 
-// Gradient of one chunk of one row.
-template <bool FIN, bool FOUT, bool NT>
+// Gradient of one chunk of one row by TEAM threads.
+template <bool FIN, bool FOUT, bool NT, int TEAM>
 __global__ __launch_bounds__(SQ_THREADS) void k_seq_bwd(SeqArgs a, SeqBwdArgs g) {
-  const int row = (int)(blockIdx.x / (unsigned)a.nchunk);
-  const int ch = (int)(blockIdx.x - (unsigned)row * (unsigned)a.nchunk);
-  const int lane = threadIdx.x & 63;
+  constexpr int STEP = 8 * TEAM;
+  const unsigned team = blockIdx.x * (SQ_THREADS / TEAM) + threadIdx.x / TEAM;
+  const int tid = threadIdx.x % TEAM, lane = threadIdx.x & 63;
+  const int row = (int)(team / (unsigned)a.nchunk);
+  const int ch = (int)(team - (unsigned)row * (unsigned)a.nchunk);
+  if (TEAM < SQ_THREADS && row >= a.rows) return;
   const int64_t label = a.labels[row];
   const int seq = sq_sequence_of(a.offsets, a.nseq, row, lane);
   const bool counted = label >= 0 && label < a.vocab && row >= a.offsets[0] && seq < a.nseq;
@@ -391,7 +407,7 @@ __global__ __launch_bounds__(SQ_THREADS) void k_seq_bwd(SeqArgs a, SeqBwdArgs g)
   const int begin = ch * a.chunk, end = min(g.cols, begin + a.chunk);
   if (!counted) {
     const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int c = begin + 8 * threadIdx.x; c < end; c += SQ_STEP)
+    for (int c = begin + 8 * tid; c < end; c += STEP)
       sq_store<FOUT, NT>(out, c, end, zero);
     return;
   }
@@ -401,7 +417,7 @@ __global__ __launch_bounds__(SQ_THREADS) void k_seq_bwd(SeqArgs a, SeqBwdArgs g)
   const float lse = g.lse[row];
   const char* p = a.logits + (int64_t)row * a.ld * (FIN ? 4 : 2);
   const int hit = (int)label;
-  for (int c = begin + 8 * threadIdx.x; c < end; c += SQ_STEP) {
+  for (int c = begin + 8 * tid; c < end; c += STEP) {
     float v[8];
     sq_load<FIN>(p, c, a.vocab, v);
 #pragma unroll
@@ -448,6 +464,14 @@ void split_rows(int64_t rows, int64_t cols, int32_t* chunk, int32_t* nchunk) {
   *nchunk = (int32_t)cdiv(steps, per);
 }
 
+// Whether a row goes to a wave (it is not split then).
+bool wave_rows(const qn_seq_batch* b, int64_t cols) {
+  return cols * (b->dtype == QN_F32 ? 4 : 2) <= SQ_WAVE_BYTES && b->rows >= SQ_FILL;
+}
+unsigned row_blocks(const SeqArgs& a, bool wave) {
+  return (unsigned)(wave ? cdiv(a.rows, SQ_THREADS / 64) : (int64_t)a.rows * a.nchunk);
+}
+
 SeqArgs seq_args(const qn_seq_batch* b, int64_t cols) {
   SeqArgs a;
   a.logits = static_cast<const char*>(b->logits);
@@ -472,11 +496,17 @@ int seq_forward(const qn_seq_batch* b, float* lse, float* logp, int32_t* status,
   hipStream_t st = (hipStream_t)stream;
   const bool f32 = b->dtype == QN_F32;
   if (b->rows > 0) {
-    const dim3 grid((unsigned)(b->rows * a.nchunk));
-    if (f32)
-      QN_LAUNCH("k_seq_rows", k_seq_rows<true>, grid, dim3(SQ_THREADS), st, a, part, lse);
-    else
-      QN_LAUNCH("k_seq_rows", k_seq_rows<false>, grid, dim3(SQ_THREADS), st, a, part, lse);
+    const bool wave = wave_rows(b, b->vocab);
+    const dim3 grid(row_blocks(a, wave)), wg(SQ_THREADS);
+#define SQ_ROWS(F32, TEAM) \
+  QN_LAUNCH("k_seq_rows", (k_seq_rows<F32, TEAM>), grid, wg, st, a, part, lse)
+    switch (2 * f32 + wave) {
+      case 0: SQ_ROWS(false, SQ_THREADS); break;
+      case 1: SQ_ROWS(false, 64); break;
+      case 2: SQ_ROWS(true, SQ_THREADS); break;
+      default: SQ_ROWS(true, 64); break;
+    }
+#undef SQ_ROWS
   }
   const dim3 grid((unsigned)(pa.pairs > 0 ? pa.pairs : b->nseq));
   if (f32)
@@ -510,11 +540,17 @@ int seq_backward(const qn_seq_batch* b, const float* lse, const float* dlogp,
   g.pairs = pairs;
   g.mean = pairs > 0 ? (float)(1.0 / pairs) : 0.0f;
   hipStream_t st = (hipStream_t)stream;
-  const dim3 grid((unsigned)(b->rows * a.nchunk)), wg(SQ_THREADS);
+  const bool wave = wave_rows(b, cols);
+  const dim3 grid(row_blocks(a, wave)), wg(SQ_THREADS);
   const bool fi = b->dtype == QN_F32, fo = dl_dtype == QN_F32;
   const bool nt = b->rows * cols * (fo ? 4 : 2) >= SQ_NT_BYTES;
-#define SQ_BWD(FI, FO, NT) \
-  QN_LAUNCH("k_seq_bwd", (k_seq_bwd<FI, FO, NT>), grid, wg, st, a, g)
+#define SQ_BWD(FI, FO, NT)                                                              \
+  do {                                                                                  \
+    if (wave)                                                                           \
+      QN_LAUNCH("k_seq_bwd", (k_seq_bwd<FI, FO, NT, 64>), grid, wg, st, a, g);          \
+    else                                                                                \
+      QN_LAUNCH("k_seq_bwd", (k_seq_bwd<FI, FO, NT, SQ_THREADS>), grid, wg, st, a, g);  \
+  } while (0)
   switch (4 * fi + 2 * fo + nt) {
     case 0: SQ_BWD(false, false, false); break;
     case 1: SQ_BWD(false, false, true); break;

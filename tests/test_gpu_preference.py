@@ -101,6 +101,7 @@ CASES = [
     ([7, 6], 32000, 0, 0, 2),
     ([1, 1], 128256, 0, 0, 0),
     ([1100, 600, 500, 300], 300, 4, 5, 20),     # rows not split
+    ([1025, 1026], 2113, 7, 0, 0),              # a wave to a row
     ([2] * 140, 64, 0, 1, 1),                   # more sequences than lanes
     ([0, 1, 0, 0, 2, 0, 1, 0] * 600, 9, 0, 2, 3),   # and than their square
 ]
@@ -284,9 +285,10 @@ def test_bad_labels_and_offsets_are_reported():
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("lens,vocab", [([30, 21], 2051), ([1500, 700], 251)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-def test_in_place_gradient(dtype):
-    prob = _problem([30, 21], 2051, dtype, pad=5, behind=2)
+def test_in_place_gradient(dtype, lens, vocab):
+    prob = _problem(lens, vocab, dtype, pad=5, behind=2)
     logits, lab, off = prob[:3]
     f = capi.qn_pref_loss_fwd(logits, lab, off, None, 0.1)
     want = capi.qn_pref_loss_bwd(logits, lab, off, f)
