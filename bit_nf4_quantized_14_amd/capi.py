@@ -896,38 +896,27 @@ def _seq_batch(fn: str, logits, labels, offsets):
         _tensor(fn, "offsets", offsets, n, torch.int64, index), n[0] - 1)
 
 
-def _seq_buffers(fn, b, like, given: dict, ws, index):
-    """({name: tensor}, {name: address}, workspace address, bytes, what keeps
-    the workspace alive) of a forward's fp32 outputs; `given` maps a name to
-    (tensor or None, length).  What the caller does not bring comes from one
-    allocation."""
+def _seq_buffers(fn, b, like, names, given, sizes, ws, index):
+    """(tensors, addresses, workspace address, bytes, what keeps the workspace
+    alive) of a forward's fp32 outputs, `sizes` elements each.  Outputs and
+    workspace come from one allocation unless the caller brings any."""
     import torch
     f32 = torch.float32
-    outs, ptrs, sizes, names = {}, {}, [], []
-    nw = 0
-    if ws is None:
-        nw = qn_seq_workspace_bytes(b.rows, b.vocab, b.nseq)
-        sizes.append(nw // 4)
-    for name, (t, n) in given.items():
-        if t is None:
-            names.append(name)
-            sizes.append(n)
-        else:
-            outs[name], ptrs[name] = t, _tensor(fn, name, t, (n,), f32, index)
-    buf = None
-    if sizes:
-        buf = like.new_empty(sum(sizes), dtype=f32)
+    nw = qn_seq_workspace_bytes(b.rows, b.vocab, b.nseq) if ws is None else 0
+    if ws is None and not any(t is not None for t in given):
+        buf = like.new_empty(nw // 4 + sum(sizes), dtype=f32)
         base = at = buf.data_ptr()
-        views = torch.split_with_sizes(buf, sizes)
         at += nw
-        for name, v, n in zip(names, views[1:] if ws is None else views,
-                              sizes[1:] if ws is None else sizes):
-            outs[name], ptrs[name] = v, at
+        ptrs = []
+        for n in sizes:
+            ptrs.append(at)
             at += 4 * n
+        return buf.split_with_sizes([nw // 4, *sizes])[1:], ptrs, base, nw, buf
+    outs = [like.new_empty(n, dtype=f32) if t is None else t for t, n in zip(given, sizes)]
+    ptrs = [_tensor(fn, k, t, (n,), f32, index) for k, t, n in zip(names, outs, sizes)]
     if ws is None:
-        return outs, ptrs, base, nw, buf
-    pw, nw = _workspace(fn, ws, index)
-    return outs, ptrs, pw, nw, ws
+        ws = like.new_empty(nw, dtype=torch.uint8)
+    return outs, ptrs, *_workspace(fn, ws, index), ws
 
 
 def _status_ptr(fn, status, index):
@@ -943,11 +932,11 @@ def qn_seq_logprob(logits, labels, offsets, lse=None, logp=None, status=None,
     index, b = _seq_batch(fn, logits, labels, offsets)
 
     def body(st):
-        o, p, pw, nw, _keep = _seq_buffers(
-            fn, b, logits, {"logp": (logp, b.nseq), "lse": (lse, b.rows)}, ws, index)
-        _check(fn, lib().qn_seq_logprob(b, p["lse"], p["logp"], _status_ptr(fn, status, index),
-                                        pw, nw, st))
-        return o["logp"], o["lse"]
+        o, p, pw, nw, _keep = _seq_buffers(fn, b, logits, ("logp", "lse"), (logp, lse),
+                                           (b.nseq, b.rows), ws, index)
+        _check(fn, lib().qn_seq_logprob(b, p[1], p[0], _status_ptr(fn, status, index), pw, nw,
+                                        st))
+        return tuple(o)
     return _run_on(index, stream, body)
 
 
@@ -976,14 +965,13 @@ def qn_pref_loss_fwd(logits, labels, offsets, ref_logp, beta: float,
     pr = None if ref_logp is None else _tensor(fn, "ref_logp", ref_logp, (nseq,), f32, index)
 
     def body(st):
-        g = out or PrefLoss(None, None, None, None)
-        o, p, pw, nw, _keep = _seq_buffers(
-            fn, b, logits, {"loss": (g.loss, pairs), "logp": (g.logp, nseq),
-                            "dlogp": (g.dlogp, nseq), "lse": (g.lse, rows)}, ws, index)
+        given = (None,) * 4 if out is None else (out.loss, out.logp, out.dlogp, out.lse)
+        o, p, pw, nw, _keep = _seq_buffers(fn, b, logits, ("loss", "logp", "dlogp", "lse"), given,
+                                           (pairs, nseq, nseq, rows), ws, index)
         _check(fn, lib().qn_pref_loss_fwd(
-            b, pr, _PrefHP(float(beta), float(label_smoothing)), p["lse"], p["logp"], p["loss"], p["dlogp"],
+            b, pr, _PrefHP(float(beta), float(label_smoothing)), p[3], p[1], p[0], p[2],
             _status_ptr(fn, status, index), pw, nw, st))
-        return PrefLoss(**o) if out is None else out
+        return PrefLoss(*o) if out is None else out
     return _run_on(index, stream, body)
 
 

@@ -566,10 +566,11 @@ size_t qn_seq_workspace_bytes(int64_t rows, int64_t vocab, int64_t nseq);
  * qn_seq_logprob -- lse_t and logp_s of a batch (device).
  * lse  : device float [rows]; 0 for rows that are not counted.
  * logp : device float [nseq] (summed in double, rounded once).
- * status_dev : device int32 or NULL.  QN_EINVAL is stored there if a label
- *        is not below vocab (that row is not counted) or if the offsets
- *        break their rule (lse and logp are then undefined; nothing outside
- *        the buffers is touched); otherwise it is left as it was.
+ * status_dev : device int32 or NULL.  QN_EINVAL is stored there if a
+ *        sequence holds a label that is not below vocab (that row is not
+ *        counted) or if the offsets break their rule (lse and logp are then
+ *        undefined; nothing outside the buffers is touched); otherwise it
+ *        is left as it was.
  * ws   : ws_bytes >= qn_seq_workspace_bytes(rows, vocab, nseq), 16-byte
  *        aligned; calls that run at the same time need workspaces of their
  *        own.
