@@ -682,7 +682,8 @@ def _run_on(index: int, stream, body):
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=index)
     if stream.device_index != index:
-        raise _bad("stream", f"the stream is on device {stream.device_index}, the tensors on {index}")
+        raise _bad("stream", f"the stream is on device {stream.device_index}, the tensors "
+                   f"on {index}")
     with torch.cuda.stream(stream):
         return body(stream.cuda_stream)
 

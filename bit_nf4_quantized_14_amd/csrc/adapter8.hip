@@ -247,18 +247,16 @@ __global__ __launch_bounds__(64 * AD_W) void k_adapter_rows(RowsJob p) {
 }
 
 // ---------------------------------------------------------------------------
-// dX of small outputs (dx_skinny): dY W', the reduction over the weight's
-// rows n, bound by streaming the
-// 4-bit weight (the 128 x 128 tiles of the GEMM spend 32 us on a 4096 x 4096
-// weight for any M up to 128: 64 workgroups, 32 dependent steps each).
+// dX of small outputs (dx_skinny): partial sums of dY W' over slices of the
+// weight's rows n.  (The 128 x 128 tiles of the GEMM spend 32 us on a 4096 x
+// 4096 weight for any M up to 128: 64 workgroups, 32 dependent steps each.)
 //
 // A workgroup owns 128 columns k, 16 MT tokens and a slice of the rows n; its
-// 8 waves take
-// the slice's steps of 32 rows in turn.  Lane l loads the packed dword of
-// columns 8 (l % 16) .. + 7 of rows 8 (l / 16) .. + 7: nibble c of the eight
-// dwords is the transposed operand (8 rows of one column) of MFMA number c,
-// whose columns are 8 i + c, i = 0 .. 15.  A code's level comes from a
-// 16-entry LDS table (16 banks, so no conflicts), is multiplied by the
+// 8 waves take the slice's steps of 32 rows in turn.  Lane l loads the packed
+// dword of columns 8 (l % 16) .. + 7 of rows 8 (l / 16) .. + 7: nibble c of
+// the eight dwords is the transposed operand (8 rows of one column) of MFMA
+// number c, whose columns are 8 i + c, i = 0 .. 15.  A code's level comes from
+// a 16-entry LDS table (16 banks, so no conflicts), is multiplied by the
 // block's constant of its row in fp32 and rounded to bf16, which is W'
 // exactly.  The waves add through LDS in a fixed order; slices are added,
 // with the adapter term, by blocks of k_adapter_cols.
