@@ -129,7 +129,7 @@ __device__ __forceinline__ void rows_load(RowsRegs<JT>& R, rsrc_t ry, rsrc_t rb,
         const int j = 16 * G::L * q + G::L * (lane & 15);
         const uint32_t at = ((uint32_t)(n + i) * (uint32_t)p.r + (uint32_t)j) * 2u;
         const bool row = n + i < p.N;
-        if constexpr (VEC && G::L > 1) {
+        if constexpr (VEC) {
           const uint32_t off = row && j < p.r ? at : G_OOB;
           if constexpr (G::L == 2) {
             R.b[h][q][i][0] = __builtin_amdgcn_raw_buffer_load_b32(rb, off, 0, 0);
@@ -744,8 +744,9 @@ void launch_adapter_rows(hipStream_t st, const RowsJob& p) {
   const dim3 grid((unsigned)(p.mt * p.slices)), wg(64 * AD_W);
   QN_RANK_DISPATCH(p.r, {
     constexpr int L = RowsCfg<JT>::L;
-    if (p.r % L == 0 && (reinterpret_cast<uintptr_t>(p.B) & (2 * L - 1)) == 0)
-      QN_LAUNCH("k_adapter_rows", (k_adapter_rows<JT, true>), grid, wg, st, p);
+    const bool vec = p.r % L == 0 && (reinterpret_cast<uintptr_t>(p.B) & (2 * L - 1)) == 0;
+    if (L > 1 && vec)
+      QN_LAUNCH("k_adapter_rows", (k_adapter_rows<JT, (L > 1)>), grid, wg, st, p);
     else
       QN_LAUNCH("k_adapter_rows", (k_adapter_rows<JT, false>), grid, wg, st, p);
   });

@@ -177,6 +177,9 @@ def _check_bwd(m, n, k, r, alpha, p=0.0, seed=0, dx_dtype=capi.QN_F32, need_dx=T
     # ranks in two parts, and row slices of each width of workgroup
     (200, 136, 192, 160, 160.0), (1500, 72, 64, 200, 200.0), (2100, 64, 64, 64, 64.0),
     (2100, 136, 64, 16, 16.0), (2100, 64, 128, 24, 24.0),
+    # B's rows one rank at a time, and whole, for each width of the rank
+    (70, 72, 64, 19, 19.0), (70, 72, 64, 131, 131.0), (70, 72, 64, 128, 128.0),
+    (70, 72, 64, 37, 37.0), (70, 72, 64, 256, 256.0),
     # several blocks of 64 tokens; the GEMM with 128- and with 256-wide tiles
     (100, 4104, 192, 8, 8.0), (1003, 64, 1024, 8, 16.0), (257, 1024, 2112, 16, 32.0),
     (2050, 264, 6208, 16, 16.0),
@@ -217,6 +220,24 @@ def test_dx_and_db_do_not_depend_on_the_checkpoint():
     assert torch.equal(dx, dx1) and torch.equal(db, db1) and not torch.equal(da, da1)
     for u, v in ((dx, dx0), (db, db0)):
         assert float((u - v).abs().max()) <= 2 * 64 * 2.0 ** -17 * float(v.abs().max())
+
+
+@pytest.mark.parametrize("r", [24, 64, 128, 160])
+def test_b_at_any_alignment(r):
+    m, n, k = 40, 72, 128
+    w, x, a, b, dy = _bwd_problem(m, n, k, r)
+    t, _ = quantize_dev(w)
+    X, A, B, DY = bf16_dev(x), bf16_dev(a), bf16_dev(b), bf16_dev(dy)
+    _, ts = capi.qlora_linear_fwd(X, t, A, B, r, 16.0)
+    x8 = capi.qn_act8_encode(X)
+    want = capi.qlora_linear_bwd_act8(DY, x8, t, A, B, r, 16.0, ts)
+    buf = torch.empty(n * r + 1, dtype=torch.bfloat16, device="cuda")
+    B2 = buf[1:].view(n, r)
+    B2.copy_(B)
+    got = capi.qlora_linear_bwd_act8(DY, x8, t, A, B2, r, 16.0, ts)
+    torch.cuda.synchronize()
+    for u, v in zip(want, got):
+        assert torch.equal(u, v)
 
 
 def test_a_broken_block_shows_in_da():
