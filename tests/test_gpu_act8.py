@@ -222,6 +222,45 @@ def test_dx_and_db_do_not_depend_on_the_checkpoint():
         assert float((u - v).abs().max()) <= 2 * 64 * 2.0 ** -17 * float(v.abs().max())
 
 
+@pytest.mark.parametrize("m,n,k,r", [(40, 72, 128, 8), (200, 264, 1088, 24)])
+def test_gradients_match_differences_of_the_forward(m, n, k, r):
+    """The layer's output Y is linear in X, in A and in B, each with the others
+    held: its difference quotient along a direction D is Y's value there, for
+    any step.  So sum(dY * Y_D) must be sum(gradient * D), here for the
+    restored X.  Each side is off by at most (n + k + 2 r + m) 2^-24, and
+    2^-16 for two splits into two bf16 terms, of the same sum with every
+    factor's magnitude."""
+    w, x, a, b, dy = _bwd_problem(m, n, k, r)
+    t, _ = quantize_dev(w)
+    A, B, DY, alpha = bf16_dev(a), bf16_dev(b), bf16_dev(dy), 2.0 * r
+    x8 = capi.qn_act8_encode(bf16_dev(x))
+    X = capi.qn_act8_decode(x8)
+    _, ts = capi.qlora_linear_fwd(X, t, A, B, r, alpha)
+    dx, da, db = capi.qlora_linear_bwd_act8(DY, x8, t, A, B, r, alpha, ts)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    zero = capi.nf4_quantize(torch.zeros((n, k), device="cuda"))
+    W = capi.nf4_dequantize(t)
+
+    def direction(like):
+        return torch.randn(like.shape, device="cuda", generator=g).bfloat16()
+    up = lambda v: v.double()  # noqa: E731
+    ab = lambda v: v.double().abs()  # noqa: E731
+    for name, grad, d in (("dX", dx, direction(X)), ("dA", da, direction(A)),
+                          ("dB", db, direction(B)), ("dX", dx, dx.bfloat16()),
+                          ("dA", da, da.bfloat16()), ("dB", db, db.bfloat16())):
+        base = t if name == "dX" else zero       # the base product has no part in dA, dB
+        x1, a1, b1 = (d if name == "dX" else X, d if name == "dA" else A,
+                      d if name == "dB" else B)
+        y, _ = capi.qlora_linear_fwd(x1, base, a1, b1, r, alpha)
+        one, two = float((up(DY) * up(y)).sum()), float((up(grad) * up(d)).sum())
+        mag = 2.0 * ab(x1) @ ab(a1).t() @ ab(b1).t()
+        if name == "dX":
+            mag = mag + ab(x1) @ ab(W).t()
+        bound = float((ab(DY) * mag).sum()) * 2 * ((n + k + 2 * r + m) * 2.0 ** -24 + 2.0 ** -16)
+        print(f"[act8 bwd] {name}: {one:.6g} {two:.6g} bound {bound:.3g}", flush=True)
+        assert abs(one - two) <= bound
+
+
 @pytest.mark.parametrize("r", [24, 64, 128, 160])
 def test_b_at_any_alignment(r):
     m, n, k = 40, 72, 128
