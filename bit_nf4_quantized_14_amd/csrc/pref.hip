@@ -527,8 +527,9 @@ int seq_backward(const qn_seq_batch* b, const float* lse, const float* dlogp,
     return QN_EINVAL;
   if (b->rows == 0) return QN_OK;
   if (lse == nullptr || !sized_ptr(dl, dl_dtype)) return QN_EINVAL;
-  // in place means element for element
-  if (dl == b->logits && (dl_dtype != b->dtype || ld_dl != b->ld)) return QN_EINVAL;
+  // in place means element for element (the pitch of one row is of no account)
+  if (dl == b->logits && (dl_dtype != b->dtype || (b->rows > 1 && ld_dl != b->ld)))
+    return QN_EINVAL;
   const SeqArgs a = seq_args(b, cols);
   SeqBwdArgs g;
   g.lse = lse;

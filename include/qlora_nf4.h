@@ -590,7 +590,8 @@ int qn_seq_logprob(const qn_seq_batch* b, float* lse, float* logp,
  *           element t * ld_dl (cols >= vocab, ld_dl >= cols); columns from
  *           vocab to cols (a head padded to a multiple of 8 words) are
  *           written as zeros.  It may be the logits' own memory (same
- *           pointer, type and pitch); any other overlap is not allowed.
+ *           pointer, type and, of several rows, pitch); any other overlap is
+ *           not allowed.
  * Errors: QN_EINVAL, QN_EHIP.
  */
 int qn_seq_logprob_bwd(const qn_seq_batch* b, const float* lse,

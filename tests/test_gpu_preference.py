@@ -296,6 +296,20 @@ def test_in_place_gradient(dtype, lens, vocab):
     assert got.data_ptr() == logits.data_ptr() and torch.equal(got, want)
 
 
+@pytest.mark.parametrize("rows", [1, 2])
+def test_in_place_gradient_of_a_padded_head(rows):
+    """Logits and gradient are the same buffer, the gradient with the
+    padding columns; a batch may have one row only."""
+    prob = _problem([rows, 0], 1003, torch.bfloat16, pad=5, masked=0.0)
+    logits, lab, off = prob[:3]
+    f = capi.qn_pref_loss_fwd(logits, lab, off, None, 0.1)
+    want = capi.qn_pref_loss_bwd(logits, lab, off, f)
+    buf = logits.as_strided((rows, 1008), (1008, 1))
+    got = capi.qn_pref_loss_bwd(logits, lab, off, f, dlogits=buf)
+    assert got.data_ptr() == logits.data_ptr() and not bool(got[:, 1003:].any())
+    assert torch.equal(got[:, :1003], want) and bool(want.any())
+
+
 def test_odd_pitches_and_guard_bands():
     """Rows that start at any element; what lies between them stays."""
     prob = _problem([5, 4], 999, torch.bfloat16, pad=4)
