@@ -955,7 +955,8 @@ def qn_pref_loss_fwd(logits, labels, offsets, ref_logp, beta: float,
                      label_smoothing: float = 0.0, out: PrefLoss | None = None,
                      status=None, ws=None, stream=None):
     """Paired log-ratio loss of sequences p (chosen) and P + p (rejected);
-    ref_logp [2P] or None for zeros; returns a PrefLoss."""
+    ref_logp [2P] or None for zeros; returns a PrefLoss (`out` when it is
+    given; its fields that are None are allocated and set)."""
     import torch
     fn = "qn_pref_loss_fwd"
     index, b = _seq_batch(fn, logits, labels, offsets)
@@ -972,7 +973,10 @@ def qn_pref_loss_fwd(logits, labels, offsets, ref_logp, beta: float,
         _check(fn, lib().qn_pref_loss_fwd(
             b, pr, _PrefHP(float(beta), float(label_smoothing)), p[3], p[1], p[0], p[2],
             _status_ptr(fn, status, index), pw, nw, st))
-        return PrefLoss(*o) if out is None else out
+        if out is None:
+            return PrefLoss(*o)
+        out.loss, out.logp, out.dlogp, out.lse = o
+        return out
     return _run_on(index, stream, body)
 
 

@@ -372,6 +372,18 @@ def test_default_stream_by_handle_and_by_object():
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+def test_outputs_that_are_not_given_are_set():
+    prob = _problem([5, 4], 100, torch.float32)
+    logits, lab, off = prob[:3]
+    want = capi.qn_pref_loss_fwd(logits, lab, off, None, 0.1)
+    loss = torch.empty(1, device="cuda")
+    out = capi.PrefLoss(loss, None, None, None)
+    assert capi.qn_pref_loss_fwd(logits, lab, off, None, 0.1, out=out) is out
+    assert out.loss is loss and torch.equal(loss, want.loss)
+    for name in ("logp", "dlogp", "lse"):
+        assert torch.equal(getattr(out, name), getattr(want, name))
+
+
 def test_graph_replays_follow_new_logits():
     prob = _problem([30, 21], 4001, torch.bfloat16, pad=7)
     logits, lab, off = prob[:3]
