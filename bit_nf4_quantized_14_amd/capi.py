@@ -733,6 +733,17 @@ def _workspace(fn: str, ws, index: int) -> tuple[int, int]:
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
+def _weight(fn: str, w: NF4Tensor, index: int) -> _NF4Struct:
+    """The struct of a weight whose buffers are on device `index` and hold its
+    size."""
+    sizes = w.sizes(w.rows, w.cols)
+    for t, n in zip((w.packed, w.qabs, w.gscale), sizes):
+        if (not t.is_cuda or t.get_device() != index or not t.is_contiguous() or
+                t.numel() < n):
+            raise _bad(fn, f"w must be contiguous, on GPU {index} and of {sizes} elements")
+    return w.as_struct()
+
+
 @dataclass
 class Act8Tensor:
     """Device buffers of an 8-bit activation checkpoint (see qn_act8 in the
@@ -836,6 +847,7 @@ def qlora_linear_bwd_act8(dy, x8: Act8Tensor, w: NF4Tensor, A, B, r: int,
     pA = _tensor(fn, "A", A, (r, K), bf, index)
     pB = _tensor(fn, "B", B, (N, r), bf, index)
     pt = _tensor(fn, "t_saved", t_saved, (M, r), f32, index)
+    wt = _weight(fn, w, index)
 
     def body(st):
         gx, gA, gB = dx, dA, dB
@@ -860,7 +872,7 @@ def qlora_linear_bwd_act8(dy, x8: Act8Tensor, w: NF4Tensor, A, B, r: int,
         else:
             pw, nw = _workspace(fn, ws, index)
         _check(fn, lib().qlora_linear_bwd_act8(
-            pdy, xt, M, w.as_struct(), pA, pB, int(r), float(alpha), pt, pdx, code,
+            pdy, xt, M, wt, pA, pB, int(r), float(alpha), pt, pdx, code,
             gA.data_ptr(), gB.data_ptr(),
             _Dropout(float(p), int(seed) & 0xFFFFFFFFFFFFFFFF), pw, nw, st))
         return gx, gA, gB

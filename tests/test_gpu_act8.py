@@ -342,3 +342,21 @@ def test_refusals_on_the_gpu():
         capi.qn_act8_encode(x, out=capi.Act8Tensor.empty(4, 64))
     with pytest.raises(capi.QNError):
         capi.qn_act8_decode(t, dtype=5)
+
+
+def test_a_weight_elsewhere_or_too_small_is_refused():
+    m, n, k, r = 4, 64, 128, 8
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    t = capi.qn_act8_encode(torch.ones((m, k), **bf))
+    dy, A, B = torch.ones((m, n), **bf), torch.ones((r, k), **bf), torch.ones((n, r), **bf)
+    ts = torch.ones((m, r), device="cuda")
+    w = capi.nf4_quantize(torch.ones((n, k), device="cuda"))
+    host, small = capi.NF4Tensor.empty(n, k, device="cpu"), capi.NF4Tensor.empty(n // 2, k)
+    for bad in (host, capi.NF4Tensor(w.packed, w.qabs, host.gscale, n, k),
+                capi.NF4Tensor(small.packed, w.qabs, w.gscale, n, k),
+                capi.NF4Tensor(w.packed, small.qabs, w.gscale, n, k)):
+        with pytest.raises(capi.QNError) as e:
+            capi.qlora_linear_bwd_act8(dy, t, bad, A, B, r, 16.0, ts)
+        assert e.value.code == capi.QN_EINVAL
+    capi.qlora_linear_bwd_act8(dy, t, w, A, B, r, 16.0, ts)
+    torch.cuda.synchronize()
