@@ -736,12 +736,15 @@ def _workspace(fn: str, ws, index: int) -> tuple[int, int]:
 def _weight(fn: str, w: NF4Tensor, index: int) -> _NF4Struct:
     """The struct of a weight whose buffers are on device `index` and hold its
     size."""
-    sizes = w.sizes(w.rows, w.cols)
-    for t, n in zip((w.packed, w.qabs, w.gscale), sizes):
-        if (not t.is_cuda or t.get_device() != index or not t.is_contiguous() or
-                t.numel() < n):
-            raise _bad(fn, f"w must be contiguous, on GPU {index} and of {sizes} elements")
-    return w.as_struct()
+    a, b, c = w.packed, w.qabs, w.gscale
+    n = w.rows * w.cols
+    nb = -(-n // QN_BLOCK)
+    if (a.get_device() == index == b.get_device() and c.get_device() == index
+            and 2 * a.numel() >= n and b.numel() >= nb and c.numel() * QN_GROUP >= nb
+            and a.is_contiguous() and b.is_contiguous() and c.is_contiguous()):
+        return _NF4Struct(a.data_ptr(), b.data_ptr(), c.data_ptr(), w.rows, w.cols)
+    raise _bad(fn, f"w must be contiguous, on GPU {index} and of "
+               f"{w.sizes(w.rows, w.cols)} elements")
 
 
 @dataclass
