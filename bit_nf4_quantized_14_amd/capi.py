@@ -734,16 +734,19 @@ def _workspace(fn: str, ws, index: int) -> tuple[int, int]:
 
 
 def _weight(fn: str, w: NF4Tensor, index: int) -> _NF4Struct:
-    """The struct of a weight whose buffers are on device `index` and hold its
-    size."""
+    """The struct of a weight whose buffers are on device `index`, of the
+    codec's types and hold its size."""
+    import torch
     a, b, c = w.packed, w.qabs, w.gscale
     n = w.rows * w.cols
     nb = -(-n // QN_BLOCK)
+    u8 = torch.uint8
     if (a.get_device() == index == b.get_device() and c.get_device() == index
+            and a.dtype is u8 and b.dtype is u8 and c.dtype is torch.float32
             and 2 * a.numel() >= n and b.numel() >= nb and c.numel() * QN_GROUP >= nb
             and a.is_contiguous() and b.is_contiguous() and c.is_contiguous()):
         return _NF4Struct(a.data_ptr(), b.data_ptr(), c.data_ptr(), w.rows, w.cols)
-    raise _bad(fn, f"w must be contiguous, on GPU {index} and of "
+    raise _bad(fn, f"w must be contiguous, on GPU {index}, uint8, uint8 and float32, and of "
                f"{w.sizes(w.rows, w.cols)} elements")
 
 
