@@ -14,13 +14,13 @@
 // loads for most of that), decode 9.4 us (5.5 TB/s); 2048 x 28672 fp32 encode
 // 54.8 us (5.4 TB/s).  Two and four blocks per eight lanes, loaded together,
 // took 12.2 and 17.1 us for the first.
+#include "act8_code.h"
 #include "act8_host.h"
 
 namespace {
 
 using namespace qn;
 
-constexpr float A8_TINY = 0x1p-100f;   // blocks below this are stored as zeros
 constexpr int A8_THREADS = 256;
 
 // Eight consecutive elements of a row starting at column c as fp32 bits
@@ -91,18 +91,11 @@ __global__ __launch_bounds__(A8_THREADS) void k_act8_encode(
   const bool bad = top >= 0x7F800000u, live = !bad && a >= A8_TINY;
   if ((g & 7) == 0)
     scale[blk] = live ? a / 127.0f : (bad ? __uint_as_float(0x7FC00000u) : 0.0f);
-  // RN(y / d), y = x 127/256, d = a/256, from the correctly rounded
-  // reciprocal: q0 = y/d to within an ulp, its remainder by one exact fma,
-  // and one correction (Markstein); a >= 2^-100 keeps the remainder of
-  // every quotient that reaches 1/2 a multiple of 2^-149.
-  const float d = a * 0x1p-8f;
-  const float inv = live ? 1.0f / d : 0.0f;
+  const Act8Div div = act8_div(live ? a : 1.0f);
   uint32_t q[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float y = __uint_as_float(b[i]) * 0.49609375f;
-    const float q0 = y * inv;
-    const float qq = fmaf(fmaf(-q0, d, y), inv, q0);
+    const float qq = act8_quotient(__uint_as_float(b[i]), div);
     // adding 1.5 2^23 rounds to the nearest even integer into the low bits
     q[i] = __float_as_uint(qq + 12582912.0f);
   }
