@@ -139,6 +139,13 @@ __device__ __forceinline__ double sq_logit(const char* row, int64_t c) {
              : (double)bf16_to_f32(reinterpret_cast<const uint16_t*>(row)[c]);
 }
 
+// A token's log-probability from its logit, the row's maximum m and l = log
+// sum exp(x - m): the logits' difference first, as l vanishes beside an m of a
+// type's lowest value, where such a row is uniform.
+__device__ __forceinline__ double sq_token(double hit, float m, double l) {
+  return (hit - (double)m) - l;
+}
+
 // Maximum and sum of one chunk of one row by TEAM threads.  Rows that are not counted are
 // not read.  Each thread keeps SQ_GROUPS 16-byte loads in flight; the last
 // round (one group at a time where at most half of the groups are left)
@@ -212,9 +219,9 @@ __global__ __launch_bounds__(SQ_THREADS) void k_seq_rows(SeqArgs a, SeqPart* __r
     if (a.nchunk > 1) {
       ws[(int64_t)row * a.nchunk + ch].part = r;
     } else {
-      const double l = (double)r.m + log((double)r.s);
-      lse[row] = (float)l;
-      ws[row].token = sq_logit<F32>(p, label) - l;
+      const double l = log((double)r.s);
+      lse[row] = (float)((double)r.m + l);
+      ws[row].token = sq_token(sq_logit<F32>(p, label), r.m, l);
     }
   }
 }
@@ -272,10 +279,10 @@ __device__ __forceinline__ double sq_rows_sum(const SeqArgs& a, const SeqPart* _
         for (int off = 4; off >= 1; off >>= 1)
           r = sq_join(r, MaxSum{__shfl_xor(r.m, off), __shfl_xor(r.s, off)});
       }
-      const double l = (double)r.m + log((double)r.s);
+      const double l = log((double)r.s);
       if (sub == 0) {
-        lse[t] = (float)l;
-        sum += hit - l;
+        lse[t] = (float)((double)r.m + l);
+        sum += sq_token(hit, r.m, l);
       }
     }
   }

@@ -10,7 +10,7 @@ import numpy as np
 def _log_softmax(row: np.ndarray) -> np.ndarray:
     m = row.max()
     with np.errstate(invalid="ignore"):
-        return row - (m + np.log(np.exp(row - m).sum()))
+        return (row - m) - np.log(np.exp(row - m).sum())
 
 
 def counted_rows(labels, offsets, vocab):
@@ -31,8 +31,9 @@ def seq_logprob(logits, labels, offsets):
         for s, t, y in counted_rows(labels, offsets, vocab):
             x = logits[t].astype(np.float64)
             m = x.max()
-            lse[t] = m + np.log(np.exp(x - m).sum())
-            logp[s] += x[y] - lse[t]
+            log_sum = np.log(np.exp(x - m).sum())
+            lse[t] = m + log_sum
+            logp[s] += (x[y] - m) - log_sum     # log_sum vanishes beside a far m
     return logp, lse
 
 
