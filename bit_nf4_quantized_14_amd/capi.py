@@ -94,7 +94,8 @@ class _SeqBatch(ctypes.Structure):
     _fields_ = [("logits", ctypes.c_void_p), ("dtype", ctypes.c_int32),
                 ("rows", ctypes.c_int64), ("vocab", ctypes.c_int64),
                 ("ld", ctypes.c_int64), ("labels", ctypes.c_void_p),
-                ("offsets", ctypes.c_void_p), ("nseq", ctypes.c_int64)]
+                ("offsets", ctypes.c_void_p), ("nseq", ctypes.c_int64),
+                ("lse_lo", ctypes.c_void_p)]
 
 
 class _PrefHP(ctypes.Structure):
@@ -943,12 +944,20 @@ def _status_ptr(fn, status, index):
     return None if status is None else _tensor(fn, "status", status, (1,), torch.int32, index)
 
 
+def _set_lse_lo(fn, b, lse_lo, index):
+    import torch
+    if lse_lo is not None:
+        b.lse_lo = _tensor(fn, "lse_lo", lse_lo, (b.rows,), torch.float32, index)
+
+
 def qn_seq_logprob(logits, labels, offsets, lse=None, logp=None, status=None,
-                   ws=None, stream=None):
+                   ws=None, stream=None, lse_lo=None):
     """Log-probability of each packed sequence and log-sum-exp of each row;
-    returns (logp [nseq], lse [rows])."""
+    returns (logp [nseq], lse [rows]).  lse_lo (fp32 [rows]), if given, is set
+    to what lse loses by its rounding, for qn_seq_logprob_bwd."""
     fn = "qn_seq_logprob"
     index, b = _seq_batch(fn, logits, labels, offsets)
+    _set_lse_lo(fn, b, lse_lo, index)
 
     def body(st):
         o, p, pw, nw, _keep = _seq_buffers(fn, b, logits, ("logp", "lse"), (logp, lse),
@@ -962,11 +971,13 @@ def qn_seq_logprob(logits, labels, offsets, lse=None, logp=None, status=None,
 @dataclass
 class PrefLoss:
     """Outputs of qn_pref_loss_fwd: loss [P], logp [2P], dlogp [2P] (the
-    derivative of a pair's loss by its sequences' logp) and lse [rows]."""
+    derivative of a pair's loss by its sequences' logp), lse [rows] and lse_lo
+    [rows] (what lse loses by its rounding)."""
     loss: "object"
     logp: "object"
     dlogp: "object"
     lse: "object"
+    lse_lo: "object" = None
 
 
 def qn_pref_loss_fwd(logits, labels, offsets, ref_logp, beta: float,
@@ -985,22 +996,26 @@ def qn_pref_loss_fwd(logits, labels, offsets, ref_logp, beta: float,
     pr = None if ref_logp is None else _tensor(fn, "ref_logp", ref_logp, (nseq,), f32, index)
 
     def body(st):
-        given = (None,) * 4 if out is None else (out.loss, out.logp, out.dlogp, out.lse)
-        o, p, pw, nw, _keep = _seq_buffers(fn, b, logits, ("loss", "logp", "dlogp", "lse"), given,
-                                           (pairs, nseq, nseq, rows), ws, index)
+        given = ((None,) * 5 if out is None
+                 else (out.loss, out.logp, out.dlogp, out.lse, out.lse_lo))
+        o, p, pw, nw, _keep = _seq_buffers(
+            fn, b, logits, ("loss", "logp", "dlogp", "lse", "lse_lo"), given,
+            (pairs, nseq, nseq, rows, rows), ws, index)
+        b.lse_lo = p[4]
         _check(fn, lib().qn_pref_loss_fwd(
             b, pr, _PrefHP(float(beta), float(label_smoothing)), p[3], p[1], p[0], p[2],
             _status_ptr(fn, status, index), pw, nw, st))
         if out is None:
             return PrefLoss(*o)
-        out.loss, out.logp, out.dlogp, out.lse = o
+        out.loss, out.logp, out.dlogp, out.lse, out.lse_lo = o
         return out
     return _run_on(index, stream, body)
 
 
-def _seq_bwd(fn, logits, labels, offsets, lse, dlogp, dloss, dlogits, dl_dtype, stream):
+def _seq_bwd(fn, logits, labels, offsets, lse, lse_lo, dlogp, dloss, dlogits, dl_dtype, stream):
     import torch
     index, b = _seq_batch(fn, logits, labels, offsets)
+    _set_lse_lo(fn, b, lse_lo, index)
     f32, rows, vocab, nseq = torch.float32, b.rows, b.vocab, b.nseq
     args = [b, _tensor(fn, "lse", lse, (rows,), f32, index),
             _tensor(fn, "dlogp", dlogp, (nseq,), f32, index)]
@@ -1034,11 +1049,13 @@ def _seq_bwd(fn, logits, labels, offsets, lse, dlogp, dloss, dlogits, dl_dtype, 
 
 
 def qn_seq_logprob_bwd(logits, labels, offsets, lse, dlogp, dlogits=None,
-                       dl_dtype: int | None = None, stream=None):
+                       dl_dtype: int | None = None, stream=None, lse_lo=None):
     """Gradient of sum(dlogp * logp) by the logits.  dlogits may have more
     columns than the logits (written as zeros) and may be the logits
-    themselves; it is allocated in dl_dtype (the logits' type) when None."""
-    return _seq_bwd("qn_seq_logprob_bwd", logits, labels, offsets, lse, dlogp, None,
+    themselves; it is allocated in dl_dtype (the logits' type) when None.
+    lse_lo as set by the forward; without it the probabilities of a row are
+    off by the rounding of its lse."""
+    return _seq_bwd("qn_seq_logprob_bwd", logits, labels, offsets, lse, lse_lo, dlogp, None,
                     dlogits, dl_dtype, stream)
 
 
@@ -1047,8 +1064,8 @@ def qn_pref_loss_bwd(logits, labels, offsets, fwd: PrefLoss, dloss=None,
     """Gradient of sum(dloss * loss) by the logits (dloss None: the mean
     loss), from what qn_pref_loss_fwd returned; dlogits as in
     qn_seq_logprob_bwd."""
-    return _seq_bwd("qn_pref_loss_bwd", logits, labels, offsets, fwd.lse, fwd.dlogp, dloss,
-                    dlogits, dl_dtype, stream)
+    return _seq_bwd("qn_pref_loss_bwd", logits, labels, offsets, fwd.lse, fwd.lse_lo, fwd.dlogp,
+                    dloss, dlogits, dl_dtype, stream)
 
 
 def qn_profile_kernel(name: str | None, starts=None, stops=None) -> int:

@@ -84,10 +84,18 @@ __device__ __forceinline__ void sq_load(const char* row, int c, int vocab, float
   }
 }
 
-// A running maximum m and s = sum exp(x - m).  m starts at -infinity, where
-// the shift is taken as 0 so that no infinity meets its own.
+// A thread's running maximum m and s = sum exp(x - m).  m starts at -infinity,
+// where the shift is taken as 0 so that no infinity meets its own.
 struct MaxSum {
   float m, s;
+};
+
+// The same of several threads, with the sum in double: the maximum's own term
+// is 1, and where a label holds nearly all of the probability the rest, which
+// is its gradient, is far below fp32's step there.
+struct RowSum {
+  float m;
+  double s;
 };
 
 __device__ __forceinline__ float sq_shift(float m) { return m == SQ_NEG_INF ? 0.0f : m; }
@@ -96,26 +104,63 @@ __device__ __forceinline__ float sq_exp(float x) {
   return __builtin_amdgcn_exp2f(x * SQ_LOG2E);
 }
 
-__device__ __forceinline__ MaxSum sq_join(const MaxSum& a, const MaxSum& b) {
-  const float m = fmaxf(a.m, b.m), z = sq_shift(m);
-  return MaxSum{m, a.s * sq_exp(a.m - z) + b.s * sq_exp(b.m - z)};
+// r's sum for a maximum m that is not below its own.
+__device__ __forceinline__ double sq_scaled(const RowSum& r, float m) {
+  return r.s * (double)sq_exp(r.m - sq_shift(m));
+}
+
+// The join of the lanes that differ in the lowest `bits` bits: first the
+// maximum, so that each lane's sum is rescaled once.
+__device__ __forceinline__ RowSum sq_join_lanes(const RowSum& r, int bits) {
+  RowSum t = r;
+#pragma unroll
+  for (int off = 1 << (bits - 1); off >= 1; off >>= 1) t.m = fmaxf(t.m, __shfl_xor(t.m, off));
+  t.s = sq_scaled(r, t.m);
+#pragma unroll
+  for (int off = 1 << (bits - 1); off >= 1; off >>= 1) t.s += __shfl_xor(t.s, off);
+  return t;
+}
+
+// The join of N of them by one thread.
+template <int N>
+__device__ __forceinline__ RowSum sq_join(const RowSum (&x)[N]) {
+  RowSum t{x[0].m, 0.0};
+#pragma unroll
+  for (int i = 1; i < N; ++i) t.m = fmaxf(t.m, x[i].m);
+#pragma unroll
+  for (int i = 0; i < N; ++i) t.s += sq_scaled(x[i], t.m);
+  return t;
 }
 
 struct SeqArgs {
   const char* logits;
   const int64_t* labels;
   const int64_t* offsets;
+  float* lse_lo;        // or null
   int64_t ld;
   int32_t vocab, chunk, rows, nseq, nchunk;
 };
 
-// The workspace of the forward: a row's partial sums, or, where one
-// workgroup takes the whole row, its token's log-probability.
+// The workspace of the forward: a row's partial sums (s - 1, whose fp32 keeps
+// what a sum next to 1 loses), or, where one workgroup takes the whole row,
+// its token's log-probability.
+struct SeqChunk {
+  float m, rest;
+};
 union SeqPart {
-  MaxSum part;     // [rows][nchunk]
+  SeqChunk part;   // [rows][nchunk]
   double token;    // [rows], nchunk == 1
 };
 static_assert(sizeof(SeqPart) == 8, "one slot for each row and workgroup");
+
+// lse of a row, m + l with l = log s, as fp32 and what that loses (beside a far
+// m all of l): the backward's exponents are differences from both.
+__device__ __forceinline__ void sq_put_lse(const SeqArgs& a, float* __restrict__ lse, int64_t row,
+                                           float m, double l) {
+  const float hi = (float)((double)m + l);
+  lse[row] = hi;
+  if (a.lse_lo != nullptr) a.lse_lo[row] = (float)(((double)m - (double)hi) + l);
+}
 
 // Adds logits to a running maximum and sum.
 template <int N>
@@ -146,8 +191,8 @@ __device__ __forceinline__ double sq_token(double hit, float m, double l) {
   return (hit - (double)m) - l;
 }
 
-// Maximum and sum of one chunk of one row by TEAM threads.  Rows that are not counted are
-// not read.  Each thread keeps SQ_GROUPS 16-byte loads in flight; the last
+// Maximum and sum of one chunk of one row by TEAM threads.  Rows that are not
+// counted are not read.  Each thread keeps SQ_GROUPS 16-byte loads in flight; the last
 // round (one group at a time where at most half of the groups are left)
 // reads a group from the end of the chunk where it would pass it, and drops
 // what another thread has.
@@ -155,7 +200,7 @@ template <bool F32, int TEAM>
 __global__ __launch_bounds__(SQ_THREADS) void k_seq_rows(SeqArgs a, SeqPart* __restrict__ ws,
                                                          float* __restrict__ lse) {
   constexpr int G = F32 ? SQ_GROUPS / 2 : SQ_GROUPS, STEP = 8 * TEAM;
-  __shared__ MaxSum red[SQ_THREADS / 64];
+  __shared__ RowSum red[SQ_THREADS / 64];
   const unsigned team = blockIdx.x * (SQ_THREADS / TEAM) + threadIdx.x / TEAM;
   const int tid = threadIdx.x % TEAM;
   const int row = (int)(team / (unsigned)a.nchunk);
@@ -165,19 +210,22 @@ __global__ __launch_bounds__(SQ_THREADS) void k_seq_rows(SeqArgs a, SeqPart* __r
   const bool counted = label >= 0 && label < a.vocab && row >= a.offsets[0] &&
                        row < a.offsets[a.nseq];
   if (!counted) {
-    if (ch == 0 && tid == 0) lse[row] = 0.0f;
+    if (ch == 0 && tid == 0) {
+      lse[row] = 0.0f;
+      if (a.lse_lo != nullptr) a.lse_lo[row] = 0.0f;
+    }
     return;
   }
   const char* p = a.logits + (int64_t)row * a.ld * (F32 ? 4 : 2);
   const int begin = ch * a.chunk, end = min(a.vocab, begin + a.chunk);
-  MaxSum r{SQ_NEG_INF, 0.0f};
+  MaxSum mine{SQ_NEG_INF, 0.0f};
   int c = begin + 8 * tid;
   int at = begin;
   for (; at + G * STEP <= end; at += G * STEP, c += G * STEP) {
     float v[8 * G];
 #pragma unroll
     for (int g = 0; g < G; ++g) sq_load8<F32>(p, c + g * STEP, v + 8 * g);
-    sq_add(r, v);
+    sq_add(mine, v);
   }
   if (end - begin >= 8) {
     for (; at < end && end - at <= STEP * (G / 2); at += STEP, c += STEP) {
@@ -186,7 +234,7 @@ __global__ __launch_bounds__(SQ_THREADS) void k_seq_rows(SeqArgs a, SeqPart* __r
       const int skip = c - (end - 8);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = i >= skip ? v[i] : SQ_NEG_INF;
-      sq_add(r, v);
+      sq_add(mine, v);
     }
     if (at < end) {
       float v[8 * G];
@@ -199,28 +247,25 @@ __global__ __launch_bounds__(SQ_THREADS) void k_seq_rows(SeqArgs a, SeqPart* __r
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[8 * g + i] = i >= skip ? v[8 * g + i] : SQ_NEG_INF;
       }
-      sq_add(r, v);
+      sq_add(mine, v);
     }
   } else {                             // a vocabulary of fewer than 8 words
     float v[8];
     sq_load<F32>(p, c, end, v);
-    sq_add(r, v);
+    sq_add(mine, v);
   }
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1)
-    r = sq_join(r, MaxSum{__shfl_xor(r.m, off), __shfl_xor(r.s, off)});
+  RowSum r = sq_join_lanes(RowSum{mine.m, (double)mine.s}, 6);
   if constexpr (TEAM == SQ_THREADS) {
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = r;
     __syncthreads();
-    if (tid == 0)
-      for (int w = 1; w < SQ_THREADS / 64; ++w) r = sq_join(r, red[w]);
+    if (tid == 0) r = sq_join(red);
   }
   if (tid == 0) {
     if (a.nchunk > 1) {
-      ws[(int64_t)row * a.nchunk + ch].part = r;
+      ws[(int64_t)row * a.nchunk + ch].part = SeqChunk{r.m, (float)(r.s - 1.0)};
     } else {
-      const double l = log((double)r.s);
-      lse[row] = (float)((double)r.m + l);
+      const double l = log(r.s);
+      sq_put_lse(a, lse, row, r.m, l);
       ws[row].token = sq_token(sq_logit<F32>(p, label), r.m, l);
     }
   }
@@ -265,23 +310,22 @@ __device__ __forceinline__ double sq_rows_sum(const SeqArgs& a, const SeqPart* _
       if (label < 0 || label >= a.vocab) continue;      // the whole team's
       const double hit = sq_logit<F32>(a.logits + t * a.ld * (F32 ? 4 : 2), label);
       const SeqPart* q = ws + t * a.nchunk;
-      MaxSum r{SQ_NEG_INF, 0.0f};
+      RowSum r{SQ_NEG_INF, 0.0};
       for (int c0 = sub; c0 < a.nchunk; c0 += 8 * team) {
-        MaxSum x[8];
+        RowSum x[9];
+        x[8] = r;
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-          x[u] = c0 + u * team < a.nchunk ? q[c0 + u * team].part : MaxSum{SQ_NEG_INF, 0.0f};
-#pragma unroll
-        for (int u = 0; u < 8; ++u) r = sq_join(r, x[u]);
+        for (int u = 0; u < 8; ++u) {
+          const SeqChunk k =
+              c0 + u * team < a.nchunk ? q[c0 + u * team].part : SeqChunk{SQ_NEG_INF, -1.0f};
+          x[u] = RowSum{k.m, 1.0 + (double)k.rest};
+        }
+        r = sq_join(x);
       }
-      if (team == 8) {
-#pragma unroll
-        for (int off = 4; off >= 1; off >>= 1)
-          r = sq_join(r, MaxSum{__shfl_xor(r.m, off), __shfl_xor(r.s, off)});
-      }
-      const double l = log((double)r.s);
+      if (team == 8) r = sq_join_lanes(r, 3);
+      const double l = log(r.s);
       if (sub == 0) {
-        lse[t] = (float)((double)r.m + l);
+        sq_put_lse(a, lse, t, r.m, l);
         sum += sq_token(hit, r.m, l);
       }
     }
@@ -421,17 +465,28 @@ __global__ __launch_bounds__(SQ_THREADS) void k_seq_bwd(SeqArgs a, SeqBwdArgs g)
   float coef = g.dlogp[seq];
   if (g.pairs > 0)
     coef *= g.dloss != nullptr ? g.dloss[seq < g.pairs ? seq : seq - g.pairs] : g.mean;
-  const float lse = g.lse[row];
+  const float lse = g.lse[row], lo = a.lse_lo != nullptr ? a.lse_lo[row] : 0.0f;
   const char* p = a.logits + (int64_t)row * a.ld * (FIN ? 4 : 2);
+  // exp(v - lse - lo), lo's part once a row: lo is at most log(vocab) either
+  // way, as lse is no further from m + log s than m is
+  const float factor = -coef * sq_exp(-lo);
   const int hit = (int)label;
   for (int c = begin + 8 * tid; c < end; c += STEP) {
     float v[8];
     sq_load<FIN>(p, c, a.vocab, v);
+    // the label's 1 - p by expm1: p may be all but 1
+    const bool here = hit >= c && hit < c + 8;
+    float own = 0.0f;
+    if (here) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = -coef * sq_exp(v[i] - lse);
-    if (hit >= c && hit < c + 8) {
+      for (int i = 0; i < 8; ++i) own = c + i == hit ? v[i] : own;
+      own = -coef * expm1f((own - lse) - lo);
+    }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += c + i == hit ? coef : 0.0f;
+    for (int i = 0; i < 8; ++i) v[i] = factor * sq_exp(v[i] - lse);
+    if (here) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = c + i == hit ? own : v[i];
     }
     if (c + 8 > a.vocab) {     // padding columns: zero whatever coef is
 #pragma unroll
@@ -484,6 +539,7 @@ SeqArgs seq_args(const qn_seq_batch* b, int64_t cols) {
   a.logits = static_cast<const char*>(b->logits);
   a.labels = b->labels;
   a.offsets = b->offsets;
+  a.lse_lo = b->lse_lo;
   a.vocab = (int32_t)b->vocab;
   a.ld = b->ld;
   a.rows = (int32_t)b->rows;

@@ -542,6 +542,11 @@ int qlora_linear_bwd_act8(const uint16_t* dy, const qn_act8* x8, int64_t M,
  *             not decrease or pass `rows`; empty sequences are allowed
  *             (logp 0).  Rows before the first or behind the last sequence
  *             are not counted.
+ *   lse_lo  : device float [rows] or NULL: lse_t minus its fp32 value, written
+ *             by the forward and read by the backward.  Without it all of a
+ *             row's probabilities in the gradient are off by one factor, exp
+ *             of the rounding of lse_t (1 + 2^-24 |lse_t| at ordinary logits,
+ *             nothing of use beside a maximum of 1e9 or a type's lowest).
  * 0 <= rows < 2^24 (logits and labels may be NULL when it is 0),
  * 1 <= nseq < 2^22, 1 <= vocab <= 2^30, ld <= 2^31.
  * A row whose logits hold a NaN or +infinity, or nothing above -infinity,
@@ -555,6 +560,7 @@ typedef struct {
   const int64_t* labels;
   const int64_t* offsets;
   int64_t nseq;
+  float* lse_lo;
 } qn_seq_batch;
 
 /* Workspace of qn_seq_logprob and qn_pref_loss_fwd (host): the partial
@@ -584,7 +590,7 @@ int qn_seq_logprob(const qn_seq_batch* b, float* lse, float* logp,
  * qn_seq_logprob_bwd -- gradient of sum_s dlogp_s logp_s (device):
  *   dl[t][v] = dlogp_s (1[v == label_t] - exp(l[t][v] - lse_t))
  * for counted rows, and 0 for all others.
- * lse     : as written by the forward for this batch.
+ * lse     : as written by the forward for this batch (b->lse_lo too).
  * dlogp   : device float [nseq].
  * dlogits : device, [rows][cols] of dl_dtype (QN_F32 or QN_BF16), row t at
  *           element t * ld_dl (cols >= vocab, ld_dl >= cols); columns from
