@@ -33,7 +33,9 @@ struct AdapterSplit {           // U = scale sum_b src[b] as three bf16 terms
   int r, jt;
   float scale;
   uint16_t* frag;               // [ceil(M / 32)][jt][3][64][8]
-  uint16_t *hi, *lo;            // [M][16 jt] terms 0 and 1, or null
+  uint16_t *hi, *lo;            // [M][ldh] terms 0 and 1, or null
+  int ldh;
+  bool third;                   // term 2 behind hi's r columns (ldh >= 2 r)
   float* full;                  // [M][16 jt] U itself, or null
   uint32_t* zero;               // zero_words words to clear on the way
   int64_t zero_words, total;
@@ -54,9 +56,9 @@ struct ColsReduce {             // out[i] = sum of slices of part[slice][i]
   int slices;
 };
 struct AdapterTranspose {       // dst [n][8 chunks] = src [valid][n]^T, bf16,
-  const uint16_t* src;          // zero past `valid`; chunks 0: nothing to do
-  uint16_t* dst;
-  int valid, n, chunks;
+  const uint16_t* src;          // `copies` of it side by side, zero past them;
+  uint16_t* dst;                // chunks 0: nothing to do
+  int valid, n, chunks, copies;
 };
 struct RowsJob {                // partial G = dY B over slices of N
   const uint16_t *dy, *B;

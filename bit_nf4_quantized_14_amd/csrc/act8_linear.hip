@@ -62,23 +62,26 @@ int linear_bwd_act8(const uint16_t* dy, const qn_act8* x8, int64_t M,
   // small outputs: dX by its own kernels, from A as it is
   const bool gemm = dx != nullptr && !dx_skinny(M, N, K);
   const bool skinny = dx != nullptr && !gemm;
+  // an fp32 dX takes s G in three terms where they fit
+  const int wide = gemm && dx_dtype == QN_F32 ? dx_three_terms(M, r) : 0;
+  const int gw = wide > 0 ? wide : L.rpad;
   // G = dY B: partial sums over slices of dY's columns
   const RowsPlan Pg = rows_plan(M, N, jt);
   launch_adapter_rows(st, RowsJob{dy, B, Mi, Ni, (int)r, Pg.mt, Pg.slices, Pg.steps,
                                   Pg.steps_per, prow});
   // s T and s G in three terms (s G also as dX needs it), A^T padded to
-  // [K][rpad] for the GEMM, the slices of a small dX; the status word
+  // [K][gw] for the GEMM, the slices of a small dX; the status word
   // and the counters of the GEMM's split tiles cleared
   const GemmSplit sp = gemm_split_plan(M, K, N, use_drop);
   float* Gf = reinterpret_cast<float*>(Gh);
   AdapterMid mid{};
   mid.t = AdapterSplit{t_saved, 0, (int)r, 1, M, (int)r, jt, s, UT, nullptr, nullptr,
-                       nullptr, nullptr, 0, 0};
+                       0, false, nullptr, nullptr, 0, 0};
   mid.g = AdapterSplit{prow, (int64_t)M * L.rpad, L.rpad, Pg.slices, M, (int)r, jt, s, UG,
-                       gemm ? Gh : nullptr, Gl, skinny ? Gf : nullptr,
+                       gemm ? Gh : nullptr, Gl, gw, wide > 0, skinny ? Gf : nullptr,
                        reinterpret_cast<uint32_t*>(split_ws),
                        (int64_t)(G_SPLIT_HDR / 4) + 2 * sp.rem, 0};
-  if (gemm) mid.a = AdapterTranspose{A, Atp, (int)r, Ki, L.rpad / 8};
+  if (gemm) mid.a = AdapterTranspose{A, Atp, (int)r, Ki, gw / 8, wide > 0 ? 2 : 1};
   if (skinny) {
     const DxPlan Px = dx_plan(M, N, K);
     mid.dx = DxSkinny{dy, w->packed, w->qabs, w->gscale, Mi, Ni, Ki, Px.cb, Px.slices,
@@ -88,7 +91,7 @@ int linear_bwd_act8(const uint16_t* dy, const qn_act8* x8, int64_t M,
   launch_adapter_mid(st, mid);
   const DropArgs* dp = use_drop ? &da : nullptr;
   if (gemm)
-    launch_gemm<true>(st, dy, w, Gh, Gl, Atp, Mi, L.rpad, dx,
+    launch_gemm<true>(st, dy, w, Gh, Gl, Atp, Mi, gw, dx,
                       (int)(dx_dtype == QN_BF16), dp, split_ws);
   // dB = dY^T (s T), dA = (s G)^T Xr
   const ColsPlan Pb = cols_plan(M, N, K, jt), Pa = cols_plan(M, K, N, jt);

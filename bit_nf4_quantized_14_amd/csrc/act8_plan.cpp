@@ -52,6 +52,7 @@ Act8BwdWorkspace act8_bwd_workspace_layout(int64_t M, int64_t N, int64_t K,
   Act8BwdWorkspace L{};
   const int jt = rank_tiles(r);
   L.rpad = 16 * jt;
+  L.gw = std::max(L.rpad, dx_three_terms(M, r));
   const RowsPlan Pg = rows_plan(M, N, jt);
   const ColsPlan Pb = cols_plan(M, N, K, jt), Pa = cols_plan(M, K, N, jt);
   const size_t frag = size_t(Pb.steps) * jt * 3 * 64 * 16;
@@ -62,9 +63,9 @@ Act8BwdWorkspace act8_bwd_workspace_layout(int64_t M, int64_t N, int64_t K,
     return at;
   };
   L.split = take(gemm_split_bytes(gemm_split_plan(M, K, N, false)));
-  L.atp = take(dx_skinny(M, N, K) ? 0 : size_t(K) * L.rpad * 2);
-  L.gh = take(size_t(M) * L.rpad * 2);
-  L.gl = take(size_t(M) * L.rpad * 2);
+  L.atp = take(dx_skinny(M, N, K) ? 0 : size_t(K) * L.gw * 2);
+  L.gh = take(size_t(M) * L.gw * 2);
+  L.gl = take(size_t(M) * L.gw * 2);
   L.prow = take(size_t(Pg.slices) * M * L.rpad * 4);
   L.ut = take(frag);
   L.ug = take(frag);

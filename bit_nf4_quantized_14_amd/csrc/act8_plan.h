@@ -70,11 +70,25 @@ inline bool act8_bwd_fits(int64_t M, int r) {
   return M < (1LL << 30) / (16 * rank_tiles(r));
 }
 
+// Columns of the dX GEMM's adapter operands.  The GEMM multiplies two bf16
+// terms of s G by A^T: what the two lose (2^-17 of s G) is below a bf16 dX's
+// own rounding but would be the largest error of an fp32 one.  That gets a third
+// term as more columns, [u0 | u2] and [u1 | 0] against [A^T | A^T], 2 r rounded
+// up to 16 (none more up to 8 ranks).  1003 x 1024 x 8192, r = 24: whole
+// backward 47.6 us with two terms, 48.1 us with three, dX's error 4.7e-7 and
+// 1.7e-7 (2048 x 1024 x 320, r = 4: 2.3e-6 and 9.3e-8).  0 where the operand
+// would pass what a buffer resource spans (2 million tokens and more at
+// r = 256): two terms there.
+inline int dx_three_terms(int64_t M, int r) {
+  const int w = 16 * (int)cdiv(2 * r, 16);
+  return M < (1LL << 30) / w ? w : 0;
+}
+
 struct Act8BwdWorkspace {
   size_t split;       // as BwdWorkspace (offset 0)
-  size_t atp;         // bf16 [K, rpad]  A transposed, zero-padded (GEMM)
-  size_t gh, gl;      // bf16 [M, rpad]  two terms of s*G for the dX GEMM, or
-                      // (dx_skinny, at gh) fp32 s*G
+  size_t atp;         // bf16 [K, gw]  A transposed, zero-padded (GEMM)
+  size_t gh, gl;      // bf16 [M, gw]  the terms of s*G for the dX GEMM, or
+                      // (dx_skinny, at gh) fp32 s*G [M, rpad]
   size_t prow;        // fp32 [slices, M, rpad] partial G
   size_t ut, ug;      // bf16 [ceil(M / 32), jt, 3, 64, 8]  s*T, s*G as three
                       // terms in operand order
@@ -83,6 +97,7 @@ struct Act8BwdWorkspace {
   size_t px;          // fp32 [slices, M, K] partial dX (dx_skinny)
   size_t total;
   int32_t rpad;
+  int32_t gw;         // rpad, or dx_three_terms where that is more
 };
 Act8BwdWorkspace act8_bwd_workspace_layout(int64_t M, int64_t N, int64_t K,
                                            int32_t r);

@@ -50,29 +50,45 @@ __device__ __forceinline__ void split_thread(const AdapterSplit& p, int64_t idx)
   uint16_t* out = p.frag + (((step * p.jt + t) * 3) * 64 + lane) * 8 + i;
   float x = p.scale * v;
   if (p.full != nullptr && m < p.M) p.full[m * 16 * p.jt + j] = x;
+  uint16_t u[3];
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
-    const uint16_t u = (uint16_t)(pack_bf16x2(x, 0.0f) & 0xFFFFu);
-    x -= bf16_to_f32(u);
-    out[512 * k] = u;
-    if (p.hi != nullptr && k < 2 && m < p.M)
-      (k == 0 ? p.hi : p.lo)[m * 16 * p.jt + j] = u;
+    u[k] = (uint16_t)(pack_bf16x2(x, 0.0f) & 0xFFFFu);
+    x -= bf16_to_f32(u[k]);
+    out[512 * k] = u[k];
+  }
+  if (p.hi == nullptr || m >= p.M) return;
+  uint16_t *hi = p.hi + m * p.ldh, *lo = p.lo + m * p.ldh;
+  if (!p.third || j < p.r) {
+    hi[j] = u[0];
+    lo[j] = u[1];
+  }
+  if (p.third) {                     // [u0 | u2 | 0] and [u1 | 0 | 0]
+    if (j < p.r) {
+      hi[p.r + j] = u[2];
+      lo[p.r + j] = 0;
+    }
+    if (j < p.ldh - 2 * p.r) hi[2 * p.r + j] = lo[2 * p.r + j] = 0;
   }
 }
 
-// dst[row][0 .. 8 chunks) = src transposed, zero past src's rows: a thread
-// gathers 8 elements of one column of src [valid][n] (neighbouring threads
-// neighbouring columns) and writes them as one chunk of dst's row.
+// dst[row][0 .. 8 chunks) = src transposed (twice side by side with two
+// copies), zero past its rows: a thread gathers 8 elements of one column of src
+// [valid][n] (neighbouring threads neighbouring columns) and writes them as one
+// chunk of dst's row.
 __device__ __forceinline__ void transpose_thread(const AdapterTranspose& p, int64_t idx) {
   if (idx >= (int64_t)p.chunks * p.n) return;
   const int ch = (int)(idx / p.n), col = (int)(idx - (int64_t)ch * p.n);
   u32x4 w;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int a = 8 * ch + 2 * i, b = a + 1;
-    const uint32_t x = a < p.valid ? p.src[(int64_t)a * p.n + col] : 0u;
-    const uint32_t y = b < p.valid ? p.src[(int64_t)b * p.n + col] : 0u;
-    w[i] = x | (y << 16);
+    uint32_t x[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int j = 8 * ch + 2 * i + k, row = j < p.valid ? j : j - p.valid;
+      x[k] = j < p.copies * p.valid ? p.src[(int64_t)row * p.n + col] : 0u;
+    }
+    w[i] = x[0] | (x[1] << 16);
   }
   reinterpret_cast<u32x4*>(p.dst)[(int64_t)col * p.chunks + ch] = w;
 }

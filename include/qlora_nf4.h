@@ -508,6 +508,10 @@ int qn_act8_decode(const qn_act8* x8, void* y, int32_t y_dtype, void* stream);
  * drop : NULL or p == 0 for no dropout.
  * ws   : ws_bytes >= qlora_bwd_act8_workspace_bytes(M, N, K, r), 16-byte
  *        aligned, with its status word as in qlora_linear_bwd.
+ * Accuracy: products of bf16 in fp32 sums, s T and s G as three bf16 terms
+ * (2^-26 of them lost); for a bf16 dX of more than a few tokens s G in two
+ * (2^-17, below that output's rounding), and so for an fp32 dX where
+ * M * 16 ceil(r / 8) >= 2^30 (2 million tokens and more at r = 256).
  * M times r (rounded up to 16, 32, 64, 128 or 256) must be below 2^30.
  * Other arguments, shape rules and errors as qlora_linear_bwd.
  */
