@@ -554,8 +554,13 @@ int qlora_linear_bwd_act8(const uint16_t* dy, const qn_act8* x8, int64_t M,
  * 0 <= rows < 2^24 (logits and labels may be NULL when it is 0),
  * 1 <= nseq < 2^22, 1 <= vocab <= 2^30, ld <= 2^31.
  * A row whose logits hold a NaN or +infinity, or nothing above -infinity,
- * has no log-probability: its sequence's logp, the loss and the gradient of
- * that row are NaN (or infinite where only the label's logit is -infinity).
+ * has no log-probability: its own gradient, its sequence's logp and its pair's
+ * loss and dlogp (so the gradient of every counted row of the pair) are NaN.
+ * A label at -infinity in a row that has others makes logp -infinity and
+ * leaves the row's gradient finite.  The loss of its pair is +infinity if it
+ * is the chosen sequence's; if the rejected one's, 0 without label smoothing
+ * and +infinity with it; dlogp is at its finite limit in both.  With such a
+ * label in both sequences the loss and dlogp are NaN.
  */
 typedef struct {
   const void* logits;
