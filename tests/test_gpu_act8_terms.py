@@ -90,3 +90,38 @@ def test_a_bf16_dx_is_the_rounded_one(m, n, k, r):
     """One rounding to bf16, of a value that two terms leave within 2^-17."""
     name, err, _, ref = next(_run(m, n, k, r, dx_dtype=capi.QN_BF16))
     assert name == "dX" and np.all(err <= np.abs(ref) * (2.0 ** -8 + 2.0 ** -16))
+
+
+@pytest.mark.parametrize("m,two", [((1 << 21) - 1, False), (1 << 21, True)])
+def test_as_many_tokens_as_a_buffer_resource_spans(m, two):
+    """The last number of tokens whose third term fits at r = 256, and the first
+    that goes without it: 2^-17 of s G may be lost there."""
+    n, k, r = 8, 64, 256
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    at = torch.arange(m, device="cuda")
+    dy = torch.zeros((m, n), **bf)
+    dy[at, at % n] = 1.0
+    x = torch.zeros((m, k), **bf)
+    x[at, at % k] = 1.0
+    a = torch.zeros((r, k), **bf)
+    a[torch.arange(k, device="cuda") * 3 + 1, torch.arange(k, device="cuda")] = 1.0
+    b = torch.randn((n, r), device="cuda", generator=g).bfloat16()
+    ts = torch.ones((m, r), device="cuda")
+    w = capi.nf4_quantize(torch.zeros((n, k), device="cuda"))
+    x8 = capi.qn_act8_encode(x)
+    dx, da, db = capi.qlora_linear_bwd_act8(dy, x8, w, a, b, r, ALPHA, ts)
+    torch.cuda.synchronize()
+    s = float(np.float32(ALPHA) / np.float32(r))
+    sg = s * b.double()                                   # s G of token m: row m % n
+    for first in range(0, m, 1 << 18):                    # a quarter million tokens at a time
+        rows = at[first:first + (1 << 18)]
+        want = sg[rows % n][:, 1:3 * k:3]
+        err = (dx[rows].double() - want).abs() / want.abs()
+        assert float(err.max()) <= (2.0 ** -17 + 4 * U if two else 8 * U), first
+    # sums of `count` equal terms: every addition may lose u of the sum
+    count = torch.bincount(at % k, minlength=k).double()
+    want = (sg.t()[:, torch.arange(k, device="cuda") % n] * count)
+    assert bool(((da.double() - want).abs() <= want.abs() * (m // k) * U).all())
+    count = torch.bincount(at % n, minlength=n).double()
+    assert bool(((db.double() - s * count[:, None]).abs() <= s * count[:, None] * (m // n) * U).all())
