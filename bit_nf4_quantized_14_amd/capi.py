@@ -916,27 +916,24 @@ def _seq_batch(fn: str, logits, labels, offsets):
         _tensor(fn, "offsets", offsets, n, torch.int64, index), n[0] - 1)
 
 
-def _seq_buffers(fn, b, like, names, given, sizes, ws, index):
-    """(tensors, addresses, workspace address, bytes, what keeps the workspace
-    alive) of a forward's fp32 outputs, `sizes` elements each.  Outputs and
-    workspace come from one allocation unless the caller brings any."""
+def _seq_output(fn, name, t, like, n, index):
+    """(tensor, address) of an fp32 output of n elements: the one given, or a
+    new one with memory of its own."""
     import torch
-    f32 = torch.float32
-    nw = qn_seq_workspace_bytes(b.rows, b.vocab, b.nseq) if ws is None else 0
-    if ws is None and not any(t is not None for t in given):
-        buf = like.new_empty(nw // 4 + sum(sizes), dtype=f32)
-        base = at = buf.data_ptr()
-        at += nw
-        ptrs = []
-        for n in sizes:
-            ptrs.append(at)
-            at += 4 * n
-        return buf.split_with_sizes([nw // 4, *sizes])[1:], ptrs, base, nw, buf
-    outs = [like.new_empty(n, dtype=f32) if t is None else t for t, n in zip(given, sizes)]
-    ptrs = [_tensor(fn, k, t, (n,), f32, index) for k, t, n in zip(names, outs, sizes)]
-    if ws is None:
-        ws = like.new_empty(nw, dtype=torch.uint8)
-    return outs, ptrs, *_workspace(fn, ws, index), ws
+    if t is not None:
+        return t, _tensor(fn, name, t, (n,), torch.float32, index)
+    t = like.new_empty(n, dtype=torch.float32)
+    return t, t.data_ptr()
+
+
+def _seq_workspace(fn, b, like, ws, index):
+    """(address, bytes, what keeps it alive) of a forward's workspace."""
+    import torch
+    if ws is not None:
+        return *_workspace(fn, ws, index), ws
+    nw = qn_seq_workspace_bytes(b.rows, b.vocab, b.nseq)
+    ws = like.new_empty(nw, dtype=torch.uint8)
+    return ws.data_ptr(), nw, ws
 
 
 def _status_ptr(fn, status, index):
@@ -960,11 +957,11 @@ def qn_seq_logprob(logits, labels, offsets, lse=None, logp=None, status=None,
     _set_lse_lo(fn, b, lse_lo, index)
 
     def body(st):
-        o, p, pw, nw, _keep = _seq_buffers(fn, b, logits, ("logp", "lse"), (logp, lse),
-                                           (b.nseq, b.rows), ws, index)
-        _check(fn, lib().qn_seq_logprob(b, p[1], p[0], _status_ptr(fn, status, index), pw, nw,
-                                        st))
-        return tuple(o)
+        lp, plp = _seq_output(fn, "logp", logp, logits, b.nseq, index)
+        ls, pls = _seq_output(fn, "lse", lse, logits, b.rows, index)
+        pw, nw, _keep = _seq_workspace(fn, b, logits, ws, index)
+        _check(fn, lib().qn_seq_logprob(b, pls, plp, _status_ptr(fn, status, index), pw, nw, st))
+        return lp, ls
     return _run_on(index, stream, body)
 
 
@@ -972,7 +969,8 @@ def qn_seq_logprob(logits, labels, offsets, lse=None, logp=None, status=None,
 class PrefLoss:
     """Outputs of qn_pref_loss_fwd: loss [P], logp [2P], dlogp [2P] (the
     derivative of a pair's loss by its sequences' logp), lse [rows] and lse_lo
-    [rows] (what lse loses by its rounding)."""
+    [rows] (what lse loses by its rounding).  Those of a call without `out`
+    share one allocation."""
     loss: "object"
     logp: "object"
     dlogp: "object"
@@ -996,11 +994,16 @@ def qn_pref_loss_fwd(logits, labels, offsets, ref_logp, beta: float,
     pr = None if ref_logp is None else _tensor(fn, "ref_logp", ref_logp, (nseq,), f32, index)
 
     def body(st):
-        given = ((None,) * 5 if out is None
-                 else (out.loss, out.logp, out.dlogp, out.lse, out.lse_lo))
-        o, p, pw, nw, _keep = _seq_buffers(
-            fn, b, logits, ("loss", "logp", "dlogp", "lse", "lse_lo"), given,
-            (pairs, nseq, nseq, rows, rows), ws, index)
+        sizes = (pairs, nseq, nseq, rows, rows)
+        if out is None:              # the fields of one result: one allocation
+            buf = logits.new_empty(pairs + 2 * (nseq + rows), dtype=f32)
+            o, p = buf.split_with_sizes(sizes), [buf.data_ptr()]
+            for n in sizes[:-1]:
+                p.append(p[-1] + 4 * n)
+        else:
+            o, p = zip(*(_seq_output(fn, k, getattr(out, k), logits, n, index) for k, n in
+                         zip(("loss", "logp", "dlogp", "lse", "lse_lo"), sizes)))
+        pw, nw, _keep = _seq_workspace(fn, b, logits, ws, index)
         b.lse_lo = p[4]
         _check(fn, lib().qn_pref_loss_fwd(
             b, pr, _PrefHP(float(beta), float(label_smoothing)), p[3], p[1], p[0], p[2],
