@@ -384,11 +384,16 @@ struct SeqBwdArgs {
 
 // Non-temporal (NT) stores leave the caches to others.  A gradient of 64 MB
 // and more does not stay in them until it is read.  Forward and backward with
-// plain and with these stores, 32000 words, alone and with a pass behind them
-// that reads the gradient: 250 MB 167 and 137 us, 253 and 236 us; 125 MB 89
-// and 74 us, 130 and 124 us; 500 MB 320 and 306 us, 486 and 492 us.  At 31 MB
-// they gained nothing alone and lost 2 us with the pass behind, so smaller
-// gradients are stored plainly.
+// plain and with NT stores, 32000 words, bf16, alone / with the head's adapter
+// gradients behind them (4096 columns, dY read twice) / with those and dX:
+//     32 MB    31, 29 /   61,   61 /  261,  263 us
+//     65 MB    48, 43 /   93,   94 /  434,  434 us
+//    131 MB    90, 76 /  154,  155 /  791,  802 us
+//    262 MB   171,142 /  293,  286 / 1215, 1210 us
+//    524 MB   321,305 /  579,  571 / 2440, 2435 us
+//   1048 MB   609,592 / 1127, 1113 / 4843, 4837 us
+// So there is no upper end; the one reader that loses from 393 MB on is a plain
+// copy of the gradient (524 MB: 488 and 491 us).  Below 64 MB plain stores.
 constexpr int64_t SQ_NT_BYTES = 64 << 20;
 
 template <bool NT, typename V>
