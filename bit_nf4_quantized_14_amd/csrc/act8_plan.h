@@ -56,6 +56,17 @@ RowsPlan rows_plan(int64_t M, int64_t N, int jt);
 //             48.5 us, 256 x 2048 x 4096 36.3 and 37.4 us, but 256 x 1024 x
 //             4096 32.2 and 31.6 us;
 //   96 tiles: 384 x 4096 x 4096 60.3 and 52.9 us.
+// With dropout the GEMM does not split its tiles (GemmSplit), so this one wins
+// wherever the rule takes it, and would further on (p = 0.1, this and the GEMM):
+//   32 tiles: 128 x 1024 x 4096 30 and 34 us, 128 x 4096 x 4096 34 and 67 us,
+//             4096 x 4096 x 128 51 and 87 us;
+//   64 tiles: 256 x 1024 x 4096 35 and 37 us, 256 x 4096 x 4096 45 and 70 us,
+//             2048 x 8192 x 512 76 and 132 us;
+//   96 tiles: 384 x 1024 x 4096 43 and 40 us, 384 x 4096 x 4096 64 and 73 us;
+//  128 tiles: 512 x 4096 x 4096 70 and 73 us, 2048 x 4096 x 1024 79 and 80 us;
+//  192 tiles: 768 x 4096 x 4096 115 and 74 us.
+// The rule is the same for both, as the workspace's size does not ask for
+// dropout and would have to hold the slices of dX for shapes that use none.
 constexpr int64_t DX_SKINNY_M = 64;
 bool dx_skinny(int64_t M, int64_t N, int64_t K);
 constexpr int64_t DX_WGS = G_CUS;
