@@ -43,24 +43,27 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 # entry points that pick the launches.
 COMMON_SOURCES = ("qn_device.h", "qn_host.h", "qn_internal.h", "plan.cpp",
                   "linear.hip")
-# kernel name prefix -> the source that defines its body
+# kernel name prefix -> the source that defines its body, and with it those
+# that shape this kernel's launches alone
 KERNEL_SOURCES = (("k_gemm", "gemm.hip"), ("k_fwd_gemm", "gemm.hip"),
                   ("k_bwd_dx_gemm", "gemm.hip"), ("k_rank", "rank.hip"),
                   ("k_dequant", "codec.hip"), ("k_quantize", "codec.hip"),
                   ("k_skinny", "skinny.hip"), ("k_merge", "merge.hip"),
-                  ("k_adamw8", "adamw.hip"), ("k_act8", "act8.hip"),
-                  ("k_adapter", "adapter8.hip"), ("k_seq", "pref.hip"))
+                  ("k_adamw8", "adamw.hip"),
+                  ("k_act8", "act8.hip", "act8_code.h", "act8_host.h"),
+                  ("k_adapter", "adapter8.hip", "act8_host.h", "act8_linear.hip",
+                   "act8_plan.cpp", "act8_plan.h"), ("k_seq", "pref.hip"))
 
 COPY_BYTES = 256 << 20   # bench.py --calibrate-copy: one 256 MiB copy
 
 
 def source_sha(kernel: str) -> str | None:
-    """sha256[:16] over the common sources and the kernel's own source, or
+    """sha256[:16] over the common sources and the kernel's own sources, or
     None for a kernel this library does not define."""
-    for prefix, fname in KERNEL_SOURCES:
+    for prefix, *own in KERNEL_SOURCES:
         if kernel.startswith(prefix):
             h = hashlib.sha256()
-            for f in COMMON_SOURCES + (fname,):
+            for f in (*COMMON_SOURCES, *own):
                 with open(os.path.join(CSRC, f), "rb") as fh:
                     h.update(fh.read())
             return h.hexdigest()[:16]
