@@ -464,7 +464,10 @@ int qlora_linear_bwd_dropout(const uint16_t* dy, const uint16_t* x,
  *   - a < 2^-100: scale 0 and codes 0;
  *   - a block with an infinity or a NaN: scale NaN and codes 0, so the whole
  *     block comes back as NaN and the fault stays visible.
- * Restored value: fp32(code * scale), or that rounded to bf16 (RNE).
+ * Restored value: fp32(code * scale), or that rounded to bf16 (RNE).  The
+ * scale's rounding can carry it past the largest finite value: fp32 magnitudes
+ * in the last step below 2^128 may come back as infinities, and in bf16 those
+ * above its largest do.
  */
 typedef struct {
   int8_t* codes;    /* device, [rows][cols] row-major */
@@ -511,7 +514,9 @@ int qn_act8_decode(const qn_act8* x8, void* y, int32_t y_dtype, void* stream);
  * Accuracy: products of bf16 in fp32 sums, s T and s G as three bf16 terms
  * (2^-26 of them lost); for a bf16 dX of more than a few tokens s G in two
  * (2^-17, below that output's rounding), and so for an fp32 dX where
- * M * 16 ceil(r / 8) >= 2^30 (2 million tokens and more at r = 256).
+ * M * 16 ceil(r / 8) >= 2^30 (2 million tokens and more at r = 256).  An
+ * infinity in dy or t_saved makes the gradients it reaches infinite or NaN (a
+ * term that is 0 may meet it).
  * M times r (rounded up to 16, 32, 64, 128 or 256) must be below 2^30.
  * Other arguments, shape rules and errors as qlora_linear_bwd.
  */

@@ -9,6 +9,8 @@ import torch
 from oracle import act8 as a8
 from bit_nf4_quantized_14_amd import capi
 
+from gpu_util import bits_host
+
 pytestmark = pytest.mark.gpu
 
 
@@ -41,3 +43,25 @@ def test_codes_next_to_half_steps(low, high):
     assert np.array_equal(t.scale.cpu().numpy().view(np.uint32), scale.view(np.uint32))
     if low == -100:
         assert codes[0, 1] == 1 and codes[1, 1] == 8
+
+
+def test_the_largest_magnitudes_restored():
+    """The largest fp32 and its neighbours, and what bf16 holds of them: bit for
+    bit with the oracle, whose product passes the largest finite value there."""
+    top = np.float32(3.4028234663852886e38)
+    near = np.array([top, np.nextafter(top, np.float32(0)), np.float32(3.3895314e38),
+                     np.float32(3.3961775e38), np.float32(1.7e38)], np.float32)
+    x = np.zeros((len(near), 130), np.float32)
+    x[:, 0], x[:, 70], x[:, 129] = near, -near, near
+    t = capi.qn_act8_encode(torch.from_numpy(x).cuda())
+    yf = capi.qn_act8_decode(t, dtype=capi.QN_F32)
+    yb = capi.qn_act8_decode(t)
+    torch.cuda.synchronize()
+    with np.errstate(over="ignore"):
+        codes, scale = a8.encode(x)
+        assert np.array_equal(t.codes.cpu().numpy(), codes)
+        assert np.array_equal(yf.cpu().numpy(), a8.decode_f32(codes, scale))
+        assert np.array_equal(bits_host(yb), a8.decode_bf16_bits(codes, scale))
+    assert np.isinf(yf.cpu().numpy()[0, 0]) and np.isfinite(yf.cpu().numpy()[2:]).all()
+    # bf16's largest comes back as itself
+    assert bool((yb[2, [0, 70, 129]].float().abs().cpu() == 3.3895313892515355e38).all())
