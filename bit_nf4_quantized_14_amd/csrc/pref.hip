@@ -192,10 +192,10 @@ __device__ __forceinline__ double sq_token(double hit, float m, double l) {
 }
 
 // Maximum and sum of one chunk of one row by TEAM threads.  Rows that are not
-// counted are not read.  Each thread keeps SQ_GROUPS 16-byte loads in flight; the last
-// round (one group at a time where at most half of the groups are left)
-// reads a group from the end of the chunk where it would pass it, and drops
-// what another thread has.
+// counted are not read.  Each thread keeps SQ_GROUPS 16-byte loads in flight;
+// the last round (one group at a time where at most half of the groups are
+// left) reads a group from the end of the chunk where it would pass it, and
+// drops what another thread has.
 template <bool F32, int TEAM>
 __global__ __launch_bounds__(SQ_THREADS) void k_seq_rows(SeqArgs a, SeqPart* __restrict__ ws,
                                                          float* __restrict__ lse) {

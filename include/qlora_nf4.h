@@ -551,8 +551,9 @@ int qlora_linear_bwd_act8(const uint16_t* dy, const qn_act8* x8, int64_t M,
  *             not decrease or pass `rows`; empty sequences are allowed
  *             (logp 0).  Rows before the first or behind the last sequence
  *             are not counted.
- *   lse_lo  : device float [rows] or NULL: lse_t minus its fp32 value, written
- *             by the forward and read by the backward.  Without it all of a
+ *   lse_lo  : device float [rows] or NULL: lse_t minus its fp32 value (0 for
+ *             rows that are not counted), written by the forward and read by
+ *             the backward.  Without it all of a
  *             row's probabilities in the gradient are off by one factor, exp
  *             of the rounding of lse_t (1 + 2^-24 |lse_t| at ordinary logits,
  *             nothing of use beside a maximum of 1e9 or a type's lowest).
