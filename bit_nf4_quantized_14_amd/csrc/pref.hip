@@ -12,11 +12,12 @@
 // the two passes cannot be one.
 //
 // Measured (MI355X; a 256 MB copy moves 5.4 TB/s), 8 pairs, 4109 tokens of
-// which 2745 count, 32000 words, bf16: maximum and sum 36 us (176 MB, 4.8
+// which 2745 count, 32000 words, bf16: maximum and sum 37 us (176 MB, 4.7
 // TB/s), sequences and loss 4.6 us, gradient 75 us (176 MB read, 263 MB
-// written, 5.8 TB/s); fp32 logits of 128256 words, 2508 tokens: 153 us (5.6
-// TB/s) and, with a bf16 gradient, 310 us (4.9 TB/s).  Below some MB the
-// three launches' own time is what is left: 3.5 + 3.5 us for 24 tokens.
+// written, 5.8 TB/s); fp32 logits of 128256 words, 2508 tokens: 152 us (5.6
+// TB/s) and, with a bf16 gradient, 311 us (4.9 TB/s).  Below some MB the
+// three launches' own time is what is left: 3.6 + 3.4 us for 24 tokens.
+// The double steps and the two-number log2 e of the sums cost 0.5 us of the 37.
 #include <cmath>
 
 #include "qn_host.h"
@@ -38,6 +39,7 @@ constexpr int64_t SQ_WAVE_BYTES = 12 << 10;
 // the bf16 case 1% longer, with 8 nothing less
 constexpr int SQ_GROUPS = 4;
 constexpr float SQ_LOG2E = 1.4426950408889634f;
+constexpr float SQ_LOG2E_LO = 1.925963e-8f;    // log2 e - SQ_LOG2E
 constexpr float SQ_NEG_INF = -__builtin_inff();
 
 // Eight consecutive logits from element c of a row, all of them inside it.
@@ -84,15 +86,12 @@ __device__ __forceinline__ void sq_load(const char* row, int c, int vocab, float
   }
 }
 
-// A thread's running maximum m and s = sum exp(x - m).  m starts at -infinity,
-// where the shift is taken as 0 so that no infinity meets its own.
-struct MaxSum {
-  float m, s;
-};
-
-// The same of several threads, with the sum in double: the maximum's own term
-// is 1, and where a label holds nearly all of the probability the rest, which
-// is its gradient, is far below fp32's step there.
+// A running maximum m and s = sum exp(x - m).  m starts at -infinity, where the
+// shift is taken as 0 so that no infinity meets its own.  s is in double: the
+// maximum's own term is 1, and where a label holds nearly all of the probability
+// the rest, which is its gradient, is far below fp32's step there; and fp32 sums
+// of many terms from few bf16 logits round one way (3e-8 of the sum at 128256
+// words), in every row alike.
 struct RowSum {
   float m;
   double s;
@@ -100,8 +99,11 @@ struct RowSum {
 
 __device__ __forceinline__ float sq_shift(float m) { return m == SQ_NEG_INF ? 0.0f : m; }
 
+// exp(x) = 2^(x log2 e), rounded once before the power.  With log2 e as one fp32
+// number every term of a sum came out too large by 1.3e-8 |x|: 3e-8 to 1e-7 of
+// a row's sum, and the same sign in every row of a sequence.
 __device__ __forceinline__ float sq_exp(float x) {
-  return __builtin_amdgcn_exp2f(x * SQ_LOG2E);
+  return __builtin_amdgcn_exp2f(fmaf(x, SQ_LOG2E, x * SQ_LOG2E_LO));
 }
 
 // r's sum for a maximum m that is not below its own.
@@ -162,20 +164,21 @@ __device__ __forceinline__ void sq_put_lse(const SeqArgs& a, float* __restrict__
   if (a.lse_lo != nullptr) a.lse_lo[row] = (float)(((double)m - (double)hi) + l);
 }
 
-// Adds logits to a running maximum and sum.
+// Adds logits to a running maximum and sum: N terms in two fp32 chains from
+// zero, then one step in double.
 template <int N>
-__device__ __forceinline__ void sq_add(MaxSum& r, const float (&v)[N]) {
+__device__ __forceinline__ void sq_add(RowSum& r, const float (&v)[N]) {
   float m = r.m;
 #pragma unroll
   for (int i = 0; i < N; ++i) m = fmaxf(m, v[i]);
   const float z = sq_shift(m);
-  float s = r.s * sq_exp(r.m - z), s2 = 0.0f;
+  float s = 0.0f, s2 = 0.0f;
 #pragma unroll
   for (int i = 0; i < N; i += 2) {
     s += sq_exp(v[i] - z);
     s2 += sq_exp(v[i + 1] - z);
   }
-  r = MaxSum{m, s + s2};
+  r = RowSum{m, sq_scaled(r, m) + ((double)s + (double)s2)};
 }
 
 template <bool F32>
@@ -218,14 +221,14 @@ __global__ __launch_bounds__(SQ_THREADS) void k_seq_rows(SeqArgs a, SeqPart* __r
   }
   const char* p = a.logits + (int64_t)row * a.ld * (F32 ? 4 : 2);
   const int begin = ch * a.chunk, end = min(a.vocab, begin + a.chunk);
-  MaxSum mine{SQ_NEG_INF, 0.0f};
+  RowSum r{SQ_NEG_INF, 0.0};
   int c = begin + 8 * tid;
   int at = begin;
   for (; at + G * STEP <= end; at += G * STEP, c += G * STEP) {
     float v[8 * G];
 #pragma unroll
     for (int g = 0; g < G; ++g) sq_load8<F32>(p, c + g * STEP, v + 8 * g);
-    sq_add(mine, v);
+    sq_add(r, v);
   }
   if (end - begin >= 8) {
     for (; at < end && end - at <= STEP * (G / 2); at += STEP, c += STEP) {
@@ -234,7 +237,7 @@ __global__ __launch_bounds__(SQ_THREADS) void k_seq_rows(SeqArgs a, SeqPart* __r
       const int skip = c - (end - 8);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = i >= skip ? v[i] : SQ_NEG_INF;
-      sq_add(mine, v);
+      sq_add(r, v);
     }
     if (at < end) {
       float v[8 * G];
@@ -247,14 +250,14 @@ __global__ __launch_bounds__(SQ_THREADS) void k_seq_rows(SeqArgs a, SeqPart* __r
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[8 * g + i] = i >= skip ? v[8 * g + i] : SQ_NEG_INF;
       }
-      sq_add(mine, v);
+      sq_add(r, v);
     }
   } else {                             // a vocabulary of fewer than 8 words
     float v[8];
     sq_load<F32>(p, c, end, v);
-    sq_add(mine, v);
+    sq_add(r, v);
   }
-  RowSum r = sq_join_lanes(RowSum{mine.m, (double)mine.s}, 6);
+  r = sq_join_lanes(r, 6);
   if constexpr (TEAM == SQ_THREADS) {
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = r;
     __syncthreads();
