@@ -39,7 +39,9 @@ EXPORTS = ("nf4_codebook", "nf4_quantize", "nf4_dequantize",
            "qn_act8_encode", "qn_act8_decode", "qlora_linear_bwd_act8",
            "qlora_bwd_act8_workspace_bytes",
            "qn_seq_workspace_bytes", "qn_seq_logprob", "qn_seq_logprob_bwd",
-           "qn_pref_loss_fwd", "qn_pref_loss_bwd")
+           "qn_pref_loss_fwd", "qn_pref_loss_bwd",
+           "qn_head_fwd_workspace_bytes", "qn_head_bwd_workspace_bytes",
+           "qn_head_loss_fwd", "qn_head_loss_bwd")
 QN_FWD_BATCH_MAX = 8
 QN_DEQUANT_BATCH_MAX = 16
 QN_CODE_NF4, QN_CODE_FP4, QN_CODE_INT4 = 0, 1, 2
@@ -100,6 +102,12 @@ class _SeqBatch(ctypes.Structure):
 
 class _PrefHP(ctypes.Structure):
     _fields_ = [("beta", ctypes.c_double), ("label_smoothing", ctypes.c_double)]
+
+
+class _Head(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("w", ctypes.c_void_p),
+                ("labels", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("dim", ctypes.c_int64), ("vocab", ctypes.c_int64)]
 
 
 _lib = None
@@ -211,6 +219,15 @@ def lib() -> ctypes.CDLL:
     L.qn_pref_loss_fwd.restype = ctypes.c_int
     L.qn_pref_loss_bwd.argtypes = [bp, vp, vp, vp, vp, i32, i64, i64, vp]
     L.qn_pref_loss_bwd.restype = ctypes.c_int
+    hdp, sz = ctypes.POINTER(_Head), ctypes.c_size_t
+    L.qn_head_fwd_workspace_bytes.argtypes = [i64, i64, i64]
+    L.qn_head_fwd_workspace_bytes.restype = sz
+    L.qn_head_bwd_workspace_bytes.argtypes = [i64, i64, i64, i32, i32]
+    L.qn_head_bwd_workspace_bytes.restype = sz
+    L.qn_head_loss_fwd.argtypes = [hdp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.qn_head_loss_fwd.restype = ctypes.c_int
+    L.qn_head_loss_bwd.argtypes = [hdp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.qn_head_loss_bwd.restype = ctypes.c_int
     L.qn_profile_kernel.argtypes = [ctypes.c_char_p, vp, vp, i32]
     L.qn_profile_kernel.restype = ctypes.c_int
     L.qn_strerror.argtypes = [ctypes.c_int]
@@ -1069,6 +1086,125 @@ def qn_pref_loss_bwd(logits, labels, offsets, fwd: PrefLoss, dloss=None,
     qn_seq_logprob_bwd."""
     return _seq_bwd("qn_pref_loss_bwd", logits, labels, offsets, fwd.lse, fwd.lse_lo, fwd.dlogp,
                     dloss, dlogits, dl_dtype, stream)
+
+
+# ---------------------------------------------------------------------------
+# Cross entropy of a vocabulary head
+# ---------------------------------------------------------------------------
+
+@dataclass
+class HeadLoss:
+    """Outputs of qn_head_loss_fwd: loss [rows], lse [rows], mean [2] (mean
+    loss of the counted rows, and their number) and lse_lo [rows] (what lse
+    loses by its rounding).  Those of a call without `out` share one
+    allocation."""
+    loss: "object"
+    lse: "object"
+    mean: "object" = None
+    lse_lo: "object" = None
+
+
+def qn_head_fwd_workspace_bytes(rows: int, dim: int, vocab: int) -> int:
+    return int(lib().qn_head_fwd_workspace_bytes(rows, dim, vocab))
+
+
+def qn_head_bwd_workspace_bytes(rows: int, dim: int, vocab: int, need_dx: bool = True,
+                                need_dw: bool = False) -> int:
+    return int(lib().qn_head_bwd_workspace_bytes(rows, dim, vocab, int(need_dx), int(need_dw)))
+
+
+def _head(fn: str, x, w, labels):
+    """(device index, qn_head) of x [rows, dim], w [vocab, dim], labels [rows]."""
+    import torch
+    index = _gpu(fn, "x", x)
+    xs, wsh = x.shape, w.shape
+    if len(xs) != 2 or len(wsh) != 2 or xs[1] != wsh[1] or wsh[0] < 1:
+        raise _bad(fn, "x must be [rows, dim], w [vocab, dim]")
+    bf = torch.bfloat16
+    return index, _Head(_tensor(fn, "x", x, xs, bf, index), _tensor(fn, "w", w, wsh, bf, index),
+                        _tensor(fn, "labels", labels, (xs[0],), torch.int64, index),
+                        xs[0], xs[1], wsh[0])
+
+
+def _head_workspace(fn: str, ws, like, index: int, need: int):
+    """(address, bytes, what keeps it alive); need 0: sizes out of range."""
+    import torch
+    if need == 0:
+        raise _bad(fn, "rows, dim or vocab out of range")
+    if ws is not None:
+        return *_workspace(fn, ws, index), ws
+    ws = like.new_empty(need, dtype=torch.uint8)
+    return ws.data_ptr(), need, ws
+
+
+def qn_head_loss_fwd(x, w, labels, out: HeadLoss | None = None, status=None, ws=None,
+                     stream=None):
+    """Cross entropy of labels [rows] (int64; negative: not counted) under the
+    logits x @ w.T of hidden states x [rows, dim] and a head w [vocab, dim],
+    both bf16; returns a HeadLoss (`out` when it is given; its fields that are
+    None are allocated and set)."""
+    import torch
+    fn = "qn_head_loss_fwd"
+    index, h = _head(fn, x, w, labels)
+    f32, rows = torch.float32, h.rows
+
+    def body(st):
+        sizes = (rows, rows, 2, rows)
+        pw, nw, _keep = _head_workspace(fn, ws, x, index, qn_head_fwd_workspace_bytes(
+            rows, h.dim, h.vocab))
+        if out is None:              # the fields of one result: one allocation
+            buf = x.new_empty(3 * rows + 2, dtype=f32)
+            o, p = buf.split_with_sizes(sizes), [buf.data_ptr()]
+            for n in sizes[:-1]:
+                p.append(p[-1] + 4 * n)
+        else:
+            o, p = zip(*(_seq_output(fn, k, getattr(out, k), x, n, index) for k, n in
+                         zip(("loss", "lse", "mean", "lse_lo"), sizes)))
+        _check(fn, lib().qn_head_loss_fwd(h, p[0], p[1], p[3], p[2],
+                                          _status_ptr(fn, status, index), pw, nw, st))
+        if out is None:
+            return HeadLoss(*o)
+        out.loss, out.lse, out.mean, out.lse_lo = o
+        return out
+    return _run_on(index, stream, body)
+
+
+def qn_head_loss_bwd(x, w, labels, fwd: HeadLoss, dloss=None, dx=None, need_dx: bool = True,
+                     dw=None, need_dw: bool = False, ws=None, stream=None):
+    """Gradient of sum(dloss * loss) (dloss None: the mean loss) from what
+    qn_head_loss_fwd returned: (dx [rows, dim], dw [vocab, dim]) in bf16, None
+    where it is neither given nor needed."""
+    import torch
+    fn = "qn_head_loss_bwd"
+    index, h = _head(fn, x, w, labels)
+    f32, bf, rows = torch.float32, torch.bfloat16, h.rows
+    if dx is not None and not need_dx:
+        raise _bad(fn, "dx given with need_dx=False")
+    need_dw = need_dw or dw is not None
+    if not need_dx and not need_dw:
+        raise _bad(fn, "no gradient is asked for")
+    plo = fwd.lse_lo
+    args = [_tensor(fn, "loss", fwd.loss, (rows,), f32, index),
+            _tensor(fn, "lse", fwd.lse, (rows,), f32, index),
+            None if plo is None else _tensor(fn, "lse_lo", plo, (rows,), f32, index),
+            None if dloss is None else _tensor(fn, "dloss", dloss, (rows,), f32, index)]
+
+    def body(st):
+        pw, nw, _keep = _head_workspace(fn, ws, x, index, qn_head_bwd_workspace_bytes(
+            rows, h.dim, h.vocab, need_dx, need_dw))
+        gx, gw = dx, dw
+        if gx is not None:
+            _tensor(fn, "dx", gx, x.shape, bf, index)
+        elif need_dx:
+            gx = torch.empty_like(x)
+        if gw is not None:
+            _tensor(fn, "dw", gw, w.shape, bf, index)
+        elif need_dw:
+            gw = torch.empty_like(w)
+        _check(fn, lib().qn_head_loss_bwd(h, *args, None if gx is None else gx.data_ptr(),
+                                          None if gw is None else gw.data_ptr(), pw, nw, st))
+        return gx, gw
+    return _run_on(index, stream, body)
 
 
 def qn_profile_kernel(name: str | None, starts=None, stops=None) -> int:

@@ -1,0 +1,52 @@
+// Launchers of the vocabulary head's products (head_gemm.hip), for the entry
+// points in head.hip.  Not part of the public C ABI.
+#pragma once
+
+#include "head_plan.h"
+#include "qn_host.h"
+
+namespace qn {
+
+// Logits of the counted rows, as tiles that stay in registers.
+struct HeadLogits {
+  const uint16_t *x, *w;       // bf16 [rows][dim], [vocab][dim]
+  const int32_t *cnt, *idx, *lab;   // counted rows, their row of x, their label
+  int rows, dim;
+  int64_t vocab;
+  // words [v0, v1) of the vocabulary
+  int64_t v0, v1;
+  // forward: statistics and label's logit
+  float2* part;                // [slices][mp]: maximum and sum without the label
+  float* hit;                  // [mp]
+  int64_t mp;
+  // backward: softmax over the other words, -1 at the label, in bf16
+  const float* lseo;           // [mp] log-sum-exp of the other words
+  uint16_t* g;                 // [mp][vp], zeros for words from v1 and rows from cnt
+  int64_t vp;
+};
+void launch_head_logits(hipStream_t st, int tile, bool bwd, const HeadLogits& a);
+
+// dX of the counted rows from a piece of G: sums over words [v0, v0 + n).
+struct HeadDx {
+  const uint16_t *g, *w;
+  const int32_t *cnt, *idx;
+  const float* scale;          // [mp] factor of a row
+  int rows, dim, slices;
+  int64_t v0, n, vp, mp;
+  uint16_t* dx;                // bf16 [rows][dim], or null: the sums go to acc
+  float* acc;                  // [slices][mp][dim]
+  bool add;                    // onto what acc holds
+};
+void launch_head_dx(hipStream_t st, int tile, const HeadDx& a);
+
+// Rows [v0, v0 + n) of dW = G^T (scaled X).
+struct HeadDw {
+  const uint16_t *g, *xs;      // [mp][vp], [mp][dim]
+  const int32_t* cnt;
+  int rows, dim;
+  int64_t v0, n, vp;
+  uint16_t* dw;
+};
+void launch_head_dw(hipStream_t st, int tile, const HeadDw& a);
+
+}  // namespace qn

@@ -1,0 +1,453 @@
+// Cross entropy of a vocabulary head without its logits in memory, forward
+// and backward: the row kernels and entry points (the products are in
+// head_gemm.hip).
+//
+//   l_tv   = sum_k x_tk w_vk
+//   loss_t = log sum_v exp l_tv - l_t,label
+//   G_tv   = c_t (softmax(l_t)_v - [v = label])     dX = G W,  dW = G^T X
+//
+// With o_t = log sum over the words other than the label of exp l_tv:
+//   loss_t = log(1 + exp(o_t - l_t,label))
+//   G_tv   = c_t (1 - exp(-loss_t)) (exp(l_tv - o_t), or -1 at the label)
+// so nothing cancels for a row whose label is nearly certain, and the
+// label's element of G, the largest, is exact in bf16: the row's factor is
+// applied to the product in fp32 (to X in bf16 where dW sums over rows).
+//
+// Rows that do not count (a negative label) are left out of the products:
+// k_head_rows lists the others, and the products run over the list.
+#include <cmath>
+
+#include "head.h"
+
+namespace {
+
+using namespace qn;
+
+constexpr int HR_THREADS = 1024;
+constexpr int HR_ROWS = 4;              // rows of a thread in a round
+
+struct HeadRows {
+  const int64_t* labels;
+  int64_t vocab;
+  int32_t rows, mp;
+  int32_t *cnt, *idx, *lab;             // cnt[0]: counted rows, cnt[1]: 0
+  int32_t* status;
+  // forward: rows that do not count become 0
+  float *loss, *lse, *lse_lo;
+  // backward
+  const float *in_loss, *in_lse, *in_lo, *dloss;
+  float *lseo, *scale;
+};
+
+// Lists the counted rows in order (one workgroup), and for the backward the
+// log-sum-exp of their other words and their factor c_t (1 - exp(-loss_t)).
+template <bool BWD>
+__global__ __launch_bounds__(HR_THREADS) void k_head_rows(HeadRows a) {
+  __shared__ int s_wave[HR_THREADS / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int base = 0;
+  for (int r0 = 0; r0 < a.rows; r0 += HR_THREADS * HR_ROWS) {
+    const int t0 = r0 + tid * HR_ROWS;
+    int64_t lab[HR_ROWS];
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < HR_ROWS; ++i) {
+      lab[i] = t0 + i < a.rows ? a.labels[t0 + i] : -1;
+      if (lab[i] >= a.vocab) {
+        if (a.status) *a.status = QN_EINVAL;
+        lab[i] = -1;
+      }
+      n += lab[i] >= 0;
+    }
+    int upto = n;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int o = __shfl_up(upto, d);
+      upto += lane >= d ? o : 0;
+    }
+    if (lane == 63) s_wave[wave] = upto;
+    __syncthreads();
+    int at = base + upto - n;
+#pragma unroll
+    for (int w = 0; w < HR_THREADS / 64; ++w) {
+      const int c = s_wave[w];
+      at += w < wave ? c : 0;
+      base += c;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < HR_ROWS; ++i) {
+      if (lab[i] >= 0) {
+        a.idx[at] = t0 + i;
+        a.lab[at] = (int32_t)lab[i];
+        ++at;
+      } else if (!BWD && t0 + i < a.rows) {
+        a.loss[t0 + i] = 0.0f;
+        a.lse[t0 + i] = 0.0f;
+        if (a.lse_lo) a.lse_lo[t0 + i] = 0.0f;
+      }
+    }
+  }
+  if (tid == 0) {
+    a.cnt[0] = base;
+    a.cnt[1] = 0;
+  }
+  if constexpr (BWD) {
+    __syncthreads();
+    const float each = base > 0 ? 1.0f / (float)base : 0.0f;
+    for (int m = tid; m < base; m += HR_THREADS) {
+      const int t = a.idx[m];
+      const float loss = a.in_loss[t];
+      const double rest = -expm1(-(double)loss);            // 1 - p(label)
+      const double lse = (double)a.in_lse[t] + (a.in_lo ? (double)a.in_lo[t] : 0.0);
+      // a label that is certain to the last bit, or the only word there is:
+      // no other word has a share
+      const bool sure = loss < 1.2e-38f;
+      a.lseo[m] = sure ? __builtin_inff() : (float)(lse + log(rest));
+      a.scale[m] = sure ? 0.0f : (float)((a.dloss ? a.dloss[t] : each) * rest);
+    }
+  }
+}
+
+constexpr int HF_ROWS = 64, HF_THREADS = 1024, HF_WAVES = HF_THREADS / 64;
+
+struct HeadFinish {
+  const int32_t* idx;
+  const float2* part;
+  const float* hit;
+  int64_t mp;
+  int32_t slices;
+  float *loss, *lse, *lse_lo, *mean;
+  int32_t* cnt;            // counted rows, then the workgroups that are done
+  double* sums;            // a workgroup's sum of losses
+};
+
+// Joins the slices of 64 rows: a wave takes every 16th slice of them, wave 0
+// joins the waves.  The workgroup that ends last forms the mean, from the
+// workgroups' sums in their order.
+__global__ __launch_bounds__(HF_THREADS) void k_head_finish(HeadFinish a) {
+  __shared__ float2 s_part[HF_WAVES][HF_ROWS];
+  __shared__ int s_last;
+  __shared__ double s_sum[HF_WAVES];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int cnt = a.cnt[0], blocks = max(1, (cnt + HF_ROWS - 1) / HF_ROWS);
+  if ((int)blockIdx.x >= blocks) return;
+  const int m = blockIdx.x * HF_ROWS + lane;
+  float mx = -__builtin_inff(), sum = 0.0f;
+  if (m < cnt) {
+    for (int s0 = wave; s0 < a.slices; s0 += 8 * HF_WAVES) {
+      float2 p[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int s = s0 + i * HF_WAVES;
+        p[i] = s < a.slices ? a.part[(int64_t)s * a.mp + m] : make_float2(-__builtin_inff(), 0.0f);
+      }
+      float top = mx;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, p[i].x);
+      const float at = top == -__builtin_inff() ? 0.0f : top;
+      sum *= expf(mx - at);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += p[i].y * expf(p[i].x - at);
+      mx = top;
+    }
+  }
+  s_part[wave][lane] = make_float2(mx, sum);
+  __syncthreads();
+  double loss = 0.0;
+  if (wave == 0 && m < cnt) {
+    double top = -__builtin_inf();
+#pragma unroll
+    for (int w = 0; w < HF_WAVES; ++w) top = fmax(top, (double)s_part[w][lane].x);
+    const double at = top == -__builtin_inf() ? 0.0 : top;
+    double all = 0.0;
+#pragma unroll
+    for (int w = 0; w < HF_WAVES; ++w)
+      all += (double)s_part[w][lane].y * exp((double)s_part[w][lane].x - at);
+    const double other = at + log(all), hit = (double)a.hit[m];
+    // log(1 + exp(d)) and max + log(1 + exp(-|d|)); two equal infinities
+    // have no difference, and the loss then none either
+    const double d = other - hit;
+    const double tail = log1p(exp(-fabs(d)));
+    loss = d > 0.0 ? d + tail : tail;
+    const double lse = d > 0.0 ? other + tail : hit + tail;
+    const int t = a.idx[m];
+    const float hi = (float)lse;
+    a.loss[t] = (float)loss;
+    a.lse[t] = hi;
+    if (a.lse_lo) a.lse_lo[t] = (float)(lse - (double)hi);
+  }
+  if (a.mean == nullptr) return;
+  if (wave == 0) {
+#pragma unroll
+    for (int d = 32; d > 0; d /= 2) loss += __shfl_xor(loss, d);
+    if (lane == 0) {
+      __hip_atomic_store(a.sums + blockIdx.x, loss, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      s_last = __hip_atomic_fetch_add(a.cnt + 1, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
+               blocks - 1;
+    }
+  }
+  __syncthreads();
+  if (!s_last) return;
+  double total = 0.0;
+  for (int i = tid; i < blocks; i += HF_THREADS)
+    total += __hip_atomic_load(a.sums + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+  for (int d = 32; d > 0; d /= 2) total += __shfl_xor(total, d);
+  if (lane == 0) s_sum[wave] = total;
+  __syncthreads();
+  if (tid == 0) {
+    total = 0.0;
+    for (int w = 0; w < HF_WAVES; ++w) total += s_sum[w];
+    a.mean[0] = cnt > 0 ? (float)(total / cnt) : 0.0f;
+    a.mean[1] = (float)cnt;
+  }
+}
+
+struct HeadFill {
+  const uint16_t* x;
+  const int64_t* labels;
+  const int32_t *cnt, *idx;
+  const float* scale;
+  int64_t vocab;
+  int32_t rows, dim;
+  uint16_t *dx, *xs;       // either may be null
+};
+
+// A workgroup to a row: zeros into dX where the row does not count, and the
+// scaled rows of X behind one another for dW.
+__global__ __launch_bounds__(256) void k_head_fill(HeadFill a) {
+  const int t = blockIdx.x, chunks = a.dim / 8;
+  if (a.dx != nullptr && t < a.rows) {
+    const int64_t lab = a.labels[t];
+    if (lab < 0 || lab >= a.vocab)
+      for (int c = threadIdx.x; c < chunks; c += 256)
+        reinterpret_cast<u32x4*>(a.dx + (int64_t)t * a.dim)[c] = u32x4{0, 0, 0, 0};
+  }
+  if (a.xs == nullptr) return;
+  if (t >= *a.cnt) return;
+  u32x4* to = reinterpret_cast<u32x4*>(a.xs + (int64_t)t * a.dim);
+  const float sc = a.scale[t];
+  const u32x4* from = reinterpret_cast<const u32x4*>(a.x + (int64_t)a.idx[t] * a.dim);
+  for (int c = threadIdx.x; c < chunks; c += 256) {
+    const u32x4 v = from[c];
+    u32x4 o;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      o[e] = pack_bf16x2(sc * bf16_to_f32(v[e] & 0xFFFFu), sc * __uint_as_float(v[e] & 0xFFFF0000u));
+    to[c] = o;
+  }
+}
+
+struct HeadDxSum {
+  const float *acc, *scale;
+  const int32_t *cnt, *idx;
+  int32_t dim, slices;
+  int64_t mp;
+  uint16_t* dx;
+};
+
+// dX of a counted row from its slices.
+__global__ __launch_bounds__(256) void k_head_dx_sum(HeadDxSum a) {
+  const int m = blockIdx.x;
+  if (m >= *a.cnt) return;
+  const int k = (blockIdx.y * 256 + threadIdx.x) * 8;
+  if (k >= a.dim) return;
+  const float sc = a.scale[m];
+  f32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
+  const float* from = a.acc + (int64_t)m * a.dim + k;
+  for (int s = 0; s < a.slices; ++s, from += a.mp * a.dim) {
+    const f32x4 u = *reinterpret_cast<const f32x4*>(from);
+    const f32x4 v = *reinterpret_cast<const f32x4*>(from + 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      lo[e] += u[e];
+      hi[e] += v[e];
+    }
+  }
+  u32x4 o;
+  o.x = pack_bf16x2(lo[0] * sc, lo[1] * sc);
+  o.y = pack_bf16x2(lo[2] * sc, lo[3] * sc);
+  o.z = pack_bf16x2(hi[0] * sc, hi[1] * sc);
+  o.w = pack_bf16x2(hi[2] * sc, hi[3] * sc);
+  *reinterpret_cast<u32x4*>(a.dx + (int64_t)a.idx[m] * a.dim + k) = o;
+}
+
+bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+bool valid_head(const qn_head* h) {
+  if (h == nullptr || !valid_head_sizes(h->rows, h->dim, h->vocab)) return false;
+  if (h->w == nullptr || !aligned16(h->w)) return false;
+  if (h->rows == 0) return true;
+  return h->x != nullptr && aligned16(h->x) && h->labels != nullptr && aligned(h->labels, 8);
+}
+
+}  // namespace
+
+extern "C" size_t qn_head_fwd_workspace_bytes(int64_t rows, int64_t dim, int64_t vocab) {
+  return valid_head_sizes(rows, dim, vocab) ? head_fwd_plan(rows, dim, vocab).total : 0;
+}
+
+extern "C" size_t qn_head_bwd_workspace_bytes(int64_t rows, int64_t dim, int64_t vocab,
+                                              int32_t need_dx, int32_t need_dw) {
+  if (!valid_head_sizes(rows, dim, vocab)) return 0;
+  return head_bwd_plan(rows, dim, vocab, need_dx != 0, need_dw != 0).total;
+}
+
+extern "C" int qn_head_loss_fwd(const qn_head* h, float* loss, float* lse, float* lse_lo,
+                                float* mean, int32_t* status_dev, void* ws, size_t ws_bytes,
+                                void* stream) {
+  if (!valid_head(h)) return QN_EINVAL;
+  if (h->rows > 0 && (loss == nullptr || lse == nullptr)) return QN_EINVAL;
+  if (!aligned(loss, 4) || !aligned(lse, 4) || !aligned(lse_lo, 4) || !aligned(mean, 4) ||
+      !aligned(status_dev, 4))
+    return QN_EINVAL;
+  const HeadFwdPlan P = head_fwd_plan(h->rows, h->dim, h->vocab);
+  if (ws == nullptr || ws_bytes < P.total || !aligned16(ws)) return QN_EWORKSPACE;
+  hipStream_t st = (hipStream_t)stream;
+  HeadRows r{};
+  r.labels = h->labels;
+  r.vocab = h->vocab;
+  r.rows = (int32_t)h->rows;
+  r.mp = (int32_t)P.mp;
+  r.cnt = ws_at<int32_t>(ws, P.cnt);
+  r.idx = ws_at<int32_t>(ws, P.idx);
+  r.lab = ws_at<int32_t>(ws, P.lab);
+  r.status = status_dev;
+  r.loss = loss;
+  r.lse = lse;
+  r.lse_lo = lse_lo;
+  QN_LAUNCH("k_head_rows", (k_head_rows<false>), dim3(1), dim3(HR_THREADS), st, r);
+  if (h->rows > 0) {
+    HeadLogits g{};
+    g.x = h->x;
+    g.w = h->w;
+    g.cnt = r.cnt;
+    g.idx = r.idx;
+    g.lab = r.lab;
+    g.rows = (int)h->rows;
+    g.dim = (int)h->dim;
+    g.vocab = g.v1 = h->vocab;
+    g.part = ws_at<float2>(ws, P.part);
+    g.hit = ws_at<float>(ws, P.hit);
+    g.mp = P.mp;
+    launch_head_logits(st, P.tile, false, g);
+  }
+  HeadFinish f{};
+  f.idx = r.idx;
+  f.part = ws_at<float2>(ws, P.part);
+  f.hit = ws_at<float>(ws, P.hit);
+  f.mp = P.mp;
+  f.slices = (int32_t)P.slices;
+  f.loss = loss;
+  f.lse = lse;
+  f.lse_lo = lse_lo;
+  f.mean = mean;
+  f.cnt = r.cnt;
+  f.sums = ws_at<double>(ws, P.sums);
+  QN_LAUNCH("k_head_finish", k_head_finish,
+            dim3((unsigned)std::max<int64_t>(1, cdiv(h->rows, HF_ROWS))), dim3(HF_THREADS), st, f);
+  return check_launch();
+}
+
+extern "C" int qn_head_loss_bwd(const qn_head* h, const float* loss, const float* lse,
+                                const float* lse_lo, const float* dloss, uint16_t* dx,
+                                uint16_t* dw, void* ws, size_t ws_bytes, void* stream) {
+  if (!valid_head(h)) return QN_EINVAL;
+  if (dx == nullptr && dw == nullptr && h->rows > 0) return QN_EINVAL;
+  if (h->rows > 0 && (loss == nullptr || lse == nullptr)) return QN_EINVAL;
+  if (!aligned(loss, 4) || !aligned(lse, 4) || !aligned(lse_lo, 4) || !aligned(dloss, 4) ||
+      !aligned16(dx) || !aligned16(dw))
+    return QN_EINVAL;
+  const bool need_dx = dx != nullptr && h->rows > 0;
+  const HeadBwdPlan P = head_bwd_plan(h->rows, h->dim, h->vocab, need_dx, dw != nullptr);
+  if (ws == nullptr || ws_bytes < P.total || !aligned16(ws)) return QN_EWORKSPACE;
+  if (!need_dx && dw == nullptr) return QN_OK;
+  hipStream_t st = (hipStream_t)stream;
+  HeadRows r{};
+  r.labels = h->labels;
+  r.vocab = h->vocab;
+  r.rows = (int32_t)h->rows;
+  r.mp = (int32_t)P.mp;
+  r.cnt = ws_at<int32_t>(ws, P.cnt);
+  r.idx = ws_at<int32_t>(ws, P.idx);
+  r.lab = ws_at<int32_t>(ws, P.lab);
+  r.in_loss = loss;
+  r.in_lse = lse;
+  r.in_lo = lse_lo;
+  r.dloss = dloss;
+  r.lseo = ws_at<float>(ws, P.lseo);
+  r.scale = ws_at<float>(ws, P.scale);
+  QN_LAUNCH("k_head_rows", (k_head_rows<true>), dim3(1), dim3(HR_THREADS), st, r);
+  HeadFill f{};
+  f.x = h->x;
+  f.labels = h->labels;
+  f.cnt = r.cnt;
+  f.idx = r.idx;
+  f.scale = r.scale;
+  f.vocab = h->vocab;
+  f.rows = (int32_t)h->rows;
+  f.dim = (int32_t)h->dim;
+  f.dx = need_dx ? dx : nullptr;
+  f.xs = dw ? ws_at<uint16_t>(ws, P.xs) : nullptr;
+  if (h->rows > 0)
+    QN_LAUNCH("k_head_fill", k_head_fill, dim3((unsigned)h->rows), dim3(256), st, f);
+
+  HeadLogits g{};
+  g.x = h->x;
+  g.w = h->w;
+  g.cnt = r.cnt;
+  g.idx = r.idx;
+  g.lab = r.lab;
+  g.rows = (int)h->rows;
+  g.dim = (int)h->dim;
+  g.vocab = h->vocab;
+  g.lseo = r.lseo;
+  g.g = ws_at<uint16_t>(ws, P.g);
+  g.mp = P.mp;
+  g.vp = P.vp;
+  HeadDx d{};
+  d.g = g.g;
+  d.w = h->w;
+  d.cnt = r.cnt;
+  d.idx = r.idx;
+  d.scale = r.scale;
+  d.rows = (int)h->rows;
+  d.dim = (int)h->dim;
+  d.slices = P.slices;
+  d.vp = P.vp;
+  d.mp = P.mp;
+  d.dx = P.direct ? dx : nullptr;
+  d.acc = ws_at<float>(ws, P.acc);
+  HeadDw e{};
+  e.g = g.g;
+  e.xs = f.xs;
+  e.cnt = r.cnt;
+  e.rows = d.rows;
+  e.dim = d.dim;
+  e.vp = P.vp;
+  e.dw = dw;
+  for (int64_t i = 0; i < P.pieces; ++i) {
+    g.v0 = d.v0 = e.v0 = i * P.vp;
+    g.v1 = std::min(h->vocab, g.v0 + P.vp);
+    d.n = e.n = g.v1 - g.v0;
+    d.add = i > 0;
+    if (h->rows > 0) launch_head_logits(st, P.tile, true, g);
+    if (need_dx) launch_head_dx(st, P.tile_dx, d);
+    if (dw) launch_head_dw(st, P.tile_dw, e);
+  }
+  if (need_dx && !P.direct) {
+    HeadDxSum s{};
+    s.acc = d.acc;
+    s.scale = r.scale;
+    s.cnt = r.cnt;
+    s.idx = r.idx;
+    s.dim = d.dim;
+    s.slices = P.slices;
+    s.mp = P.mp;
+    s.dx = dx;
+    QN_LAUNCH("k_head_dx_sum", k_head_dx_sum,
+              dim3((unsigned)h->rows, (unsigned)cdiv(h->dim, 2048)), dim3(256), st, s);
+  }
+  return check_launch();
+}

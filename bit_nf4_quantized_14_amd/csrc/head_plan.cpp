@@ -1,0 +1,82 @@
+// Plans and workspace layouts of the vocabulary head's loss (plain C++).
+#include <algorithm>
+
+#include "head_plan.h"
+
+namespace qn {
+
+namespace {
+
+// Output tiles by what fills the GPU: the largest whose grid has a workgroup
+// for every CU.
+int pick_tile(int64_t np, int64_t nq) {
+  if (nq <= 32) return HT_SMALL;
+  if (nq > 128 && cdiv(np, 256) * cdiv(nq, 256) >= G_CUS) return HT_256;
+  return HT_128;
+}
+
+size_t take(size_t* at, size_t bytes) {
+  const size_t o = *at;
+  *at += align256(bytes);
+  return o;
+}
+
+}  // namespace
+
+bool valid_head_sizes(int64_t rows, int64_t dim, int64_t vocab) {
+  return rows >= 0 && rows < HEAD_MAX_ROWS && dim >= 8 && dim % 8 == 0 && dim <= HEAD_MAX_DIM &&
+         vocab >= 1 && vocab <= HEAD_MAX_VOCAB && rows * dim <= HEAD_MAX_X;
+}
+
+HeadFwdPlan head_fwd_plan(int64_t rows, int64_t dim, int64_t vocab) {
+  HeadFwdPlan P{};
+  (void)dim;
+  P.tile = pick_tile(vocab, rows);
+  P.mp = cdiv(std::max<int64_t>(rows, 1), 256) * 256;
+  P.slices = cdiv(vocab, head_bp(P.tile)) * (head_bp(P.tile) / head_wave_p(P.tile));
+  size_t at = 0;
+  P.cnt = take(&at, 256);
+  P.idx = take(&at, size_t(P.mp) * 4);
+  P.lab = take(&at, size_t(P.mp) * 4);
+  P.hit = take(&at, size_t(P.mp) * 4);
+  P.part = take(&at, size_t(P.slices) * P.mp * 8);
+  P.sums = take(&at, size_t(P.mp / 64) * 8);
+  P.total = at;
+  return P;
+}
+
+HeadBwdPlan head_bwd_plan(int64_t rows, int64_t dim, int64_t vocab, bool need_dx, bool need_dw) {
+  HeadBwdPlan P{};
+  P.mp = cdiv(std::max<int64_t>(rows, 1), 256) * 256;
+  // A piece of G of at most 256 MB, but 8192 words at least: dX's sums are
+  // read and written once per piece.
+  const int64_t cap = std::max<int64_t>(8192, (int64_t(128) << 20) / P.mp / 256 * 256);
+  const int64_t vt = cdiv(vocab, 256) * 256;
+  P.pieces = cdiv(vt, std::min(cap, vt));
+  P.vp = cdiv(cdiv(vt, P.pieces), 256) * 256;
+  P.pieces = cdiv(vt, P.vp);
+  P.tile = pick_tile(std::min(P.vp, vocab), rows);
+  P.tile_dx = pick_tile(dim, rows);
+  P.tile_dw = pick_tile(dim, std::min(P.vp, vocab));
+  P.slices = 1;
+  if (need_dx) {
+    const int64_t tiles = cdiv(dim, head_bp(P.tile_dx)) * cdiv(rows, head_bq(P.tile_dx));
+    const int64_t want = cdiv(2 * G_CUS, std::max<int64_t>(1, tiles));
+    if (tiles < G_CUS)
+      P.slices = (int)std::max<int64_t>(1, std::min<int64_t>({want, P.vp / 512, 64}));
+  }
+  P.direct = P.slices == 1 && P.pieces == 1;
+  size_t at = 0;
+  P.cnt = take(&at, 256);
+  P.idx = take(&at, size_t(P.mp) * 4);
+  P.lab = take(&at, size_t(P.mp) * 4);
+  P.lseo = take(&at, size_t(P.mp) * 4);
+  P.scale = take(&at, size_t(P.mp) * 4);
+  P.g = take(&at, size_t(P.mp) * P.vp * 2);
+  P.xs = take(&at, need_dw ? size_t(P.mp) * dim * 2 : 0);
+  P.acc = take(&at, need_dx && !P.direct ? size_t(P.slices) * P.mp * dim * 4 : 0);
+  P.total = at;
+  return P;
+}
+
+}  // namespace qn

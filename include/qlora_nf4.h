@@ -657,6 +657,88 @@ int qn_pref_loss_bwd(const qn_seq_batch* b, const float* lse,
                      void* stream);
 
 /*
+ * Cross entropy of a vocabulary head.
+ *
+ * Supervised fine-tuning scores every answer token by the head's softmax
+ * ("QLoRA Guide", How QLoRA Works: the loss is the base model's, only the
+ * adapters are trained); the head itself stays dense in bf16.  Its logits are
+ * the step's largest tensor and are never written to memory here: they are
+ * formed tile by tile, reduced in the forward and formed again in the
+ * backward, which keeps their gradient for a piece of the vocabulary at a
+ * time.
+ *   l_tv   = sum_k x_tk w_vk            (bf16 products, fp32 sums)
+ *   lse_t  = log sum_{v < vocab} exp(l_tv)
+ *   loss_t = lse_t - l_t,label
+ * A row is counted when 0 <= label_t < vocab; others cost no products.
+ *   x      : device bf16 [rows][dim], 16-byte aligned;
+ *   w      : device bf16 [vocab][dim], 16-byte aligned;
+ *   labels : device int64 [rows]; negative (for instance -100): the row is
+ *            not counted.
+ * 0 <= rows < 2^24 (x and labels may be NULL when it is 0), dim a multiple of
+ * 8 up to 2^20, 1 <= vocab <= 2^28, rows * dim <= 2^30.
+ * A row whose logits hold a NaN or +infinity has no loss: its loss, lse and
+ * dX row are NaN, and so are the mean and every element of dW.  A label at
+ * -infinity in a row that has others makes its loss +infinity and leaves its
+ * gradient finite.
+ */
+typedef struct {
+  const uint16_t* x;
+  const uint16_t* w;
+  const int64_t* labels;
+  int64_t rows, dim, vocab;
+} qn_head;
+
+/* Workspaces of the two calls (host); 0 for invalid sizes.  need_dx, need_dw:
+ * which gradients the call is asked for. */
+size_t qn_head_fwd_workspace_bytes(int64_t rows, int64_t dim, int64_t vocab);
+size_t qn_head_bwd_workspace_bytes(int64_t rows, int64_t dim, int64_t vocab,
+                                   int32_t need_dx, int32_t need_dw);
+
+/*
+ * qn_head_loss_fwd -- loss and log-sum-exp of each row (device).
+ * loss, lse : device float [rows]; 0 for rows that are not counted.  loss is
+ *          formed as log(1 + exp(o_t - l_t,label)), o_t the log-sum-exp of the
+ *          other words, so a label that is nearly certain keeps its digits.
+ * lse_lo : device float [rows] or NULL: lse_t minus its fp32 value, for the
+ *          backward (of use beside logits of some thousands).
+ * mean   : device float [2] or NULL: the mean loss of the counted rows (0 if
+ *          there are none; summed in double), and their number.
+ * status_dev : device int32 or NULL.  QN_EINVAL is stored there if a label is
+ *          not below vocab (that row is not counted); otherwise it is left as
+ *          it was.
+ * ws     : ws_bytes >= qn_head_fwd_workspace_bytes(rows, dim, vocab), 16-byte
+ *          aligned; calls that run at the same time need workspaces of their
+ *          own.
+ * No output may overlap an input, another output or the workspace.
+ * Errors: QN_EINVAL, QN_EWORKSPACE, QN_EHIP.
+ */
+int qn_head_loss_fwd(const qn_head* h, float* loss, float* lse, float* lse_lo,
+                     float* mean, int32_t* status_dev, void* ws,
+                     size_t ws_bytes, void* stream);
+
+/*
+ * qn_head_loss_bwd -- gradient of sum_t dloss_t loss_t (device):
+ *   G_tv = dloss_t (softmax(l_t)_v - 1[v == label_t]),  dX = G W,  dW = G^T X
+ * loss, lse, lse_lo : as written by the forward for this head (lse_lo may be
+ *         NULL).
+ * dloss : device float [rows], read for counted rows only, or NULL for 1 / n
+ *         each, n the number of counted rows (the mean loss).
+ * dx    : device bf16 [rows][dim], 16-byte aligned, or NULL; zeros for rows
+ *         that are not counted.
+ * dw    : device bf16 [vocab][dim], 16-byte aligned, or NULL (a frozen head).
+ *         dx and dw may not both be NULL unless rows is 0.
+ * Accuracy: fp32 sums of bf16 products.  G enters them in bf16 relative to
+ * the row's label element, which is exact; the row's factor dloss_t (1 -
+ * softmax_label) multiplies dX in fp32, and X in bf16 for dW.
+ * ws    : ws_bytes >= qn_head_bwd_workspace_bytes(rows, dim, vocab, dx !=
+ *         NULL, dw != NULL), 16-byte aligned, as above.
+ * Overlap and errors as qn_head_loss_fwd.
+ */
+int qn_head_loss_bwd(const qn_head* h, const float* loss, const float* lse,
+                     const float* lse_lo, const float* dloss, uint16_t* dx,
+                     uint16_t* dw, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * qlora_linear_fwd_batch -- qlora_linear_fwd for up to QN_FWD_BATCH_MAX
  * projections with few tokens (M <= 16 each), as one pair of launches
  * (device).
