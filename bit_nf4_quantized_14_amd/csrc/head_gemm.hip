@@ -30,10 +30,6 @@ constexpr int HD_BK = 64;
 // a step whose loads all lie past the reduction's end
 constexpr int HD_PAST = 1 << 22;
 
-__device__ __forceinline__ u32x4 buf_load16(rsrc_t r, uint32_t vo, int so) {
-  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, vo, so, 0));
-}
-
 // Tile shapes: BP x BQ by WP x WQ waves.
 template <int TILE>
 struct HeadCfg {
@@ -46,40 +42,45 @@ struct HeadCfg {
   static_assert(WTP == head_wave_p(TILE), "statistics entries");
 };
 
-// One operand's tile of DIM positions x 64 reduction elements.
+// s_waitcnt vmcnt(n) expcnt(7) lgkmcnt(0) (gfx9 encoding)
+#define HEAD_WAIT_VM(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | (7 << 4) | (((n) >> 4) << 14))
+
+// Workgroup barrier alone: the callers wait for what has to be visible.
+__device__ __forceinline__ void head_barrier() {
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_s_barrier();
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
+// 16 bytes a lane into LDS, lane l's at lds + 16 l (`lds` the same in the wave).
+__device__ __forceinline__ void load_lds16(rsrc_t r, char* lds, uint32_t vo, int so) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, vo, so, 0, 0);
+}
+
+// One operand's tile of DIM positions x 64 reduction elements.  A stage is
+// loaded straight into LDS, 16 bytes a lane: slot q = tid + NT i lies at byte
+// 16 q, and the swizzle is in which chunk of its row the slot's lane loads.
 template <int DIM, bool T, int NT>
 struct HeadOp {
-  static constexpr int CH = DIM * 8 / NT;        // 16-byte chunks of a thread
-  static constexpr int BYTES = DIM * HD_BK * 2;
+  static constexpr int CH = DIM * 8 / NT;        // 16-byte slots of a thread
+  static constexpr int READS = T ? 2 : 1;        // LDS reads of a fragment
   static_assert(CH * NT == DIM * 8, "tile loads");
+  // the swizzles below are the same for all slots of a thread
+  static_assert(T ? NT / (DIM / 8) % 4 == 0 : NT / 8 % 16 == 0, "slots' rows");
 
-  // N: position (row) of chunk i of thread tid, and its reduction offset
-  static __device__ __forceinline__ int row_n(int tid, int i) { return (tid + NT * i) >> 3; }
-  static __device__ __forceinline__ int red_n(int tid) { return 8 * (tid & 7); }
-  // T: reduction row of chunk i, and its first position
-  static __device__ __forceinline__ int red_t(int tid, int i) { return (tid + NT * i) / (DIM / 8); }
-  static __device__ __forceinline__ int col_t(int tid) { return 8 * (tid % (DIM / 8)); }
-  static_assert(NT % (DIM / 8) == 0, "a thread's chunks share their columns");
-
-  static __device__ __forceinline__ void store(const u32x4 (&v)[CH], char* lds, int tid) {
-#pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int q = tid + NT * i;
-      int at;
-      if constexpr (!T) {
-        const int row = q >> 3;
-        at = row * 128 + (((q & 7) ^ ((row >> 1) & 7)) << 4);
-      } else {
-        const int row = q / (DIM / 8), c = q % (DIM / 8);
-        at = row * (DIM * 2) + ((c ^ swz_t(row)) << 4);
-      }
-      *reinterpret_cast<u32x4*>(lds + at) = v[i];
-    }
-  }
   // 16-byte chunk XOR of reduction row r of a T tile: the four rows of a
   // transposed read's phase (64 bytes each) land in different quarters of the
-  // 64 banks (DIM >= 128; in a row of 64 bytes they do by themselves).
+  // 64 banks (DIM >= 128; four rows of 64 bytes do by themselves).
   static __device__ __forceinline__ int swz_t(int r) { return DIM >= 128 ? 4 * (r & 3) : 0; }
+
+  // N: position (row) of slot i of thread tid, and its reduction offset
+  static __device__ __forceinline__ int row_n(int tid, int i) { return (tid + NT * i) >> 3; }
+  static __device__ __forceinline__ int red_n(int tid) { return 8 * ((tid & 7) ^ ((tid >> 4) & 7)); }
+  // T: reduction row of slot i, and its first position
+  static __device__ __forceinline__ int red_t(int tid, int i) { return (tid + NT * i) / (DIM / 8); }
+  static __device__ __forceinline__ int col_t(int tid) {
+    return 8 * ((tid % (DIM / 8)) ^ swz_t(tid / (DIM / 8)));
+  }
 
   // Fragment of positions base .. base + 31, reduction 16 kk .. 16 kk + 15:
   // lane l takes position base + l % 32, elements 8 (l / 32) .. + 7.
@@ -111,10 +112,10 @@ struct HeadOp {
 };
 
 // Where an operand's tile comes from.  N: `base` is the tile's first row, vo[i]
-// the byte offset of chunk i at reduction 0 (G_OOB for a row outside), the
+// the byte offset of slot i at reduction 0 (G_OOB for a row outside), the
 // reduction's elements from `end` on read as zeros.  T: `base` is reduction
 // row 0 at the operand's first column, `pitch` bytes a row, vo[i] the offset
-// of chunk i inside a step (G_OOB for columns outside), rows from `end` on
+// of slot i inside a step (G_OOB for columns outside), rows from `end` on
 // read as zeros by the resource's range.
 template <int DIM, bool T, int NT>
 struct HeadLoader {
@@ -124,86 +125,92 @@ struct HeadLoader {
   int64_t pitch;         // T
   int end;
   uint32_t vo[O::CH];
-  __device__ __forceinline__ void load(u32x4 (&v)[O::CH], int red0, int tid) const {
+  __device__ __forceinline__ void load(char* lds, int red0, int wave, int tid) const {
+    rsrc_t r;
+    bool ok = true;
     if constexpr (!T) {
-      const rsrc_t r = make_rsrc(base, bytes);
-      const bool ok = red0 + O::red_n(tid) < end;
-#pragma unroll
-      for (int i = 0; i < O::CH; ++i) v[i] = buf_load16(r, ok ? vo[i] : G_OOB, red0 * 2);
+      r = make_rsrc(base, bytes);
+      ok = red0 + O::red_n(tid) < end;
     } else {
       const int64_t left = (int64_t)(end - red0) * pitch;
-      const rsrc_t r = make_rsrc(base + red0 * pitch,
-                                 (uint32_t)(left <= 0 ? 0 : (left < 64 * pitch ? left : 64 * pitch)));
-#pragma unroll
-      for (int i = 0; i < O::CH; ++i) v[i] = buf_load16(r, vo[i], 0);
+      r = make_rsrc(base + red0 * pitch,
+                    (uint32_t)(left <= 0 ? 0 : (left < 64 * pitch ? left : 64 * pitch)));
     }
+#pragma unroll
+    for (int i = 0; i < O::CH; ++i)
+      load_lds16(r, lds + wave * 1024 + NT * 16 * i, ok ? vo[i] : G_OOB, T ? 0 : red0 * 2);
   }
 };
 
-// Reduction steps [s0, s1) into acc.
-template <int TILE, bool PT, bool QT>
-__device__ __forceinline__ void head_mainloop(
-    const HeadLoader<HeadCfg<TILE>::BP, PT, HeadCfg<TILE>::NT>& lp,
-    const HeadLoader<HeadCfg<TILE>::BQ, QT, HeadCfg<TILE>::NT>& lq, char* sP0, char* sP1,
-    char* sQ0, char* sQ1, int s0, int s1, int wp, int wq, int tid, int lane,
-    f32x16 (&acc)[HeadCfg<TILE>::TP][HeadCfg<TILE>::TQ]) {
+// Reduction steps [s0, s1) into acc.  Fragments are read one slice of 16
+// ahead, the first slice of a step during the last one of the step before.  So
+// when a step comes to its last slice, its own stage has been read by
+// everyone (barrier) and the next must have landed: the loads of the stage
+// after that go out there and have the rest of a step's time.
+template <int TILE, class LP, class LQ, int TP, int TQ>
+__device__ __forceinline__ void head_mainloop(const LP& lp, const LQ& lq, char* sP0, char* sP1,
+                                              char* sQ0, char* sQ1, int s0, int s1, int wave,
+                                              int tid, int lane, f32x16 (&acc)[TP][TQ]) {
   using C = HeadCfg<TILE>;
-  using OP = HeadOp<C::BP, PT, C::NT>;
-  using OQ = HeadOp<C::BQ, QT, C::NT>;
-  constexpr int MPK = C::TP * C::TQ;                                // MFMAs per k16 slice
-  constexpr int RD = C::TP * (PT ? 2 : 1) + C::TQ * (QT ? 2 : 1);   // LDS reads per slice
-  constexpr int WR = OP::CH + OQ::CH;                               // LDS writes per step
-  constexpr int RDM = (RD + MPK - 1) / MPK, WRM = (WR + MPK - 1) / MPK;
-  u32x4 vp[OP::CH], vq[OQ::CH];
-  lp.load(vp, s0 * HD_BK, tid);
-  lq.load(vq, s0 * HD_BK, tid);
-  OP::store(vp, sP0, tid);
-  OQ::store(vq, sQ0, tid);
-  __syncthreads();
+  using OP = typename LP::O;
+  using OQ = typename LQ::O;
+  constexpr int MPK = TP * TQ;                                      // MFMAs per k16 slice
+  constexpr int RD = TP * OP::READS + TQ * OQ::READS;               // LDS reads per slice
+  constexpr int LD = OP::CH + OQ::CH;                               // loads per step
+  constexpr int RDM = (RD + MPK - 1) / MPK, LDM = (LD + MPK - 1) / MPK;
+  const int wp = wave / C::WQ, wq = wave % C::WQ;
+  lp.load(sP0, s0 * HD_BK, wave, tid);
+  lq.load(sQ0, s0 * HD_BK, wave, tid);
+  const int one = s0 + 1 < s1 ? s0 + 1 : HD_PAST;
+  lp.load(sP1, one * HD_BK, wave, tid);
+  lq.load(sQ1, one * HD_BK, wave, tid);
+  HEAD_WAIT_VM(LD);
+  head_barrier();
+  u32x4 a[2][TP], b[2][TQ];
+  auto frags = [&](const char* sp, const char* sq, int kk) {
+#pragma unroll
+    for (int i = 0; i < TP; ++i)
+      a[kk & 1][i] = OP::frag(sp, wp * C::WTP + 32 * i, kk, lane);
+#pragma unroll
+    for (int j = 0; j < TQ; ++j)
+      b[kk & 1][j] = OQ::frag(sq, wq * C::WTQ + 32 * j, kk, lane);
+  };
+  frags(sP0, sQ0, 0);
   // steps past the end load zeros: the loop runs whole pairs
   for (int st = s0; st < s1; st += 2) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const char *cp = h ? sP1 : sP0, *cq = h ? sQ1 : sQ0;
-      char *np = h ? sP0 : sP1, *nq = h ? sQ0 : sQ1;
-      const int next = st + h + 1 < s1 ? st + h + 1 : HD_PAST;
-      lp.load(vp, next * HD_BK, tid);
-      lq.load(vq, next * HD_BK, tid);
-      u32x4 a[2][C::TP], b[2][C::TQ];
-      auto frags = [&](int kk) {
-#pragma unroll
-        for (int i = 0; i < C::TP; ++i)
-          a[kk & 1][i] = OP::frag(cp, wp * C::WTP + 32 * i, kk, lane);
-#pragma unroll
-        for (int j = 0; j < C::TQ; ++j)
-          b[kk & 1][j] = OQ::frag(cq, wq * C::WTQ + 32 * j, kk, lane);
-      };
-      frags(0);
-      __builtin_amdgcn_sched_barrier(0);
+      char *cp = h ? sP1 : sP0, *cq = h ? sQ1 : sQ0;
+      const char *np = h ? sP0 : sP1, *nq = h ? sQ0 : sQ1;
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
         if (kk < 3) {
-          frags(kk + 1);
+          frags(cp, cq, kk + 1);
         } else {
-          OP::store(vp, np, tid);
-          OQ::store(vq, nq, tid);
+          HEAD_WAIT_VM(0);
+          head_barrier();
+          __builtin_amdgcn_sched_barrier(0);
+          const int next = st + h + 2 < s1 ? st + h + 2 : HD_PAST;
+          lp.load(cp, next * HD_BK, wave, tid);
+          lq.load(cq, next * HD_BK, wave, tid);
+          frags(np, nq, 0);
         }
 #pragma unroll
         for (int g = 0; g < MPK; ++g) {
-          const int i = g / C::TQ, j = g % C::TQ;
+          const int i = g / TQ, j = g % TQ;
           acc[i][j] = mfma32(a[kk & 1][i], b[kk & 1][j], acc[i][j]);
         }
 #pragma unroll
         for (int g = 0; g < MPK; ++g) {
           __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                     // MFMA
-          if (kk < 3 && g * RDM < RD) __builtin_amdgcn_sched_group_barrier(0x100, RDM, 0);
-          if (kk == 3 && g * WRM < WR) __builtin_amdgcn_sched_group_barrier(0x200, WRM, 0);
+          if (g * RDM < RD) __builtin_amdgcn_sched_group_barrier(0x100, RDM, 0); // LDS read
+          if (kk == 3 && g * LDM < LD) __builtin_amdgcn_sched_group_barrier(0x020, LDM, 0);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
-      __syncthreads();
     }
   }
+  HEAD_WAIT_VM(0);   // nothing of this workgroup's is on its way into LDS
 }
 
 // Tile `i` of tq x tp tiles in groups of four tile columns walked along P, so
@@ -288,8 +295,7 @@ __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_logits(HeadLogits a)
   }
   f32x16 acc[C::TP][C::TQ];
   zero_acc<TILE>(acc);
-  head_mainloop<TILE, false, false>(lp, lq, sP0, sP1, sQ0, sQ1, 0, (a.dim + HD_BK - 1) / HD_BK, wp,
-                                    wq, tid, lane, acc);
+  head_mainloop<TILE>(lp, lq, sP0, sP1, sQ0, sQ1, 0, (a.dim + HD_BK - 1) / HD_BK, wave, tid, lane, acc);
 
   // word of accumulator v of tile i: pw + 32 i + 8 (v / 4) + v % 4
   const int64_t pw = p0 + wp * C::WTP + 4 * (lane >> 5);
@@ -381,7 +387,7 @@ __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_dx(HeadDx a) {
   const int s1 = (int)((int64_t)steps * (slice + 1) / a.slices);
   f32x16 acc[C::TP][C::TQ];
   zero_acc<TILE>(acc);
-  head_mainloop<TILE, true, false>(lp, lq, sP0, sP1, sQ0, sQ1, s0, s1, wp, wq, tid, lane, acc);
+  head_mainloop<TILE>(lp, lq, sP0, sP1, sQ0, sQ1, s0, s1, wave, tid, lane, acc);
 
 #pragma unroll
   for (int j = 0; j < C::TQ; ++j) {
@@ -453,8 +459,7 @@ __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_dw(HeadDw a) {
   }
   f32x16 acc[C::TP][C::TQ];
   zero_acc<TILE>(acc);
-  head_mainloop<TILE, true, true>(lp, lq, sP0, sP1, sQ0, sQ1, 0, (cnt + HD_BK - 1) / HD_BK, wp, wq,
-                                  tid, lane, acc);
+  head_mainloop<TILE>(lp, lq, sP0, sP1, sQ0, sQ1, 0, (cnt + HD_BK - 1) / HD_BK, wave, tid, lane, acc);
 #pragma unroll
   for (int j = 0; j < C::TQ; ++j) {
     const int v = q0 + wq * C::WTQ + 32 * j + (lane & 31);
