@@ -21,7 +21,7 @@ struct HeadLogits {
   int64_t mp;
   // backward: softmax over the other words, -1 at the label, in bf16
   const float* lseo;           // [mp] log-sum-exp of the other words
-  uint16_t* g;                 // [mp][vp], zeros for words from v1 and rows from cnt
+  uint16_t* g;                 // [mp / 256][vp / 64][256][64], zeros for words from v1
   int64_t vp;
 };
 void launch_head_logits(hipStream_t st, int tile, bool bwd, const HeadLogits& a);
@@ -41,7 +41,7 @@ void launch_head_dx(hipStream_t st, int tile, const HeadDx& a);
 
 // Rows [v0, v0 + n) of dW = G^T (scaled X).
 struct HeadDw {
-  const uint16_t *g, *xs;      // [mp][vp], [mp][dim]
+  const uint16_t *g, *xs;      // as above, [mp][dim]
   const int32_t* cnt;
   int rows, dim;
   int64_t v0, n, vp;

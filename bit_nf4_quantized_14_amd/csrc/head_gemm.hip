@@ -27,8 +27,6 @@ using namespace qn;
 constexpr float HD_LOG2E = 1.4426950408889634f;
 constexpr float HD_NEG_INF = -__builtin_inff();
 constexpr int HD_BK = 64;
-// a step whose loads all lie past the reduction's end
-constexpr int HD_PAST = 1 << 22;
 
 // Tile shapes: BP x BQ by WP x WQ waves.
 template <int TILE>
@@ -39,6 +37,9 @@ struct HeadCfg {
   static constexpr int NT = 64 * WP * WQ;
   static constexpr int WTP = BP / WP, WTQ = BQ / WQ;    // a wave's part
   static constexpr int TP = WTP / 32, TQ = WTQ / 32;    // its 32 x 32 tiles
+  // stages in LDS of the operand that comes from far (the weight, or G for
+  // dW) and of the other one
+  static constexpr int RFAR = TILE == HT_SMALL ? 4 : 3, RNEAR = TILE == HT_SMALL ? 4 : 2;
   static_assert(WTP == head_wave_p(TILE), "statistics entries");
 };
 
@@ -52,9 +53,31 @@ __device__ __forceinline__ void head_barrier() {
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 
-// 16 bytes a lane into LDS, lane l's at lds + 16 l (`lds` the same in the wave).
-__device__ __forceinline__ void load_lds16(rsrc_t r, char* lds, uint32_t vo, int so) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, vo, so, 0, 0);
+// A buffer resource in scalar registers, for the loads below.
+typedef uint32_t HeadRsrc __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ HeadRsrc head_rsrc(const char* base, uint32_t bytes) {
+  const uint64_t at = reinterpret_cast<uint64_t>(base);
+  HeadRsrc r;
+  r.x = (uint32_t)at;
+  r.y = (uint32_t)(at >> 32) & 0xFFFFu;
+  r.z = bytes;
+  r.w = G_RSRC_FLAGS;
+  return r;
+}
+
+// 16 bytes a lane from offset vo + so into LDS, lane l's at byte lds + 16 l;
+// lds, r and so are the same in the whole wave.  Written as assembly because
+// the compiler, which cannot tell the stages apart, would wait for all of
+// these loads at the next read of any stage; the waits are HEAD_WAIT_VM and
+// the barriers of the main loop.
+__device__ __forceinline__ void load_lds16(const HeadRsrc& r, uint32_t lds, uint32_t vo, int so) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dwordx4 %1, %2, %3 offen lds"
+      :
+      : "s"(lds), "v"(vo), "s"(r), "s"(so)
+      : "memory", "m0");
 }
 
 // One operand's tile of DIM positions x 64 reduction elements.  A stage is
@@ -82,22 +105,31 @@ struct HeadOp {
     return 8 * ((tid % (DIM / 8)) ^ swz_t(tid / (DIM / 8)));
   }
 
-  // Fragment of positions base .. base + 31, reduction 16 kk .. 16 kk + 15:
-  // lane l takes position base + l % 32, elements 8 (l / 32) .. + 7.
-  static __device__ __forceinline__ u32x4 frag(const char* lds, int base, int kk, int lane) {
+  // Byte of this lane's first read of the fragment of positions base .. base +
+  // 31 in a stage, and the fragment of slice kk (reduction 16 kk .. 16 kk +
+  // 15) from there: lane l takes position base + l % 32, elements 8 (l / 32) ..
+  // + 7.  N: the slice is in bits 5 and 6 of the byte, and 32 positions
+  // further is 4096 bytes further.
+  static __device__ __forceinline__ int frag_at(int base, int lane) {
     if constexpr (!T) {
-      const int r = base + (lane & 31), c = 2 * kk + (lane >> 5);
-      return *reinterpret_cast<const u32x4*>(lds + r * 128 + ((c ^ ((r >> 1) & 7)) << 4));
+      const int r = base + (lane & 31);
+      return r * 128 + (((lane >> 5) ^ ((r >> 1) & 7)) << 4);
     } else {
       // each transposed read serves 4 reduction rows: in a group of 16
       // lanes, lane q = 4 j + p addresses row j, positions 4 p .. 4 p + 3, and
       // receives position q of the four rows
+      const int grp = lane >> 4, q = lane & 15;
+      const int row = 8 * (grp >> 1) + (q >> 2), col = base + 16 * (grp & 1) + 4 * (q & 3);
+      return row * (DIM * 2) + (((col >> 3) ^ swz_t(row)) << 4) + 2 * (col & 7);
+    }
+  }
+  static __device__ __forceinline__ u32x4 frag(const char* at, int kk) {
+    if constexpr (!T) {
+      return *reinterpret_cast<const u32x4*>(at);
+    } else {
       typedef short s16x4 __attribute__((ext_vector_type(4)));
       typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-      const int grp = lane >> 4, q = lane & 15;
-      const int row = 16 * kk + 8 * (grp >> 1) + (q >> 2);
-      const int col = base + 16 * (grp & 1) + 4 * (q & 3);
-      const char* p = lds + row * (DIM * 2) + (((col >> 3) ^ swz_t(row)) << 4) + 2 * (col & 7);
+      const char* p = at + 16 * kk * (DIM * 2);
       const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(const_cast<char*>(p)));
       const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
           (lds_s16x4*)(const_cast<char*>(p + 4 * (DIM * 2))));
@@ -109,106 +141,195 @@ struct HeadOp {
       return r;
     }
   }
+  // The fragments of a wave's COUNT tiles from position `first` of the stage at
+  // byte `stage`.
+  template <int COUNT>
+  struct Reader {
+    int at[T ? COUNT : 1];
+    __device__ __forceinline__ Reader(int first, int lane) {
+#pragma unroll
+      for (int i = 0; i < (T ? COUNT : 1); ++i) at[i] = frag_at(first + 32 * i, lane);
+    }
+    __device__ __forceinline__ u32x4 read(const char* lds, int stage, int i, int kk) const {
+      if constexpr (T)
+        return frag(lds + (at[i] + stage), kk);
+      else
+        return frag(lds + (((at[0] + stage) ^ (kk << 5)) + 4096 * i), kk);
+    }
+  };
 };
 
-// Where an operand's tile comes from.  N: `base` is the tile's first row, vo[i]
-// the byte offset of slot i at reduction 0 (G_OOB for a row outside), the
-// reduction's elements from `end` on read as zeros.  T: `base` is reduction
-// row 0 at the operand's first column, `pitch` bytes a row, vo[i] the offset
-// of slot i inside a step (G_OOB for columns outside), rows from `end` on
-// read as zeros by the resource's range.
-template <int DIM, bool T, int NT>
+// G lies in blocks of 256 rows x 64 words, so that an operand's stage is
+// contiguous memory however many words a piece has.
+__device__ __forceinline__ int64_t g_block(int m, int64_t v, int64_t vp) {
+  return ((int64_t)(m >> 8) * (vp >> 6) + (v >> 6)) * (256 * HD_BK);
+}
+
+// Where an operand's tile comes from; load() fetches one step after another.
+// N: `base` is the tile's first row, vo[i] the byte offset of slot i in step 0
+// (G_OOB for a row outside); the reduction's elements from `left` on read as
+// zeros.  T: `base` is the step's first reduction row at the operand's first
+// column, vo[i] the offset of slot i inside a step (G_OOB for columns
+// outside); rows from `left` on read as zeros by the resource's range.  TG: as T
+// for G, `vp_bytes` from one block of 256 rows to the next.
+enum HeadKind { HK_N, HK_T, HK_TG };
+template <int DIM, int KIND, int NT>
 struct HeadLoader {
-  using O = HeadOp<DIM, T, NT>;
+  using O = HeadOp<DIM, KIND != HK_N, NT>;
   const char* base;
-  uint32_t bytes;        // N: range of the resource
-  int64_t pitch;         // T
-  int end;
+  uint32_t bytes;        // range of the resource (N, T: of one step)
+  int step_bytes;        // N, T: to the next step
+  int64_t vp_bytes;      // TG
+  int so, left;          // N: offset of the next step; all: reduction left
   uint32_t vo[O::CH];
-  __device__ __forceinline__ void load(char* lds, int red0, int wave, int tid) const {
-    rsrc_t r;
-    bool ok = true;
-    if constexpr (!T) {
-      r = make_rsrc(base, bytes);
-      ok = red0 + O::red_n(tid) < end;
+  // the first step; `end` of the reduction
+  __device__ __forceinline__ void start(int step, int end) {
+    left = end - step * HD_BK;
+    so = 0;
+    if constexpr (KIND == HK_N)
+      so = step * step_bytes;
+    else if constexpr (KIND == HK_T)
+      base += (int64_t)step * step_bytes;
+    else
+      so = step;
+  }
+  // the next step: begin(), slot(i) for every i, end()
+  HeadRsrc r;
+  bool ok;
+  __device__ __forceinline__ void begin(int tid) {
+    ok = true;
+    if constexpr (KIND == HK_N) {
+      r = head_rsrc(base, bytes);
+      ok = O::red_n(tid) < left;
+    } else if constexpr (KIND == HK_T) {
+      const int rows = left < 0 ? 0 : (left < HD_BK ? left : HD_BK);
+      r = head_rsrc(base, __builtin_amdgcn_readfirstlane((uint32_t)rows * bytes));
     } else {
-      const int64_t left = (int64_t)(end - red0) * pitch;
-      r = make_rsrc(base + red0 * pitch,
-                    (uint32_t)(left <= 0 ? 0 : (left < 64 * pitch ? left : 64 * pitch)));
+      r = head_rsrc(base + (so >> 2) * vp_bytes + (so & 3) * (HD_BK * 128), 0x7fffffffu);
     }
-#pragma unroll
-    for (int i = 0; i < O::CH; ++i)
-      load_lds16(r, lds + wave * 1024 + NT * 16 * i, ok ? vo[i] : G_OOB, T ? 0 : red0 * 2);
+  }
+  __device__ __forceinline__ void slot(uint32_t lds, int i, int wave, int tid) {
+    if constexpr (KIND == HK_TG) ok = O::red_t(tid, i) < left;
+    load_lds16(r, lds + wave * 1024 + NT * 16 * i, KIND == HK_T || ok ? vo[i] : G_OOB,
+               KIND == HK_N ? so : 0);
+  }
+  __device__ __forceinline__ void end() {
+    left -= HD_BK;
+    if constexpr (KIND == HK_N)
+      so += step_bytes;
+    else if constexpr (KIND == HK_T)
+      base += step_bytes;
+    else
+      ++so;
   }
 };
 
-// Reduction steps [s0, s1) into acc.  Fragments are read one slice of 16
+// `steps` reduction steps into acc.  Fragments are read one slice of 16
 // ahead, the first slice of a step during the last one of the step before.  So
-// when a step comes to its last slice, its own stage has been read by
-// everyone (barrier) and the next must have landed: the loads of the stage
-// after that go out there and have the rest of a step's time.
-template <int TILE, class LP, class LQ, int TP, int TQ>
-__device__ __forceinline__ void head_mainloop(const LP& lp, const LQ& lq, char* sP0, char* sP1,
-                                              char* sQ0, char* sQ1, int s0, int s1, int wave,
+// when a step comes to its last slice, its own stages have been read by
+// everyone (barrier) and the next ones must have landed; the loads into the
+// free stages go out there.  The operand that comes from far has a stage more
+// than the other: its loads have a step's time more.
+template <int TILE, int RP, int RQ, class LP, class LQ, int TP, int TQ>
+__device__ __forceinline__ void head_mainloop(LP& lp, LQ& lq, char* lds, int steps, int wave,
                                               int tid, int lane, f32x16 (&acc)[TP][TQ]) {
   using C = HeadCfg<TILE>;
   using OP = typename LP::O;
   using OQ = typename LQ::O;
+  constexpr int PB = C::BP * HD_BK * 2, QB = C::BQ * HD_BK * 2;     // bytes of a stage
   constexpr int MPK = TP * TQ;                                      // MFMAs per k16 slice
+  constexpr int FR = TP + TQ;                                       // fragments per slice
   constexpr int RD = TP * OP::READS + TQ * OQ::READS;               // LDS reads per slice
   constexpr int LD = OP::CH + OQ::CH;                               // loads per step
-  constexpr int RDM = (RD + MPK - 1) / MPK, LDM = (LD + MPK - 1) / MPK;
+  constexpr int RDM = (RD + MPK - 1) / MPK;
+  constexpr int RMIN = RP < RQ ? RP : RQ, RMAX = RP < RQ ? RQ : RP;
+  static_assert(RMAX - RMIN <= 1 && RMIN >= 2, "one operand is at most one step ahead");
+  // loads still out when all of the next step's have landed
+  constexpr int OUT = (RMIN - 2) * LD + (RP > RQ ? OP::CH : 0) + (RQ > RP ? OQ::CH : 0);
   const int wp = wave / C::WQ, wq = wave % C::WQ;
-  lp.load(sP0, s0 * HD_BK, wave, tid);
-  lq.load(sQ0, s0 * HD_BK, wave, tid);
-  const int one = s0 + 1 < s1 ? s0 + 1 : HD_PAST;
-  lp.load(sP1, one * HD_BK, wave, tid);
-  lq.load(sQ1, one * HD_BK, wave, tid);
-  HEAD_WAIT_VM(LD);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void*)lds;
+  const typename OP::template Reader<TP> rp(wp * C::WTP, lane);
+  const typename OQ::template Reader<TQ> rq(wq * C::WTQ, lane);
+  // Load n of a step: the near operand's first.
+  auto load = [&](int n, int sp, int sq) {
+    constexpr int FIRST = RP > RQ ? OQ::CH : OP::CH;
+    if (n < FIRST) {
+      if (RP > RQ) lq.slot(lds0 + sq, n, wave, tid);
+      else lp.slot(lds0 + sp, n, wave, tid);
+    } else {
+      if (RP > RQ) lp.slot(lds0 + sp, n - FIRST, wave, tid);
+      else lq.slot(lds0 + sq, n - FIRST, wave, tid);
+    }
+  };
+  // in the order of the loop, where the far operand is a step ahead
+#pragma unroll
+  for (int s = 0; s < RMAX; ++s) {
+    const int sp = s - (RMAX - RP), sq = s - (RMAX - RQ);
+    if (sp >= 0 && RP <= RQ) {
+      lp.begin(tid);
+      for (int i = 0; i < OP::CH; ++i) lp.slot(lds0 + sp * PB, i, wave, tid);
+      lp.end();
+    }
+    if (sq >= 0) {
+      lq.begin(tid);
+      for (int i = 0; i < OQ::CH; ++i) lq.slot(lds0 + RP * PB + sq * QB, i, wave, tid);
+      lq.end();
+    }
+    if (sp >= 0 && RP > RQ) {
+      lp.begin(tid);
+      for (int i = 0; i < OP::CH; ++i) lp.slot(lds0 + sp * PB, i, wave, tid);
+      lp.end();
+    }
+  }
+  HEAD_WAIT_VM(OUT + LD);
   head_barrier();
   u32x4 a[2][TP], b[2][TQ];
-  auto frags = [&](const char* sp, const char* sq, int kk) {
-#pragma unroll
-    for (int i = 0; i < TP; ++i)
-      a[kk & 1][i] = OP::frag(sp, wp * C::WTP + 32 * i, kk, lane);
-#pragma unroll
-    for (int j = 0; j < TQ; ++j)
-      b[kk & 1][j] = OQ::frag(sq, wq * C::WTQ + 32 * j, kk, lane);
+  // Fragment n of slice kk
+  auto frag = [&](int n, int sp, int sq, int kk) {
+    if (n < TP)
+      a[kk & 1][n] = rp.read(lds, sp, n, kk);
+    else
+      b[kk & 1][n - TP] = rq.read(lds, sq, n - TP, kk);
   };
-  frags(sP0, sQ0, 0);
-  // steps past the end load zeros: the loop runs whole pairs
-  for (int st = s0; st < s1; st += 2) {
+  int sp = 0, sq = RP * PB;        // this step's stages
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      char *cp = h ? sP1 : sP0, *cq = h ? sQ1 : sQ0;
-      const char *np = h ? sP0 : sP1, *nq = h ? sQ0 : sQ1;
+  for (int n = 0; n < FR; ++n) frag(n, sp, sq, 0);
+  for (int st = 0; st < steps; ++st) {
+    const int np = sp + PB == RP * PB ? 0 : sp + PB;
+    const int nq = sq + QB == RP * PB + RQ * QB ? RP * PB : sq + QB;
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        if (kk < 3) {
-          frags(cp, cq, kk + 1);
-        } else {
-          HEAD_WAIT_VM(0);
-          head_barrier();
-          __builtin_amdgcn_sched_barrier(0);
-          const int next = st + h + 2 < s1 ? st + h + 2 : HD_PAST;
-          lp.load(cp, next * HD_BK, wave, tid);
-          lq.load(cq, next * HD_BK, wave, tid);
-          frags(np, nq, 0);
-        }
+    for (int kk = 0; kk < 4; ++kk) {
+      if (kk < 3) {
 #pragma unroll
-        for (int g = 0; g < MPK; ++g) {
-          const int i = g / TQ, j = g % TQ;
-          acc[i][j] = mfma32(a[kk & 1][i], b[kk & 1][j], acc[i][j]);
-        }
-#pragma unroll
-        for (int g = 0; g < MPK; ++g) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                     // MFMA
-          if (g * RDM < RD) __builtin_amdgcn_sched_group_barrier(0x100, RDM, 0); // LDS read
-          if (kk == 3 && g * LDM < LD) __builtin_amdgcn_sched_group_barrier(0x020, LDM, 0);
-        }
+        for (int n = 0; n < FR; ++n) frag(n, sp, sq, kk + 1);
+      } else {
+        HEAD_WAIT_VM(OUT);
+        head_barrier();
         __builtin_amdgcn_sched_barrier(0);
+        lp.begin(tid);
+        lq.begin(tid);
+#pragma unroll
+        for (int n = 0; n < (LD > FR ? LD : FR); ++n) {
+          if (n < FR) frag(n, np, nq, 0);
+          if (n < LD) load(n, sp, sq);
+        }
+        lp.end();
+        lq.end();
       }
+#pragma unroll
+      for (int g = 0; g < MPK; ++g) {
+        const int i = g / TQ, j = g % TQ;
+        acc[i][j] = mfma32(a[kk & 1][i], b[kk & 1][j], acc[i][j]);
+      }
+#pragma unroll
+      for (int g = 0; g < MPK; ++g) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                     // MFMA
+        if (g * RDM < RD) __builtin_amdgcn_sched_group_barrier(0x100, RDM, 0); // LDS read
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
+    sp = np;
+    sq = nq;
   }
   HEAD_WAIT_VM(0);   // nothing of this workgroup's is on its way into LDS
 }
@@ -256,19 +377,17 @@ __device__ __forceinline__ void pack_rows(const float (&x)[16], u32x4 (&out)[2])
   }
 }
 
-#define HEAD_LDS(C)                                                       \
-  __shared__ __attribute__((aligned(16))) char sP0[C::BP * HD_BK * 2];    \
-  __shared__ __attribute__((aligned(16))) char sP1[C::BP * HD_BK * 2];    \
-  __shared__ __attribute__((aligned(16))) char sQ0[C::BQ * HD_BK * 2];    \
-  __shared__ __attribute__((aligned(16))) char sQ1[C::BQ * HD_BK * 2];    \
-  const int tid = threadIdx.x, lane = tid & 63;                           \
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);              \
+#define HEAD_LDS(C, RP, RQ)                                                            \
+  constexpr int RINGP = RP, RINGQ = RQ;                                                \
+  __shared__ __attribute__((aligned(1024))) char lds[(RP * C::BP + RQ * C::BQ) * HD_BK * 2]; \
+  const int tid = threadIdx.x, lane = tid & 63;                                        \
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);                           \
   const int wp = wave / C::WQ, wq = wave % C::WQ
 
 template <int TILE, bool BWD>
 __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_logits(HeadLogits a) {
   using C = HeadCfg<TILE>;
-  HEAD_LDS(C);
+  HEAD_LDS(C, C::RFAR, C::RNEAR);
   const int cnt = *a.cnt;
   int tp, tq;
   if (!head_tile_at(blockIdx.x, (int)((a.v1 - a.v0 + C::BP - 1) / C::BP), (cnt + C::BQ - 1) / C::BQ,
@@ -276,13 +395,15 @@ __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_logits(HeadLogits a)
     return;
   const int64_t p0 = a.v0 + (int64_t)tp * C::BP;      // first word
   const int q0 = tq * C::BQ;                          // first counted row
-  HeadLoader<C::BP, false, C::NT> lp;
-  HeadLoader<C::BQ, false, C::NT> lq;
+  HeadLoader<C::BP, HK_N, C::NT> lp;
+  HeadLoader<C::BQ, HK_N, C::NT> lq;
   using OP = typename decltype(lp)::O;
   using OQ = typename decltype(lq)::O;
   lp.base = reinterpret_cast<const char*>(a.w + p0 * a.dim);
   lp.bytes = (uint32_t)(min<int64_t>(C::BP, a.vocab - p0) * a.dim * 2);
-  lp.end = lq.end = a.dim;
+  lp.step_bytes = lq.step_bytes = HD_BK * 2;
+  lp.start(0, a.dim);
+  lq.start(0, a.dim);
 #pragma unroll
   for (int i = 0; i < OP::CH; ++i)
     lp.vo[i] = (uint32_t)(OP::row_n(tid, i) * a.dim + OP::red_n(tid)) * 2;
@@ -295,7 +416,7 @@ __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_logits(HeadLogits a)
   }
   f32x16 acc[C::TP][C::TQ];
   zero_acc<TILE>(acc);
-  head_mainloop<TILE>(lp, lq, sP0, sP1, sQ0, sQ1, 0, (a.dim + HD_BK - 1) / HD_BK, wave, tid, lane, acc);
+  head_mainloop<TILE, RINGP, RINGQ>(lp, lq, lds, (a.dim + HD_BK - 1) / HD_BK, wave, tid, lane, acc);
 
   // word of accumulator v of tile i: pw + 32 i + 8 (v / 4) + v % 4
   const int64_t pw = p0 + wp * C::WTP + 4 * (lane >> 5);
@@ -346,7 +467,8 @@ __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_logits(HeadLogits a)
           x[v] = !row || o >= left ? 0.0f : (o == lab ? -1.0f : e);
         }
         pack_rows(x, out);
-        uint16_t* g = a.g + (int64_t)m * a.vp + (p0 - a.v0) + wp * C::WTP + 32 * i + 8 * (lane >> 5);
+        const int64_t v = (p0 - a.v0) + wp * C::WTP + 32 * i;
+        uint16_t* g = a.g + g_block(m, v, a.vp) + (m & 255) * HD_BK + (v & 63) + 8 * (lane >> 5);
         *reinterpret_cast<u32x4*>(g) = out[0];
         *reinterpret_cast<u32x4*>(g + 16) = out[1];
       }
@@ -357,37 +479,40 @@ __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_logits(HeadLogits a)
 template <int TILE>
 __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_dx(HeadDx a) {
   using C = HeadCfg<TILE>;
-  HEAD_LDS(C);
+  HEAD_LDS(C, C::RFAR, C::RNEAR);
   const int cnt = *a.cnt;
   const int tiles_p = (a.dim + C::BP - 1) / C::BP;
   int tp, tq;
   if (!head_tile_at(blockIdx.x, tiles_p, (cnt + C::BQ - 1) / C::BQ, tp, tq)) return;
   const int slice = blockIdx.y;
   const int k0 = tp * C::BP, q0 = tq * C::BQ;
-  HeadLoader<C::BP, true, C::NT> lp;
-  HeadLoader<C::BQ, false, C::NT> lq;
+  HeadLoader<C::BP, HK_T, C::NT> lp;
+  HeadLoader<C::BQ, HK_N, C::NT> lq;
   using OP = typename decltype(lp)::O;
   using OQ = typename decltype(lq)::O;
   lp.base = reinterpret_cast<const char*>(a.w + a.v0 * a.dim);
-  lp.pitch = (int64_t)a.dim * 2;
-  lp.end = (int)a.n;
+  lp.bytes = (uint32_t)a.dim * 2;
+  lp.step_bytes = a.dim * (HD_BK * 2);
 #pragma unroll
   for (int i = 0; i < OP::CH; ++i) {
     const int k = k0 + OP::col_t(tid);
     lp.vo[i] = k < a.dim ? (uint32_t)(OP::red_t(tid, i) * a.dim + k) * 2 : G_OOB;
   }
-  lq.base = reinterpret_cast<const char*>(a.g + (int64_t)q0 * a.vp);
-  lq.bytes = (uint32_t)(C::BQ * a.vp * 2);
-  lq.end = (int)a.vp;
+  lq.base = reinterpret_cast<const char*>(a.g + g_block(q0, 0, a.vp) + (q0 & 255) * HD_BK);
+  lq.bytes = 0x7fffffffu;
+  lq.step_bytes = 256 * HD_BK * 2;
 #pragma unroll
   for (int i = 0; i < OQ::CH; ++i)
-    lq.vo[i] = (uint32_t)(OQ::row_n(tid, i) * a.vp + OQ::red_n(tid)) * 2;
+    lq.vo[i] = (uint32_t)(OQ::row_n(tid, i) * HD_BK + OQ::red_n(tid)) * 2;
   const int steps = (int)((a.n + HD_BK - 1) / HD_BK);
-  const int s0 = (int)((int64_t)steps * slice / a.slices);
-  const int s1 = (int)((int64_t)steps * (slice + 1) / a.slices);
+  const int each = steps / a.slices, rest = steps % a.slices;
+  const int s0 = __builtin_amdgcn_readfirstlane(slice * each + min(slice, rest));
+  const int s1 = __builtin_amdgcn_readfirstlane(s0 + each + (slice < rest));
   f32x16 acc[C::TP][C::TQ];
   zero_acc<TILE>(acc);
-  head_mainloop<TILE>(lp, lq, sP0, sP1, sQ0, sQ1, s0, s1, wave, tid, lane, acc);
+  lp.start(s0, (int)a.n);
+  lq.start(s0, (int)a.vp);
+  head_mainloop<TILE, RINGP, RINGQ>(lp, lq, lds, s1 - s0, wave, tid, lane, acc);
 
 #pragma unroll
   for (int j = 0; j < C::TQ; ++j) {
@@ -432,21 +557,23 @@ __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_dx(HeadDx a) {
 template <int TILE>
 __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_dw(HeadDw a) {
   using C = HeadCfg<TILE>;
-  HEAD_LDS(C);
+  HEAD_LDS(C, C::RNEAR, C::RFAR);
   const int cnt = *a.cnt;
   int tp, tq;
   if (!head_tile_at(blockIdx.x, (a.dim + C::BP - 1) / C::BP, (int)((a.n + C::BQ - 1) / C::BQ), tp, tq))
     return;
   const int k0 = tp * C::BP, q0 = tq * C::BQ;
-  HeadLoader<C::BP, true, C::NT> lp;
-  HeadLoader<C::BQ, true, C::NT> lq;
+  HeadLoader<C::BP, HK_T, C::NT> lp;
+  HeadLoader<C::BQ, HK_TG, C::NT> lq;
   using OP = typename decltype(lp)::O;
   using OQ = typename decltype(lq)::O;
   lp.base = reinterpret_cast<const char*>(a.xs);
-  lp.pitch = (int64_t)a.dim * 2;
-  lq.base = reinterpret_cast<const char*>(a.g);
-  lq.pitch = a.vp * 2;
-  lp.end = lq.end = cnt;
+  lp.bytes = (uint32_t)a.dim * 2;
+  lp.step_bytes = a.dim * (HD_BK * 2);
+  lp.start(0, cnt);
+  lq.start(0, cnt);
+  lq.base = reinterpret_cast<const char*>(a.g + g_block(0, q0, a.vp));
+  lq.vp_bytes = a.vp * (256 * 2);
 #pragma unroll
   for (int i = 0; i < OP::CH; ++i) {
     const int k = k0 + OP::col_t(tid);
@@ -454,12 +581,14 @@ __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_dw(HeadDw a) {
   }
 #pragma unroll
   for (int i = 0; i < OQ::CH; ++i) {
-    const int v = q0 + OQ::col_t(tid);
-    lq.vo[i] = v < a.vp ? (uint32_t)(OQ::red_t(tid, i) * a.vp + v) * 2 : G_OOB;
+    const int v = (q0 & 63) + OQ::col_t(tid);
+    lq.vo[i] = q0 + OQ::col_t(tid) < a.vp
+                   ? (uint32_t)((v >> 6) * (256 * HD_BK) + OQ::red_t(tid, i) * HD_BK + (v & 63)) * 2
+                   : G_OOB;
   }
   f32x16 acc[C::TP][C::TQ];
   zero_acc<TILE>(acc);
-  head_mainloop<TILE>(lp, lq, sP0, sP1, sQ0, sQ1, 0, (cnt + HD_BK - 1) / HD_BK, wave, tid, lane, acc);
+  head_mainloop<TILE, RINGP, RINGQ>(lp, lq, lds, (cnt + HD_BK - 1) / HD_BK, wave, tid, lane, acc);
 #pragma unroll
   for (int j = 0; j < C::TQ; ++j) {
     const int v = q0 + wq * C::WTQ + 32 * j + (lane & 31);
