@@ -41,7 +41,9 @@ EXPORTS = ("nf4_codebook", "nf4_quantize", "nf4_dequantize",
            "qn_seq_workspace_bytes", "qn_seq_logprob", "qn_seq_logprob_bwd",
            "qn_pref_loss_fwd", "qn_pref_loss_bwd",
            "qn_head_fwd_workspace_bytes", "qn_head_bwd_workspace_bytes",
-           "qn_head_loss_fwd", "qn_head_loss_bwd")
+           "qn_head_loss_fwd", "qn_head_loss_bwd",
+           "qn_orth_workspace_bytes", "qn_orthogonalize",
+           "qn_muon_workspace_bytes", "qn_muon_step")
 QN_FWD_BATCH_MAX = 8
 QN_DEQUANT_BATCH_MAX = 16
 QN_CODE_NF4, QN_CODE_FP4, QN_CODE_INT4 = 0, 1, 2
@@ -108,6 +110,29 @@ class _Head(ctypes.Structure):
     _fields_ = [("x", ctypes.c_void_p), ("w", ctypes.c_void_p),
                 ("labels", ctypes.c_void_p), ("rows", ctypes.c_int64),
                 ("dim", ctypes.c_int64), ("vocab", ctypes.c_int64)]
+
+
+class _OrthHP(ctypes.Structure):
+    _fields_ = [("coef", ctypes.c_double * 3), ("eps", ctypes.c_double),
+                ("steps", ctypes.c_int32)]
+
+
+class _OrthJob(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("x_dtype", ctypes.c_int32),
+                ("y", ctypes.c_void_p), ("y_dtype", ctypes.c_int32),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
+
+
+class _MuonJob(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("g", ctypes.c_void_p),
+                ("m", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64)]
+
+
+class _MuonHP(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("momentum", ctypes.c_double),
+                ("weight_decay", ctypes.c_double), ("grad_scale", ctypes.c_double),
+                ("nesterov", ctypes.c_int32), ("orth", _OrthHP)]
 
 
 _lib = None
@@ -228,6 +253,15 @@ def lib() -> ctypes.CDLL:
     L.qn_head_loss_fwd.restype = ctypes.c_int
     L.qn_head_loss_bwd.argtypes = [hdp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     L.qn_head_loss_bwd.restype = ctypes.c_int
+    op, mp, ohp, mhp = (ctypes.POINTER(s) for s in (_OrthJob, _MuonJob, _OrthHP, _MuonHP))
+    L.qn_orth_workspace_bytes.argtypes = [op, i32]
+    L.qn_orth_workspace_bytes.restype = sz
+    L.qn_orthogonalize.argtypes = [op, i32, ohp, vp, sz, vp]
+    L.qn_orthogonalize.restype = ctypes.c_int
+    L.qn_muon_workspace_bytes.argtypes = [mp, i32]
+    L.qn_muon_workspace_bytes.restype = sz
+    L.qn_muon_step.argtypes = [mp, i32, mhp, vp, sz, vp]
+    L.qn_muon_step.restype = ctypes.c_int
     L.qn_profile_kernel.argtypes = [ctypes.c_char_p, vp, vp, i32]
     L.qn_profile_kernel.restype = ctypes.c_int
     L.qn_strerror.argtypes = [ctypes.c_int]
@@ -1205,6 +1239,117 @@ def qn_head_loss_bwd(x, w, labels, fwd: HeadLoss, dloss=None, dx=None, need_dx: 
                                           None if gw is None else gw.data_ptr(), pw, nw, st))
         return gx, gw
     return _run_on(index, stream, body)
+
+
+# ---------------------------------------------------------------------------
+# Orthogonalised matrices and the momentum step with them
+# ---------------------------------------------------------------------------
+
+ORTH_COEF = (3.4445, -4.7750, 2.0315)
+
+
+def _orth_hp(steps, coef, eps) -> _OrthHP:
+    return _OrthHP((ctypes.c_double * 3)(*(float(c) for c in coef)), float(eps), int(steps))
+
+
+def _matrix(fn: str, name: str, t, index: int | None):
+    """(device index, (rows, cols)) of a dense matrix."""
+    if index is None:
+        index = _gpu(fn, name, t)
+    if t.dim() != 2 or t.shape[0] < 1 or t.shape[1] < 1:
+        raise _bad(fn, f"{name} must be [rows, cols]")
+    _tensor(fn, name, t, t.shape, None, index)
+    return index, t.shape
+
+
+def qn_orthogonalize(x, out=None, dtype: int | None = None, steps: int = 5, coef=ORTH_COEF,
+                     eps: float = 1e-7, ws=None, stream=None):
+    """Newton-Schulz steps on a matrix [rows, cols] (fp32 or bf16, the fewer
+    of rows and cols at most 256), or on a list of them in one call; returns
+    the result in `dtype` (x's type), or the list of them.  out: a tensor (or a
+    list) to write to, which may be x itself with the same type."""
+    import torch
+    fn = "qn_orthogonalize"
+    many = isinstance(x, (list, tuple))
+    xs = list(x) if many else [x]
+    outs = [None] * len(xs) if out is None else (list(out) if many else [out])
+    if not xs or len(outs) != len(xs):
+        raise _bad(fn, "x and out must be as many matrices")
+    index = None
+    for t in xs:
+        index, _ = _matrix(fn, "x", t, index)
+
+    def body(st):
+        arr = (_OrthJob * len(xs))()
+        for i, t in enumerate(xs):
+            code = _dtype_code(fn, "x", t)
+            y = outs[i]
+            if y is None:
+                y = outs[i] = torch.empty_like(t, dtype=_torch_dtype(
+                    fn, code if dtype is None else dtype))
+            arr[i] = _OrthJob(t.data_ptr(), code, _tensor(fn, "out", y, t.shape, None, index),
+                              _dtype_code(fn, "out", y), t.shape[0], t.shape[1])
+        need = int(lib().qn_orth_workspace_bytes(arr, len(xs)))
+        if need == 0:
+            raise _bad(fn, "a matrix's size is out of range")
+        if ws is None:
+            w = torch.empty(need, dtype=torch.uint8, device=xs[0].device)
+            pw = w.data_ptr()
+        else:
+            pw, need = _workspace(fn, ws, index)
+        _check(fn, lib().qn_orthogonalize(arr, len(xs), _orth_hp(steps, coef, eps), pw, need, st))
+        return outs if many else outs[0]
+    return _run_on(index, stream, body)
+
+
+class MuonBatch:
+    """Descriptors of a qn_muon_step call, with its workspace, kept alive with
+    the tensors they point to.  jobs: sequence of (p, g, m): a bf16 parameter
+    [rows, cols], its fp32 gradient and its fp32 momentum (None: zeros of its
+    own), which the steps read and update where they lie.  Steps of one batch
+    that run at the same time (on different streams) share its workspace and
+    must not."""
+
+    def __init__(self, jobs):
+        import torch
+        fn = "MuonBatch"
+        jobs = list(jobs)
+        if not jobs:
+            raise _bad(fn, "no parameters")
+        f32 = torch.float32
+        self.index, self.keep, self.momenta = None, [], []
+        arr = (_MuonJob * len(jobs))()
+        for i, (p, g, m) in enumerate(jobs):
+            self.index, shape = _matrix(fn, "p", p, self.index)
+            if m is None:
+                m = torch.zeros(shape, dtype=f32, device=p.device)
+            arr[i] = _MuonJob(_tensor(fn, "p", p, shape, torch.bfloat16, self.index),
+                              _tensor(fn, "g", g, shape, f32, self.index),
+                              _tensor(fn, "m", m, shape, f32, self.index), shape[0], shape[1])
+            self.keep += [p, g]
+            self.momenta.append(m)
+        self.arr, self.count = arr, len(jobs)
+        self.ws_bytes = int(lib().qn_muon_workspace_bytes(arr, self.count))
+        if self.ws_bytes == 0:
+            raise _bad(fn, "a parameter's size is out of range")
+        self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=jobs[0][0].device)
+
+
+def qn_muon_workspace_bytes(batch: MuonBatch) -> int:
+    return int(lib().qn_muon_workspace_bytes(batch.arr, batch.count))
+
+
+def qn_muon_step(batch: MuonBatch, lr=0.02, momentum=0.95, nesterov=True, weight_decay=0.0,
+                 grad_scale=1.0, steps: int = 5, coef=ORTH_COEF, eps: float = 1e-7, stream=None):
+    """One momentum step with orthogonalised updates on a MuonBatch's
+    parameters and momenta, in place."""
+    hp = _MuonHP(float(lr), float(momentum), float(weight_decay), float(grad_scale),
+                 int(bool(nesterov)), _orth_hp(steps, coef, eps))
+
+    def body(st):
+        _check("qn_muon_step", lib().qn_muon_step(batch.arr, batch.count, hp, batch.ws.data_ptr(),
+                                                  batch.ws_bytes, st))
+    _run_on(batch.index, stream, body)
 
 
 def qn_profile_kernel(name: str | None, starts=None, stops=None) -> int:

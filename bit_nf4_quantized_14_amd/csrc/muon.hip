@@ -1,0 +1,790 @@
+// Orthogonalised matrices by Newton-Schulz products, and the momentum step
+// whose update they are (K. Jordan et al., "Muon: An optimizer for hidden
+// layers in neural networks", 2024).
+//
+//   X_0 = U / (|U|_F + eps),  A_k = X_k X_k^T,
+//   X_{k+1} = (a I + b A_k + c A_k^2) X_k
+//
+// An adapter's matrix has a short side r <= 256.  All X_k are U times a
+// polynomial of one r x r matrix, so no step but the first and the last
+// touches U:
+//   A_0 = U U^T / (|U| + eps)^2 (|U|^2 its trace)          k_orth_gram
+//   P_k = a I + b A_k + c A_k^2,  A_{k+1} = P_k A_k P_k,
+//   Q = P_{s-1} ... P_0 / (|U| + eps)                       k_orth_poly
+//   O = Q U                                                 k_orth_apply
+// The r x r matrices are held in 64 bits: a small singular value grows by a =
+// 3.44 with every step, so an error d in A_0 moves its direction's factor by
+// about 1.4 (11.9^0 + ... + 11.9^(s-1)) d, 3e4 d after five steps.
+//
+// A matrix is seen as r rows ("short" index i) of its long side l, wherever
+// they lie: element (i, l) at i L + l (wide) or l r + i (tall).
+#include <algorithm>
+#include <cmath>
+
+#include "muon_plan.h"
+#include "qn_host.h"
+
+namespace {
+
+using namespace qn;
+
+typedef double f64x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+struct OrthJob {
+  const void* g;        // gradient, or the matrix
+  float* m;             // momentum
+  void* out;            // parameter (in place), or the result
+  int32_t L, r;
+  int32_t tall, vec;
+  int32_t slices;
+  float step;           // lr times the matrix's scale
+};
+struct OrthBatch {
+  OrthJob job[ORTH_JOBS];
+  int32_t count, steps, max_slices;
+  int32_t gfirst[ORTH_JOBS + 1];    // first workgroup of a job in k_orth_gram
+  int32_t afirst[ORTH_JOBS + 1];    // and in k_orth_apply
+  double a, b, c, eps;
+  float mu, gs, decay;
+  int32_t nesterov;
+  double* part;                     // [job][max_slices][pairs][4][64]
+  float* q;                         // [job][16 rt][16 rt]
+  double* inv;                      // [job]
+  double* mats;                     // [job][ORTH_MATS][16 rt][16 rt]
+};
+static_assert(sizeof(OrthBatch) <= 4096, "kernel arguments");
+
+// What U is: a matrix of fp32 or bf16, or the momentum's (Nesterov) update.
+enum OrthMode { OM_F32 = 0, OM_BF16 = 1, OM_MUON = 2 };
+
+__device__ __forceinline__ int job_of(const int32_t* first, int count, int block) {
+  int j = 0;
+  while (j + 1 < count && block >= first[j + 1]) ++j;
+  return j;
+}
+
+template <int RT>
+struct OrthCfg {
+  static constexpr int RP = 16 * RT, LC = orth_chunk(RT), NT = orth_threads(RT);
+  static constexpr int PITCH = LC + 4;         // floats; rows 4 banks apart
+  static constexpr int G4 = RP * LC / 4 / NT;  // groups of 4 elements of a thread
+  static constexpr int PAIRS = orth_pairs(RT);
+  static_assert(G4 * NT * 4 == RP * LC, "chunk");
+};
+
+// m' = mu m + g gs; u = g gs + mu m' (Nesterov) or m'.  Every operation
+// rounds once, in this order.
+__device__ __forceinline__ float muon_u(float g, float& m, const OrthBatch& b) {
+#pragma clang fp contract(off)
+  const float gg = g * b.gs;
+  m = b.mu * m + gg;
+  return b.nesterov ? gg + b.mu * m : m;
+}
+
+// Group k of thread tid: four elements that are neighbours in memory (`e` the
+// first's index there, from the chunk's first), n of them inside the matrix.
+template <int RT>
+struct OrthGroup4 {
+  using C = OrthCfg<RT>;
+  int64_t e;
+  int n;
+  int i[4], l[4];       // their places in the chunk
+  __device__ __forceinline__ OrthGroup4(const OrthJob& J, int chunk, int tid, int k) {
+    const int at = (tid + C::NT * k) * 4;
+    const int l0 = chunk * C::LC, nl = min(C::LC, J.L - l0);
+    if (!J.tall) {
+      i[0] = at / C::LC;
+      l[0] = at % C::LC;
+      e = (int64_t)i[0] * J.L + l0 + l[0];
+      n = i[0] < J.r ? max(0, min(4, nl - l[0])) : 0;
+#pragma unroll
+      for (int x = 1; x < 4; ++x) {
+        i[x] = i[0];
+        l[x] = l[0] + x;
+      }
+    } else {
+      e = (int64_t)l0 * J.r + at;
+      n = max(0, min(4, nl * J.r - at));
+      const float inv = 1.0f / (float)J.r;
+      // exact: at < 2^14, and a quotient is 1 / 512 from a whole number
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        l[x] = (int)(((float)(at + x) + 0.5f) * inv);
+        i[x] = at + x - l[x] * J.r;
+      }
+    }
+  }
+  // whether the group belongs to the chunk at all (a tall chunk has r of RP
+  // rows)
+  __device__ __forceinline__ bool in(const OrthJob& J, int tid, int k) const {
+    return !J.tall || (tid + C::NT * k) * 4 < C::LC * J.r;
+  }
+};
+
+template <class T4, class T>
+__device__ __forceinline__ void load4(const T* p, int n, bool vec, T (&v)[4]) {
+  if (vec && n == 4) {
+    const T4 x = *reinterpret_cast<const T4*>(p);
+    __builtin_memcpy(v, &x, sizeof(x));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = i < n ? p[i] : T(0);
+  }
+}
+template <class T4, class T>
+__device__ __forceinline__ void store4(T* p, int n, bool vec, const T (&v)[4]) {
+  if (vec && n == 4) {
+    T4 x;
+    __builtin_memcpy(&x, v, sizeof(x));
+    *reinterpret_cast<T4*>(p) = x;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) p[i] = v[i];
+  }
+}
+
+// U of a group; with OM_MUON also the new momentum.
+template <int MODE, int RT>
+__device__ __forceinline__ void orth_load(const OrthJob& J, const OrthBatch& b,
+                                          const OrthGroup4<RT>& at, float (&u)[4], float (&m)[4]) {
+  const bool vec = J.vec != 0;
+  if constexpr (MODE == OM_BF16) {
+    uint16_t v[4];
+    load4<u32x2>(static_cast<const uint16_t*>(J.g) + at.e, at.n, vec, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = bf16_to_f32(v[i]);
+  } else if constexpr (MODE == OM_F32) {
+    load4<f32x4>(static_cast<const float*>(J.g) + at.e, at.n, vec, u);
+  } else {
+    float g[4];
+    load4<f32x4>(static_cast<const float*>(J.g) + at.e, at.n, vec, g);
+    load4<f32x4>(static_cast<const float*>(J.m) + at.e, at.n, vec, m);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = muon_u(g[i], m[i], b);
+    // outside the matrix g and m are 0, and so is u
+  }
+}
+
+template <int RT>
+__device__ __forceinline__ void orth_put(float* s, const OrthJob& J, const OrthGroup4<RT>& at,
+                                         const float (&u)[4]) {
+  using C = OrthCfg<RT>;
+  if (!J.tall) {
+    *reinterpret_cast<f32x4*>(s + at.i[0] * C::PITCH + at.l[0]) = f32x4{u[0], u[1], u[2], u[3]};
+  } else {
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      // a chunk of r LC elements may end inside a group
+      if (at.l[x] < C::LC) s[at.i[x] * C::PITCH + at.l[x]] = u[x];
+    }
+  }
+}
+
+// Rows of the chunk that a tall matrix does not have.
+template <int RT>
+__device__ __forceinline__ void orth_pad(float* s, const OrthJob& J, int tid) {
+  using C = OrthCfg<RT>;
+  if (J.tall)
+    for (int x = J.r * C::PITCH + tid; x < C::RP * C::PITCH; x += C::NT) s[x] = 0.0f;
+}
+
+// Pair p of tile rows i >= j, in the order (0,0) (1,0) (1,1) (2,0) ...
+__device__ __forceinline__ void orth_pair(int p, int& i, int& j) {
+  i = 0;
+  while ((i + 1) * (i + 2) / 2 <= p) ++i;
+  j = p - i * (i + 1) / 2;
+}
+
+// Partial Gram matrices: workgroup (job, slice) sums u u^T over its chunks
+// with v_mfma_f64_16x16x4_f64 (lane l gives row l % 16, reduction l / 16 of
+// either operand; accumulator v holds row 4 v + l / 16, column l % 16).
+// Up to 64 rows a wave takes every fourth group of four positions and all
+// pairs of tiles, above that all positions and every fourth (eighth) pair.
+template <int MODE, int RT>
+__global__ __launch_bounds__(orth_threads(RT)) void k_orth_gram(OrthBatch b) {
+  using C = OrthCfg<RT>;
+  constexpr int WAVES = C::NT / 64;
+  constexpr bool SPLIT = RT <= 4;                        // positions over the waves
+  constexpr int NP = SPLIT ? C::PAIRS : (C::PAIRS + WAVES - 1) / WAVES;
+  __shared__ __attribute__((aligned(16))) float s[C::RP * C::PITCH];
+  __shared__ double red[SPLIT ? C::PAIRS * 256 : 1];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int jx = job_of(b.gfirst, b.count, blockIdx.x);
+  const OrthJob& J = b.job[jx];
+  const int slice = blockIdx.x - b.gfirst[jx];
+  const int chunks = (J.L + C::LC - 1) / C::LC;
+  const int c0 = (int)((int64_t)chunks * slice / J.slices);
+  const int c1 = (int)((int64_t)chunks * (slice + 1) / J.slices);
+  f64x4 acc[NP];
+#pragma unroll
+  for (int p = 0; p < NP; ++p) acc[p] = f64x4{0, 0, 0, 0};
+  orth_pad<RT>(s, J, tid);
+  for (int c = c0; c < c1; ++c) {
+#pragma unroll
+    for (int k = 0; k < C::G4; ++k) {
+      const OrthGroup4<RT> at(J, c, tid, k);
+      if (!at.in(J, tid, k)) continue;
+      float u[4], m[4];
+      orth_load<MODE, RT>(J, b, at, u, m);
+      orth_put<RT>(s, J, at, u);
+    }
+    __syncthreads();
+    const float* from = s + (lane & 15) * C::PITCH + (lane >> 4);
+    if constexpr (SPLIT) {
+#pragma unroll 4
+      for (int k = wave; k < C::LC / 4; k += WAVES) {
+        double x[RT];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) x[t] = (double)from[16 * t * C::PITCH + 4 * k];
+        int p = 0;
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int j = 0; j <= i; ++j, ++p)
+            acc[p] = __builtin_amdgcn_mfma_f64_16x16x4f64(x[i], x[j], acc[p], 0, 0, 0);
+      }
+    } else {
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        int i, j;
+        orth_pair(min(wave + WAVES * p, C::PAIRS - 1), i, j);
+        const float *fi = from + 16 * i * C::PITCH, *fj = from + 16 * j * C::PITCH;
+#pragma unroll 4
+        for (int k = 0; k < C::LC / 4; ++k)
+          acc[p] = __builtin_amdgcn_mfma_f64_16x16x4f64((double)fi[4 * k], (double)fj[4 * k],
+                                                        acc[p], 0, 0, 0);
+      }
+    }
+    __syncthreads();
+  }
+  double* to = b.part + ((int64_t)jx * b.max_slices + slice) * (C::PAIRS * 256);
+  if constexpr (SPLIT) {
+    for (int w = 0; w < WAVES; ++w) {
+      if (wave == w) {
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            double* r = red + (p * 4 + v) * 64 + lane;
+            *r = w == 0 ? acc[p][v] : *r + acc[p][v];
+          }
+      }
+      __syncthreads();
+    }
+    for (int x = tid; x < C::PAIRS * 256; x += C::NT) to[x] = red[x];
+  } else {
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+      if (wave + WAVES * p < C::PAIRS)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) to[((wave + WAVES * p) * 4 + v) * 64 + lane] = acc[p][v];
+  }
+}
+
+// Sum of a Gram element's partials, four at a time in flight.
+__device__ __forceinline__ double orth_sum(const double* part, int64_t stride, int slices) {
+  double s = 0.0;
+  for (int i = 0; i < slices; i += 8) {
+    double v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = i + k < slices ? part[(i + k) * stride] : 0.0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += v[k];
+  }
+  return s;
+}
+
+// Rows and columns of element x (accumulator layout) of the pairs.
+__device__ __forceinline__ void orth_place(int x, int& row, int& col) {
+  int i, j;
+  orth_pair(x >> 8, i, j);
+  row = 16 * i + 4 * ((x >> 6) & 3) + ((x & 63) >> 4);
+  col = 16 * j + (x & 15);
+}
+
+// The polynomials of a matrix with at most 64 rows: one workgroup, everything
+// in LDS.  All matrices are polynomials of A_0: symmetric, and they commute,
+// so X Y is formed as X Y^T from rows alone, its tiles on and below the
+// diagonal, and mirrored.
+template <int RT>
+struct OrthPoly {
+  static constexpr int RP = 16 * RT, PITCH = RP + 4;      // doubles
+  static constexpr int NT = RT == 4 ? 512 : 256, WAVES = NT / 64;
+  static constexpr int PAIRS = orth_pairs(RT);
+  static __device__ __forceinline__ void mul(double* dst, const double* x, const double* y,
+                                             int wave, int lane) {
+    for (int p = wave; p < PAIRS; p += WAVES) {
+      int i, j;
+      orth_pair(p, i, j);
+      const double* fx = x + (16 * i + (lane & 15)) * PITCH + (lane >> 4);
+      const double* fy = y + (16 * j + (lane & 15)) * PITCH + (lane >> 4);
+      f64x4 acc = {0, 0, 0, 0};
+#pragma unroll
+      for (int k = 0; k < RP; k += 4)
+        acc = __builtin_amdgcn_mfma_f64_16x16x4f64(fx[k], fy[k], acc, 0, 0, 0);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int row = 16 * i + 4 * v + (lane >> 4), col = 16 * j + (lane & 15);
+        dst[row * PITCH + col] = acc[v];
+        if (i != j) dst[col * PITCH + row] = acc[v];
+      }
+    }
+    __syncthreads();
+  }
+};
+
+template <int RT>
+__global__ __launch_bounds__(OrthPoly<RT>::NT) void k_orth_poly(OrthBatch b) {
+  using C = OrthPoly<RT>;
+  __shared__ double lds[4 * C::RP * C::PITCH];
+  __shared__ double s_norm;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const OrthJob& J = b.job[blockIdx.x];
+  double *A = lds, *P = lds + C::RP * C::PITCH, *Q = P + C::RP * C::PITCH,
+         *X = Q + C::RP * C::PITCH;
+  const double* part = b.part + (int64_t)blockIdx.x * b.max_slices * (C::PAIRS * 256);
+  for (int x = tid; x < C::PAIRS * 256; x += C::NT) {
+    int row, col;
+    orth_place(x, row, col);
+    const double v = orth_sum(part + x, C::PAIRS * 256, J.slices);
+    A[row * C::PITCH + col] = v;
+    if ((row >> 4) != (col >> 4)) A[col * C::PITCH + row] = v;
+  }
+  __syncthreads();
+  if (wave == 0) {
+    double t = lane < C::RP ? A[lane * C::PITCH + lane] : 0.0;
+#pragma unroll
+    for (int d = 32; d > 0; d /= 2) t += __shfl_xor(t, d);
+    if (lane == 0) s_norm = 1.0 / (sqrt(t) + b.eps);
+  }
+  __syncthreads();
+  const double inv = s_norm;
+  for (int x = tid; x < C::RP * C::RP; x += C::NT) {
+    const int row = x / C::RP, col = x % C::RP;
+    A[row * C::PITCH + col] = (A[row * C::PITCH + col] * inv) * inv;
+    Q[row * C::PITCH + col] = row == col ? 1.0 : 0.0;
+  }
+  __syncthreads();
+  for (int st = 0; st < b.steps; ++st) {
+    C::mul(P, A, A, wave, lane);
+    for (int x = tid; x < C::RP * C::RP; x += C::NT) {
+      const int at = (x / C::RP) * C::PITCH + x % C::RP;
+      P[at] = (x / C::RP == x % C::RP ? b.a : 0.0) + b.b * A[at] + b.c * P[at];
+    }
+    __syncthreads();
+    if (st > 0) C::mul(X, P, Q, wave, lane);
+    double* R = st > 0 ? Q : X;          // free
+    if (st + 1 < b.steps) {
+      C::mul(R, P, A, wave, lane);
+      C::mul(A, R, P, wave, lane);
+    }
+    if (st > 0) {
+      double* t = Q;
+      Q = X;
+      X = t;
+    } else {
+      double* t = Q;
+      Q = P;
+      P = t;
+    }
+  }
+  float* q = b.q + (int64_t)blockIdx.x * C::RP * C::RP;
+  for (int x = tid; x < C::RP * C::RP; x += C::NT)
+    q[x] = (float)(Q[(x / C::RP) * C::PITCH + x % C::RP] * inv);
+}
+
+// The same for 65 to 256 rows, where a matrix fills more than a CU's LDS: one
+// launch for each set of products that do not wait for one another.
+template <int RT>
+__global__ __launch_bounds__(256) void k_orth_sum(OrthBatch b) {
+  constexpr int RP = 16 * RT, PAIRS = orth_pairs(RT);
+  const int jx = blockIdx.y, x = blockIdx.x * 256 + threadIdx.x;
+  int row, col;
+  orth_place(x, row, col);
+  const double v = orth_sum(b.part + (int64_t)jx * b.max_slices * (PAIRS * 256) + x, PAIRS * 256,
+                            b.job[jx].slices);
+  double* A = b.mats + (int64_t)jx * ORTH_MATS * RP * RP;
+  A[row * RP + col] = v;
+  if ((row >> 4) != (col >> 4)) A[col * RP + row] = v;
+}
+
+template <int RT>
+__global__ __launch_bounds__(1024) void k_orth_norm(OrthBatch b) {
+  constexpr int RP = 16 * RT;
+  __shared__ double s_sum[4];
+  const int tid = threadIdx.x, lane = tid & 63;
+  double* A = b.mats + (int64_t)blockIdx.x * ORTH_MATS * RP * RP;
+  if (tid < 256) {
+    double t = tid < RP ? A[tid * RP + tid] : 0.0;
+#pragma unroll
+    for (int d = 32; d > 0; d /= 2) t += __shfl_xor(t, d);
+    if (lane == 0) s_sum[tid >> 6] = t;
+  }
+  __syncthreads();
+  const double inv = 1.0 / (sqrt(((s_sum[0] + s_sum[1]) + s_sum[2]) + s_sum[3]) + b.eps);
+  if (tid == 0) b.inv[blockIdx.x] = inv;
+  for (int x = tid; x < RP * RP; x += 1024) A[x] = (A[x] * inv) * inv;
+}
+
+// dst = x y, for one or two products (blockIdx.z), 32 x 32 elements of the
+// lower half to a workgroup.  OB_P: a I + b x + c x y instead.  OB_Q: into q in
+// fp32, over the norm, instead of dst.
+enum { OB_P = 1, OB_Q = 2 };
+struct OrthMul {
+  int8_t dst, x, y, kind;       // matrices of a job
+};
+template <int RT>
+__global__ __launch_bounds__(256) void k_orth_mul(OrthBatch b, OrthMul m0, OrthMul m1) {
+  constexpr int RP = 16 * RT;
+  const OrthMul m = blockIdx.z == 0 ? m0 : m1;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int bi, bj;
+  orth_pair(blockIdx.x, bi, bj);
+  const int i = 2 * bi + (wave >> 1), j = 2 * bj + (wave & 1);
+  double* base = b.mats + (int64_t)blockIdx.y * ORTH_MATS * RP * RP;
+  const double* X = base + m.x * RP * RP;
+  // lane l takes reduction elements 16 k + 4 (l / 16) .. + 3 of its row
+  const f64x4* fx = reinterpret_cast<const f64x4*>(X + (16 * i + (lane & 15)) * RP + 4 * (lane >> 4));
+  const f64x4* fy = reinterpret_cast<const f64x4*>(base + m.y * RP * RP +
+                                                   (16 * j + (lane & 15)) * RP + 4 * (lane >> 4));
+  f64x4 acc = {0, 0, 0, 0};
+#pragma unroll 8
+  for (int k = 0; k < RP / 16; ++k) {
+    const f64x4 u = fx[4 * k], v = fy[4 * k];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      acc = __builtin_amdgcn_mfma_f64_16x16x4f64(u[e], v[e], acc, 0, 0, 0);
+  }
+  double* D = base + m.dst * RP * RP;
+  float* q = b.q + (int64_t)blockIdx.y * RP * RP;
+  const double inv = m.kind & OB_Q ? b.inv[blockIdx.y] : 0.0;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const int row = 16 * i + 4 * v + (lane >> 4), col = 16 * j + (lane & 15);
+    double d = acc[v];
+    if (m.kind & OB_P) d = (row == col ? b.a : 0.0) + b.b * X[row * RP + col] + b.c * d;
+    if (m.kind & OB_Q) {
+      q[row * RP + col] = (float)(d * inv);
+      if (bi != bj) q[col * RP + row] = (float)(d * inv);
+    } else {
+      D[row * RP + col] = d;
+      if (bi != bj) D[col * RP + row] = d;
+    }
+  }
+}
+
+// O = Q U of one chunk (v_mfma_f32_16x16x4_f32: lane l gives row or column l
+// % 16, reduction l / 16; accumulator v holds row 4 (l / 16) + v), and what
+// becomes of it: the result, or the parameter's step with the new momentum.
+template <int MODE, int RT, bool OUT_BF16>
+__global__ __launch_bounds__(orth_threads(RT)) void k_orth_apply(OrthBatch b) {
+  using C = OrthCfg<RT>;
+  constexpr int WAVES = C::NT / 64;
+  constexpr int IT = RT > WAVES ? RT / WAVES : 1;       // tile rows of a wave
+  __shared__ __attribute__((aligned(16))) float s[C::RP * C::PITCH];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int jx = job_of(b.afirst, b.count, blockIdx.x);
+  const OrthJob& J = b.job[jx];
+  const int chunk = blockIdx.x - b.afirst[jx];
+  float m[C::G4][4];
+  orth_pad<RT>(s, J, tid);
+#pragma unroll
+  for (int k = 0; k < C::G4; ++k) {
+    const OrthGroup4<RT> at(J, chunk, tid, k);
+    if (!at.in(J, tid, k)) continue;
+    float u[4];
+    orth_load<MODE, RT>(J, b, at, u, m[k]);
+    orth_put<RT>(s, J, at, u);
+  }
+  __syncthreads();
+  // a wave's tile rows ti, ti + WAVES, ... and its four tiles of positions
+  const int ti = RT >= WAVES ? wave : wave % RT, tl = RT >= WAVES ? 0 : 4 * (wave / RT);
+  f32x4 acc[IT][4];
+#pragma unroll
+  for (int i = 0; i < IT; ++i)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) acc[i][t] = f32x4{0, 0, 0, 0};
+  const float* q = b.q + (int64_t)jx * C::RP * C::RP;
+#pragma unroll 2
+  for (int k = 0; k < RT; ++k) {
+    // lane l takes reduction elements 16 k + 4 (l / 16) .. + 3
+    f32x4 a[IT];
+#pragma unroll
+    for (int i = 0; i < IT; ++i)
+      a[i] = *reinterpret_cast<const f32x4*>(q + (16 * (ti + WAVES * i) + (lane & 15)) * C::RP +
+                                             16 * k + 4 * (lane >> 4));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float* from = s + (16 * k + 4 * (lane >> 4) + e) * C::PITCH + 16 * tl + (lane & 15);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const float x = from[16 * t];
+#pragma unroll
+        for (int i = 0; i < IT; ++i)
+          acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i][e], x, acc[i][t], 0, 0, 0);
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < IT; ++i)
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        s[(16 * (ti + WAVES * i) + 4 * (lane >> 4) + v) * C::PITCH + 16 * (tl + t) + (lane & 15)] =
+            acc[i][t][v];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < C::G4; ++k) {
+    const OrthGroup4<RT> at(J, chunk, tid, k);
+    if (!at.in(J, tid, k) || at.n == 0) continue;
+    float o[4];
+    if (!J.tall) {
+      const f32x4 x = *reinterpret_cast<const f32x4*>(s + at.i[0] * C::PITCH + at.l[0]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = x[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = at.l[e] < C::LC ? s[at.i[e] * C::PITCH + at.l[e]] : 0.0f;
+    }
+    const bool vec = J.vec != 0;
+    if constexpr (MODE == OM_MUON) {
+      uint16_t* p = static_cast<uint16_t*>(J.out) + at.e;
+      uint16_t v[4];
+      load4<u32x2>(p, at.n, vec, v);
+      {
+#pragma clang fp contract(off)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          o[e] = bf16_to_f32(v[e]) * b.decay - J.step * o[e];
+      }
+      const uint32_t lo = pack_bf16x2(o[0], o[1]), hi = pack_bf16x2(o[2], o[3]);
+      const uint16_t w[4] = {(uint16_t)lo, (uint16_t)(lo >> 16), (uint16_t)hi, (uint16_t)(hi >> 16)};
+      store4<u32x2>(p, at.n, vec, w);
+      store4<f32x4>(J.m + at.e, at.n, vec, m[k]);
+    } else if constexpr (OUT_BF16) {
+      const uint32_t lo = pack_bf16x2(o[0], o[1]), hi = pack_bf16x2(o[2], o[3]);
+      const uint16_t w[4] = {(uint16_t)lo, (uint16_t)(lo >> 16), (uint16_t)hi, (uint16_t)(hi >> 16)};
+      store4<u32x2>(static_cast<uint16_t*>(J.out) + at.e, at.n, vec, w);
+    } else {
+      store4<f32x4>(static_cast<float*>(J.out) + at.e, at.n, vec, o);
+    }
+  }
+}
+
+template <int RT>
+void poly_launch(hipStream_t st, const OrthBatch& b) {
+  if constexpr (RT < ORTH_BIG) {
+    QN_LAUNCH("k_orth_poly", (k_orth_poly<RT>), dim3(b.count), dim3(OrthPoly<RT>::NT), st, b);
+  } else {
+    constexpr int PAIRS = orth_pairs(RT), BLOCKS = orth_pairs(RT / 2);
+    QN_LAUNCH("k_orth_sum", (k_orth_sum<RT>), dim3(PAIRS, b.count), dim3(256), st, b);
+    QN_LAUNCH("k_orth_norm", (k_orth_norm<RT>), dim3(b.count), dim3(1024), st, b);
+    auto mul = [&](int n, OrthMul x, OrthMul y) {
+      QN_LAUNCH("k_orth_mul", (k_orth_mul<RT>), dim3(BLOCKS, b.count, n), dim3(256), st, b, x, y);
+    };
+    // matrices: 0 is A; P, Q and two free ones take turns in 1 .. 4
+    int8_t P = 1, Q = 2, F = 3, G = 4;
+    for (int s = 0; s < b.steps; ++s) {
+      const bool last = s + 1 == b.steps;
+      mul(1, OrthMul{P, 0, 0, int8_t(s == 0 && last ? OB_P | OB_Q : OB_P)}, OrthMul{});
+      if (s == 0) {
+        if (!last) mul(1, OrthMul{G, P, 0, 0}, OrthMul{});
+      } else if (last) {
+        mul(1, OrthMul{F, P, Q, OB_Q}, OrthMul{});
+      } else {
+        mul(2, OrthMul{F, P, Q, 0}, OrthMul{G, P, 0, 0});
+      }
+      if (!last) mul(1, OrthMul{0, G, P, 0}, OrthMul{});
+      std::swap(Q, s == 0 ? P : F);
+    }
+  }
+}
+
+template <int MODE, int RT, bool OUT_BF16>
+void group_launch(hipStream_t st, OrthBatch b) {
+  using C = OrthCfg<RT>;
+  b.gfirst[0] = b.afirst[0] = 0;
+  for (int j = 0; j < b.count; ++j) {
+    b.gfirst[j + 1] = b.gfirst[j] + b.job[j].slices;
+    b.afirst[j + 1] = b.afirst[j] + (int32_t)cdiv(b.job[j].L, C::LC);
+  }
+  QN_LAUNCH("k_orth_gram", (k_orth_gram<MODE, RT>), dim3(b.gfirst[b.count]), dim3(C::NT), st, b);
+  poly_launch<RT>(st, b);
+  QN_LAUNCH("k_orth_apply", (k_orth_apply<MODE, RT, OUT_BF16>), dim3(b.afirst[b.count]),
+            dim3(C::NT), st, b);
+}
+
+template <int MODE, bool OUT_BF16>
+void group_rt(hipStream_t st, int rt, const OrthBatch& b) {
+  switch (rt) {
+    case 1: group_launch<MODE, 1, OUT_BF16>(st, b); break;
+    case 2: group_launch<MODE, 2, OUT_BF16>(st, b); break;
+    case 4: group_launch<MODE, 4, OUT_BF16>(st, b); break;
+    case 8: group_launch<MODE, 8, OUT_BF16>(st, b); break;
+    default: group_launch<MODE, 16, OUT_BF16>(st, b); break;
+  }
+}
+
+OrthBatch batch_of(const OrthGroup& g, const qn_orth_hparams& h, void* ws) {
+  OrthBatch b{};
+  b.count = g.count;
+  b.steps = h.steps;
+  b.max_slices = g.max_slices;
+  b.a = h.coef[0];
+  b.b = h.coef[1];
+  b.c = h.coef[2];
+  b.eps = h.eps;
+  b.part = ws_at<double>(ws, g.part);
+  b.q = ws_at<float>(ws, g.q);
+  b.inv = ws_at<double>(ws, g.inv);
+  b.mats = ws_at<double>(ws, g.mats);
+  return b;
+}
+
+bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+uintptr_t size_of(int32_t dtype) { return dtype == QN_BF16 ? 2 : 4; }
+
+OrthJob job_of_shape(const OrthShape& s, int32_t slices) {
+  OrthJob J{};
+  J.L = (int32_t)s.len();
+  J.r = s.r();
+  J.tall = s.tall();
+  J.slices = slices;
+  return J;
+}
+
+bool valid_hparams(const qn_orth_hparams* h) {
+  return h != nullptr && h->steps >= 1 && h->steps <= QN_ORTH_MAX_STEPS && std::isfinite(h->eps) &&
+         h->eps > 0.0 && std::isfinite(h->coef[0]) && std::isfinite(h->coef[1]) &&
+         std::isfinite(h->coef[2]);
+}
+
+template <class Job>
+OrthShape shape_of(const Job& j) { return OrthShape{j.rows, j.cols}; }
+
+template <class Job, class Kind>
+size_t batch_bytes(const Job* jobs, int32_t count, int kinds, Kind kind) {
+  size_t most = 0;
+  orth_for_groups(count, kinds, [&](int i) { return shape_of(jobs[i]); }, kind,
+                  [&](const OrthGroup& g) {
+                    most = std::max(most, g.total);
+                    return true;
+                  });
+  return most;
+}
+
+bool valid_count(const void* jobs, int32_t count) {
+  return jobs != nullptr && count >= 1 && count <= QN_ORTH_BATCH_MAX;
+}
+
+bool valid_orth_jobs(const qn_orth_job* jobs, int32_t count) {
+  if (!valid_count(jobs, count)) return false;
+  for (int i = 0; i < count; ++i) {
+    const qn_orth_job& j = jobs[i];
+    if (!valid_orth(shape_of(j))) return false;
+    if (j.x_dtype != QN_F32 && j.x_dtype != QN_BF16) return false;
+    if (j.y_dtype != QN_F32 && j.y_dtype != QN_BF16) return false;
+  }
+  return true;
+}
+
+bool valid_muon_jobs(const qn_muon_job* jobs, int32_t count) {
+  if (!valid_count(jobs, count)) return false;
+  for (int i = 0; i < count; ++i)
+    if (!valid_orth(shape_of(jobs[i]))) return false;
+  return true;
+}
+
+int orth_kind(const qn_orth_job& j) { return 2 * (j.x_dtype == QN_BF16) + (j.y_dtype == QN_BF16); }
+
+}  // namespace
+
+extern "C" size_t qn_orth_workspace_bytes(const qn_orth_job* jobs, int32_t count) {
+  if (!valid_orth_jobs(jobs, count)) return 0;
+  return batch_bytes(jobs, count, 4, [&](int i) { return orth_kind(jobs[i]); });
+}
+
+extern "C" size_t qn_muon_workspace_bytes(const qn_muon_job* jobs, int32_t count) {
+  if (!valid_muon_jobs(jobs, count)) return 0;
+  return batch_bytes(jobs, count, 1, [](int) { return 0; });
+}
+
+extern "C" int qn_orthogonalize(const qn_orth_job* jobs, int32_t count, const qn_orth_hparams* hp,
+                                void* ws, size_t ws_bytes, void* stream) {
+  if (!valid_orth_jobs(jobs, count) || !valid_hparams(hp)) return QN_EINVAL;
+  for (int i = 0; i < count; ++i) {
+    const qn_orth_job& j = jobs[i];
+    if (j.x == nullptr || j.y == nullptr || !aligned(j.x, size_of(j.x_dtype)) ||
+        !aligned(j.y, size_of(j.y_dtype)) || (j.x == j.y && j.x_dtype != j.y_dtype))
+      return QN_EINVAL;
+  }
+  if (ws == nullptr || !aligned16(ws) || ws_bytes < qn_orth_workspace_bytes(jobs, count))
+    return QN_EWORKSPACE;
+  hipStream_t st = (hipStream_t)stream;
+  orth_for_groups(
+      count, 4, [&](int i) { return shape_of(jobs[i]); }, [&](int i) { return orth_kind(jobs[i]); },
+      [&](const OrthGroup& g) {
+        OrthBatch b = batch_of(g, *hp, ws);
+        for (int i = 0; i < g.count; ++i) {
+          const qn_orth_job& j = jobs[g.index[i]];
+          OrthJob J = job_of_shape(shape_of(j), g.slices[i]);
+          J.g = j.x;
+          J.out = j.y;
+          J.vec = (J.tall || J.L % 4 == 0) && aligned(j.x, 4 * size_of(j.x_dtype)) &&
+                  aligned(j.y, 4 * size_of(j.y_dtype));
+          b.job[i] = J;
+        }
+        switch (g.kind) {
+          case 0: group_rt<OM_F32, false>(st, g.rt, b); break;
+          case 1: group_rt<OM_F32, true>(st, g.rt, b); break;
+          case 2: group_rt<OM_BF16, false>(st, g.rt, b); break;
+          default: group_rt<OM_BF16, true>(st, g.rt, b); break;
+        }
+        return true;
+      });
+  return check_launch();
+}
+
+extern "C" int qn_muon_step(const qn_muon_job* jobs, int32_t count, const qn_muon_hparams* hp,
+                            void* ws, size_t ws_bytes, void* stream) {
+  if (!valid_muon_jobs(jobs, count) || hp == nullptr || !valid_hparams(&hp->orth))
+    return QN_EINVAL;
+  if (!std::isfinite(hp->lr) || !std::isfinite(hp->weight_decay) || !std::isfinite(hp->grad_scale) ||
+      !(hp->momentum >= 0.0 && hp->momentum < 1.0))
+    return QN_EINVAL;
+  for (int i = 0; i < count; ++i) {
+    const qn_muon_job& j = jobs[i];
+    if (j.p == nullptr || j.g == nullptr || j.m == nullptr || !aligned(j.p, 2) || !aligned(j.g, 4) ||
+        !aligned(j.m, 4))
+      return QN_EINVAL;
+  }
+  if (ws == nullptr || !aligned16(ws) || ws_bytes < qn_muon_workspace_bytes(jobs, count))
+    return QN_EWORKSPACE;
+  hipStream_t st = (hipStream_t)stream;
+  orth_for_groups(
+      count, 1, [&](int i) { return shape_of(jobs[i]); }, [](int) { return 0; },
+      [&](const OrthGroup& g) {
+        OrthBatch b = batch_of(g, hp->orth, ws);
+        b.mu = (float)hp->momentum;
+        b.gs = (float)hp->grad_scale;
+        b.decay = (float)(1.0 - hp->lr * hp->weight_decay);
+        b.nesterov = hp->nesterov != 0;
+        for (int i = 0; i < g.count; ++i) {
+          const qn_muon_job& j = jobs[g.index[i]];
+          OrthJob J = job_of_shape(shape_of(j), g.slices[i]);
+          J.g = j.g;
+          J.m = j.m;
+          J.out = j.p;
+          J.vec = (J.tall || J.L % 4 == 0) && aligned16(j.g) && aligned16(j.m) && aligned(j.p, 8);
+          J.step = (float)(hp->lr * std::sqrt(std::max(1.0, (double)j.rows / (double)j.cols)));
+          b.job[i] = J;
+        }
+        group_rt<OM_MUON, true>(st, g.rt, b);
+        return true;
+      });
+  return check_launch();
+}

@@ -739,6 +739,85 @@ int qn_head_loss_bwd(const qn_head* h, const float* loss, const float* lse,
                      uint16_t* dw, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * Orthogonalised matrices and the momentum step with them.
+ *
+ * The adapters' second optimizer: an update that is near orthogonal moves all
+ * directions of an adapter alike (K. Jordan et al., "Muon: An optimizer for
+ * hidden layers in neural networks", 2024).  For a matrix U,
+ *   X_0 = U / (|U|_F + eps)
+ *   X_{k+1} = a X_k + b (X_k X_k^T) X_k + c (X_k X_k^T)^2 X_k,  k < steps
+ * with (a, b, c) = coef, the products from the side of the fewer rows or
+ * columns.  At (3.4445, -4.7750, 2.0315) and 5 steps the singular values of
+ * the result lie near 1.
+ * Matrices are dense row-major [rows][cols], min(rows, cols) <= QN_MAX_RANK
+ * (an adapter's A and B), rows * cols < 2^31, aligned to their element.  The
+ * X_k X_k^T and their products are formed in 64 bits, U times their product
+ * in fp32.  A zero matrix gives zeros.  A NaN or infinity makes the results
+ * of its own matrix NaN (a momentum and parameter also where U is finite).
+ * Calls that run at the same time need workspaces of their own; they must be
+ * 16-byte aligned.
+ */
+#define QN_ORTH_MAX_STEPS 16
+#define QN_ORTH_BATCH_MAX 65536
+
+typedef struct {
+  double coef[3];
+  double eps;            /* > 0 */
+  int32_t steps;         /* 1 .. QN_ORTH_MAX_STEPS */
+} qn_orth_hparams;
+
+typedef struct {
+  const void* x;         /* device [rows][cols] of x_dtype */
+  int32_t x_dtype;       /* QN_F32 or QN_BF16 */
+  void* y;               /* device [rows][cols] of y_dtype; may be x itself,
+                            with the same type */
+  int32_t y_dtype;
+  int64_t rows, cols;
+} qn_orth_job;
+
+/* qn_orthogonalize -- X_steps of every job's x into its y (device).
+ * jobs : host array of `count` (1 .. QN_ORTH_BATCH_MAX) descriptors; no y
+ *        may overlap another job's x or y.
+ * ws   : ws_bytes >= qn_orth_workspace_bytes(jobs, count) (0 for an invalid
+ *        batch; the pointers are not looked at).
+ * Errors: QN_EINVAL, QN_EWORKSPACE, QN_EHIP. */
+size_t qn_orth_workspace_bytes(const qn_orth_job* jobs, int32_t count);
+int qn_orthogonalize(const qn_orth_job* jobs, int32_t count,
+                     const qn_orth_hparams* hp, void* ws, size_t ws_bytes,
+                     void* stream);
+
+/*
+ * qn_muon_step -- one step on every job's parameter (device).  In fp32, each
+ * operation rounded once, host constants rounded once from double:
+ *   g = g * grad_scale;  m = momentum * m + g
+ *   u = nesterov ? g + momentum * m : m
+ *   p = bf16_rne(p * (1 - lr * weight_decay) - (lr * s) * X_steps(u))
+ * with s = sqrt(max(1, rows / cols)).
+ * p : bf16, updated in place;  g : fp32;  m : fp32, updated in place (zeros
+ *     before the first step).  No job's p or m may overlap anything else.
+ * hp: 0 <= momentum < 1, the others finite.
+ * ws : ws_bytes >= qn_muon_workspace_bytes(jobs, count).
+ * Errors: QN_EINVAL, QN_EWORKSPACE, QN_EHIP.
+ */
+typedef struct {
+  uint16_t* p;
+  const float* g;
+  float* m;
+  int64_t rows, cols;
+} qn_muon_job;
+
+typedef struct {
+  double lr, momentum, weight_decay, grad_scale;
+  int32_t nesterov;
+  qn_orth_hparams orth;
+} qn_muon_hparams;
+
+size_t qn_muon_workspace_bytes(const qn_muon_job* jobs, int32_t count);
+int qn_muon_step(const qn_muon_job* jobs, int32_t count,
+                 const qn_muon_hparams* hp, void* ws, size_t ws_bytes,
+                 void* stream);
+
+/*
  * qlora_linear_fwd_batch -- qlora_linear_fwd for up to QN_FWD_BATCH_MAX
  * projections with few tokens (M <= 16 each), as one pair of launches
  * (device).

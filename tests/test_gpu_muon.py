@@ -1,0 +1,177 @@
+"""Orthogonalised matrices and the momentum step on the GPU against float64.
+
+Bounds are counted, u = 2^-24 being half an fp32 step, 2^-8 half a bf16 step:
+* O = Q U: Q is rounded to fp32 once, the products are summed in fp32 (r + 2
+  roundings of sum_j |Q_ij U_jl|, Q = O U^+ bounded through its own rows:
+  |Q_ij| <= |Q|_2 <= a^steps / |U|);
+* Q itself: the Gram matrix has (len + r) 2^-53 of its trace, which moves Q by
+  at most AMP times that, AMP = 1.4 a^steps (a^(2 steps) - 1) / (a^2 - 1), the
+  derivative of the composed polynomial at 0, its steepest place;
+* outputs are rounded once; the momentum is exact in fp32 steps.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle.muon as om
+from bit_nf4_quantized_14_amd import capi
+from gpu_util import DEV, f64_host
+
+pytestmark = pytest.mark.gpu
+
+U, H = 2.0 ** -24, 2.0 ** -8
+A = om.COEF[0]
+
+
+def bound(u, steps=5):
+    """Per position of the long side: bound of |O - exact|."""
+    x = u.astype(np.float64)
+    x = x if x.shape[0] <= x.shape[1] else x.T
+    norm = np.sqrt((x * x).sum())
+    if norm == 0:
+        return np.zeros(u.shape)
+    r, n = x.shape
+    q = A ** steps / norm
+    amp = 1.4 * A ** steps * (A ** (2 * steps) - 1) / (A ** 2 - 1) / norm
+    fp32 = (r + 3) * U * q * np.abs(x).sum(0)
+    fp64 = amp * (n + 8 * r) * 2.0 ** -53 * np.sqrt((x * x).sum(0))
+    e = np.broadcast_to(fp32 + fp64, x.shape)
+    return e if u.shape[0] <= u.shape[1] else e.T
+
+
+def matrix(rows, cols, seed, kind="falling"):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(rows, cols, generator=g)
+    if kind == "falling":        # singular values over two decades
+        r = min(rows, cols)
+        w = torch.logspace(0, -2, r)
+        x = x * (w[:, None] if rows <= cols else w[None, :])
+    elif kind == "low":          # rank 1, others rounding
+        x = torch.randn(rows, 1, generator=g) @ torch.randn(1, cols, generator=g)
+    return x * 1e-3
+
+
+def check_orth(x, y, steps=5, out=None):
+    xn = f64_host(x)
+    ref = om.orthogonalize(xn, steps)
+    err = np.abs(f64_host(y) - ref)
+    h = H if y.dtype is torch.bfloat16 else U
+    b = bound(xn, steps)
+    assert (err <= b * (1 + h) + h * np.abs(ref) + 1e-38).all(), (err.max(), b.max())
+
+
+SHAPES = [(1, 1), (1, 7), (5, 1), (3, 1000), (1000, 3), (16, 16), (16, 2048), (2048, 16), (17, 33),
+          (20, 1999), (1003, 20), (32, 515), (33, 100), (64, 64), (64, 4100), (257, 64), (63, 255),
+          (65, 66), (100, 300), (300, 100), (128, 129), (200, 2000), (256, 256), (255, 1000),
+          (1001, 256)]
+
+
+@pytest.mark.parametrize("rows,cols", SHAPES)
+@pytest.mark.parametrize("xt", [torch.float32, torch.bfloat16])
+def test_orthogonalize(rows, cols, xt):
+    x = matrix(rows, cols, rows * 7 + cols).to(xt)
+    for code in (capi.QN_F32, capi.QN_BF16):
+        check_orth(x, capi.qn_orthogonalize(x.to(DEV), dtype=code))
+
+
+@pytest.mark.parametrize("rows,cols", [(8, 100), (64, 200), (130, 140)])
+@pytest.mark.parametrize("steps", [1, 2, 3, 7])
+def test_steps(rows, cols, steps):
+    x = matrix(rows, cols, 5)
+    check_orth(x, capi.qn_orthogonalize(x.to(DEV), steps=steps), steps)
+
+
+@pytest.mark.parametrize("rows,cols", [(16, 700), (700, 48), (96, 256)])
+def test_low_rank(rows, cols):
+    x = matrix(rows, cols, 6, "low")
+    check_orth(x, capi.qn_orthogonalize(x.to(DEV)))
+
+
+def test_singular_values_near_one():
+    x = matrix(64, 1000, 9)
+    s = np.linalg.svd(f64_host(capi.qn_orthogonalize(x.to(DEV))), compute_uv=False)
+    assert s.min() > 0.3 and s.max() < 1.3
+
+
+def test_list_of_mixed_matrices_in_one_call():
+    shapes = [SHAPES[i % len(SHAPES)] for i in range(90)]
+    xs = [matrix(r, c, i).to(torch.bfloat16 if i % 3 else torch.float32).to(DEV)
+          for i, (r, c) in enumerate(shapes)]
+    ys = capi.qn_orthogonalize(xs)
+    for x, y in zip(xs, ys):
+        assert y.dtype is x.dtype
+        check_orth(x.cpu(), y)
+
+
+def test_in_place_and_unaligned():
+    buf = torch.zeros(70 * 33 + 5, device=DEV)
+    x = matrix(33, 70, 2)
+    v = buf[1:1 + 33 * 70].view(33, 70)
+    v.copy_(x)
+    assert capi.qn_orthogonalize(v, out=v) is v
+    check_orth(x, v)
+    assert buf[0] == 0 and (buf[1 + 33 * 70:] == 0).all()
+
+
+def test_zero_and_not_finite():
+    zero, bad, good = torch.zeros(16, 100), matrix(16, 100, 1), matrix(16, 100, 2)
+    bad[3, 50] = float("inf")
+    ys = capi.qn_orthogonalize([t.to(DEV) for t in (zero, bad, good)])
+    assert (ys[0] == 0).all() and torch.isnan(ys[1]).all()
+    check_orth(good, ys[2])
+
+
+def muon_case(shapes, seed):
+    g = torch.Generator().manual_seed(seed)
+    jobs = []
+    for i, (r, c) in enumerate(shapes):
+        jobs.append(((torch.randn(r, c, generator=g) * 0.02).bfloat16(), matrix(r, c, seed + i),
+                     matrix(r, c, seed + 50 + i) * 5))
+    return jobs
+
+
+def check_muon(jobs, batch, steps_done=1, **hp):
+    """One step of the batch against the oracle; jobs are updated from it."""
+    capi.qn_muon_step(batch, **hp)
+    lr, mu = hp.get("lr", 0.02), hp.get("momentum", 0.95)
+    for i, (p, g, m) in enumerate(jobs):
+        kw = dict(weight_decay=hp.get("weight_decay", 0.0), grad_scale=hp.get("grad_scale", 1.0),
+                  nesterov=hp.get("nesterov", True))
+        want, mn = om.step(f64_host(p), g.numpy(), m.numpy(), lr, mu, **kw)
+        got_p, got_m = batch.keep[2 * i].cpu(), batch.momenta[i].cpu()
+        assert np.array_equal(got_m.numpy().view(np.uint32), mn.view(np.uint32)), i
+        s = np.sqrt(max(1.0, p.shape[0] / p.shape[1]))
+        _, u = om.momentum(g.numpy(), m.numpy(), mu, kw["grad_scale"], kw["nesterov"])
+        o = np.abs(om.orthogonalize(u))
+        slack = lr * s * bound(u) + 4 * U * (np.abs(f64_host(p)) + lr * s * o)
+        err = np.abs(f64_host(got_p) - want)
+        assert (err <= H * np.abs(want) + slack * (1 + H) + 1e-38).all(), (i, err.max())
+        jobs[i] = (got_p, g, got_m)
+
+
+@pytest.mark.parametrize("shapes", [[(16, 512), (1024, 16)], [(1, 64), (64, 1), (4, 4)],
+                                    [(20, 1999), (1003, 20)], [(64, 640), (130, 64), (64, 64)],
+                                    [(100, 260), (256, 300), (301, 200)]])
+def test_muon_steps(shapes):
+    jobs = muon_case(shapes, 3)
+    batch = capi.MuonBatch([tuple(t.to(DEV) for t in j) for j in jobs])
+    for hp in (dict(lr=0.02, weight_decay=0.01), dict(lr=0.1, momentum=0.9, nesterov=False),
+               dict(grad_scale=0.37)):
+        check_muon(jobs, batch, **hp)
+
+
+def test_muon_batch_beyond_one_launch():
+    shapes = [(8, 64 + i) if i % 2 else (70 + i, 8) for i in range(70)]
+    jobs = muon_case(shapes, 11)
+    batch = capi.MuonBatch([tuple(t.to(DEV) for t in j) for j in jobs])
+    check_muon(jobs, batch)
+
+
+def test_muon_zero_gradient_only_decays():
+    p = (torch.randn(16, 100) * 0.02).bfloat16()
+    z = torch.zeros(16, 100)
+    jobs = [(p, z, z)]
+    batch = capi.MuonBatch([(p.to(DEV), z.to(DEV), None)])
+    check_muon(jobs, batch, lr=0.5, weight_decay=0.5)
+    assert (batch.momenta[0] == 0).all()
