@@ -35,10 +35,10 @@ struct OrthJob {
   const void* g;        // gradient, or the matrix
   float* m;             // momentum
   void* out;            // parameter (in place), or the result
-  int32_t L, r;
-  int32_t tall, vec;
-  int32_t slices;
   float step;           // lr times the matrix's scale
+  int32_t L;            // long side
+  int16_t r, slices;    // short side, partial Gram matrices
+  uint8_t tall, vec;    // layout; whether groups of 4 are aligned
 };
 struct OrthBatch {
   OrthJob job[ORTH_JOBS];
@@ -145,25 +145,20 @@ __device__ __forceinline__ void store4(T* p, int n, bool vec, const T (&v)[4]) {
   }
 }
 
-// U of a group; with OM_MUON also the new momentum.
+// A group's elements of the matrix, or of the gradient and the momentum: 0
+// outside the matrix.
 template <int MODE, int RT>
-__device__ __forceinline__ void orth_load(const OrthJob& J, const OrthBatch& b,
-                                          const OrthGroup4<RT>& at, float (&u)[4], float (&m)[4]) {
+__device__ __forceinline__ void orth_fetch(const OrthJob& J, const OrthGroup4<RT>& at, float (&u)[4],
+                                           float (&m)[4]) {
   const bool vec = J.vec != 0;
   if constexpr (MODE == OM_BF16) {
     uint16_t v[4];
     load4<u32x2>(static_cast<const uint16_t*>(J.g) + at.e, at.n, vec, v);
 #pragma unroll
     for (int i = 0; i < 4; ++i) u[i] = bf16_to_f32(v[i]);
-  } else if constexpr (MODE == OM_F32) {
-    load4<f32x4>(static_cast<const float*>(J.g) + at.e, at.n, vec, u);
   } else {
-    float g[4];
-    load4<f32x4>(static_cast<const float*>(J.g) + at.e, at.n, vec, g);
-    load4<f32x4>(static_cast<const float*>(J.m) + at.e, at.n, vec, m);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = muon_u(g[i], m[i], b);
-    // outside the matrix g and m are 0, and so is u
+    load4<f32x4>(static_cast<const float*>(J.g) + at.e, at.n, vec, u);
+    if constexpr (MODE == OM_MUON) load4<f32x4>(static_cast<const float*>(J.m) + at.e, at.n, vec, m);
   }
 }
 
@@ -182,12 +177,19 @@ __device__ __forceinline__ void orth_put(float* s, const OrthJob& J, const OrthG
   }
 }
 
-// Rows of the chunk that a tall matrix does not have.
-template <int RT>
+// Row 4 e + x of a tile as row 4 x + e, and back.
+__device__ __forceinline__ int orth_swap(int i) { return 4 * (i & 3) + (i >> 2); }
+
+// Rows of the chunk that a tall matrix does not have (SWAP: where orth_swap
+// puts them).
+template <int RT, bool SWAP>
 __device__ __forceinline__ void orth_pad(float* s, const OrthJob& J, int tid) {
   using C = OrthCfg<RT>;
-  if (J.tall)
-    for (int x = J.r * C::PITCH + tid; x < C::RP * C::PITCH; x += C::NT) s[x] = 0.0f;
+  if (!J.tall) return;
+  for (int x = tid; x < C::RP * C::PITCH; x += C::NT) {
+    const int row = x / C::PITCH;
+    if ((SWAP ? orth_swap(row) : row) >= J.r) s[x] = 0.0f;
+  }
 }
 
 // Pair p of tile rows i >= j, in the order (0,0) (1,0) (1,1) (2,0) ...
@@ -220,16 +222,30 @@ __global__ __launch_bounds__(orth_threads(RT)) void k_orth_gram(OrthBatch b) {
   f64x4 acc[NP];
 #pragma unroll
   for (int p = 0; p < NP; ++p) acc[p] = f64x4{0, 0, 0, 0};
-  orth_pad<RT>(s, J, tid);
-  for (int c = c0; c < c1; ++c) {
+  orth_pad<RT, false>(s, J, tid);
+  // the next chunk's elements are on their way while this one's are used
+  // (not where the pairs' sums take the registers)
+  constexpr bool AHEAD = RT < 16;
+  float u[C::G4][4], m[MODE == OM_MUON ? C::G4 : 1][4];
+  auto fetch = [&](int c) {
 #pragma unroll
     for (int k = 0; k < C::G4; ++k) {
       const OrthGroup4<RT> at(J, c, tid, k);
-      if (!at.in(J, tid, k)) continue;
-      float u[4], m[4];
-      orth_load<MODE, RT>(J, b, at, u, m);
-      orth_put<RT>(s, J, at, u);
+      orth_fetch<MODE, RT>(J, at, u[k], m[MODE == OM_MUON ? k : 0]);
     }
+  };
+  if (AHEAD) fetch(c0);
+  for (int c = c0; c < c1; ++c) {
+    if (!AHEAD) fetch(c);
+#pragma unroll
+    for (int k = 0; k < C::G4; ++k) {
+      const OrthGroup4<RT> at(J, c, tid, k);
+      if constexpr (MODE == OM_MUON)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[k][e] = muon_u(u[k][e], m[k][e], b);
+      if (at.in(J, tid, k)) orth_put<RT>(s, J, at, u[k]);
+    }
+    if (AHEAD && c + 1 < c1) fetch(c + 1);
     __syncthreads();
     const float* from = s + (lane & 15) * C::PITCH + (lane >> 4);
     if constexpr (SPLIT) {
@@ -283,149 +299,225 @@ __global__ __launch_bounds__(orth_threads(RT)) void k_orth_gram(OrthBatch b) {
   }
 }
 
-// Sum of a Gram element's partials, four at a time in flight.
-__device__ __forceinline__ double orth_sum(const double* part, int64_t stride, int slices) {
-  double s = 0.0;
-  for (int i = 0; i < slices; i += 8) {
+// Adds up a matrix's partial Gram matrices, a workgroup to a pair of tiles:
+// four threads take every fourth partial of an element each.
+__global__ __launch_bounds__(1024) void k_orth_sum(OrthBatch b, int pairs) {
+  __shared__ double s[4][256];
+  const int jx = blockIdx.y, x = threadIdx.x & 255, part = threadIdx.x >> 8;
+  const int slices = b.job[jx].slices;
+  const int64_t stride = pairs * 256;
+  double* base = b.part + (int64_t)jx * b.max_slices * stride + blockIdx.x * 256 + x;
+  double t = 0.0;
+  for (int i = part; i < slices; i += 32) {
     double v[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = i + k < slices ? part[(i + k) * stride] : 0.0;
+    for (int k = 0; k < 8; ++k) v[k] = i + 4 * k < slices ? base[(i + 4 * k) * stride] : 0.0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s += v[k];
+    for (int k = 0; k < 8; ++k) t += v[k];
   }
-  return s;
+  s[part][x] = t;
+  __syncthreads();
+  if (part == 0) *base = (s[0][x] + s[1][x]) + (s[2][x] + s[3][x]);
 }
 
-// Rows and columns of element x (accumulator layout) of the pairs.
-__device__ __forceinline__ void orth_place(int x, int& row, int& col) {
-  int i, j;
-  orth_pair(x >> 8, i, j);
-  row = 16 * i + 4 * ((x >> 6) & 3) + ((x & 63) >> 4);
-  col = 16 * j + (x & 15);
-}
-
-// The polynomials of a matrix with at most 64 rows: one workgroup, everything
-// in LDS.  All matrices are polynomials of A_0: symmetric, and they commute,
-// so X Y is formed as X Y^T from rows alone, its tiles on and below the
-// diagonal, and mirrored.
+// Products of symmetric matrices that commute, in tiles of 16 x 16 as
+// v_mfma_f64_16x16x4_f64 leaves them: tile (i, j) has element (16 i + 4 v + l /
+// 16, 16 j + l % 16) in register v of lane l.  That is also the first operand's
+// layout for rows 16 j .. and reduction 16 i + 4 v .., and the second's for
+// columns 16 j .., so a stored tile is read by its lane as it was written.  A
+// product's tiles on and below the diagonal are formed, the others are their
+// mirror images.
 template <int RT>
 struct OrthPoly {
-  static constexpr int RP = 16 * RT, PITCH = RP + 4;      // doubles
-  static constexpr int NT = RT == 4 ? 512 : 256, WAVES = NT / 64;
-  static constexpr int PAIRS = orth_pairs(RT);
-  static __device__ __forceinline__ void mul(double* dst, const double* x, const double* y,
-                                             int wave, int lane) {
-    for (int p = wave; p < PAIRS; p += WAVES) {
-      int i, j;
-      orth_pair(p, i, j);
-      const double* fx = x + (16 * i + (lane & 15)) * PITCH + (lane >> 4);
-      const double* fy = y + (16 * j + (lane & 15)) * PITCH + (lane >> 4);
-      f64x4 acc = {0, 0, 0, 0};
+  static constexpr int RP = 16 * RT, NT = RT == 4 ? 1024 : 256, WAVES = NT / 64;
+  static constexpr int PAIRS = orth_pairs(RT), MAT = RT * RT * 256;
+  static_assert(2 * PAIRS <= 2 * WAVES, "two tiles to a wave at most");
+  static __device__ __forceinline__ double* tile(double* m, int i, int j) {
+    return m + (i * RT + j) * 256;
+  }
+  static __device__ __forceinline__ f64x4 mul(double* x, double* y, int i, int j, int lane) {
+    f64x4 acc = {0, 0, 0, 0};
 #pragma unroll
-      for (int k = 0; k < RP; k += 4)
-        acc = __builtin_amdgcn_mfma_f64_16x16x4f64(fx[k], fy[k], acc, 0, 0, 0);
+    for (int t = 0; t < RT; ++t) {
+      const double *a = tile(x, t, i) + lane, *c = tile(y, t, j) + lane;
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int row = 16 * i + 4 * v + (lane >> 4), col = 16 * j + (lane & 15);
-        dst[row * PITCH + col] = acc[v];
-        if (i != j) dst[col * PITCH + row] = acc[v];
-      }
+      for (int v = 0; v < 4; ++v)
+        acc = __builtin_amdgcn_mfma_f64_16x16x4f64(a[64 * v], c[64 * v], acc, 0, 0, 0);
     }
-    __syncthreads();
+    return acc;
+  }
+  static __device__ __forceinline__ void put(double* m, int i, int j, int lane, const f64x4& x) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      tile(m, i, j)[64 * v + lane] = x[v];
+      if (i != j) tile(m, j, i)[16 * (lane & 15) + 4 * v + (lane >> 4)] = x[v];
+    }
   }
 };
 
+// The polynomials of a matrix with 17 to 64 rows: one workgroup, everything in
+// LDS.  A product's result waits in registers until all have read its place.
 template <int RT>
 __global__ __launch_bounds__(OrthPoly<RT>::NT) void k_orth_poly(OrthBatch b) {
   using C = OrthPoly<RT>;
-  __shared__ double lds[4 * C::RP * C::PITCH];
-  __shared__ double s_norm;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const OrthJob& J = b.job[blockIdx.x];
-  double *A = lds, *P = lds + C::RP * C::PITCH, *Q = P + C::RP * C::PITCH,
-         *X = Q + C::RP * C::PITCH;
+  __shared__ double A[C::MAT];
+  __shared__ double P[C::MAT];
+  __shared__ double Q[C::MAT];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const double* part = b.part + (int64_t)blockIdx.x * b.max_slices * (C::PAIRS * 256);
-  for (int x = tid; x < C::PAIRS * 256; x += C::NT) {
-    int row, col;
-    orth_place(x, row, col);
-    const double v = orth_sum(part + x, C::PAIRS * 256, J.slices);
-    A[row * C::PITCH + col] = v;
-    if ((row >> 4) != (col >> 4)) A[col * C::PITCH + row] = v;
-  }
-  __syncthreads();
-  if (wave == 0) {
-    double t = lane < C::RP ? A[lane * C::PITCH + lane] : 0.0;
+  int i, j;
+  f64x4 x, y;
+  if (wave < C::PAIRS) {
+    orth_pair(wave, i, j);
 #pragma unroll
-    for (int d = 32; d > 0; d /= 2) t += __shfl_xor(t, d);
-    if (lane == 0) s_norm = 1.0 / (sqrt(t) + b.eps);
+    for (int v = 0; v < 4; ++v) x[v] = part[wave * 256 + 64 * v + lane];
+    C::put(A, i, j, lane, x);
   }
   __syncthreads();
-  const double inv = s_norm;
-  for (int x = tid; x < C::RP * C::RP; x += C::NT) {
-    const int row = x / C::RP, col = x % C::RP;
-    A[row * C::PITCH + col] = (A[row * C::PITCH + col] * inv) * inv;
-    Q[row * C::PITCH + col] = row == col ? 1.0 : 0.0;
-  }
+  double t = 0.0;
+  if (lane < 16)
+#pragma unroll
+    for (int k = 0; k < RT; ++k)
+      t += C::tile(A, k, k)[64 * (lane >> 2) + 16 * (lane & 3) + lane];
+#pragma unroll
+  for (int d = 8; d > 0; d /= 2) t += __shfl_xor(t, d);
+  const double inv = 1.0 / (sqrt(__shfl(t, 0)) + b.eps);
+  __syncthreads();
+  for (int k = tid; k < C::MAT; k += C::NT) A[k] = (A[k] * inv) * inv;
   __syncthreads();
   for (int st = 0; st < b.steps; ++st) {
-    C::mul(P, A, A, wave, lane);
-    for (int x = tid; x < C::RP * C::RP; x += C::NT) {
-      const int at = (x / C::RP) * C::PITCH + x % C::RP;
-      P[at] = (x / C::RP == x % C::RP ? b.a : 0.0) + b.b * A[at] + b.c * P[at];
+    const bool last = st + 1 == b.steps;
+    if (wave < C::PAIRS) {          // P = a I + b A + c A A
+      orth_pair(wave, i, j);
+      x = C::mul(A, A, i, j, lane);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const double d = i == j && 4 * v + (lane >> 4) == (lane & 15) ? b.a : 0.0;
+        x[v] = d + b.b * C::tile(A, i, j)[64 * v + lane] + b.c * x[v];
+      }
+      C::put(P, i, j, lane, x);
+      if (st == 0) C::put(Q, i, j, lane, x);
     }
     __syncthreads();
-    if (st > 0) C::mul(X, P, Q, wave, lane);
-    double* R = st > 0 ? Q : X;          // free
-    if (st + 1 < b.steps) {
-      C::mul(R, P, A, wave, lane);
-      C::mul(A, R, P, wave, lane);
-    }
-    if (st > 0) {
-      double* t = Q;
-      Q = X;
-      X = t;
-    } else {
-      double* t = Q;
-      Q = P;
-      P = t;
+    // products 0 .. PAIRS - 1: Q = P Q, the others: A = P A
+    const int n0 = st == 0 ? C::PAIRS : 0, n1 = last ? C::PAIRS : 2 * C::PAIRS;
+    const int u0 = n0 + wave, u1 = u0 + C::WAVES;
+    auto mul = [&](int u) {
+      double* m = u < C::PAIRS ? Q : A;
+      orth_pair(u < C::PAIRS ? u : u - C::PAIRS, i, j);
+      return C::mul(P, m, i, j, lane);
+    };
+    auto put = [&](int u, const f64x4& v) {
+      orth_pair(u < C::PAIRS ? u : u - C::PAIRS, i, j);
+      C::put(u < C::PAIRS ? Q : A, i, j, lane, v);
+    };
+    if (u0 < n1) x = mul(u0);
+    if (u1 < n1) y = mul(u1);
+    __syncthreads();
+    if (u0 < n1) put(u0, x);
+    if (u1 < n1) put(u1, y);
+    __syncthreads();
+    if (!last) {                    // A = (P A) P
+      if (wave < C::PAIRS) {
+        orth_pair(wave, i, j);
+        x = C::mul(A, P, i, j, lane);
+      }
+      __syncthreads();
+      if (wave < C::PAIRS) C::put(A, i, j, lane, x);
+      __syncthreads();
     }
   }
   float* q = b.q + (int64_t)blockIdx.x * C::RP * C::RP;
-  for (int x = tid; x < C::RP * C::RP; x += C::NT)
-    q[x] = (float)(Q[(x / C::RP) * C::PITCH + x % C::RP] * inv);
+  for (int k = tid; k < C::MAT; k += C::NT) {
+    const int ti = (k >> 8) / RT, tj = (k >> 8) % RT;
+    const int row = 16 * ti + 4 * ((k >> 6) & 3) + ((k & 63) >> 4), col = 16 * tj + (k & 15);
+    q[row * C::RP + col] = (float)(Q[k] * inv);
+  }
 }
 
-// The same for 65 to 256 rows, where a matrix fills more than a CU's LDS: one
-// launch for each set of products that do not wait for one another.
-template <int RT>
-__global__ __launch_bounds__(256) void k_orth_sum(OrthBatch b) {
-  constexpr int RP = 16 * RT, PAIRS = orth_pairs(RT);
-  const int jx = blockIdx.y, x = blockIdx.x * 256 + threadIdx.x;
-  int row, col;
-  orth_place(x, row, col);
-  const double v = orth_sum(b.part + (int64_t)jx * b.max_slices * (PAIRS * 256) + x, PAIRS * 256,
-                            b.job[jx].slices);
-  double* A = b.mats + (int64_t)jx * ORTH_MATS * RP * RP;
-  A[row * RP + col] = v;
-  if ((row >> 4) != (col >> 4)) A[col * RP + row] = v;
+// The same for at most 16 rows, by one wave in registers, from the partial
+// Gram matrices: every operand is a register as the instruction left it.
+// `sum` holds 4 x 256 doubles; all four waves get the result, Q[l % 16][4 v + l /
+// 16] in element v.
+__device__ __forceinline__ f32x4 orth_poly_tile(const OrthBatch& b, int jx, int slices, double* sum,
+                                                int wave, int lane) {
+  const double* part = b.part + (int64_t)jx * b.max_slices * 256 + lane;
+  f64x4 A = {0, 0, 0, 0};
+#pragma unroll 4
+  for (int s = wave; s < slices; s += 4)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) A[v] += part[s * 256 + 64 * v];
+#pragma unroll
+  for (int v = 0; v < 4; ++v) sum[wave * 256 + 64 * v + lane] = A[v];
+  __syncthreads();
+  double t = 0.0;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const double* s = sum + 64 * v + lane;
+    A[v] = (s[0] + s[256]) + (s[512] + s[768]);
+    t += 4 * v + (lane >> 4) == (lane & 15) ? A[v] : 0.0;
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d /= 2) t += __shfl_xor(t, d);
+  const double inv = 1.0 / (sqrt(t) + b.eps);
+#pragma unroll
+  for (int v = 0; v < 4; ++v) A[v] = (A[v] * inv) * inv;
+  auto mul = [](const f64x4& x, const f64x4& y) {
+    f64x4 acc = {0, 0, 0, 0};
+#pragma unroll
+    for (int v = 0; v < 4; ++v) acc = __builtin_amdgcn_mfma_f64_16x16x4f64(x[v], y[v], acc, 0, 0, 0);
+    return acc;
+  };
+  f64x4 Q;
+  for (int st = 0; st < b.steps; ++st) {
+    f64x4 P = mul(A, A);
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      P[v] = (4 * v + (lane >> 4) == (lane & 15) ? b.a : 0.0) + b.b * A[v] + b.c * P[v];
+    const f64x4 R = mul(P, A);
+    Q = st == 0 ? P : mul(P, Q);
+    A = mul(R, P);
+  }
+  f32x4 q;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) q[v] = (float)(Q[v] * inv);
+  return q;
 }
 
+// The polynomials for 65 to 256 rows, where a matrix fills more than a CU's
+// LDS: one launch for each set of products that do not wait for one another.
+// First: the Gram matrix over the squared norm, its rows in order.
 template <int RT>
 __global__ __launch_bounds__(1024) void k_orth_norm(OrthBatch b) {
-  constexpr int RP = 16 * RT;
-  __shared__ double s_sum[4];
-  const int tid = threadIdx.x, lane = tid & 63;
-  double* A = b.mats + (int64_t)blockIdx.x * ORTH_MATS * RP * RP;
-  if (tid < 256) {
-    double t = tid < RP ? A[tid * RP + tid] : 0.0;
-#pragma unroll
-    for (int d = 32; d > 0; d /= 2) t += __shfl_xor(t, d);
-    if (lane == 0) s_sum[tid >> 6] = t;
+  constexpr int RP = 16 * RT, PAIRS = orth_pairs(RT);
+  __shared__ double s_sum[16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const double* part = b.part + (int64_t)blockIdx.y * b.max_slices * (PAIRS * 256);
+  double t = 0.0;
+  if (tid < RP) {
+    const int k = tid >> 4, x = tid & 15;
+    t = part[(k * (k + 1) / 2 + k) * 256 + 64 * (x >> 2) + 16 * (x & 3) + x];
   }
+#pragma unroll
+  for (int d = 32; d > 0; d /= 2) t += __shfl_xor(t, d);
+  if (lane == 0) s_sum[wave] = t;
   __syncthreads();
-  const double inv = 1.0 / (sqrt(((s_sum[0] + s_sum[1]) + s_sum[2]) + s_sum[3]) + b.eps);
-  if (tid == 0) b.inv[blockIdx.x] = inv;
-  for (int x = tid; x < RP * RP; x += 1024) A[x] = (A[x] * inv) * inv;
+  t = 0.0;
+#pragma unroll
+  for (int w = 0; w < RP / 64; ++w) t += s_sum[w];
+  const double inv = 1.0 / (sqrt(t) + b.eps);
+  if (blockIdx.x == 0 && tid == 0) b.inv[blockIdx.y] = inv;
+  // four pairs of tiles to a workgroup
+  const int p = 4 * blockIdx.x + (tid >> 8), x = tid & 255;
+  if (p >= PAIRS) return;
+  int i, j;
+  orth_pair(p, i, j);
+  const int row = 16 * i + 4 * (x >> 6) + ((x & 63) >> 4), col = 16 * j + (x & 15);
+  const double v = (part[p * 256 + x] * inv) * inv;
+  double* A = b.mats + (int64_t)blockIdx.y * ORTH_MATS * RP * RP;
+  A[row * RP + col] = v;
+  if (i != j) A[col * RP + row] = v;
 }
 
 // dst = x y, for one or two products (blockIdx.z), 32 x 32 elements of the
@@ -488,16 +580,26 @@ __global__ __launch_bounds__(orth_threads(RT)) void k_orth_apply(OrthBatch b) {
   const int jx = job_of(b.afirst, b.count, blockIdx.x);
   const OrthJob& J = b.job[jx];
   const int chunk = blockIdx.x - b.afirst[jx];
+  __shared__ double sum[RT == 1 ? 1024 : 1];
   float m[C::G4][4];
-  orth_pad<RT>(s, J, tid);
+  orth_pad<RT, RT == 1>(s, J, tid);
 #pragma unroll
   for (int k = 0; k < C::G4; ++k) {
-    const OrthGroup4<RT> at(J, chunk, tid, k);
+    OrthGroup4<RT> at(J, chunk, tid, k);
     if (!at.in(J, tid, k)) continue;
     float u[4];
-    orth_load<MODE, RT>(J, b, at, u, m[k]);
+    orth_fetch<MODE, RT>(J, at, u, m[k]);
+    if constexpr (MODE == OM_MUON)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) u[e] = muon_u(u[e], m[k][e], b);
+    // with one tile, row 4 e + x goes to row 4 x + e: Q's reduction index
+    if constexpr (RT == 1)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) at.i[e] = orth_swap(at.i[e]);
     orth_put<RT>(s, J, at, u);
   }
+  f32x4 q1;
+  if constexpr (RT == 1) q1 = orth_poly_tile(b, jx, J.slices, sum, wave, lane);
   __syncthreads();
   // a wave's tile rows ti, ti + WAVES, ... and its four tiles of positions
   const int ti = RT >= WAVES ? wave : wave % RT, tl = RT >= WAVES ? 0 : 4 * (wave / RT);
@@ -513,8 +615,9 @@ __global__ __launch_bounds__(orth_threads(RT)) void k_orth_apply(OrthBatch b) {
     f32x4 a[IT];
 #pragma unroll
     for (int i = 0; i < IT; ++i)
-      a[i] = *reinterpret_cast<const f32x4*>(q + (16 * (ti + WAVES * i) + (lane & 15)) * C::RP +
-                                             16 * k + 4 * (lane >> 4));
+      a[i] = RT == 1 ? q1
+                     : *reinterpret_cast<const f32x4*>(q + (16 * (ti + WAVES * i) + (lane & 15)) * C::RP +
+                                                       16 * k + 4 * (lane >> 4));
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float* from = s + (16 * k + 4 * (lane >> 4) + e) * C::PITCH + 16 * tl + (lane & 15);
@@ -577,12 +680,15 @@ __global__ __launch_bounds__(orth_threads(RT)) void k_orth_apply(OrthBatch b) {
 
 template <int RT>
 void poly_launch(hipStream_t st, const OrthBatch& b) {
-  if constexpr (RT < ORTH_BIG) {
+  if constexpr (RT == 1) return;       // k_orth_apply forms them itself
+  constexpr int PAIRS = orth_pairs(RT);
+  if (b.max_slices > 1)
+    QN_LAUNCH("k_orth_sum", k_orth_sum, dim3(PAIRS, b.count), dim3(1024), st, b, PAIRS);
+  if constexpr (RT > 1 && RT < ORTH_BIG) {
     QN_LAUNCH("k_orth_poly", (k_orth_poly<RT>), dim3(b.count), dim3(OrthPoly<RT>::NT), st, b);
-  } else {
-    constexpr int PAIRS = orth_pairs(RT), BLOCKS = orth_pairs(RT / 2);
-    QN_LAUNCH("k_orth_sum", (k_orth_sum<RT>), dim3(PAIRS, b.count), dim3(256), st, b);
-    QN_LAUNCH("k_orth_norm", (k_orth_norm<RT>), dim3(b.count), dim3(1024), st, b);
+  } else if constexpr (RT >= ORTH_BIG) {
+    constexpr int BLOCKS = orth_pairs(RT / 2);
+    QN_LAUNCH("k_orth_norm", (k_orth_norm<RT>), dim3((PAIRS + 3) / 4, b.count), dim3(1024), st, b);
     auto mul = [&](int n, OrthMul x, OrthMul y) {
       QN_LAUNCH("k_orth_mul", (k_orth_mul<RT>), dim3(BLOCKS, b.count, n), dim3(256), st, b, x, y);
     };
@@ -651,9 +757,9 @@ uintptr_t size_of(int32_t dtype) { return dtype == QN_BF16 ? 2 : 4; }
 OrthJob job_of_shape(const OrthShape& s, int32_t slices) {
   OrthJob J{};
   J.L = (int32_t)s.len();
-  J.r = s.r();
+  J.r = (int16_t)s.r();
   J.tall = s.tall();
-  J.slices = slices;
+  J.slices = (int16_t)slices;
   return J;
 }
 

@@ -6,9 +6,9 @@
 namespace qn {
 
 void orth_plan(OrthGroup* g, const OrthGroupShapes& s) {
-  // about 1024 workgroups in all, and few partial matrices where one workgroup
-  // has to add them up
-  const int rt = g->rt, most = rt < ORTH_BIG ? 32 : 64;
+  // about 1024 workgroups in all, and few partial matrices where every user
+  // adds them up itself
+  const int rt = g->rt, most = rt == 1 ? 32 : ORTH_MAX_SLICES;
   for (int i = 0; i < g->count; ++i) {
     const int64_t chunks = cdiv(s.len[i], orth_chunk(rt));
     g->slices[i] = (int32_t)std::max<int64_t>(

@@ -6,7 +6,7 @@
 
 namespace qn {
 
-constexpr int ORTH_JOBS = 32;               // matrices of one launch
+constexpr int ORTH_JOBS = 64;               // matrices of one launch
 constexpr int64_t ORTH_MAX_NUMEL = int64_t(1) << 31;
 
 // Matrices whose short side takes rt tiles of 16 (1, 2, 4, 8 or 16), chunks of
@@ -14,8 +14,10 @@ constexpr int64_t ORTH_MAX_NUMEL = int64_t(1) << 31;
 constexpr int orth_chunk(int rt) { return rt == 1 ? 256 : (rt == 2 ? 128 : 64); }
 constexpr int orth_threads(int rt) { return rt == 16 ? 512 : 256; }
 constexpr int orth_pairs(int rt) { return rt * (rt + 1) / 2; }
-// from here on a matrix's polynomials take launches of their own
+// from here on a matrix's polynomials take launches of their own; with one
+// tile they are formed where they are used
 constexpr int ORTH_BIG = 8;
+constexpr int ORTH_MAX_SLICES = 128;        // partial Gram matrices of one matrix
 constexpr int ORTH_MATS = 5;                // 64-bit matrices of one that does
 
 struct OrthShape {
