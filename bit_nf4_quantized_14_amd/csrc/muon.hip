@@ -90,6 +90,7 @@ struct OrthGroup4 {
   int64_t e;
   int n;
   int i[4], l[4];       // their places in the chunk
+  bool in_row;          // wide: in a row that the matrix has
   __device__ __forceinline__ OrthGroup4(const OrthJob& J, int chunk, int tid, int k) {
     const int at = (tid + C::NT * k) * 4;
     const int l0 = chunk * C::LC, nl = min(C::LC, J.L - l0);
@@ -97,13 +98,15 @@ struct OrthGroup4 {
       i[0] = at / C::LC;
       l[0] = at % C::LC;
       e = (int64_t)i[0] * J.L + l0 + l[0];
-      n = i[0] < J.r ? max(0, min(4, nl - l[0])) : 0;
+      in_row = i[0] < J.r;
+      n = in_row ? max(0, min(4, nl - l[0])) : 0;
 #pragma unroll
       for (int x = 1; x < 4; ++x) {
         i[x] = i[0];
         l[x] = l[0] + x;
       }
     } else {
+      in_row = true;
       e = (int64_t)l0 * J.r + at;
       n = max(0, min(4, nl * J.r - at));
       const float inv = 1.0f / (float)J.r;
@@ -167,7 +170,8 @@ __device__ __forceinline__ void orth_put(float* s, const OrthJob& J, const OrthG
                                          const float (&u)[4]) {
   using C = OrthCfg<RT>;
   if (!J.tall) {
-    *reinterpret_cast<f32x4*>(s + at.i[0] * C::PITCH + at.l[0]) = f32x4{u[0], u[1], u[2], u[3]};
+    if (at.in_row)
+      *reinterpret_cast<f32x4*>(s + at.i[0] * C::PITCH + at.l[0]) = f32x4{u[0], u[1], u[2], u[3]};
   } else {
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
@@ -177,15 +181,89 @@ __device__ __forceinline__ void orth_put(float* s, const OrthJob& J, const OrthG
   }
 }
 
+// Where a thread's groups of four lie when the chunk is whole, groups are
+// aligned and none crosses a row of the matrix: their places do not change
+// from chunk to chunk, and element x of a group is x or x PITCH floats behind
+// its first in LDS.
+template <int RT>
+struct OrthMap {
+  using C = OrthCfg<RT>;
+  bool tall;
+  int at[C::G4];          // place in LDS, -1: no group
+  int64_t off[C::G4];     // from the chunk's first element
+  __device__ __forceinline__ OrthMap(const OrthJob& J, int tid) {
+    tall = J.tall != 0;
+    const float inv = 1.0f / (float)J.r;
+#pragma unroll
+    for (int k = 0; k < C::G4; ++k) {
+      const int x = (tid + C::NT * k) * 4;
+      if (!tall) {
+        const int i = x / C::LC, l = x % C::LC;
+        at[k] = i < J.r ? i * C::PITCH + l : -1;
+        off[k] = (int64_t)i * J.L + l;
+      } else {
+        const int l = (int)(((float)x + 0.5f) * inv), i = x - l * J.r;   // as in OrthGroup4
+        at[k] = l < C::LC ? i * C::PITCH + l : -1;
+        off[k] = x;
+      }
+    }
+  }
+  // a chunk's first element
+  static __device__ __forceinline__ int64_t first(const OrthJob& J, int c) {
+    return (int64_t)c * C::LC * (J.tall ? J.r : 1);
+  }
+  // whether chunk c goes this way
+  static __device__ __forceinline__ bool ok(const OrthJob& J, int c) {
+    return J.vec && (c + 1) * (int64_t)C::LC <= J.L && (!J.tall || J.r % 4 == 0);
+  }
+};
+
+// The matrix's elements (or gradient and momentum) of a whole chunk.
+template <int MODE, int RT>
+__device__ __forceinline__ void orth_fetch(const OrthJob& J, const OrthMap<RT>& map, int c, int k,
+                                           float (&u)[4], float (&m)[4]) {
+  if (map.at[k] < 0) return;
+  const int64_t e = OrthMap<RT>::first(J, c) + map.off[k];
+  if constexpr (MODE == OM_BF16) {
+    const u32x2 v = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(J.g) + e);
+    u[0] = bf16_to_f32(v.x & 0xFFFFu);
+    u[1] = __uint_as_float(v.x & 0xFFFF0000u);
+    u[2] = bf16_to_f32(v.y & 0xFFFFu);
+    u[3] = __uint_as_float(v.y & 0xFFFF0000u);
+  } else {
+    const f32x4 v = *reinterpret_cast<const f32x4*>(static_cast<const float*>(J.g) + e);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) u[x] = v[x];
+    if constexpr (MODE == OM_MUON) {
+      const f32x4 w = *reinterpret_cast<const f32x4*>(J.m + e);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) m[x] = w[x];
+    }
+  }
+}
+
+template <int RT>
+__device__ __forceinline__ void orth_put(float* s, const OrthMap<RT>& map, int k,
+                                         const float (&u)[4]) {
+  if (map.at[k] < 0) return;
+  float* to = s + map.at[k];
+  if (!map.tall) {
+    *reinterpret_cast<f32x4*>(to) = f32x4{u[0], u[1], u[2], u[3]};
+  } else {
+#pragma unroll
+    for (int x = 0; x < 4; ++x) to[x * OrthCfg<RT>::PITCH] = u[x];
+  }
+}
+
 // Row 4 e + x of a tile as row 4 x + e, and back.
 __device__ __forceinline__ int orth_swap(int i) { return 4 * (i & 3) + (i >> 2); }
 
-// Rows of the chunk that a tall matrix does not have (SWAP: where orth_swap
-// puts them).
+// Rows of the chunk that the matrix does not have (SWAP: where orth_swap puts
+// them).
 template <int RT, bool SWAP>
 __device__ __forceinline__ void orth_pad(float* s, const OrthJob& J, int tid) {
   using C = OrthCfg<RT>;
-  if (!J.tall) return;
+  if (J.r == C::RP) return;
   for (int x = tid; x < C::RP * C::PITCH; x += C::NT) {
     const int row = x / C::PITCH;
     if ((SWAP ? orth_swap(row) : row) >= J.r) s[x] = 0.0f;
@@ -226,24 +304,36 @@ __global__ __launch_bounds__(orth_threads(RT)) void k_orth_gram(OrthBatch b) {
   // the next chunk's elements are on their way while this one's are used
   // (not where the pairs' sums take the registers)
   constexpr bool AHEAD = RT < 16;
-  float u[C::G4][4], m[MODE == OM_MUON ? C::G4 : 1][4];
+  const OrthMap<RT> map(J, tid);
+  float u[C::G4][4] = {}, m[MODE == OM_MUON ? C::G4 : 1][4] = {};
   auto fetch = [&](int c) {
+    if (OrthMap<RT>::ok(J, c)) {
 #pragma unroll
-    for (int k = 0; k < C::G4; ++k) {
-      const OrthGroup4<RT> at(J, c, tid, k);
-      orth_fetch<MODE, RT>(J, at, u[k], m[MODE == OM_MUON ? k : 0]);
+      for (int k = 0; k < C::G4; ++k)
+        orth_fetch<MODE, RT>(J, map, c, k, u[k], m[MODE == OM_MUON ? k : 0]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < C::G4; ++k)
+        orth_fetch<MODE, RT>(J, OrthGroup4<RT>(J, c, tid, k), u[k], m[MODE == OM_MUON ? k : 0]);
     }
   };
   if (AHEAD) fetch(c0);
   for (int c = c0; c < c1; ++c) {
     if (!AHEAD) fetch(c);
+    if constexpr (MODE == OM_MUON)
 #pragma unroll
-    for (int k = 0; k < C::G4; ++k) {
-      const OrthGroup4<RT> at(J, c, tid, k);
-      if constexpr (MODE == OM_MUON)
+      for (int k = 0; k < C::G4; ++k)
 #pragma unroll
         for (int e = 0; e < 4; ++e) u[k][e] = muon_u(u[k][e], m[k][e], b);
-      if (at.in(J, tid, k)) orth_put<RT>(s, J, at, u[k]);
+    if (OrthMap<RT>::ok(J, c)) {
+#pragma unroll
+      for (int k = 0; k < C::G4; ++k) orth_put<RT>(s, map, k, u[k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < C::G4; ++k) {
+        const OrthGroup4<RT> at(J, c, tid, k);
+        if (at.in(J, tid, k)) orth_put<RT>(s, J, at, u[k]);
+      }
     }
     if (AHEAD && c + 1 < c1) fetch(c + 1);
     __syncthreads();
@@ -567,6 +657,30 @@ __global__ __launch_bounds__(256) void k_orth_mul(OrthBatch b, OrthMul m0, OrthM
   }
 }
 
+// What becomes of four elements of O: the result, or the parameter's step and
+// the new momentum.
+template <int MODE, bool OUT_BF16>
+__device__ __forceinline__ void orth_finish(const OrthJob& J, const OrthBatch& b, int64_t e, int n,
+                                            bool vec, float (&o)[4], const float (&m)[4]) {
+  if constexpr (MODE == OM_MUON) {
+    uint16_t v[4];
+    load4<u32x2>(static_cast<const uint16_t*>(J.out) + e, n, vec, v);
+    {
+#pragma clang fp contract(off)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) o[x] = bf16_to_f32(v[x]) * b.decay - J.step * o[x];
+    }
+    store4<f32x4>(J.m + e, n, vec, m);
+  }
+  if constexpr (OUT_BF16) {
+    const uint32_t lo = pack_bf16x2(o[0], o[1]), hi = pack_bf16x2(o[2], o[3]);
+    const uint16_t w[4] = {(uint16_t)lo, (uint16_t)(lo >> 16), (uint16_t)hi, (uint16_t)(hi >> 16)};
+    store4<u32x2>(static_cast<uint16_t*>(J.out) + e, n, vec, w);
+  } else {
+    store4<f32x4>(static_cast<float*>(J.out) + e, n, vec, o);
+  }
+}
+
 // O = Q U of one chunk (v_mfma_f32_16x16x4_f32: lane l gives row or column l
 // % 16, reduction l / 16; accumulator v holds row 4 (l / 16) + v), and what
 // becomes of it: the result, or the parameter's step with the new momentum.
@@ -583,20 +697,35 @@ __global__ __launch_bounds__(orth_threads(RT)) void k_orth_apply(OrthBatch b) {
   __shared__ double sum[RT == 1 ? 1024 : 1];
   float m[C::G4][4];
   orth_pad<RT, RT == 1>(s, J, tid);
+  const bool whole = OrthMap<RT>::ok(J, chunk);
+  const OrthMap<RT> map(J, tid);
+  {
+    float u[C::G4][4] = {};
 #pragma unroll
-  for (int k = 0; k < C::G4; ++k) {
-    OrthGroup4<RT> at(J, chunk, tid, k);
-    if (!at.in(J, tid, k)) continue;
-    float u[4];
-    orth_fetch<MODE, RT>(J, at, u, m[k]);
+    for (int k = 0; k < C::G4; ++k) {
+      if (whole)
+        orth_fetch<MODE, RT>(J, map, chunk, k, u[k], m[k]);
+      else
+        orth_fetch<MODE, RT>(J, OrthGroup4<RT>(J, chunk, tid, k), u[k], m[k]);
+    }
     if constexpr (MODE == OM_MUON)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) u[e] = muon_u(u[e], m[k][e], b);
-    // with one tile, row 4 e + x goes to row 4 x + e: Q's reduction index
-    if constexpr (RT == 1)
+      for (int k = 0; k < C::G4; ++k)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) at.i[e] = orth_swap(at.i[e]);
-    orth_put<RT>(s, J, at, u);
+        for (int e = 0; e < 4; ++e) u[k][e] = muon_u(u[k][e], m[k][e], b);
+#pragma unroll
+    for (int k = 0; k < C::G4; ++k) {
+      // with one tile, row 4 e + x goes to row 4 x + e: Q's reduction index
+      if (whole && RT > 1) {
+        orth_put<RT>(s, map, k, u[k]);
+      } else {
+        OrthGroup4<RT> at(J, chunk, tid, k);
+        if (RT == 1)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) at.i[e] = orth_swap(at.i[e]);
+        if (at.in(J, tid, k)) orth_put<RT>(s, J, at, u[k]);
+      }
+    }
   }
   f32x4 q1;
   if constexpr (RT == 1) q1 = orth_poly_tile(b, jx, J.slices, sum, wave, lane);
@@ -642,38 +771,25 @@ __global__ __launch_bounds__(orth_threads(RT)) void k_orth_apply(OrthBatch b) {
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < C::G4; ++k) {
-    const OrthGroup4<RT> at(J, chunk, tid, k);
-    if (!at.in(J, tid, k) || at.n == 0) continue;
     float o[4];
-    if (!J.tall) {
-      const f32x4 x = *reinterpret_cast<const f32x4*>(s + at.i[0] * C::PITCH + at.l[0]);
+    if (whole) {
+      if (map.at[k] < 0) continue;
+      const float* from = s + map.at[k];
+      if (!map.tall) {
+        const f32x4 x = *reinterpret_cast<const f32x4*>(from);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = x[e];
+        for (int e = 0; e < 4; ++e) o[e] = x[e];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = from[e * C::PITCH];
+      }
+      orth_finish<MODE, OUT_BF16>(J, b, OrthMap<RT>::first(J, chunk) + map.off[k], 4, true, o, m[k]);
     } else {
+      const OrthGroup4<RT> at(J, chunk, tid, k);
+      if (!at.in(J, tid, k) || at.n == 0) continue;
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[e] = at.l[e] < C::LC ? s[at.i[e] * C::PITCH + at.l[e]] : 0.0f;
-    }
-    const bool vec = J.vec != 0;
-    if constexpr (MODE == OM_MUON) {
-      uint16_t* p = static_cast<uint16_t*>(J.out) + at.e;
-      uint16_t v[4];
-      load4<u32x2>(p, at.n, vec, v);
-      {
-#pragma clang fp contract(off)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          o[e] = bf16_to_f32(v[e]) * b.decay - J.step * o[e];
-      }
-      const uint32_t lo = pack_bf16x2(o[0], o[1]), hi = pack_bf16x2(o[2], o[3]);
-      const uint16_t w[4] = {(uint16_t)lo, (uint16_t)(lo >> 16), (uint16_t)hi, (uint16_t)(hi >> 16)};
-      store4<u32x2>(p, at.n, vec, w);
-      store4<f32x4>(J.m + at.e, at.n, vec, m[k]);
-    } else if constexpr (OUT_BF16) {
-      const uint32_t lo = pack_bf16x2(o[0], o[1]), hi = pack_bf16x2(o[2], o[3]);
-      const uint16_t w[4] = {(uint16_t)lo, (uint16_t)(lo >> 16), (uint16_t)hi, (uint16_t)(hi >> 16)};
-      store4<u32x2>(static_cast<uint16_t*>(J.out) + at.e, at.n, vec, w);
-    } else {
-      store4<f32x4>(static_cast<float*>(J.out) + at.e, at.n, vec, o);
+      orth_finish<MODE, OUT_BF16>(J, b, at.e, at.n, J.vec != 0, o, m[k]);
     }
   }
 }
