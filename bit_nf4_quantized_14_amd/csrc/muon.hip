@@ -58,6 +58,16 @@ static_assert(sizeof(OrthBatch) <= 4096, "kernel arguments");
 // What U is: a matrix of fp32 or bf16, or the momentum's (Nesterov) update.
 enum OrthMode { OM_F32 = 0, OM_BF16 = 1, OM_MUON = 2 };
 
+// Workgroup barrier for what is in LDS: waits for this wave's LDS operations
+// alone (s_waitcnt lgkmcnt(0)), not for its loads on the way, as
+// __syncthreads() does.
+__device__ __forceinline__ void lds_barrier() {
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_s_waitcnt(0xC07F);
+  __builtin_amdgcn_s_barrier();
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
 __device__ __forceinline__ int job_of(const int32_t* first, int count, int block) {
   int j = 0;
   while (j + 1 < count && block >= first[j + 1]) ++j;
@@ -319,13 +329,24 @@ __global__ __launch_bounds__(orth_threads(RT)) void k_orth_gram(OrthBatch b) {
   };
   if (AHEAD) fetch(c0);
   for (int c = c0; c < c1; ++c) {
-    if (!AHEAD) fetch(c);
-    if constexpr (MODE == OM_MUON)
+    if constexpr (MODE == OM_MUON && AHEAD)
 #pragma unroll
       for (int k = 0; k < C::G4; ++k)
 #pragma unroll
         for (int e = 0; e < 4; ++e) u[k][e] = muon_u(u[k][e], m[k][e], b);
-    if (OrthMap<RT>::ok(J, c)) {
+    if (!AHEAD) {
+#pragma unroll 4
+      for (int k = 0; k < C::G4; ++k) {
+        const OrthGroup4<RT> at(J, c, tid, k);
+        if (!at.in(J, tid, k)) continue;
+        float x[4], y[4];
+        orth_fetch<MODE, RT>(J, at, x, y);
+        if constexpr (MODE == OM_MUON)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = muon_u(x[e], y[e], b);
+        orth_put<RT>(s, J, at, x);
+      }
+    } else if (OrthMap<RT>::ok(J, c)) {
 #pragma unroll
       for (int k = 0; k < C::G4; ++k) orth_put<RT>(s, map, k, u[k]);
     } else {
@@ -336,7 +357,7 @@ __global__ __launch_bounds__(orth_threads(RT)) void k_orth_gram(OrthBatch b) {
       }
     }
     if (AHEAD && c + 1 < c1) fetch(c + 1);
-    __syncthreads();
+    lds_barrier();
     const float* from = s + (lane & 15) * C::PITCH + (lane >> 4);
     if constexpr (SPLIT) {
 #pragma unroll 4
@@ -363,7 +384,7 @@ __global__ __launch_bounds__(orth_threads(RT)) void k_orth_gram(OrthBatch b) {
                                                         acc[p], 0, 0, 0);
       }
     }
-    __syncthreads();
+    lds_barrier();
   }
   double* to = b.part + ((int64_t)jx * b.max_slices + slice) * (C::PAIRS * 256);
   if constexpr (SPLIT) {
@@ -416,113 +437,102 @@ __global__ __launch_bounds__(1024) void k_orth_sum(OrthBatch b, int pairs) {
 // layout for rows 16 j .. and reduction 16 i + 4 v .., and the second's for
 // columns 16 j .., so a stored tile is read by its lane as it was written.  A
 // product's tiles on and below the diagonal are formed, the others are their
-// mirror images.
+// mirror images.  Register v of lane l lies at 64 v + (l ^ 4 v): a mirrored
+// store, where 16 lanes go to 16 lanes of one register or another, then
+// spreads over all banks (at 64 v + l it took 64 cycles, 45% of the kernel).
 template <int RT>
 struct OrthPoly {
   static constexpr int RP = 16 * RT, NT = RT == 4 ? 1024 : 256, WAVES = NT / 64;
   static constexpr int PAIRS = orth_pairs(RT), MAT = RT * RT * 256;
-  static_assert(2 * PAIRS <= 2 * WAVES, "two tiles to a wave at most");
+  static_assert(PAIRS <= WAVES, "a tile to a wave");
   static __device__ __forceinline__ double* tile(double* m, int i, int j) {
     return m + (i * RT + j) * 256;
   }
+  static __device__ __forceinline__ int at(int v, int lane) { return 64 * v + (lane ^ (4 * v)); }
   static __device__ __forceinline__ f64x4 mul(double* x, double* y, int i, int j, int lane) {
     f64x4 acc = {0, 0, 0, 0};
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-      const double *a = tile(x, t, i) + lane, *c = tile(y, t, j) + lane;
+      const double *a = tile(x, t, i), *c = tile(y, t, j);
 #pragma unroll
       for (int v = 0; v < 4; ++v)
-        acc = __builtin_amdgcn_mfma_f64_16x16x4f64(a[64 * v], c[64 * v], acc, 0, 0, 0);
+        acc = __builtin_amdgcn_mfma_f64_16x16x4f64(a[at(v, lane)], c[at(v, lane)], acc, 0, 0, 0);
     }
     return acc;
   }
   static __device__ __forceinline__ void put(double* m, int i, int j, int lane, const f64x4& x) {
+    const int mv = (lane & 15) >> 2, ml = 16 * (lane & 3) + (lane >> 4);
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      tile(m, i, j)[64 * v + lane] = x[v];
-      if (i != j) tile(m, j, i)[16 * (lane & 15) + 4 * v + (lane >> 4)] = x[v];
+      tile(m, i, j)[at(v, lane)] = x[v];
+      if (i != j) tile(m, j, i)[at(mv, ml + 4 * v)] = x[v];
     }
   }
 };
 
 // The polynomials of a matrix with 17 to 64 rows: one workgroup, everything in
-// LDS.  A product's result waits in registers until all have read its place.
+// LDS, a barrier after each set of products that do not wait for one another.
 template <int RT>
 __global__ __launch_bounds__(OrthPoly<RT>::NT) void k_orth_poly(OrthBatch b) {
   using C = OrthPoly<RT>;
-  __shared__ double A[C::MAT];
-  __shared__ double P[C::MAT];
-  __shared__ double Q[C::MAT];
+  __shared__ double lds[5 * C::MAT];
+  double *A = lds, *P = A + C::MAT, *R = P + C::MAT, *Q = R + C::MAT, *Q2 = Q + C::MAT;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const double* part = b.part + (int64_t)blockIdx.x * b.max_slices * (C::PAIRS * 256);
   int i, j;
-  f64x4 x, y;
-  if (wave < C::PAIRS) {
-    orth_pair(wave, i, j);
-#pragma unroll
-    for (int v = 0; v < 4; ++v) x[v] = part[wave * 256 + 64 * v + lane];
-    C::put(A, i, j, lane, x);
-  }
-  __syncthreads();
+  orth_pair(min(wave, C::PAIRS - 1), i, j);
+  f64x4 x;
+  // the trace, by every wave
   double t = 0.0;
   if (lane < 16)
 #pragma unroll
     for (int k = 0; k < RT; ++k)
-      t += C::tile(A, k, k)[64 * (lane >> 2) + 16 * (lane & 3) + lane];
+      t += part[(k * (k + 1) / 2 + k) * 256 + 64 * (lane >> 2) + 16 * (lane & 3) + lane];
 #pragma unroll
   for (int d = 8; d > 0; d /= 2) t += __shfl_xor(t, d);
   const double inv = 1.0 / (sqrt(__shfl(t, 0)) + b.eps);
-  __syncthreads();
-  for (int k = tid; k < C::MAT; k += C::NT) A[k] = (A[k] * inv) * inv;
+  if (wave < C::PAIRS) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) x[v] = (part[wave * 256 + 64 * v + lane] * inv) * inv;
+    C::put(A, i, j, lane, x);
+  }
   __syncthreads();
   for (int st = 0; st < b.steps; ++st) {
     const bool last = st + 1 == b.steps;
     if (wave < C::PAIRS) {          // P = a I + b A + c A A
-      orth_pair(wave, i, j);
       x = C::mul(A, A, i, j, lane);
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         const double d = i == j && 4 * v + (lane >> 4) == (lane & 15) ? b.a : 0.0;
-        x[v] = d + b.b * C::tile(A, i, j)[64 * v + lane] + b.c * x[v];
+        x[v] = d + b.b * C::tile(A, i, j)[C::at(v, lane)] + b.c * x[v];
       }
       C::put(P, i, j, lane, x);
-      if (st == 0) C::put(Q, i, j, lane, x);
+      if (st == 0) C::put(Q2, i, j, lane, x);
     }
     __syncthreads();
-    // products 0 .. PAIRS - 1: Q = P Q, the others: A = P A
-    const int n0 = st == 0 ? C::PAIRS : 0, n1 = last ? C::PAIRS : 2 * C::PAIRS;
-    const int u0 = n0 + wave, u1 = u0 + C::WAVES;
-    auto mul = [&](int u) {
-      double* m = u < C::PAIRS ? Q : A;
-      orth_pair(u < C::PAIRS ? u : u - C::PAIRS, i, j);
-      return C::mul(P, m, i, j, lane);
-    };
-    auto put = [&](int u, const f64x4& v) {
-      orth_pair(u < C::PAIRS ? u : u - C::PAIRS, i, j);
-      C::put(u < C::PAIRS ? Q : A, i, j, lane, v);
-    };
-    if (u0 < n1) x = mul(u0);
-    if (u1 < n1) y = mul(u1);
-    __syncthreads();
-    if (u0 < n1) put(u0, x);
-    if (u1 < n1) put(u1, y);
+    // products 0 .. PAIRS - 1: P Q, the others: P A
+    for (int u = (st == 0 ? C::PAIRS : 0) + wave; u < (last ? C::PAIRS : 2 * C::PAIRS);
+         u += C::WAVES) {
+      const bool q = u < C::PAIRS;
+      int ui, uj;
+      orth_pair(q ? u : u - C::PAIRS, ui, uj);
+      C::put(q ? Q2 : R, ui, uj, lane, C::mul(P, q ? Q : A, ui, uj, lane));
+    }
+    double* s = Q;
+    Q = Q2;
+    Q2 = s;
     __syncthreads();
     if (!last) {                    // A = (P A) P
-      if (wave < C::PAIRS) {
-        orth_pair(wave, i, j);
-        x = C::mul(A, P, i, j, lane);
-      }
-      __syncthreads();
-      if (wave < C::PAIRS) C::put(A, i, j, lane, x);
+      if (wave < C::PAIRS) C::put(A, i, j, lane, C::mul(R, P, i, j, lane));
       __syncthreads();
     }
   }
   float* q = b.q + (int64_t)blockIdx.x * C::RP * C::RP;
   for (int k = tid; k < C::MAT; k += C::NT) {
-    const int ti = (k >> 8) / RT, tj = (k >> 8) % RT;
-    const int row = 16 * ti + 4 * ((k >> 6) & 3) + ((k & 63) >> 4), col = 16 * tj + (k & 15);
-    q[row * C::RP + col] = (float)(Q[k] * inv);
+    const int ti = (k >> 8) / RT, tj = (k >> 8) % RT, v = (k >> 6) & 3, l = k & 63;
+    q[(16 * ti + 4 * v + (l >> 4)) * C::RP + 16 * tj + (l & 15)] =
+        (float)(C::tile(Q, ti, tj)[C::at(v, l)] * inv);
   }
 }
 
@@ -565,9 +575,8 @@ __device__ __forceinline__ f32x4 orth_poly_tile(const OrthBatch& b, int jx, int 
 #pragma unroll
     for (int v = 0; v < 4; ++v)
       P[v] = (4 * v + (lane >> 4) == (lane & 15) ? b.a : 0.0) + b.b * A[v] + b.c * P[v];
-    const f64x4 R = mul(P, A);
     Q = st == 0 ? P : mul(P, Q);
-    A = mul(R, P);
+    if (st + 1 < b.steps) A = mul(mul(P, A), P);
   }
   f32x4 q;
 #pragma unroll

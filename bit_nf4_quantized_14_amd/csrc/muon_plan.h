@@ -13,6 +13,8 @@ constexpr int64_t ORTH_MAX_NUMEL = int64_t(1) << 31;
 // orth_chunk(rt) positions of the long side.
 constexpr int orth_chunk(int rt) { return rt == 1 ? 256 : (rt == 2 ? 128 : 64); }
 constexpr int orth_threads(int rt) { return rt == 16 ? 512 : 256; }
+// workgroups of k_orth_gram on a CU at a time (its registers)
+constexpr int orth_gram_wgs(int rt) { return rt <= 2 ? 4 : (rt == 4 ? 3 : (rt == 8 ? 2 : 1)); }
 constexpr int orth_pairs(int rt) { return rt * (rt + 1) / 2; }
 // from here on a matrix's polynomials take launches of their own; with one
 // tile they are formed where they are used
