@@ -31,11 +31,12 @@ struct HeadDx {
   const uint16_t *g, *w;
   const int32_t *cnt, *idx;
   const float* scale;          // [mp] factor of a row
-  int rows, dim, slices;
-  int64_t v0, n, vp, mp;
-  uint16_t* dx;                // bf16 [rows][dim], or null: the sums go to acc
-  float* acc;                  // [slices][mp][dim]
-  bool add;                    // onto what acc holds
+  int rows, dim, wgs;
+  int64_t v0, n, vp;
+  uint16_t* dx;                // bf16 [rows][dim], written with the last piece
+  float* acc;                  // [mp][dim], sums of the pieces so far
+  float* part;                 // parts of tiles (HeadDeal)
+  bool first, last;            // piece
 };
 void launch_head_dx(hipStream_t st, int tile, const HeadDx& a);
 

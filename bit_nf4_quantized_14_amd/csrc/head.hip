@@ -239,40 +239,6 @@ __global__ __launch_bounds__(256) void k_head_fill(HeadFill a) {
   }
 }
 
-struct HeadDxSum {
-  const float *acc, *scale;
-  const int32_t *cnt, *idx;
-  int32_t dim, slices;
-  int64_t mp;
-  uint16_t* dx;
-};
-
-// dX of a counted row from its slices.
-__global__ __launch_bounds__(256) void k_head_dx_sum(HeadDxSum a) {
-  const int m = blockIdx.x;
-  if (m >= *a.cnt) return;
-  const int k = (blockIdx.y * 256 + threadIdx.x) * 8;
-  if (k >= a.dim) return;
-  const float sc = a.scale[m];
-  f32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
-  const float* from = a.acc + (int64_t)m * a.dim + k;
-  for (int s = 0; s < a.slices; ++s, from += a.mp * a.dim) {
-    const f32x4 u = *reinterpret_cast<const f32x4*>(from);
-    const f32x4 v = *reinterpret_cast<const f32x4*>(from + 4);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      lo[e] += u[e];
-      hi[e] += v[e];
-    }
-  }
-  u32x4 o;
-  o.x = pack_bf16x2(lo[0] * sc, lo[1] * sc);
-  o.y = pack_bf16x2(lo[2] * sc, lo[3] * sc);
-  o.z = pack_bf16x2(hi[0] * sc, hi[1] * sc);
-  o.w = pack_bf16x2(hi[2] * sc, hi[3] * sc);
-  *reinterpret_cast<u32x4*>(a.dx + (int64_t)a.idx[m] * a.dim + k) = o;
-}
-
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
 bool valid_head(const qn_head* h) {
@@ -414,11 +380,11 @@ extern "C" int qn_head_loss_bwd(const qn_head* h, const float* loss, const float
   d.scale = r.scale;
   d.rows = (int)h->rows;
   d.dim = (int)h->dim;
-  d.slices = P.slices;
+  d.wgs = P.dx_wgs;
   d.vp = P.vp;
-  d.mp = P.mp;
-  d.dx = P.direct ? dx : nullptr;
+  d.dx = dx;
   d.acc = ws_at<float>(ws, P.acc);
+  d.part = ws_at<float>(ws, P.part);
   HeadDw e{};
   e.g = g.g;
   e.xs = f.xs;
@@ -431,23 +397,11 @@ extern "C" int qn_head_loss_bwd(const qn_head* h, const float* loss, const float
     g.v0 = d.v0 = e.v0 = i * P.vp;
     g.v1 = std::min(h->vocab, g.v0 + P.vp);
     d.n = e.n = g.v1 - g.v0;
-    d.add = i > 0;
+    d.first = i == 0;
+    d.last = i + 1 == P.pieces;
     if (h->rows > 0) launch_head_logits(st, P.tile, true, g);
     if (need_dx) launch_head_dx(st, P.tile_dx, d);
     if (dw) launch_head_dw(st, P.tile_dw, e);
-  }
-  if (need_dx && !P.direct) {
-    HeadDxSum s{};
-    s.acc = d.acc;
-    s.scale = r.scale;
-    s.cnt = r.cnt;
-    s.idx = r.idx;
-    s.dim = d.dim;
-    s.slices = P.slices;
-    s.mp = P.mp;
-    s.dx = dx;
-    QN_LAUNCH("k_head_dx_sum", k_head_dx_sum,
-              dim3((unsigned)h->rows, (unsigned)cdiv(h->dim, 2048)), dim3(256), st, s);
   }
   return check_launch();
 }

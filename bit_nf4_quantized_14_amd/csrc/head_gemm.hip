@@ -476,82 +476,178 @@ __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_logits(HeadLogits a)
   }
 }
 
+// Tile (tp, tq) of dX's product by its place in the order of the steps: as
+// head_tile_at's, without the XCDs.
+__device__ __forceinline__ void dx_tile(int i, int tp, int tq, int& p, int& q) {
+  const int group = i / (4 * tp), first = 4 * group, n = min(4, tq - first);
+  const int in = i - group * 4 * tp;
+  q = first + in % n;
+  p = in / n;
+}
+
+// One 32 x 32 tile of sums where it belongs: dX, or the sums of the pieces so
+// far.  Its rows are columns k0 .. of dX, its column l % 32 is counted row m.
+__device__ __forceinline__ void dx_store(const HeadDx& a, float (&x)[16], int k0, int m, int cnt,
+                                         int lane) {
+  if (m >= cnt) return;
+  if (!a.first || !a.last) {
+    float* at = a.acc + (int64_t)m * a.dim;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int k = k0 + 8 * g + 4 * (lane >> 5);
+      if (k >= a.dim) continue;
+      f32x4 o = {0, 0, 0, 0};
+      if (!a.first) o = *reinterpret_cast<const f32x4*>(at + k);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = x[4 * g + e] += o[e];
+      if (!a.last) *reinterpret_cast<f32x4*>(at + k) = o;
+    }
+    if (!a.last) return;
+  }
+  const float sc = a.scale[m];
+  u32x4 out[2];
+#pragma unroll
+  for (int v = 0; v < 16; ++v) x[v] *= sc;
+  pack_rows(x, out);
+  uint16_t* to = a.dx + (int64_t)a.idx[m] * a.dim;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int k = k0 + 16 * h + 8 * (lane >> 5);
+    if (k < a.dim) *reinterpret_cast<u32x4*>(to + k) = out[h];
+  }
+}
+
+// A workgroup's tiles and parts of tiles (HeadDeal): whole tiles go where they
+// belong, parts to `part`.
 template <int TILE>
 __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_dx(HeadDx a) {
   using C = HeadCfg<TILE>;
   HEAD_LDS(C, C::RFAR, C::RNEAR);
   const int cnt = *a.cnt;
-  const int tiles_p = (a.dim + C::BP - 1) / C::BP;
-  int tp, tq;
-  if (!head_tile_at(blockIdx.x, tiles_p, (cnt + C::BQ - 1) / C::BQ, tp, tq)) return;
-  const int slice = blockIdx.y;
-  const int k0 = tp * C::BP, q0 = tq * C::BQ;
-  HeadLoader<C::BP, HK_T, C::NT> lp;
-  HeadLoader<C::BQ, HK_N, C::NT> lq;
-  using OP = typename decltype(lp)::O;
-  using OQ = typename decltype(lq)::O;
-  lp.base = reinterpret_cast<const char*>(a.w + a.v0 * a.dim);
-  lp.bytes = (uint32_t)a.dim * 2;
-  lp.step_bytes = a.dim * (HD_BK * 2);
-#pragma unroll
-  for (int i = 0; i < OP::CH; ++i) {
-    const int k = k0 + OP::col_t(tid);
-    lp.vo[i] = k < a.dim ? (uint32_t)(OP::red_t(tid, i) * a.dim + k) * 2 : G_OOB;
+  const int tiles_p = (a.dim + C::BP - 1) / C::BP, tiles_q = (cnt + C::BQ - 1) / C::BQ;
+  const HeadDeal d = head_deal(a.wgs, tiles_p * tiles_q, (int)((a.n + HD_BK - 1) / HD_BK));
+  const int whole = d.tiles / d.wgs;                // rounds of whole tiles
+  // workgroups are dealt round the 8 XCDs; each works on neighbouring tiles
+  const int xcd = blockIdx.x & 7, in = blockIdx.x >> 3, per = d.wgs >> 3;
+  const int h0 = d.rest * xcd / 8, h1 = d.rest * (xcd + 1) / 8;   // its heads
+  const bool is_head = in < h1 - h0;
+  const int e = xcd * per - h0 + in - (h1 - h0);    // extra workgroup, if not
+  int64_t at = 0, end = 0;
+  if (d.extra > 0 && !is_head) {
+    at = head_tail_first(d, e);
+    end = head_tail_first(d, e + 1);
   }
-  lq.base = reinterpret_cast<const char*>(a.g + g_block(q0, 0, a.vp) + (q0 & 255) * HD_BK);
-  lq.bytes = 0x7fffffffu;
-  lq.step_bytes = 256 * HD_BK * 2;
+  for (int seg = 0;; ++seg) {
+    int tile, s0 = 0, s1 = d.steps, slot = -1;
+    if (seg < whole) {
+      tile = seg * d.wgs + xcd * per + in;
+    } else if (is_head) {
+      if (seg > whole) break;
+      tile = whole * d.wgs + h0 + in;
+      s1 = d.head;
+      if (d.extra > 0) slot = h0 + in;
+    } else {
+      if (at >= end) break;
+      const int tail = d.steps - d.head, t = (int)(at / tail);
+      s0 = d.head + (int)(at - (int64_t)t * tail);
+      s1 = (int)min<int64_t>(d.steps, s0 + (end - at));
+      at += s1 - s0;
+      tile = whole * d.wgs + t;
+      slot = d.rest + t + e;
+    }
+    tile = __builtin_amdgcn_readfirstlane(tile);
+    s0 = __builtin_amdgcn_readfirstlane(s0);
+    s1 = __builtin_amdgcn_readfirstlane(s1);
+    int tp, tq;
+    dx_tile(tile, tiles_p, tiles_q, tp, tq);
+    const int k0 = tp * C::BP, q0 = tq * C::BQ;
+    HeadLoader<C::BP, HK_T, C::NT> lp;
+    HeadLoader<C::BQ, HK_N, C::NT> lq;
+    using OP = typename decltype(lp)::O;
+    using OQ = typename decltype(lq)::O;
+    lp.base = reinterpret_cast<const char*>(a.w + a.v0 * a.dim);
+    lp.bytes = (uint32_t)a.dim * 2;
+    lp.step_bytes = a.dim * (HD_BK * 2);
 #pragma unroll
-  for (int i = 0; i < OQ::CH; ++i)
-    lq.vo[i] = (uint32_t)(OQ::row_n(tid, i) * HD_BK + OQ::red_n(tid)) * 2;
-  const int steps = (int)((a.n + HD_BK - 1) / HD_BK);
-  const int each = steps / a.slices, rest = steps % a.slices;
-  const int s0 = __builtin_amdgcn_readfirstlane(slice * each + min(slice, rest));
-  const int s1 = __builtin_amdgcn_readfirstlane(s0 + each + (slice < rest));
-  f32x16 acc[C::TP][C::TQ];
-  zero_acc<TILE>(acc);
-  lp.start(s0, (int)a.n);
-  lq.start(s0, (int)a.vp);
-  head_mainloop<TILE, RINGP, RINGQ>(lp, lq, lds, s1 - s0, wave, tid, lane, acc);
-
+    for (int i = 0; i < OP::CH; ++i) {
+      const int k = k0 + OP::col_t(tid);
+      lp.vo[i] = k < a.dim ? (uint32_t)(OP::red_t(tid, i) * a.dim + k) * 2 : G_OOB;
+    }
+    lq.base = reinterpret_cast<const char*>(a.g + g_block(q0, 0, a.vp) + (q0 & 255) * HD_BK);
+    lq.bytes = 0x7fffffffu;
+    lq.step_bytes = 256 * HD_BK * 2;
 #pragma unroll
-  for (int j = 0; j < C::TQ; ++j) {
-    const int m = q0 + wq * C::WTQ + 32 * j + (lane & 31);
-    const bool row = m < cnt;
-    const float sc = row && a.dx ? a.scale[m] : 0.0f;
-    const int64_t to = row && a.dx ? (int64_t)a.idx[m] * a.dim : 0;
+    for (int i = 0; i < OQ::CH; ++i)
+      lq.vo[i] = (uint32_t)(OQ::row_n(tid, i) * HD_BK + OQ::red_n(tid)) * 2;
+    lp.start(s0, (int)a.n);
+    lq.start(s0, (int)a.vp);
+    f32x16 acc[C::TP][C::TQ];
+    zero_acc<TILE>(acc);
+    if (seg > 0) __syncthreads();      // the last segment's stages have been read
+    head_mainloop<TILE, RINGP, RINGQ>(lp, lq, lds, s1 - s0, wave, tid, lane, acc);
+    if (slot < 0) {
 #pragma unroll
-    for (int i = 0; i < C::TP; ++i) {
-      const int kc = k0 + wp * C::WTP + 32 * i;
-      if (a.dx) {
-        float x[16];
-        u32x4 out[2];
+      for (int j = 0; j < C::TQ; ++j)
 #pragma unroll
-        for (int v = 0; v < 16; ++v) x[v] = acc[i][j][v] * sc;
-        pack_rows(x, out);
+        for (int i = 0; i < C::TP; ++i) {
+          float v[16];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int k = kc + 16 * h + 8 * (lane >> 5);
-          if (row && k < a.dim) *reinterpret_cast<u32x4*>(a.dx + to + k) = out[h];
+          for (int x = 0; x < 16; ++x) v[x] = acc[i][j][x];
+          dx_store(a, v, k0 + wp * C::WTP + 32 * i, q0 + wq * C::WTQ + 32 * j + (lane & 31), cnt,
+                   lane);
         }
-      } else {
+    } else {
+      f32x4* to = reinterpret_cast<f32x4*>(a.part + (int64_t)slot * (C::BP * C::BQ));
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int k = kc + 8 * g + 4 * (lane >> 5);
-          if (!row || k >= a.dim) continue;
-          f32x4* at = reinterpret_cast<f32x4*>(a.acc + ((int64_t)slice * a.mp + m) * a.dim + k);
-          f32x4 x = {acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
-                     acc[i][j][4 * g + 3]};
-          if (a.add) {
-            const f32x4 o = *at;
+      for (int i = 0; i < C::TP; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] += o[e];
-          }
-          *at = x;
-        }
-      }
+        for (int j = 0; j < C::TQ; ++j)
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            to[((i * C::TQ + j) * 4 + g) * C::NT + tid] =
+                f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
+                      acc[i][j][4 * g + 3]};
     }
   }
+}
+
+// The last round's tiles from their parts: the head, then the tail's in order.
+// A workgroup takes the 32 x 32 tile blockIdx.y of every wave of tile
+// blockIdx.x.
+template <int TILE>
+__global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_dx_join(HeadDx a) {
+  using C = HeadCfg<TILE>;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wp = wave / C::WQ, wq = wave % C::WQ;
+  const int cnt = *a.cnt;
+  const int tiles_p = (a.dim + C::BP - 1) / C::BP, tiles_q = (cnt + C::BQ - 1) / C::BQ;
+  const HeadDeal d = head_deal(a.wgs, tiles_p * tiles_q, (int)((a.n + HD_BK - 1) / HD_BK));
+  const int t = blockIdx.x;
+  if (d.extra == 0 || t >= d.rest) return;
+  const int tail = d.steps - d.head;
+  const int e0 = head_tail_owner(d, (int64_t)t * tail);
+  const int e1 = head_tail_owner(d, (int64_t)(t + 1) * tail - 1);
+  int tp, tq;
+  dx_tile(d.tiles - d.rest + t, tiles_p, tiles_q, tp, tq);
+  const int i = blockIdx.y / C::TQ, j = blockIdx.y % C::TQ;
+  const int64_t size = C::BP * C::BQ / 4;           // of a part, in groups of four
+  const f32x4* from = reinterpret_cast<const f32x4*>(a.part) + (i * C::TQ + j) * 4 * C::NT + tid;
+  f32x4 sum[4];
+#pragma unroll
+  for (int g = 0; g < 4; ++g) sum[g] = from[t * size + g * C::NT];
+#pragma unroll 4
+  for (int e = e0; e <= e1; ++e)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const f32x4 v = from[(d.rest + t + e) * size + g * C::NT];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) sum[g][x] += v[x];
+    }
+  float x[16];
+#pragma unroll
+  for (int v = 0; v < 16; ++v) x[v] = sum[v >> 2][v & 3];
+  dx_store(a, x, tp * C::BP + wp * C::WTP + 32 * i, tq * C::BQ + wq * C::WTQ + 32 * j + (lane & 31),
+           cnt, lane);
 }
 
 template <int TILE>
@@ -634,8 +730,11 @@ void launch_head_logits(hipStream_t st, int tile, bool bwd, const HeadLogits& a)
 template <int TILE>
 static void dx_t(hipStream_t st, const HeadDx& a) {
   using C = HeadCfg<TILE>;
-  const dim3 grid((unsigned)(cdiv(a.dim, C::BP) * cdiv(a.rows, C::BQ)), (unsigned)a.slices);
-  QN_LAUNCH("k_head_dx", (k_head_dx<TILE>), grid, dim3(C::NT), st, a);
+  QN_LAUNCH("k_head_dx", (k_head_dx<TILE>), dim3((unsigned)a.wgs), dim3(C::NT), st, a);
+  // tiles of the last round: at most those of a.rows, fewer than a.wgs
+  const dim3 grid((unsigned)std::min<int64_t>(a.wgs, cdiv(a.dim, C::BP) * cdiv(a.rows, C::BQ)),
+                  C::TP * C::TQ);
+  QN_LAUNCH("k_head_dx_join", (k_head_dx_join<TILE>), grid, dim3(C::NT), st, a);
 }
 
 void launch_head_dx(hipStream_t st, int tile, const HeadDx& a) {

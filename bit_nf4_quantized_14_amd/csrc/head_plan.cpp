@@ -56,16 +56,11 @@ HeadBwdPlan head_bwd_plan(int64_t rows, int64_t dim, int64_t vocab, bool need_dx
   P.vp = cdiv(cdiv(vt, P.pieces), 256) * 256;
   P.pieces = cdiv(vt, P.vp);
   P.tile = pick_tile(std::min(P.vp, vocab), rows);
-  P.tile_dx = pick_tile(dim, rows);
   P.tile_dw = pick_tile(dim, std::min(P.vp, vocab));
-  P.slices = 1;
-  if (need_dx) {
-    const int64_t tiles = cdiv(dim, head_bp(P.tile_dx)) * cdiv(rows, head_bq(P.tile_dx));
-    const int64_t want = cdiv(2 * G_CUS, std::max<int64_t>(1, tiles));
-    if (tiles < G_CUS)
-      P.slices = (int)std::max<int64_t>(1, std::min<int64_t>({want, P.vp / 512, 64}));
-  }
-  P.direct = P.slices == 1 && P.pieces == 1;
+  // The steps of dX's product are dealt evenly however few tiles there are, so
+  // its tiles are the largest that the rows fill.
+  P.tile_dx = rows <= 32 ? HT_SMALL : (rows <= 128 ? HT_128 : HT_256);
+  P.dx_wgs = P.tile_dx == HT_256 ? G_CUS : 2 * G_CUS;
   size_t at = 0;
   P.cnt = take(&at, 256);
   P.idx = take(&at, size_t(P.mp) * 4);
@@ -74,7 +69,9 @@ HeadBwdPlan head_bwd_plan(int64_t rows, int64_t dim, int64_t vocab, bool need_dx
   P.scale = take(&at, size_t(P.mp) * 4);
   P.g = take(&at, size_t(P.mp) * P.vp * 2);
   P.xs = take(&at, need_dw ? size_t(P.mp) * dim * 2 : 0);
-  P.acc = take(&at, need_dx && !P.direct ? size_t(P.slices) * P.mp * dim * 4 : 0);
+  P.acc = take(&at, need_dx && P.pieces > 1 ? size_t(P.mp) * dim * 4 : 0);
+  // at most 8/10 of the workgroups have heads: head_parts() < 2 dx_wgs
+  P.part = take(&at, need_dx ? size_t(P.dx_wgs) * 2 * head_bp(P.tile_dx) * head_bq(P.tile_dx) * 4 : 0);
   P.total = at;
   return P;
 }

@@ -22,6 +22,52 @@ constexpr int head_bq(int t) { return t == HT_256 ? 256 : (t == HT_128 ? 128 : 3
 // rows of D that one statistics entry covers: a wave's part of a tile
 constexpr int head_wave_p(int t) { return t == HT_256 ? 128 : (t == HT_128 ? 64 : 32); }
 
+#if defined(__HIPCC__)
+#define HEAD_HD __host__ __device__ inline
+#else
+#define HEAD_HD inline
+#endif
+
+// How the product for dX is dealt to G workgroups that run at once.  Of T tiles
+// the first T - T % G go to them whole, round after round.  The rest R = T % G
+// would leave G - R of them idle for a tile's time, so (where R is at most 8/10
+// of G) R workgroups take the first `head` steps of a tile each, in step with
+// one another, and the others the steps behind them, one tile after another
+// in equal runs.  A tile's parts are joined afterwards.
+struct HeadDeal {
+  int wgs, tiles, steps;
+  int rest;             // tiles of the last round
+  int head;             // steps of its first parts; `steps`: they are whole
+  int extra;            // workgroups for the others
+  int64_t tails;        // steps for them, in all
+};
+HEAD_HD HeadDeal head_deal(int wgs, int tiles, int steps) {
+  HeadDeal d{wgs, tiles, steps, tiles % wgs, steps, 0, 0};
+  if (d.rest == 0 || 10 * d.rest > 8 * wgs) return d;
+  const int each = (int)(((int64_t)steps * d.rest + wgs - 1) / wgs);
+  const int head = each > 8 ? each : 8;    // fewer cost more to join than they save
+  if (head >= steps) return d;
+  d.head = head;
+  d.extra = wgs - d.rest;
+  d.tails = (int64_t)d.rest * (steps - head);
+  return d;
+}
+// The first of the tails' steps that extra workgroup e takes (e = extra: the
+// end).
+HEAD_HD int64_t head_tail_first(const HeadDeal& d, int e) {
+  const int64_t each = d.tails / d.extra, more = d.tails % d.extra;
+  return e * each + (e < more ? e : more);
+}
+// The extra workgroup that takes step s of the tails.
+HEAD_HD int head_tail_owner(const HeadDeal& d, int64_t s) {
+  const int64_t each = d.tails / d.extra, more = d.tails % d.extra;
+  return (int)(s < more * (each + 1) ? s / (each + 1) : more + (s - more * (each + 1)) / each);
+}
+// Parts in memory: tile t of the last round has its head at t, and what extra
+// workgroup e did of its tail at rest + t + e (from one part of the tails to
+// the next, t or e grows by one, or both).
+HEAD_HD int head_parts(const HeadDeal& d) { return d.extra > 0 ? 2 * d.rest + d.extra : 0; }
+
 bool valid_head_sizes(int64_t rows, int64_t dim, int64_t vocab);
 
 struct HeadFwdPlan {
@@ -37,9 +83,8 @@ struct HeadBwdPlan {
   int64_t mp;
   int64_t vp;            // words of a piece (a multiple of 256)
   int64_t pieces;
-  int slices;            // of the words of a piece, in the product for dX
-  bool direct;           // dX from its product itself (one piece, one slice)
-  size_t cnt, idx, lab, lseo, scale, g, xs, acc, total;
+  int dx_wgs;            // workgroups of the product for dX
+  size_t cnt, idx, lab, lseo, scale, g, xs, acc, part, total;
 };
 HeadBwdPlan head_bwd_plan(int64_t rows, int64_t dim, int64_t vocab, bool need_dx, bool need_dw);
 
