@@ -7,6 +7,25 @@
 
 namespace qn {
 
+// The rows of a call, and the lists made of them: in a launch of their own, or
+// (up to HEAD_FEW rows) by each workgroup of the logits' kernel, the first of
+// which leaves them in memory.
+constexpr int HEAD_FEW = 32;
+struct HeadRows {
+  const int64_t* labels;
+  int64_t vocab;
+  int32_t rows, dim;
+  int32_t *cnt, *idx, *lab;             // cnt[0]: counted rows, cnt[1]: 0
+  int32_t* status;
+  // forward: rows that do not count become 0
+  float *loss, *lse, *lse_lo;
+  // backward
+  const float *in_loss, *in_lse, *in_lo, *dloss;
+  float *lseo, *scale;
+  const uint16_t* x;
+  uint16_t *dx, *xs;                    // either may be null
+};
+
 // Logits of the counted rows, as tiles that stay in registers.
 struct HeadLogits {
   const uint16_t *x, *w;       // bf16 [rows][dim], [vocab][dim]
@@ -16,15 +35,18 @@ struct HeadLogits {
   // words [v0, v1) of the vocabulary
   int64_t v0, v1;
   // forward: statistics and label's logit
-  float2* part;                // [slices][mp]: maximum and sum without the label
+  float2* part;                // [slices][mp]: maximum (to base 2) and sum
+                               // without the label, of 128 words
   float* hit;                  // [mp]
   int64_t mp;
   // backward: softmax over the other words, -1 at the label, in bf16
-  const float* lseo;           // [mp] log-sum-exp of the other words
+  const float* lseo;           // [mp] log2 of the sum over the other words
   uint16_t* g;                 // [mp / 256][vp / 64][256][64], zeros for words from v1
   int64_t vp;
 };
-void launch_head_logits(hipStream_t st, int tile, bool bwd, const HeadLogits& a);
+// few: the rows' lists are not made yet (tile HT_SMALL)
+void launch_head_logits(hipStream_t st, int tile, bool bwd, bool few, const HeadLogits& a,
+                        const HeadRows& rows);
 
 // dX of the counted rows from a piece of G: sums over words [v0, v0 + n).
 struct HeadDx {

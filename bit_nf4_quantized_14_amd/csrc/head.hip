@@ -17,7 +17,7 @@
 // k_head_rows lists the others, and the products run over the list.
 #include <cmath>
 
-#include "head.h"
+#include "head_rows.h"
 
 namespace {
 
@@ -25,19 +25,6 @@ using namespace qn;
 
 constexpr int HR_THREADS = 1024;
 constexpr int HR_ROWS = 4;              // rows of a thread in a round
-
-struct HeadRows {
-  const int64_t* labels;
-  int64_t vocab;
-  int32_t rows, mp;
-  int32_t *cnt, *idx, *lab;             // cnt[0]: counted rows, cnt[1]: 0
-  int32_t* status;
-  // forward: rows that do not count become 0
-  float *loss, *lse, *lse_lo;
-  // backward
-  const float *in_loss, *in_lse, *in_lo, *dloss;
-  float *lseo, *scale;
-};
 
 // Lists the counted rows in order (one workgroup), and for the backward the
 // log-sum-exp of their other words and their factor c_t (1 - exp(-loss_t)).
@@ -95,17 +82,8 @@ __global__ __launch_bounds__(HR_THREADS) void k_head_rows(HeadRows a) {
   if constexpr (BWD) {
     __syncthreads();
     const float each = base > 0 ? 1.0f / (float)base : 0.0f;
-    for (int m = tid; m < base; m += HR_THREADS) {
-      const int t = a.idx[m];
-      const float loss = a.in_loss[t];
-      const double rest = -expm1(-(double)loss);            // 1 - p(label)
-      const double lse = (double)a.in_lse[t] + (a.in_lo ? (double)a.in_lo[t] : 0.0);
-      // a label that is certain to the last bit, or the only word there is:
-      // no other word has a share
-      const bool sure = loss < 1.2e-38f;
-      a.lseo[m] = sure ? __builtin_inff() : (float)(lse + log(rest));
-      a.scale[m] = sure ? 0.0f : (float)((a.dloss ? a.dloss[t] : each) * rest);
-    }
+    for (int m = tid; m < base; m += HR_THREADS)
+      head_row_bwd(a, a.idx[m], each, a.lseo[m], a.scale[m]);
   }
 }
 
@@ -133,6 +111,7 @@ __global__ __launch_bounds__(HF_THREADS) void k_head_finish(HeadFinish a) {
   const int cnt = a.cnt[0], blocks = max(1, (cnt + HF_ROWS - 1) / HF_ROWS);
   if ((int)blockIdx.x >= blocks) return;
   const int m = blockIdx.x * HF_ROWS + lane;
+  // logarithms to base 2
   float mx = -__builtin_inff(), sum = 0.0f;
   if (m < cnt) {
     for (int s0 = wave; s0 < a.slices; s0 += 8 * HF_WAVES) {
@@ -146,9 +125,9 @@ __global__ __launch_bounds__(HF_THREADS) void k_head_finish(HeadFinish a) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) top = fmaxf(top, p[i].x);
       const float at = top == -__builtin_inff() ? 0.0f : top;
-      sum *= expf(mx - at);
+      sum *= __builtin_amdgcn_exp2f(mx - at);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum += p[i].y * expf(p[i].x - at);
+      for (int i = 0; i < 8; ++i) sum += p[i].y * __builtin_amdgcn_exp2f(p[i].x - at);
       mx = top;
     }
   }
@@ -156,14 +135,15 @@ __global__ __launch_bounds__(HF_THREADS) void k_head_finish(HeadFinish a) {
   __syncthreads();
   double loss = 0.0;
   if (wave == 0 && m < cnt) {
-    double top = -__builtin_inf();
+    float top = -__builtin_inff();
 #pragma unroll
-    for (int w = 0; w < HF_WAVES; ++w) top = fmax(top, (double)s_part[w][lane].x);
-    const double at = top == -__builtin_inf() ? 0.0 : top;
+    for (int w = 0; w < HF_WAVES; ++w) top = fmaxf(top, s_part[w][lane].x);
+    const float from = top == -__builtin_inff() ? 0.0f : top;
     double all = 0.0;
 #pragma unroll
     for (int w = 0; w < HF_WAVES; ++w)
-      all += (double)s_part[w][lane].y * exp((double)s_part[w][lane].x - at);
+      all += (double)(s_part[w][lane].y * __builtin_amdgcn_exp2f(s_part[w][lane].x - from));
+    const double at = (double)from / HEAD_LOG2E;
     const double other = at + log(all), hit = (double)a.hit[m];
     // log(1 + exp(d)) and max + log(1 + exp(-|d|)); two equal infinities
     // have no difference, and the loss then none either
@@ -204,39 +184,9 @@ __global__ __launch_bounds__(HF_THREADS) void k_head_finish(HeadFinish a) {
   }
 }
 
-struct HeadFill {
-  const uint16_t* x;
-  const int64_t* labels;
-  const int32_t *cnt, *idx;
-  const float* scale;
-  int64_t vocab;
-  int32_t rows, dim;
-  uint16_t *dx, *xs;       // either may be null
-};
-
-// A workgroup to a row: zeros into dX where the row does not count, and the
-// scaled rows of X behind one another for dW.
-__global__ __launch_bounds__(256) void k_head_fill(HeadFill a) {
-  const int t = blockIdx.x, chunks = a.dim / 8;
-  if (a.dx != nullptr && t < a.rows) {
-    const int64_t lab = a.labels[t];
-    if (lab < 0 || lab >= a.vocab)
-      for (int c = threadIdx.x; c < chunks; c += 256)
-        reinterpret_cast<u32x4*>(a.dx + (int64_t)t * a.dim)[c] = u32x4{0, 0, 0, 0};
-  }
-  if (a.xs == nullptr) return;
-  if (t >= *a.cnt) return;
-  u32x4* to = reinterpret_cast<u32x4*>(a.xs + (int64_t)t * a.dim);
-  const float sc = a.scale[t];
-  const u32x4* from = reinterpret_cast<const u32x4*>(a.x + (int64_t)a.idx[t] * a.dim);
-  for (int c = threadIdx.x; c < chunks; c += 256) {
-    const u32x4 v = from[c];
-    u32x4 o;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      o[e] = pack_bf16x2(sc * bf16_to_f32(v[e] & 0xFFFFu), sc * __uint_as_float(v[e] & 0xFFFF0000u));
-    to[c] = o;
-  }
+// A workgroup to a row (head_fill_row).
+__global__ __launch_bounds__(256) void k_head_fill(HeadRows a) {
+  head_fill_row(a, blockIdx.x, *a.cnt, a.idx, a.scale, threadIdx.x, 256);
 }
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
@@ -275,7 +225,8 @@ extern "C" int qn_head_loss_fwd(const qn_head* h, float* loss, float* lse, float
   r.labels = h->labels;
   r.vocab = h->vocab;
   r.rows = (int32_t)h->rows;
-  r.mp = (int32_t)P.mp;
+  r.dim = (int32_t)h->dim;
+  r.x = h->x;
   r.cnt = ws_at<int32_t>(ws, P.cnt);
   r.idx = ws_at<int32_t>(ws, P.idx);
   r.lab = ws_at<int32_t>(ws, P.lab);
@@ -283,7 +234,8 @@ extern "C" int qn_head_loss_fwd(const qn_head* h, float* loss, float* lse, float
   r.loss = loss;
   r.lse = lse;
   r.lse_lo = lse_lo;
-  QN_LAUNCH("k_head_rows", (k_head_rows<false>), dim3(1), dim3(HR_THREADS), st, r);
+  const bool few = h->rows > 0 && h->rows <= HEAD_FEW;
+  if (!few) QN_LAUNCH("k_head_rows", (k_head_rows<false>), dim3(1), dim3(HR_THREADS), st, r);
   if (h->rows > 0) {
     HeadLogits g{};
     g.x = h->x;
@@ -297,7 +249,7 @@ extern "C" int qn_head_loss_fwd(const qn_head* h, float* loss, float* lse, float
     g.part = ws_at<float2>(ws, P.part);
     g.hit = ws_at<float>(ws, P.hit);
     g.mp = P.mp;
-    launch_head_logits(st, P.tile, false, g);
+    launch_head_logits(st, P.tile, false, few, g, r);
   }
   HeadFinish f{};
   f.idx = r.idx;
@@ -334,7 +286,8 @@ extern "C" int qn_head_loss_bwd(const qn_head* h, const float* loss, const float
   r.labels = h->labels;
   r.vocab = h->vocab;
   r.rows = (int32_t)h->rows;
-  r.mp = (int32_t)P.mp;
+  r.dim = (int32_t)h->dim;
+  r.x = h->x;
   r.cnt = ws_at<int32_t>(ws, P.cnt);
   r.idx = ws_at<int32_t>(ws, P.idx);
   r.lab = ws_at<int32_t>(ws, P.lab);
@@ -344,20 +297,12 @@ extern "C" int qn_head_loss_bwd(const qn_head* h, const float* loss, const float
   r.dloss = dloss;
   r.lseo = ws_at<float>(ws, P.lseo);
   r.scale = ws_at<float>(ws, P.scale);
-  QN_LAUNCH("k_head_rows", (k_head_rows<true>), dim3(1), dim3(HR_THREADS), st, r);
-  HeadFill f{};
-  f.x = h->x;
-  f.labels = h->labels;
-  f.cnt = r.cnt;
-  f.idx = r.idx;
-  f.scale = r.scale;
-  f.vocab = h->vocab;
-  f.rows = (int32_t)h->rows;
-  f.dim = (int32_t)h->dim;
-  f.dx = need_dx ? dx : nullptr;
-  f.xs = dw ? ws_at<uint16_t>(ws, P.xs) : nullptr;
-  if (h->rows > 0)
-    QN_LAUNCH("k_head_fill", k_head_fill, dim3((unsigned)h->rows), dim3(256), st, f);
+  r.dx = need_dx ? dx : nullptr;
+  r.xs = dw ? ws_at<uint16_t>(ws, P.xs) : nullptr;
+  const bool few = h->rows > 0 && h->rows <= HEAD_FEW;
+  if (!few) QN_LAUNCH("k_head_rows", (k_head_rows<true>), dim3(1), dim3(HR_THREADS), st, r);
+  if (h->rows > HEAD_FEW)
+    QN_LAUNCH("k_head_fill", k_head_fill, dim3((unsigned)h->rows), dim3(256), st, r);
 
   HeadLogits g{};
   g.x = h->x;
@@ -387,7 +332,7 @@ extern "C" int qn_head_loss_bwd(const qn_head* h, const float* loss, const float
   d.part = ws_at<float>(ws, P.part);
   HeadDw e{};
   e.g = g.g;
-  e.xs = f.xs;
+  e.xs = r.xs;
   e.cnt = r.cnt;
   e.rows = d.rows;
   e.dim = d.dim;
@@ -399,7 +344,7 @@ extern "C" int qn_head_loss_bwd(const qn_head* h, const float* loss, const float
     d.n = e.n = g.v1 - g.v0;
     d.first = i == 0;
     d.last = i + 1 == P.pieces;
-    if (h->rows > 0) launch_head_logits(st, P.tile, true, g);
+    if (h->rows > 0) launch_head_logits(st, P.tile, true, few && i == 0, g, r);
     if (need_dx) launch_head_dx(st, P.tile_dx, d);
     if (dw) launch_head_dw(st, P.tile_dw, e);
   }

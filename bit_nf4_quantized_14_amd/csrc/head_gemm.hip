@@ -18,7 +18,7 @@
 // 3), and read transposed with ds_read_b64_tr_b16.  LDS holds two stages;
 // the next stage's loads are issued at the start of a step and written
 // behind the step's last MFMAs.
-#include "head.h"
+#include "head_rows.h"
 
 namespace {
 
@@ -33,14 +33,13 @@ template <int TILE>
 struct HeadCfg {
   static constexpr int BP = head_bp(TILE), BQ = head_bq(TILE);
   static constexpr int WP = TILE == HT_SMALL ? 4 : 2;
-  static constexpr int WQ = TILE == HT_256 ? 4 : (TILE == HT_128 ? 2 : 1);
+  static constexpr int WQ = TILE == HT_256 || TILE == HT_HALF ? 4 : (TILE == HT_128 ? 2 : 1);
   static constexpr int NT = 64 * WP * WQ;
   static constexpr int WTP = BP / WP, WTQ = BQ / WQ;    // a wave's part
   static constexpr int TP = WTP / 32, TQ = WTQ / 32;    // its 32 x 32 tiles
   // stages in LDS of the operand that comes from far (the weight, or G for
   // dW) and of the other one
   static constexpr int RFAR = TILE == HT_SMALL ? 4 : 3, RNEAR = TILE == HT_SMALL ? 4 : 2;
-  static_assert(WTP == head_wave_p(TILE), "statistics entries");
 };
 
 // s_waitcnt vmcnt(n) expcnt(7) lgkmcnt(0) (gfx9 encoding)
@@ -58,9 +57,9 @@ typedef uint32_t HeadRsrc __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ HeadRsrc head_rsrc(const char* base, uint32_t bytes) {
   const uint64_t at = reinterpret_cast<uint64_t>(base);
   HeadRsrc r;
-  r.x = (uint32_t)at;
-  r.y = (uint32_t)(at >> 32) & 0xFFFFu;
-  r.z = bytes;
+  r.x = __builtin_amdgcn_readfirstlane((uint32_t)at);
+  r.y = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32)) & 0xFFFFu;
+  r.z = __builtin_amdgcn_readfirstlane(bytes);
   r.w = G_RSRC_FLAGS;
   return r;
 }
@@ -69,7 +68,8 @@ __device__ __forceinline__ HeadRsrc head_rsrc(const char* base, uint32_t bytes) 
 // lds, r and so are the same in the whole wave.  Written as assembly because
 // the compiler, which cannot tell the stages apart, would wait for all of
 // these loads at the next read of any stage; the waits are HEAD_WAIT_VM and
-// the barriers of the main loop.
+// the barriers of the main loop.  m0 is only ever set right before its use, in
+// compiled code too.
 __device__ __forceinline__ void load_lds16(const HeadRsrc& r, uint32_t lds, uint32_t vo, int so) {
   asm volatile(
       "s_mov_b32 m0, %0\n\t"
@@ -77,7 +77,7 @@ __device__ __forceinline__ void load_lds16(const HeadRsrc& r, uint32_t lds, uint
       "buffer_load_dwordx4 %1, %2, %3 offen lds"
       :
       : "s"(lds), "v"(vo), "s"(r), "s"(so)
-      : "memory", "m0");
+      : "memory");
 }
 
 // One operand's tile of DIM positions x 64 reduction elements.  A stage is
@@ -203,7 +203,7 @@ struct HeadLoader {
       ok = O::red_n(tid) < left;
     } else if constexpr (KIND == HK_T) {
       const int rows = left < 0 ? 0 : (left < HD_BK ? left : HD_BK);
-      r = head_rsrc(base, __builtin_amdgcn_readfirstlane((uint32_t)rows * bytes));
+      r = head_rsrc(base, (uint32_t)rows * bytes);
     } else {
       r = head_rsrc(base + (so >> 2) * vp_bytes + (so & 3) * (HD_BK * 128), 0x7fffffffu);
     }
@@ -224,28 +224,64 @@ struct HeadLoader {
   }
 };
 
+// The stages of a main loop: RP of the first operand from byte 0 of the LDS,
+// RQ of the second behind them.
+template <int TILE, int RP, int RQ, class LP, class LQ>
+struct HeadStages {
+  using C = HeadCfg<TILE>;
+  using OP = typename LP::O;
+  using OQ = typename LQ::O;
+  static constexpr int PB = C::BP * HD_BK * 2, QB = C::BQ * HD_BK * 2;   // bytes of a stage
+  static constexpr int LD = OP::CH + OQ::CH;                             // loads per step
+  static constexpr int RMIN = RP < RQ ? RP : RQ, RMAX = RP < RQ ? RQ : RP;
+  static_assert(RMAX - RMIN <= 1 && RMIN >= 2, "one operand is at most one step ahead");
+  // loads still out when all of the next step's have landed
+  static constexpr int OUT = (RMIN - 2) * LD + (RP > RQ ? OP::CH : 0) + (RQ > RP ? OQ::CH : 0);
+
+  // The first stages, in the order of the loop, where the far operand is a
+  // step ahead.
+  static __device__ __forceinline__ void fill(LP& lp, LQ& lq, uint32_t lds0, int wave, int tid) {
+#pragma unroll
+    for (int s = 0; s < RMAX; ++s) {
+      const int sp = s - (RMAX - RP), sq = s - (RMAX - RQ);
+      if (sp >= 0 && RP <= RQ) {
+        lp.begin(tid);
+        for (int i = 0; i < OP::CH; ++i) lp.slot(lds0 + sp * PB, i, wave, tid);
+        lp.end();
+      }
+      if (sq >= 0) {
+        lq.begin(tid);
+        for (int i = 0; i < OQ::CH; ++i) lq.slot(lds0 + RP * PB + sq * QB, i, wave, tid);
+        lq.end();
+      }
+      if (sp >= 0 && RP > RQ) {
+        lp.begin(tid);
+        for (int i = 0; i < OP::CH; ++i) lp.slot(lds0 + sp * PB, i, wave, tid);
+        lp.end();
+      }
+    }
+  }
+};
+
 // `steps` reduction steps into acc.  Fragments are read one slice of 16
 // ahead, the first slice of a step during the last one of the step before.  So
 // when a step comes to its last slice, its own stages have been read by
 // everyone (barrier) and the next ones must have landed; the loads into the
 // free stages go out there.  The operand that comes from far has a stage more
 // than the other: its loads have a step's time more.
-template <int TILE, int RP, int RQ, class LP, class LQ, int TP, int TQ>
+// FILLED: the first stages are on their way already, with stores behind them.
+template <int TILE, int RP, int RQ, bool FILLED, class LP, class LQ, int TP, int TQ>
 __device__ __forceinline__ void head_mainloop(LP& lp, LQ& lq, char* lds, int steps, int wave,
                                               int tid, int lane, f32x16 (&acc)[TP][TQ]) {
   using C = HeadCfg<TILE>;
-  using OP = typename LP::O;
-  using OQ = typename LQ::O;
-  constexpr int PB = C::BP * HD_BK * 2, QB = C::BQ * HD_BK * 2;     // bytes of a stage
+  using S = HeadStages<TILE, RP, RQ, LP, LQ>;
+  using OP = typename S::OP;
+  using OQ = typename S::OQ;
+  constexpr int PB = S::PB, QB = S::QB, LD = S::LD;
   constexpr int MPK = TP * TQ;                                      // MFMAs per k16 slice
   constexpr int FR = TP + TQ;                                       // fragments per slice
   constexpr int RD = TP * OP::READS + TQ * OQ::READS;               // LDS reads per slice
-  constexpr int LD = OP::CH + OQ::CH;                               // loads per step
   constexpr int RDM = (RD + MPK - 1) / MPK;
-  constexpr int RMIN = RP < RQ ? RP : RQ, RMAX = RP < RQ ? RQ : RP;
-  static_assert(RMAX - RMIN <= 1 && RMIN >= 2, "one operand is at most one step ahead");
-  // loads still out when all of the next step's have landed
-  constexpr int OUT = (RMIN - 2) * LD + (RP > RQ ? OP::CH : 0) + (RQ > RP ? OQ::CH : 0);
   const int wp = wave / C::WQ, wq = wave % C::WQ;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void*)lds;
   const typename OP::template Reader<TP> rp(wp * C::WTP, lane);
@@ -261,27 +297,12 @@ __device__ __forceinline__ void head_mainloop(LP& lp, LQ& lq, char* lds, int ste
       else lq.slot(lds0 + sq, n - FIRST, wave, tid);
     }
   };
-  // in the order of the loop, where the far operand is a step ahead
-#pragma unroll
-  for (int s = 0; s < RMAX; ++s) {
-    const int sp = s - (RMAX - RP), sq = s - (RMAX - RQ);
-    if (sp >= 0 && RP <= RQ) {
-      lp.begin(tid);
-      for (int i = 0; i < OP::CH; ++i) lp.slot(lds0 + sp * PB, i, wave, tid);
-      lp.end();
-    }
-    if (sq >= 0) {
-      lq.begin(tid);
-      for (int i = 0; i < OQ::CH; ++i) lq.slot(lds0 + RP * PB + sq * QB, i, wave, tid);
-      lq.end();
-    }
-    if (sp >= 0 && RP > RQ) {
-      lp.begin(tid);
-      for (int i = 0; i < OP::CH; ++i) lp.slot(lds0 + sp * PB, i, wave, tid);
-      lp.end();
-    }
+  if constexpr (FILLED) {
+    HEAD_WAIT_VM(0);
+  } else {
+    S::fill(lp, lq, lds0, wave, tid);
+    HEAD_WAIT_VM(S::OUT + LD);
   }
-  HEAD_WAIT_VM(OUT + LD);
   head_barrier();
   u32x4 a[2][TP], b[2][TQ];
   // Fragment n of slice kk
@@ -303,7 +324,7 @@ __device__ __forceinline__ void head_mainloop(LP& lp, LQ& lq, char* lds, int ste
 #pragma unroll
         for (int n = 0; n < FR; ++n) frag(n, sp, sq, kk + 1);
       } else {
-        HEAD_WAIT_VM(OUT);
+        HEAD_WAIT_VM(S::OUT);
         head_barrier();
         __builtin_amdgcn_sched_barrier(0);
         lp.begin(tid);
@@ -349,6 +370,14 @@ __device__ __forceinline__ bool head_tile_at(int pid, int tp, int tq, int& p, in
   return true;
 }
 
+// The same order without the XCDs.
+__device__ __forceinline__ void dx_tile(int i, int tp, int tq, int& p, int& q) {
+  const int group = i / (4 * tp), first = 4 * group, n = min(4, tq - first);
+  const int in = i - group * 4 * tp;
+  q = first + in % n;
+  p = in / n;
+}
+
 template <int TILE>
 __device__ __forceinline__ void zero_acc(f32x16 (&acc)[HeadCfg<TILE>::TP][HeadCfg<TILE>::TQ]) {
 #pragma unroll
@@ -384,88 +413,88 @@ __device__ __forceinline__ void pack_rows(const float (&x)[16], u32x4 (&out)[2])
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);                           \
   const int wp = wave / C::WQ, wq = wave % C::WQ
 
+// Logits p0 .. of counted rows q0 .. as they leave the main loop: statistics or
+// G.  lab and lseo are those of counted rows; `red` is LDS for the statistics of
+// the waves that share an entry (null: none do).
 template <int TILE, bool BWD>
-__global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_logits(HeadLogits a) {
+__device__ __forceinline__ void logits_finish(
+    const HeadLogits& a, f32x16 (&acc)[HeadCfg<TILE>::TP][HeadCfg<TILE>::TQ], int64_t p0, int q0,
+    int cnt, const int32_t* labs, const float* lseos, float2* red, int wp, int wq, int lane) {
   using C = HeadCfg<TILE>;
-  HEAD_LDS(C, C::RFAR, C::RNEAR);
-  const int cnt = *a.cnt;
-  int tp, tq;
-  if (!head_tile_at(blockIdx.x, (int)((a.v1 - a.v0 + C::BP - 1) / C::BP), (cnt + C::BQ - 1) / C::BQ,
-                    tp, tq))
-    return;
-  const int64_t p0 = a.v0 + (int64_t)tp * C::BP;      // first word
-  const int q0 = tq * C::BQ;                          // first counted row
-  HeadLoader<C::BP, HK_N, C::NT> lp;
-  HeadLoader<C::BQ, HK_N, C::NT> lq;
-  using OP = typename decltype(lp)::O;
-  using OQ = typename decltype(lq)::O;
-  lp.base = reinterpret_cast<const char*>(a.w + p0 * a.dim);
-  lp.bytes = (uint32_t)(min<int64_t>(C::BP, a.vocab - p0) * a.dim * 2);
-  lp.step_bytes = lq.step_bytes = HD_BK * 2;
-  lp.start(0, a.dim);
-  lq.start(0, a.dim);
-#pragma unroll
-  for (int i = 0; i < OP::CH; ++i)
-    lp.vo[i] = (uint32_t)(OP::row_n(tid, i) * a.dim + OP::red_n(tid)) * 2;
-  lq.base = reinterpret_cast<const char*>(a.x);
-  lq.bytes = (uint32_t)((int64_t)a.rows * a.dim * 2);
-#pragma unroll
-  for (int i = 0; i < OQ::CH; ++i) {
-    const int m = q0 + OQ::row_n(tid, i);
-    lq.vo[i] = m < cnt ? (uint32_t)((int64_t)a.idx[m] * a.dim + OQ::red_n(tid)) * 2 : G_OOB;
-  }
-  f32x16 acc[C::TP][C::TQ];
-  zero_acc<TILE>(acc);
-  head_mainloop<TILE, RINGP, RINGQ>(lp, lq, lds, (a.dim + HD_BK - 1) / HD_BK, wave, tid, lane, acc);
-
   // word of accumulator v of tile i: pw + 32 i + 8 (v / 4) + v % 4
   const int64_t pw = p0 + wp * C::WTP + 4 * (lane >> 5);
+  const int left = (int)min<int64_t>(a.v1 - pw, C::WTP);   // words of this part, from pw
+  const bool ragged = __any(left < C::WTP - 4 * (lane >> 5));
+  float2 st[C::TQ];
 #pragma unroll
   for (int j = 0; j < C::TQ; ++j) {
     const int m = q0 + wq * C::WTQ + 32 * j + (lane & 31);
     const bool row = m < cnt;
     // the label's distance from the lane's first word, where this lane holds
     // it (its partner l ^ 32 has the other four words of every eight)
-    const int64_t far = row ? (int64_t)a.lab[m] - pw : -1;
+    const int64_t far = row ? (int64_t)labs[m] - pw : -1;
     const int lab = far >= 0 && far < C::WTP && (far & 4) == 0 ? (int)far : -1;
-    const int left = (int)min<int64_t>(a.v1 - pw, C::WTP);   // words of this part, from pw
     if constexpr (!BWD) {
-      float mx = HD_NEG_INF, hit = 0.0f;
+      // in few parts is a word's label, or the vocabulary's end
+      if (__any(lab >= 0)) {
+        float hit = 0.0f;
+#pragma unroll
+        for (int i = 0; i < C::TP; ++i)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) {
+            const bool is = 32 * i + 8 * (v >> 2) + (v & 3) == lab;
+            hit = is ? acc[i][j][v] : hit;
+            acc[i][j][v] = is ? HD_NEG_INF : acc[i][j][v];
+          }
+        if (lab >= 0) a.hit[m] = hit;
+      }
+      if (ragged)
+#pragma unroll
+        for (int i = 0; i < C::TP; ++i)
+#pragma unroll
+          for (int v = 0; v < 16; ++v)
+            acc[i][j][v] = 32 * i + 8 * (v >> 2) + (v & 3) >= left ? HD_NEG_INF : acc[i][j][v];
+      float mx = HD_NEG_INF;
 #pragma unroll
       for (int i = 0; i < C::TP; ++i)
 #pragma unroll
-        for (int v = 0; v < 16; ++v) {
-          const int o = 32 * i + 8 * (v >> 2) + (v & 3);
-          float x = acc[i][j][v];
-          hit = o == lab ? x : hit;
-          x = o == lab || o >= left ? HD_NEG_INF : x;
-          acc[i][j][v] = x;
-          mx = fmaxf(mx, x);
-        }
-      if (lab >= 0) a.hit[m] = hit;
+        for (int v = 0; v < 16; ++v) mx = fmaxf(mx, acc[i][j][v]);
       mx = fmaxf(mx, __shfl_xor(mx, 32));
+      // the maximum to base 2 is only where the sum is held from: its rounding
+      // is no error
+      mx *= HD_LOG2E;
       const float at = mx == HD_NEG_INF ? 0.0f : mx;
-      float sum = 0.0f;
+      float sum[2] = {0.0f, 0.0f};
 #pragma unroll
       for (int i = 0; i < C::TP; ++i)
 #pragma unroll
         for (int v = 0; v < 16; ++v)
-          sum += __builtin_amdgcn_exp2f((acc[i][j][v] - at) * HD_LOG2E);
-      sum += __shfl_xor(sum, 32);
-      if (lane < 32 && row)
-        a.part[(int64_t)((int)((p0 - a.v0) / C::WTP) + wp) * a.mp + m] = make_float2(mx, sum);
+          sum[v & 1] += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][v], HD_LOG2E, -at));
+      st[j] = make_float2(mx, sum[0] + sum[1]);
+      st[j].y += __shfl_xor(st[j].y, 32);
+      if constexpr (C::WTP == HEAD_SLICE) {
+        if (lane < 32 && row)
+          a.part[(int64_t)((int)((p0 - a.v0) / HEAD_SLICE) + wp) * a.mp + m] = st[j];
+      } else {
+        if (lane < 32) red[wp * C::BQ + wq * C::WTQ + 32 * j + lane] = st[j];
+      }
     } else {
-      const float lseo = row ? a.lseo[m] : 0.0f;
+      // rows behind the last counted one are read by nobody
+      const float lseo = row ? lseos[m] : 0.0f;
+      const bool any = __any(lab >= 0);
 #pragma unroll
       for (int i = 0; i < C::TP; ++i) {
         float x[16];
         u32x4 out[2];
 #pragma unroll
-        for (int v = 0; v < 16; ++v) {
-          const int o = 32 * i + 8 * (v >> 2) + (v & 3);
-          const float e = __builtin_amdgcn_exp2f((acc[i][j][v] - lseo) * HD_LOG2E);
-          x[v] = !row || o >= left ? 0.0f : (o == lab ? -1.0f : e);
-        }
+        for (int v = 0; v < 16; ++v)
+          x[v] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][v], HD_LOG2E, -lseo));
+        if (any || ragged)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) {
+            const int o = 32 * i + 8 * (v >> 2) + (v & 3);
+            x[v] = o >= left ? 0.0f : (o == lab ? -1.0f : x[v]);
+          }
         pack_rows(x, out);
         const int64_t v = (p0 - a.v0) + wp * C::WTP + 32 * i;
         uint16_t* g = a.g + g_block(m, v, a.vp) + (m & 255) * HD_BK + (v & 63) + 8 * (lane >> 5);
@@ -474,15 +503,192 @@ __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_logits(HeadLogits a)
       }
     }
   }
+  if constexpr (!BWD && C::WTP != HEAD_SLICE) {
+    static_assert(C::BP == HEAD_SLICE, "an entry to a tile");
+    __syncthreads();
+    const int tid = threadIdx.x;
+    if (tid < C::BQ && q0 + tid < cnt) {
+      float2 t = red[tid];
+#pragma unroll
+      for (int w = 1; w < C::WP; ++w) {
+        const float2 o = red[w * C::BQ + tid];
+        const float top = fmaxf(t.x, o.x), at = top == HD_NEG_INF ? 0.0f : top;
+        t.y = t.y * __builtin_amdgcn_exp2f(t.x - at) + o.y * __builtin_amdgcn_exp2f(o.x - at);
+        t.x = top;
+      }
+      a.part[(p0 - a.v0) / HEAD_SLICE * a.mp + q0 + tid] = t;
+    }
+  }
 }
 
-// Tile (tp, tq) of dX's product by its place in the order of the steps: as
-// head_tile_at's, without the XCDs.
-__device__ __forceinline__ void dx_tile(int i, int tp, int tq, int& p, int& q) {
-  const int group = i / (4 * tp), first = 4 * group, n = min(4, tq - first);
-  const int in = i - group * 4 * tp;
-  q = first + in % n;
-  p = in / n;
+// The loads of a tile of logits.
+template <int TILE>
+struct LogitsTile {
+  using C = HeadCfg<TILE>;
+  using LP = HeadLoader<C::BP, HK_N, C::NT>;
+  using LQ = HeadLoader<C::BQ, HK_N, C::NT>;
+  LP lp;
+  LQ lq;
+  __device__ __forceinline__ void set(const HeadLogits& a, int64_t p0, int q0, int cnt,
+                                      const int32_t* idx, int tid) {
+    using OP = typename LP::O;
+    using OQ = typename LQ::O;
+    lp.base = reinterpret_cast<const char*>(a.w + p0 * a.dim);
+    lp.bytes = (uint32_t)(min<int64_t>(C::BP, a.vocab - p0) * a.dim * 2);
+    lp.step_bytes = lq.step_bytes = HD_BK * 2;
+    lp.start(0, a.dim);
+    lq.start(0, a.dim);
+#pragma unroll
+    for (int i = 0; i < OP::CH; ++i)
+      lp.vo[i] = (uint32_t)(OP::row_n(tid, i) * a.dim + OP::red_n(tid)) * 2;
+    lq.base = reinterpret_cast<const char*>(a.x);
+    lq.bytes = (uint32_t)((int64_t)a.rows * a.dim * 2);
+#pragma unroll
+    for (int i = 0; i < OQ::CH; ++i) {
+      const int m = q0 + OQ::row_n(tid, i);
+      lq.vo[i] = m < cnt ? (uint32_t)((int64_t)idx[m] * a.dim + OQ::red_n(tid)) * 2 : G_OOB;
+    }
+  }
+};
+
+// A tile to a workgroup (HT_128, HT_SMALL).  FEW: every workgroup lists the
+// counted rows itself, and the first leaves the list in memory.
+template <int TILE, bool BWD, bool FEW>
+__global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_logits(HeadLogits a, HeadRows rows) {
+  using C = HeadCfg<TILE>;
+  HEAD_LDS(C, C::RFAR, C::RNEAR);
+  __shared__ int32_t s_idx[FEW ? HEAD_FEW : 1], s_lab[FEW ? HEAD_FEW : 1], s_cnt;
+  __shared__ float s_lseo[FEW ? HEAD_FEW : 1], s_scale[FEW ? HEAD_FEW : 1];
+  const int32_t *idx = a.idx, *labs = a.lab;
+  const float* lseos = a.lseo;
+  int cnt;
+  if constexpr (FEW) {
+    if (wave == 0) {
+      const bool first = blockIdx.x == 0;
+      int64_t lab = lane < rows.rows ? rows.labels[lane] : -1;
+      if (lab >= rows.vocab) {
+        if (first && rows.status) *rows.status = QN_EINVAL;
+        lab = -1;
+      }
+      const uint64_t on = __ballot(lab >= 0);
+      const int n = __popcll(on), m = __popcll(on & ((uint64_t(1) << lane) - 1));
+      if (lab >= 0) {
+        s_idx[m] = lane;
+        s_lab[m] = (int32_t)lab;
+        if (first) rows.idx[m] = lane;
+        if constexpr (BWD) {
+          float lseo, scale;
+          head_row_bwd(rows, lane, 1.0f / (float)n, lseo, scale);
+          s_lseo[m] = lseo;
+          s_scale[m] = scale;
+          if (first) rows.scale[m] = scale;
+        }
+      } else if (!BWD && first && lane < rows.rows) {
+        rows.loss[lane] = 0.0f;
+        rows.lse[lane] = 0.0f;
+        if (rows.lse_lo) rows.lse_lo[lane] = 0.0f;
+      }
+      if (lane == 0) {
+        s_cnt = n;
+        if (first) {
+          rows.cnt[0] = n;
+          rows.cnt[1] = 0;
+        }
+      }
+    }
+    __syncthreads();
+    idx = s_idx;
+    labs = s_lab;
+    lseos = s_lseo;
+    cnt = __builtin_amdgcn_readfirstlane(s_cnt);
+    if constexpr (BWD)
+      for (int t = blockIdx.x; t < rows.rows; t += gridDim.x)
+        head_fill_row(rows, t, cnt, s_idx, s_scale, tid, C::NT);
+  } else {
+    cnt = *a.cnt;
+  }
+  int tp, tq;
+  if (!head_tile_at(blockIdx.x, (int)((a.v1 - a.v0 + C::BP - 1) / C::BP), (cnt + C::BQ - 1) / C::BQ,
+                    tp, tq))
+    return;
+  const int64_t p0 = a.v0 + (int64_t)tp * C::BP;      // first word
+  const int q0 = tq * C::BQ;                          // first counted row
+  LogitsTile<TILE> t;
+  t.set(a, p0, q0, cnt, idx, tid);
+  f32x16 acc[C::TP][C::TQ];
+  zero_acc<TILE>(acc);
+  head_mainloop<TILE, RINGP, RINGQ, false>(t.lp, t.lq, lds, (a.dim + HD_BK - 1) / HD_BK, wave, tid,
+                                           lane, acc);
+  if constexpr (!BWD) head_barrier();                 // the stages have been read
+  logits_finish<TILE, BWD>(a, acc, p0, q0, cnt, labs, lseos, reinterpret_cast<float2*>(lds), wp, wq,
+                           lane);
+}
+
+// Workgroups that run at once take tiles HT_256 round after round, each round's
+// on one XCD next to one another; the next tile's first stages are on their way
+// while a tile's logits are reduced.  Where the last round has tiles for at most
+// half of the workgroups, they are halved.
+template <bool BWD>
+__global__ __launch_bounds__(512) void k_head_logits_large(HeadLogits a) {
+  using C = HeadCfg<HT_256>;
+  HEAD_LDS(C, C::RFAR, C::RNEAR);
+  const int cnt = *a.cnt;
+  const int tiles_p = (int)((a.v1 - a.v0 + C::BP - 1) / C::BP), tiles_q = (cnt + C::BQ - 1) / C::BQ;
+  const int tiles = tiles_p * tiles_q, wgs = gridDim.x;
+  const int whole = tiles / wgs, rest = tiles % wgs;
+  const int xcd = blockIdx.x & 7, in = blockIdx.x >> 3, per = wgs >> 3;
+  const bool halve = 2 * rest <= wgs;
+  const int units = halve ? 2 * rest : rest;
+  const int u0 = units * xcd / 8, u1 = units * (xcd + 1) / 8;
+  const int unit = in < u1 - u0 ? u0 + in : -1;       // of the last round
+  const int rounds = whole + (unit >= 0 && !halve);
+  const int steps = (a.dim + HD_BK - 1) / HD_BK;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void*)lds;
+  using T = LogitsTile<HT_256>;
+  using S = HeadStages<HT_256, RINGP, RINGQ, T::LP, T::LQ>;
+  T t;
+  int64_t p0 = 0;
+  int q0 = 0;
+  auto place = [&](int r) {
+    int tp, tq;
+    dx_tile(__builtin_amdgcn_readfirstlane(r < whole ? r * wgs + xcd * per + in : whole * wgs + unit),
+            tiles_p, tiles_q, tp, tq);
+    p0 = a.v0 + (int64_t)tp * C::BP;
+    q0 = tq * C::BQ;
+  };
+  if (rounds > 0) {
+    place(0);
+    t.set(a, p0, q0, cnt, a.idx, tid);
+    S::fill(t.lp, t.lq, lds0, wave, tid);
+  }
+  for (int r = 0; r < rounds; ++r) {
+    f32x16 acc[C::TP][C::TQ];
+    zero_acc<HT_256>(acc);
+    head_mainloop<HT_256, RINGP, RINGQ, true>(t.lp, t.lq, lds, steps, wave, tid, lane, acc);
+    const int64_t p = p0;
+    const int q = q0;
+    head_barrier();                                   // the stages have been read
+    if (r + 1 < rounds) {
+      place(r + 1);
+      t.set(a, p0, q0, cnt, a.idx, tid);
+      S::fill(t.lp, t.lq, lds0, wave, tid);
+    }
+    logits_finish<HT_256, BWD>(a, acc, p, q, cnt, a.lab, a.lseo, nullptr, wp, wq, lane);
+  }
+  if (!halve || unit < 0) return;
+  using H = HeadCfg<HT_HALF>;
+  int tp, tq;
+  dx_tile(__builtin_amdgcn_readfirstlane(whole * wgs + unit / 2), tiles_p, tiles_q, tp, tq);
+  p0 = a.v0 + (int64_t)tp * C::BP;
+  q0 = tq * C::BQ + (unit & 1) * H::BQ;
+  if (q0 >= cnt) return;
+  LogitsTile<HT_HALF> th;
+  th.set(a, p0, q0, cnt, a.idx, tid);
+  f32x16 acc[H::TP][H::TQ];
+  zero_acc<HT_HALF>(acc);
+  head_mainloop<HT_HALF, H::RFAR, H::RNEAR, false>(th.lp, th.lq, lds, steps, wave, tid, lane, acc);
+  logits_finish<HT_HALF, BWD>(a, acc, p0, q0, cnt, a.lab, a.lseo, nullptr, wave / H::WQ, wave % H::WQ,
+                              lane);
 }
 
 // One 32 x 32 tile of sums where it belongs: dX, or the sums of the pieces so
@@ -584,7 +790,7 @@ __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_dx(HeadDx a) {
     f32x16 acc[C::TP][C::TQ];
     zero_acc<TILE>(acc);
     if (seg > 0) __syncthreads();      // the last segment's stages have been read
-    head_mainloop<TILE, RINGP, RINGQ>(lp, lq, lds, s1 - s0, wave, tid, lane, acc);
+    head_mainloop<TILE, RINGP, RINGQ, false>(lp, lq, lds, s1 - s0, wave, tid, lane, acc);
     if (slot < 0) {
 #pragma unroll
       for (int j = 0; j < C::TQ; ++j)
@@ -684,7 +890,7 @@ __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_dw(HeadDw a) {
   }
   f32x16 acc[C::TP][C::TQ];
   zero_acc<TILE>(acc);
-  head_mainloop<TILE, RINGP, RINGQ>(lp, lq, lds, (cnt + HD_BK - 1) / HD_BK, wave, tid, lane, acc);
+  head_mainloop<TILE, RINGP, RINGQ, false>(lp, lq, lds, (cnt + HD_BK - 1) / HD_BK, wave, tid, lane, acc);
 #pragma unroll
   for (int j = 0; j < C::TQ; ++j) {
     const int v = q0 + wq * C::WTQ + 32 * j + (lane & 31);
@@ -709,21 +915,32 @@ __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_dw(HeadDw a) {
 
 namespace qn {
 
-template <int TILE>
-static void logits_t(hipStream_t st, bool bwd, const HeadLogits& a) {
+template <int TILE, bool FEW>
+static void logits_t(hipStream_t st, bool bwd, const HeadLogits& a, const HeadRows& rows) {
   using C = HeadCfg<TILE>;
   const dim3 grid((unsigned)(cdiv(a.v1 - a.v0, C::BP) * cdiv(a.rows, C::BQ))), wg(C::NT);
   if (bwd)
-    QN_LAUNCH("k_head_logits", (k_head_logits<TILE, true>), grid, wg, st, a);
+    QN_LAUNCH("k_head_logits", (k_head_logits<TILE, true, FEW>), grid, wg, st, a, rows);
   else
-    QN_LAUNCH("k_head_logits", (k_head_logits<TILE, false>), grid, wg, st, a);
+    QN_LAUNCH("k_head_logits", (k_head_logits<TILE, false, FEW>), grid, wg, st, a, rows);
 }
 
-void launch_head_logits(hipStream_t st, int tile, bool bwd, const HeadLogits& a) {
-  switch (tile) {
-    case HT_256: logits_t<HT_256>(st, bwd, a); break;
-    case HT_128: logits_t<HT_128>(st, bwd, a); break;
-    default: logits_t<HT_SMALL>(st, bwd, a); break;
+void launch_head_logits(hipStream_t st, int tile, bool bwd, bool few, const HeadLogits& a,
+                        const HeadRows& rows) {
+  if (tile == HT_SMALL) {
+    if (few)
+      logits_t<HT_SMALL, true>(st, bwd, a, rows);
+    else
+      logits_t<HT_SMALL, false>(st, bwd, a, rows);
+  } else if (tile == HT_128) {
+    logits_t<HT_128, false>(st, bwd, a, rows);
+  } else {
+    const int64_t tiles = cdiv(a.v1 - a.v0, 256) * cdiv(a.rows, 256);
+    const dim3 grid((unsigned)std::min<int64_t>(G_CUS, cdiv(tiles, 8) * 8)), wg(512);
+    if (bwd)
+      QN_LAUNCH("k_head_logits", (k_head_logits_large<true>), grid, wg, st, a);
+    else
+      QN_LAUNCH("k_head_logits", (k_head_logits_large<false>), grid, wg, st, a);
   }
 }
 

@@ -33,7 +33,7 @@ HeadFwdPlan head_fwd_plan(int64_t rows, int64_t dim, int64_t vocab) {
   (void)dim;
   P.tile = pick_tile(vocab, rows);
   P.mp = cdiv(std::max<int64_t>(rows, 1), 256) * 256;
-  P.slices = cdiv(vocab, head_bp(P.tile)) * (head_bp(P.tile) / head_wave_p(P.tile));
+  P.slices = cdiv(vocab, head_bp(P.tile)) * (head_bp(P.tile) / HEAD_SLICE);
   size_t at = 0;
   P.cnt = take(&at, 256);
   P.idx = take(&at, size_t(P.mp) * 4);

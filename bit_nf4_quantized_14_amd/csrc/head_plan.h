@@ -16,11 +16,14 @@ constexpr int64_t HEAD_MAX_DIM = int64_t(1) << 20;
 
 // Output tiles: P positions (vocabulary, or columns of dX and dW) by Q
 // positions (tokens, or words of dW).
-enum HeadTile { HT_256 = 0, HT_128 = 1, HT_SMALL = 2 };
-constexpr int head_bp(int t) { return t == HT_256 ? 256 : 128; }
-constexpr int head_bq(int t) { return t == HT_256 ? 256 : (t == HT_128 ? 128 : 32); }
-// rows of D that one statistics entry covers: a wave's part of a tile
-constexpr int head_wave_p(int t) { return t == HT_256 ? 128 : (t == HT_128 ? 64 : 32); }
+// HT_HALF: of a tile HT_256 half its tokens.
+enum HeadTile { HT_256 = 0, HT_128 = 1, HT_SMALL = 2, HT_HALF = 3 };
+constexpr int head_bp(int t) { return t == HT_256 || t == HT_HALF ? 256 : 128; }
+constexpr int head_bq(int t) {
+  return t == HT_256 ? 256 : (t == HT_SMALL ? 32 : 128);
+}
+// words of a row that one statistics entry covers
+constexpr int64_t HEAD_SLICE = 128;
 
 #if defined(__HIPCC__)
 #define HEAD_HD __host__ __device__ inline

@@ -53,8 +53,8 @@ KERNEL_SOURCES = (("k_gemm", "gemm.hip"), ("k_fwd_gemm", "gemm.hip"),
                   ("k_act8", "act8.hip", "act8_code.h", "act8_host.h"),
                   ("k_adapter", "adapter8.hip", "act8_host.h", "act8_linear.hip",
                    "act8_plan.cpp", "act8_plan.h"), ("k_seq", "pref.hip"),
-                  ("k_head", "head.hip", "head.h", "head_gemm.hip", "head_plan.cpp",
-                   "head_plan.h"),
+                  ("k_head", "head.hip", "head.h", "head_rows.h", "head_gemm.hip",
+                   "head_plan.cpp", "head_plan.h"),
                   ("k_orth", "muon.hip", "muon_plan.cpp", "muon_plan.h"))
 
 COPY_BYTES = 256 << 20   # bench.py --calibrate-copy: one 256 MiB copy
