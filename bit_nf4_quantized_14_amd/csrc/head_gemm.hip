@@ -841,7 +841,7 @@ __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_dx_join(HeadDx a) {
   f32x4 sum[4];
 #pragma unroll
   for (int g = 0; g < 4; ++g) sum[g] = from[t * size + g * C::NT];
-#pragma unroll 4
+#pragma unroll 8
   for (int e = e0; e <= e1; ++e)
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
