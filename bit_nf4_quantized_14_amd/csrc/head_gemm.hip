@@ -723,12 +723,20 @@ __device__ __forceinline__ void dx_store(const HeadDx& a, float (&x)[16], int k0
   }
 }
 
+// Stages of dX's product.  With few tokens G comes from as far as the weight
+// does: two stages of it cost 64 tokens 83 us, five 59, where reading W takes 50.
+template <int TILE>
+struct DxRing {
+  static constexpr int P = TILE == HT_256 ? 3 : (TILE == HT_128 ? 5 : 4);
+  static constexpr int Q = TILE == HT_256 ? 2 : (TILE == HT_128 ? 5 : 4);
+};
+
 // A workgroup's tiles and parts of tiles (HeadDeal): whole tiles go where they
 // belong, parts to `part`.
 template <int TILE>
 __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_dx(HeadDx a) {
   using C = HeadCfg<TILE>;
-  HEAD_LDS(C, C::RFAR, C::RNEAR);
+  HEAD_LDS(C, DxRing<TILE>::P, DxRing<TILE>::Q);
   const int cnt = *a.cnt;
   const int tiles_p = (a.dim + C::BP - 1) / C::BP, tiles_q = (cnt + C::BQ - 1) / C::BQ;
   const HeadDeal d = head_deal(a.wgs, tiles_p * tiles_q, (int)((a.n + HD_BK - 1) / HD_BK));
@@ -739,7 +747,7 @@ __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_dx(HeadDx a) {
   const bool is_head = in < h1 - h0;
   const int e = xcd * per - h0 + in - (h1 - h0);    // extra workgroup, if not
   int64_t at = 0, end = 0;
-  if (d.extra > 0 && !is_head) {
+  if (d.extra > 0 && !is_head && e < d.extra) {
     at = head_tail_first(d, e);
     end = head_tail_first(d, e + 1);
   }
@@ -784,7 +792,8 @@ __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_dx(HeadDx a) {
     lq.step_bytes = 256 * HD_BK * 2;
 #pragma unroll
     for (int i = 0; i < OQ::CH; ++i)
-      lq.vo[i] = (uint32_t)(OQ::row_n(tid, i) * HD_BK + OQ::red_n(tid)) * 2;
+      lq.vo[i] = q0 + OQ::row_n(tid, i) < cnt
+                     ? (uint32_t)(OQ::row_n(tid, i) * HD_BK + OQ::red_n(tid)) * 2 : G_OOB;
     lp.start(s0, (int)a.n);
     lq.start(s0, (int)a.vp);
     f32x16 acc[C::TP][C::TQ];
@@ -836,24 +845,32 @@ __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_dx_join(HeadDx a) {
   int tp, tq;
   dx_tile(d.tiles - d.rest + t, tiles_p, tiles_q, tp, tq);
   const int i = blockIdx.y / C::TQ, j = blockIdx.y % C::TQ;
+  const int m = tq * C::BQ + wq * C::WTQ + 32 * j;
+  if (m >= cnt) return;                             // no row of this wave's tile
   const int64_t size = C::BP * C::BQ / 4;           // of a part, in groups of four
   const f32x4* from = reinterpret_cast<const f32x4*>(a.part) + (i * C::TQ + j) * 4 * C::NT + tid;
   f32x4 sum[4];
 #pragma unroll
   for (int g = 0; g < 4; ++g) sum[g] = from[t * size + g * C::NT];
-#pragma unroll 8
-  for (int e = e0; e <= e1; ++e)
+  from += (d.rest + t) * size;
+  for (int e = e0; e <= e1; e += 8) {
+    f32x4 v[8][4];
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const f32x4 v = from[(d.rest + t + e) * size + g * C::NT];
+    for (int k = 0; k < 8; ++k)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) sum[g][x] += v[x];
-    }
+      for (int g = 0; g < 4; ++g)
+        v[k][g] = e + k <= e1 ? from[(e + k) * size + g * C::NT] : f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) sum[g][x] += v[k][g][x];
+  }
   float x[16];
 #pragma unroll
   for (int v = 0; v < 16; ++v) x[v] = sum[v >> 2][v & 3];
-  dx_store(a, x, tp * C::BP + wp * C::WTP + 32 * i, tq * C::BQ + wq * C::WTQ + 32 * j + (lane & 31),
-           cnt, lane);
+  dx_store(a, x, tp * C::BP + wp * C::WTP + 32 * i, m + (lane & 31), cnt, lane);
 }
 
 template <int TILE>

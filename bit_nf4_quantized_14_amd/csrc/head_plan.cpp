@@ -65,9 +65,11 @@ HeadBwdPlan head_bwd_plan(int64_t rows, int64_t dim, int64_t vocab, bool need_dx
   P.tile = pick_tile(std::min(P.vp, vocab), rows);
   P.tile_dw = pick_tile(dim, std::min(P.vp, vocab));
   // The steps of dX's product are dealt evenly however few tiles there are, so
-  // its tiles are the largest that the rows fill.
-  P.tile_dx = rows <= 32 ? HT_SMALL : (rows <= 128 ? HT_128 : HT_256);
-  P.dx_wgs = P.tile_dx == HT_256 ? G_CUS : 2 * G_CUS;
+  // its tiles are the largest that the rows fill, unless a workgroup's share of
+  // such tiles were less than 24 steps.
+  const int64_t share = cdiv(dim, 256) * cdiv(rows, 256) * cdiv(std::min(P.vp, vocab), 64) / G_CUS;
+  P.tile_dx = rows <= 32 ? HT_SMALL : (rows <= 128 || share < 24 ? HT_128 : HT_256);
+  P.dx_wgs = P.tile_dx == HT_SMALL ? 2 * G_CUS : G_CUS;
   size_t at = 0;
   P.cnt = take(&at, 256);
   P.idx = take(&at, size_t(P.mp) * 4);

@@ -51,8 +51,9 @@ HEAD_HD HeadDeal head_deal(int wgs, int tiles, int steps) {
   const int head = each > 8 ? each : 8;    // fewer cost more to join than they save
   if (head >= steps) return d;
   d.head = head;
-  d.extra = wgs - d.rest;
   d.tails = (int64_t)d.rest * (steps - head);
+  const int64_t runs = (d.tails + head - 1) / head;
+  d.extra = runs < wgs - d.rest ? (int)runs : wgs - d.rest;
   return d;
 }
 // The first of the tails' steps that extra workgroup e takes (e = extra: the
