@@ -87,7 +87,7 @@ __global__ __launch_bounds__(HR_THREADS) void k_head_rows(HeadRows a) {
   }
 }
 
-constexpr int HF_ROWS = 64, HF_THREADS = 1024, HF_WAVES = HF_THREADS / 64;
+constexpr int HF_ROWS = 64, HF_THREADS = 1024, HF_WAVES = HF_THREADS / 64, HF_AHEAD = 16;
 
 struct HeadFinish {
   const int32_t* idx;
@@ -111,23 +111,26 @@ __global__ __launch_bounds__(HF_THREADS) void k_head_finish(HeadFinish a) {
   const int cnt = a.cnt[0], blocks = max(1, (cnt + HF_ROWS - 1) / HF_ROWS);
   if ((int)blockIdx.x >= blocks) return;
   const int m = blockIdx.x * HF_ROWS + lane;
-  // logarithms to base 2
-  float mx = -__builtin_inff(), sum = 0.0f;
+  // logarithms to base 2; as many entries in flight as 32000 words have
+  float mx = -__builtin_inff(), sum = 0.0f, hit = 0.0f;
+  int t = 0;
   if (m < cnt) {
-    for (int s0 = wave; s0 < a.slices; s0 += 8 * HF_WAVES) {
-      float2 p[8];
+    hit = a.hit[m];
+    t = a.idx[m];
+    for (int s0 = wave; s0 < a.slices; s0 += HF_AHEAD * HF_WAVES) {
+      float2 p[HF_AHEAD];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < HF_AHEAD; ++i) {
         const int s = s0 + i * HF_WAVES;
         p[i] = s < a.slices ? a.part[(int64_t)s * a.mp + m] : make_float2(-__builtin_inff(), 0.0f);
       }
       float top = mx;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) top = fmaxf(top, p[i].x);
+      for (int i = 0; i < HF_AHEAD; ++i) top = fmaxf(top, p[i].x);
       const float at = top == -__builtin_inff() ? 0.0f : top;
       sum *= __builtin_amdgcn_exp2f(mx - at);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum += p[i].y * __builtin_amdgcn_exp2f(p[i].x - at);
+      for (int i = 0; i < HF_AHEAD; ++i) sum += p[i].y * __builtin_amdgcn_exp2f(p[i].x - at);
       mx = top;
     }
   }
@@ -144,14 +147,13 @@ __global__ __launch_bounds__(HF_THREADS) void k_head_finish(HeadFinish a) {
     for (int w = 0; w < HF_WAVES; ++w)
       all += (double)(s_part[w][lane].y * __builtin_amdgcn_exp2f(s_part[w][lane].x - from));
     const double at = (double)from / HEAD_LOG2E;
-    const double other = at + log(all), hit = (double)a.hit[m];
+    const double other = at + log(all);
     // log(1 + exp(d)) and max + log(1 + exp(-|d|)); two equal infinities
     // have no difference, and the loss then none either
-    const double d = other - hit;
+    const double d = other - (double)hit;
     const double tail = log1p(exp(-fabs(d)));
     loss = d > 0.0 ? d + tail : tail;
-    const double lse = d > 0.0 ? other + tail : hit + tail;
-    const int t = a.idx[m];
+    const double lse = d > 0.0 ? other + tail : (double)hit + tail;
     const float hi = (float)lse;
     a.loss[t] = (float)loss;
     a.lse[t] = hi;
@@ -161,7 +163,11 @@ __global__ __launch_bounds__(HF_THREADS) void k_head_finish(HeadFinish a) {
   if (wave == 0) {
 #pragma unroll
     for (int d = 32; d > 0; d /= 2) loss += __shfl_xor(loss, d);
-    if (lane == 0) {
+    if (lane == 0 && blocks == 1) {
+      a.mean[0] = cnt > 0 ? (float)(loss / cnt) : 0.0f;
+      a.mean[1] = (float)cnt;
+      s_last = 0;
+    } else if (lane == 0) {
       __hip_atomic_store(a.sums + blockIdx.x, loss, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       s_last = __hip_atomic_fetch_add(a.cnt + 1, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
                blocks - 1;
