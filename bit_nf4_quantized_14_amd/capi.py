@@ -1333,6 +1333,9 @@ class MuonBatch:
         if self.ws_bytes == 0:
             raise _bad(fn, "a parameter's size is out of range")
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=jobs[0][0].device)
+        # what is allocated here belongs to the stream that is current now
+        self.own = [self.ws] + [m for (_, _, m0), m in zip(jobs, self.momenta) if m0 is None]
+        self.stream = _raw_stream(self.index)
 
 
 def qn_muon_workspace_bytes(batch: MuonBatch) -> int:
@@ -1347,6 +1350,10 @@ def qn_muon_step(batch: MuonBatch, lr=0.02, momentum=0.95, nesterov=True, weight
                  int(bool(nesterov)), _orth_hp(steps, coef, eps))
 
     def body(st):
+        if st != batch.stream:       # freed only when that stream is done with them
+            import torch
+            for t in batch.own:
+                t.record_stream(torch.cuda.current_stream(batch.index))
         _check("qn_muon_step", lib().qn_muon_step(batch.arr, batch.count, hp, batch.ws.data_ptr(),
                                                   batch.ws_bytes, st))
     _run_on(batch.index, stream, body)

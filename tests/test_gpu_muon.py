@@ -175,3 +175,88 @@ def test_muon_zero_gradient_only_decays():
     batch = capi.MuonBatch([(p.to(DEV), z.to(DEV), None)])
     check_muon(jobs, batch, lr=0.5, weight_decay=0.5)
     assert (batch.momenta[0] == 0).all()
+
+
+def test_muon_views_of_any_alignment_and_guard_bands():
+    # every layout's slow path: odd starts, odd lengths, ranks that fit no group
+    shapes = [(5, 301), (301, 5), (16, 257), (259, 16), (64, 130), (131, 64)]
+    for start in (1, 2, 3):
+        jobs = muon_case(shapes, 40 + start)
+        total = sum(r * c for r, c in shapes) + 64
+        bufs = [torch.full((total,), 7.0, dtype=t, device=DEV)
+                for t in (torch.bfloat16, torch.float32, torch.float32)]
+        at, dev = start, []
+        for j in jobs:
+            n = j[0].numel()
+            views = tuple(b[at:at + n].view(j[0].shape) for b in bufs)
+            for v, t in zip(views, j):
+                v.copy_(t)
+            dev.append(views)
+            at += n + 3
+        batch = capi.MuonBatch(dev)
+        check_muon(jobs, batch, weight_decay=0.1)
+        mask = torch.ones(total, dtype=torch.bool, device=DEV)
+        at = start
+        for j in jobs:
+            mask[at:at + j[0].numel()] = False
+            at += j[0].numel() + 3
+        for b in bufs:
+            assert (b[mask] == 7).all()
+
+
+def test_workspace_is_not_passed():
+    xs = [matrix(r, c, 3).to(DEV) for r, c in ((64, 500), (128, 300), (16, 900), (30, 31))]
+    arr = (capi._OrthJob * 4)(*(capi._OrthJob(x.data_ptr(), 0, x.data_ptr(), 0, *x.shape) for x in xs))
+    n = capi.lib().qn_orth_workspace_bytes(arr, 4)
+    raw = torch.full((n + 8192,), 0x5A, dtype=torch.uint8, device=DEV)
+    ys = capi.qn_orthogonalize(xs, ws=raw[:n])
+    torch.cuda.synchronize()
+    assert (raw[n:] == 0x5A).all()
+    for x, y in zip(xs, ys):
+        check_orth(x.cpu(), y)
+
+
+def test_graph_of_steps_matches_eager_steps():
+    from test_gpu_graphs import _capture, _eager_noise
+    shapes = [(16, 512), (700, 16), (24, 100), (64, 300), (96, 200), (256, 256)]
+    jobs = muon_case(shapes, 5)
+    eager = capi.MuonBatch([tuple(t.to(DEV) for t in j) for j in jobs])
+    graph = capi.MuonBatch([tuple(t.to(DEV) for t in j) for j in jobs])
+    capi.qn_muon_step(eager)
+    capi.qn_muon_step(graph)
+    g = _capture(lambda: capi.qn_muon_step(graph))
+    for rep in range(4):
+        g.replay()
+        capi.qn_muon_step(eager)
+        torch.cuda.synchronize()
+        for i in range(len(shapes)):
+            assert torch.equal(eager.keep[2 * i], graph.keep[2 * i]), (rep, i)
+            assert torch.equal(eager.momenta[i], graph.momenta[i]), (rep, i)
+        _eager_noise()
+
+
+def test_steps_on_another_stream():
+    jobs = muon_case([(16, 512), (700, 48)], 6)
+    a = capi.MuonBatch([tuple(t.to(DEV) for t in j) for j in jobs])
+    b = capi.MuonBatch([tuple(t.to(DEV) for t in j) for j in jobs])
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        capi.qn_muon_step(a)
+        capi.qn_muon_step(b, stream=s)
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(a.keep[2 * i], b.keep[2 * i])
+        assert torch.equal(a.momenta[i], b.momenta[i])
+
+
+def test_not_finite_gradient_keeps_to_its_matrix():
+    jobs = muon_case([(16, 200), (200, 16), (64, 100)], 8)
+    clean = capi.MuonBatch([tuple(t.to(DEV) for t in j) for j in jobs])
+    bad = capi.MuonBatch([tuple(t.to(DEV) for t in j) for j in jobs])
+    bad.keep[2 * 1 + 1][5, 5] = float("nan")
+    capi.qn_muon_step(clean)
+    capi.qn_muon_step(bad)
+    assert torch.isnan(bad.keep[2]).all()
+    for i in (0, 2):
+        assert torch.equal(clean.keep[2 * i], bad.keep[2 * i])

@@ -1,0 +1,151 @@
+"""Argument checks of the head's loss and of the orthogonalised updates, before
+any launch (no GPU): the C entry points' codes and the binding's errors."""
+
+import ctypes
+import os
+
+import pytest
+import torch
+
+from bit_nf4_quantized_14_amd import capi
+
+pytestmark = pytest.mark.skipif(not os.path.exists(capi.LIB_PATH),
+                                reason="libqlora_nf4.so not built")
+
+P = 0x10000
+BIG = 1 << 40
+EINVAL, EWORKSPACE = capi.QN_EINVAL, capi.QN_EWORKSPACE
+
+
+def _head(x=P, w=P, labels=P, rows=64, dim=128, vocab=1000):
+    return ctypes.byref(capi._Head(x, w, labels, rows, dim, vocab))
+
+
+BAD_SIZES = (dict(rows=-1), dict(rows=1 << 24), dict(dim=0), dict(dim=4), dict(dim=132),
+             dict(dim=(1 << 20) + 8), dict(vocab=0), dict(vocab=(1 << 28) + 1),
+             dict(rows=(1 << 23), dim=136))
+BAD_HEADS = (*BAD_SIZES, dict(x=None), dict(x=P + 8), dict(w=None), dict(w=P + 8),
+             dict(labels=None), dict(labels=P + 4))
+
+
+def test_head_refusals():
+    L = capi.lib()
+
+    def fwd(h=None, loss=P, lse=P, lo=None, mean=P, st=None, ws=P, n=BIG):
+        return L.qn_head_loss_fwd(None if h == 0 else (h or _head()), loss, lse, lo, mean, st, ws, n,
+                                  None)
+
+    def bwd(h=None, loss=P, lse=P, lo=None, dl=None, dx=P, dw=P, ws=P, n=BIG):
+        return L.qn_head_loss_bwd(None if h == 0 else (h or _head()), loss, lse, lo, dl, dx, dw, ws,
+                                  n, None)
+    for fn in (fwd, bwd):
+        assert fn(0) == EINVAL
+        for bad in BAD_HEADS:
+            assert fn(_head(**bad)) == EINVAL, bad
+        for bad in (dict(loss=None), dict(lse=None), dict(loss=P + 2), dict(lse=P + 2),
+                    dict(lo=P + 2)):
+            assert fn(**bad) == EINVAL, bad
+        assert fn(ws=None) == EWORKSPACE and fn(ws=P + 8) == EWORKSPACE
+    assert fwd(mean=P + 2) == EINVAL and fwd(st=P + 2) == EINVAL
+    for bad in (dict(dl=P + 2), dict(dx=P + 8), dict(dw=P + 8), dict(dx=None, dw=None)):
+        assert bwd(**bad) == EINVAL, bad
+    assert fwd(n=capi.qn_head_fwd_workspace_bytes(64, 128, 1000) - 1) == EWORKSPACE
+    for dx, dw in ((P, None), (None, P), (P, P)):
+        need = capi.qn_head_bwd_workspace_bytes(64, 128, 1000, dx is not None, dw is not None)
+        assert need > 0 and bwd(dx=dx, dw=dw, n=need - 1) == EWORKSPACE
+    # no rows and no gradient of the weight: nothing to do, nothing needed but the weight
+    assert bwd(_head(x=None, labels=None, rows=0), loss=None, lse=None, dx=None, dw=None) == 0
+    assert bwd(_head(x=None, labels=None, rows=0, w=None), dx=None, dw=None) == EINVAL
+    for bad in BAD_SIZES:
+        s = dict(rows=64, dim=128, vocab=1000) | bad
+        assert capi.qn_head_fwd_workspace_bytes(**s) == 0
+        assert capi.qn_head_bwd_workspace_bytes(**s, need_dw=True) == 0
+
+
+def test_head_workspaces_stay_bounded():
+    # G is kept for a piece of the vocabulary: 256 MB, or 8192 words
+    for rows, dim, vocab in ((4096, 4096, 128256), (65536, 4096, 128256), (1, 8192, 262144)):
+        mp = -(-rows // 256) * 256
+        g = max(2 * mp * 8192, 256 << 20)
+        rest = mp * dim * 4 + 2 * 256 * 256 * 256 * 4 + 64 * mp + 4096
+        assert capi.qn_head_bwd_workspace_bytes(rows, dim, vocab) <= g + rest
+        assert capi.qn_head_fwd_workspace_bytes(rows, dim, vocab) <= mp * (vocab // 16 + 64) + 8192
+
+
+def _orth_hp(coef=(1.0, 1.0, 1.0), eps=1e-7, steps=5):
+    return capi._OrthHP((ctypes.c_double * 3)(*coef), eps, steps)
+
+
+NAN, INF = float("nan"), float("inf")
+BAD_HP = (dict(steps=0), dict(steps=17), dict(eps=0.0), dict(eps=-1.0), dict(eps=NAN),
+          dict(eps=INF), dict(coef=(NAN, 1.0, 1.0)), dict(coef=(1.0, INF, 1.0)),
+          dict(coef=(1.0, 1.0, NAN)))
+BAD_SHAPES = ((0, 16), (16, 0), (-1, 16), (257, 257), (1000, 257), (16, 1 << 27), (1, 1 << 31))
+
+
+def test_orthogonalize_refusals():
+    L = capi.lib()
+
+    def call(job=(P, 0, P, 1, 16, 64), count=1, hp=None, ws=P, n=BIG):
+        arr = None if job is None else (capi._OrthJob * 1)(capi._OrthJob(*job))
+        return L.qn_orthogonalize(arr, count, hp if hp is not None else ctypes.byref(_orth_hp()), ws,
+                                  n, None)
+    assert call(None) == EINVAL
+    for c in (0, -1, 65537):
+        assert call(count=c) == EINVAL
+    for bad in ((None, 0, P, 0, 16, 64), (P, 0, None, 0, 16, 64), (P + 2, 0, P, 0, 16, 64),
+                (P, 0, P + 2, 0, 16, 64), (P + 1, 1, P, 0, 16, 64), (P, 2, P, 0, 16, 64),
+                (P, 0, P, 7, 16, 64), (P, 0, P, 1, 16, 64)[:2] + (P, 1, 16, 64),
+                *((P, 0, P + 64, 0, *s) for s in BAD_SHAPES)):
+        assert call(bad) == EINVAL, bad                  # in place: the same type
+    for bad in BAD_HP:
+        assert call((P, 0, P, 0, 16, 64), hp=ctypes.byref(_orth_hp(**bad))) == EINVAL, bad
+    assert L.qn_orthogonalize((capi._OrthJob * 1)(capi._OrthJob(P, 0, P, 0, 16, 64)), 1, None, P, BIG,
+                              None) == EINVAL
+    arr = (capi._OrthJob * 1)(capi._OrthJob(P, 0, P, 0, 16, 64))
+    need = L.qn_orth_workspace_bytes(arr, 1)
+    ok = (P, 0, P, 0, 16, 64)
+    assert need > 0 and call(ok, n=need - 1) == EWORKSPACE
+    assert call(ok, ws=None) == EWORKSPACE and call(ok, ws=P + 8) == EWORKSPACE
+    for s in BAD_SHAPES:
+        assert L.qn_orth_workspace_bytes((capi._OrthJob * 1)(capi._OrthJob(P, 0, P, 0, *s)), 1) == 0
+
+
+def test_muon_refusals():
+    L = capi.lib()
+
+    def call(job=(P, P, P, 16, 64), count=1, ws=P, n=BIG, orth=None, **kw):
+        h = dict(lr=0.1, momentum=0.9, weight_decay=0.0, grad_scale=1.0) | kw
+        hp = capi._MuonHP(h["lr"], h["momentum"], h["weight_decay"], h["grad_scale"], 1,
+                          _orth_hp(**(orth or {})))
+        return L.qn_muon_step((capi._MuonJob * 1)(capi._MuonJob(*job)), count, ctypes.byref(hp), ws, n,
+                              None)
+    for bad in ((None, P, P, 16, 64), (P, None, P, 16, 64), (P, P, None, 16, 64),
+                (P + 1, P, P, 16, 64), (P, P + 2, P, 16, 64), (P, P, P + 2, 16, 64),
+                *((P, P, P, *s) for s in BAD_SHAPES)):
+        assert call(bad) == EINVAL, bad
+    for bad in (dict(lr=NAN), dict(lr=INF), dict(momentum=1.0), dict(momentum=-0.1),
+                dict(momentum=NAN), dict(weight_decay=INF), dict(grad_scale=NAN)):
+        assert call(**bad) == EINVAL, bad
+    for bad in BAD_HP:
+        assert call(orth=bad) == EINVAL, bad
+    assert call(count=0) == EINVAL
+    need = L.qn_muon_workspace_bytes((capi._MuonJob * 1)(capi._MuonJob(P, P, P, 16, 64)), 1)
+    assert need > 0 and call(n=need - 1) == EWORKSPACE and call(ws=P + 8) == EWORKSPACE
+    assert L.qn_muon_step(None, 1, ctypes.byref(capi._MuonHP()), P, BIG, None) == EINVAL
+    assert L.qn_muon_step((capi._MuonJob * 1)(capi._MuonJob(P, P, P, 16, 64)), 1, None, P, BIG,
+                          None) == EINVAL
+
+
+def test_binding_refuses_host_tensors_and_odd_arguments():
+    x, w, lab = torch.zeros(4, 64).bfloat16(), torch.zeros(9, 64).bfloat16(), torch.zeros(4).long()
+    f = capi.HeadLoss(torch.zeros(4), torch.zeros(4))
+    m = torch.zeros(4, 8)
+    for call in (lambda: capi.qn_head_loss_fwd(x, w, lab),
+                 lambda: capi.qn_head_loss_bwd(x, w, lab, f),
+                 lambda: capi.qn_orthogonalize(m), lambda: capi.qn_orthogonalize([]),
+                 lambda: capi.qn_orthogonalize([m], out=[m, m]),
+                 lambda: capi.MuonBatch([(m.bfloat16(), m, m)]), lambda: capi.MuonBatch([])):
+        with pytest.raises(capi.QNError) as e:
+            call()
+        assert e.value.code == EINVAL
