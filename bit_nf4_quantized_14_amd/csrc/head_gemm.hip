@@ -286,15 +286,19 @@ __device__ __forceinline__ void head_mainloop(LP& lp, LQ& lq, char* lds, int ste
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void*)lds;
   const typename OP::template Reader<TP> rp(wp * C::WTP, lane);
   const typename OQ::template Reader<TQ> rq(wq * C::WTQ, lane);
-  // Load n of a step: the near operand's first.
+  // Load n of a step goes out in its last slice, into the stages just read;
+  // where one operand has a stage more, its loads (the last FAR of a step) follow
+  // in the first three slices of the next step.  Spread like this they are in
+  // the way of fewer matrix instructions: 2048 rows x 8192 by 64128 words 1678 us
+  // with all of them in the last slice, 1582 so.
+  constexpr int FAR = RP > RQ ? OP::CH : (RQ > RP ? OQ::CH : 0), NEAR = LD - FAR;
   auto load = [&](int n, int sp, int sq) {
-    constexpr int FIRST = RP > RQ ? OQ::CH : OP::CH;
-    if (n < FIRST) {
-      if (RP > RQ) lq.slot(lds0 + sq, n, wave, tid);
-      else lp.slot(lds0 + sp, n, wave, tid);
+    if constexpr (RP > RQ) {
+      if (n < NEAR) lq.slot(lds0 + sq, n, wave, tid);
+      else lp.slot(lds0 + sp, n - NEAR, wave, tid);
     } else {
-      if (RP > RQ) lp.slot(lds0 + sp, n - FIRST, wave, tid);
-      else lq.slot(lds0 + sq, n - FIRST, wave, tid);
+      if (n < OP::CH) lp.slot(lds0 + sp, n, wave, tid);
+      else lq.slot(lds0 + sq, n - OP::CH, wave, tid);
     }
   };
   if constexpr (FILLED) {
@@ -313,6 +317,7 @@ __device__ __forceinline__ void head_mainloop(LP& lp, LQ& lq, char* lds, int ste
       b[kk & 1][n - TP] = rq.read(lds, sq, n - TP, kk);
   };
   int sp = 0, sq = RP * PB;        // this step's stages
+  int fp = 0, fq = 0;              // the step's before
 #pragma unroll
   for (int n = 0; n < FR; ++n) frag(n, sp, sq, 0);
   for (int st = 0; st < steps; ++st) {
@@ -320,22 +325,33 @@ __device__ __forceinline__ void head_mainloop(LP& lp, LQ& lq, char* lds, int ste
     const int nq = sq + QB == RP * PB + RQ * QB ? RP * PB : sq + QB;
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
-      if (kk < 3) {
-#pragma unroll
-        for (int n = 0; n < FR; ++n) frag(n, sp, sq, kk + 1);
-      } else {
+      // loads of this slice: [l0, l1)
+      int l0 = 0, l1 = 0;
+      if (kk == 3) {
         HEAD_WAIT_VM(S::OUT);
         head_barrier();
         __builtin_amdgcn_sched_barrier(0);
         lp.begin(tid);
         lq.begin(tid);
+        l1 = NEAR;
+      } else if (FAR > 0 && st > 0) {
+        l0 = NEAR + FAR * kk / 3;
+        l1 = NEAR + FAR * (kk + 1) / 3;
+      }
 #pragma unroll
-        for (int n = 0; n < (LD > FR ? LD : FR); ++n) {
-          if (n < FR) frag(n, np, nq, 0);
-          if (n < LD) load(n, sp, sq);
+      for (int n = 0; n < (LD > FR ? LD : FR); ++n) {
+        if (n < FR) {
+          if (kk < 3) frag(n, sp, sq, kk + 1);
+          else frag(n, np, nq, 0);
         }
-        lp.end();
-        lq.end();
+        if (l0 + n < l1) load(l0 + n, kk == 3 ? sp : fp, kk == 3 ? sq : fq);
+      }
+      if (kk == 3) {
+        if (RP <= RQ) lp.end();
+        if (RQ <= RP) lq.end();
+      } else if (kk == 2 && st > 0) {
+        if (RP > RQ) lp.end();
+        if (RQ > RP) lq.end();
       }
 #pragma unroll
       for (int g = 0; g < MPK; ++g) {
@@ -349,33 +365,33 @@ __device__ __forceinline__ void head_mainloop(LP& lp, LQ& lq, char* lds, int ste
       }
       __builtin_amdgcn_sched_barrier(0);
     }
+    fp = sp;
+    fq = sq;
     sp = np;
     sq = nq;
   }
   HEAD_WAIT_VM(0);   // nothing of this workgroup's is on its way into LDS
 }
 
-// Tile `i` of tq x tp tiles in groups of four tile columns walked along P, so
-// that any 32 consecutive indices cover about 4 x 8 tiles, and consecutive
-// runs of them go to one XCD (workgroups are dealt round the 8 XCDs).
+// Tiles in groups of four tile columns walked along P (of all, where they are
+// eight at most: the weight is then read once; 2.5% at 2048 rows x 8192), so
+// that any 32 consecutive indices cover about 4 x 8 tiles.
+__device__ __forceinline__ void head_tile(int i, int tp, int tq, int& p, int& q) {
+  const int g = tq <= 8 ? tq : 4;
+  const int group = i / (g * tp), first = g * group, n = min(g, tq - first);
+  const int in = i - group * g * tp;
+  q = first + in % n;
+  p = in / n;
+}
+
+// Consecutive runs of them go to one XCD (workgroups are dealt round the 8).
 __device__ __forceinline__ bool head_tile_at(int pid, int tp, int tq, int& p, int& q) {
   const int total = tp * tq;
   if (pid >= total) return false;
   const int x = pid & 7, each = total >> 3, rest = total & 7;
   const int i = x * each + min(x, rest) + (pid >> 3);
-  const int group = i / (4 * tp), first = 4 * group, n = min(4, tq - first);
-  const int in = i - group * 4 * tp;
-  q = first + in % n;
-  p = in / n;
+  head_tile(i, tp, tq, p, q);
   return true;
-}
-
-// The same order without the XCDs.
-__device__ __forceinline__ void dx_tile(int i, int tp, int tq, int& p, int& q) {
-  const int group = i / (4 * tp), first = 4 * group, n = min(4, tq - first);
-  const int in = i - group * 4 * tp;
-  q = first + in % n;
-  p = in / n;
 }
 
 template <int TILE>
@@ -651,7 +667,7 @@ __global__ __launch_bounds__(512) void k_head_logits_large(HeadLogits a) {
   int q0 = 0;
   auto place = [&](int r) {
     int tp, tq;
-    dx_tile(__builtin_amdgcn_readfirstlane(r < whole ? r * wgs + xcd * per + in : whole * wgs + unit),
+    head_tile(__builtin_amdgcn_readfirstlane(r < whole ? r * wgs + xcd * per + in : whole * wgs + unit),
             tiles_p, tiles_q, tp, tq);
     p0 = a.v0 + (int64_t)tp * C::BP;
     q0 = tq * C::BQ;
@@ -678,7 +694,7 @@ __global__ __launch_bounds__(512) void k_head_logits_large(HeadLogits a) {
   if (!halve || unit < 0) return;
   using H = HeadCfg<HT_HALF>;
   int tp, tq;
-  dx_tile(__builtin_amdgcn_readfirstlane(whole * wgs + unit / 2), tiles_p, tiles_q, tp, tq);
+  head_tile(__builtin_amdgcn_readfirstlane(whole * wgs + unit / 2), tiles_p, tiles_q, tp, tq);
   p0 = a.v0 + (int64_t)tp * C::BP;
   q0 = tq * C::BQ + (unit & 1) * H::BQ;
   if (q0 >= cnt) return;
@@ -773,7 +789,7 @@ __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_dx(HeadDx a) {
     s0 = __builtin_amdgcn_readfirstlane(s0);
     s1 = __builtin_amdgcn_readfirstlane(s1);
     int tp, tq;
-    dx_tile(tile, tiles_p, tiles_q, tp, tq);
+    head_tile(tile, tiles_p, tiles_q, tp, tq);
     const int k0 = tp * C::BP, q0 = tq * C::BQ;
     HeadLoader<C::BP, HK_T, C::NT> lp;
     HeadLoader<C::BQ, HK_N, C::NT> lq;
@@ -843,7 +859,7 @@ __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_dx_join(HeadDx a) {
   const int e0 = head_tail_owner(d, (int64_t)t * tail);
   const int e1 = head_tail_owner(d, (int64_t)(t + 1) * tail - 1);
   int tp, tq;
-  dx_tile(d.tiles - d.rest + t, tiles_p, tiles_q, tp, tq);
+  head_tile(d.tiles - d.rest + t, tiles_p, tiles_q, tp, tq);
   const int i = blockIdx.y / C::TQ, j = blockIdx.y % C::TQ;
   const int m = tq * C::BQ + wq * C::WTQ + 32 * j;
   if (m >= cnt) return;                             // no row of this wave's tile
