@@ -71,9 +71,13 @@ static int check_deal(int wgs, int tiles, int steps) {
            e <= head_tail_owner(d, (int64_t)(t + 1) * tail - 1); ++e)
         if (slots.count(d.rest + t + e) == 0) return fail("part", wgs, tiles, steps);
     }
-    // an even deal: nobody has more than its share and the smallest part
-    if (most > (int64_t)whole * steps + std::max<int64_t>(8, cdiv((int64_t)d.rest * steps, wgs)))
+    // nobody has more than its share, 10/8 of it where tails are kept in step, or the
+    // smallest part
+    const int64_t share = cdiv((int64_t)d.rest * steps, wgs);
+    if (most > (int64_t)whole * steps +
+                   std::max<int64_t>(2 * HEAD_PART, d.each > 0 ? share * 10 / 8 + 2 : share))
       return fail("share", wgs, tiles, steps);
+    if (d.extra > wgs - d.rest) return fail("extra", wgs, tiles, steps);
   }
   return 0;
 }
