@@ -8,8 +8,8 @@
 namespace qn {
 
 // The rows of a call, and the lists made of them: in a launch of their own, or
-// (up to HEAD_FEW rows) by each workgroup of the logits' kernel, the first of
-// which leaves them in memory.
+// (up to HEAD_FEW rows) by each workgroup of the logits' kernel for the first
+// piece of the vocabulary, the first of which leaves them in memory.
 constexpr int HEAD_FEW = 32;
 struct HeadRows {
   const int64_t* labels;

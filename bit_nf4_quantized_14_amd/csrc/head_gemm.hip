@@ -591,13 +591,19 @@ __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_logits(HeadLogits a,
       if (lab >= 0) {
         s_idx[m] = lane;
         s_lab[m] = (int32_t)lab;
-        if (first) rows.idx[m] = lane;
+        if (first) {
+          rows.idx[m] = lane;
+          rows.lab[m] = (int32_t)lab;
+        }
         if constexpr (BWD) {
           float lseo, scale;
           head_row_bwd(rows, lane, 1.0f / (float)n, lseo, scale);
           s_lseo[m] = lseo;
           s_scale[m] = scale;
-          if (first) rows.scale[m] = scale;
+          if (first) {
+            rows.lseo[m] = lseo;
+            rows.scale[m] = scale;
+          }
         }
       } else if (!BWD && first && lane < rows.rows) {
         rows.loss[lane] = 0.0f;

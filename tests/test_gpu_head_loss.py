@@ -258,6 +258,17 @@ def test_many_rows(rows, dim, vocab):
     assert bool((err <= bx * (1 + H) + H * dx.abs() + 1e-30).all()), float(err.max())
 
 
+@pytest.mark.parametrize("rows", [1, 5, 20])
+def test_few_rows_over_pieces_of_the_vocabulary(rows):
+    # more words than a piece has: labels in the first piece, in the second, at
+    # its edges and in the last word
+    dim, vocab = 8, 1040000
+    x, w, lab = make(rows, dim, vocab, rows, skip=0.2)
+    edge = torch.tensor([vocab - 1, 0, 520191, 520192, vocab - 2])[:rows]
+    lab[:len(edge)] = edge
+    check(x, w, lab, need_dw=True)
+
+
 def test_gradient_against_differences():
     # dx and dw along directions of single steps of the inputs' grid; the third
     # derivative of a row's loss along d is at most (2 |w d|_max)^3
