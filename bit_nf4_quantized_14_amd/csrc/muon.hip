@@ -304,7 +304,7 @@ __global__ __launch_bounds__(orth_threads(RT)) void k_orth_gram(OrthBatch b) {
   const int jx = job_of(b.gfirst, b.count, blockIdx.x);
   const OrthJob& J = b.job[jx];
   const int slice = blockIdx.x - b.gfirst[jx];
-  const int chunks = (J.L + C::LC - 1) / C::LC;
+  const int chunks = J.L / C::LC + (J.L % C::LC != 0);      // J.L + LC may pass 31 bits
   const int c0 = (int)((int64_t)chunks * slice / J.slices);
   const int c1 = (int)((int64_t)chunks * (slice + 1) / J.slices);
   f64x4 acc[NP];
@@ -890,7 +890,7 @@ OrthJob job_of_shape(const OrthShape& s, int32_t slices) {
 
 bool valid_hparams(const qn_orth_hparams* h) {
   return h != nullptr && h->steps >= 1 && h->steps <= QN_ORTH_MAX_STEPS && std::isfinite(h->eps) &&
-         h->eps > 0.0 && std::isfinite(h->coef[0]) && std::isfinite(h->coef[1]) &&
+         h->eps >= QN_ORTH_MIN_EPS && std::isfinite(h->coef[0]) && std::isfinite(h->coef[1]) &&
          std::isfinite(h->coef[2]);
 }
 

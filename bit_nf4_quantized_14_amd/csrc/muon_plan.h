@@ -7,6 +7,9 @@
 namespace qn {
 
 constexpr int ORTH_JOBS = 64;               // matrices of one launch
+// chunks of one launch that has several matrices: a workgroup each, and a grid's
+// threads are counted in 32 bits (one matrix has at most 2^23 chunks)
+constexpr int64_t ORTH_CHUNKS = int64_t(1) << 22;
 constexpr int64_t ORTH_MAX_NUMEL = int64_t(1) << 31;
 
 // Matrices whose short side takes rt tiles of 16 (1, 2, 4, 8 or 16), chunks of
@@ -60,10 +63,13 @@ void orth_for_groups(int count, int kinds, Shape shape, Kind kind, Body body) {
       for (int i = 0; i < count;) {
         OrthGroup g{};
         OrthGroupShapes s{};
+        int64_t chunks = 0;
         g.rt = rt;
         g.kind = k;
         for (; i < count && g.count < ORTH_JOBS; ++i) {
           if (kind(i) != k || rank_tiles(shape(i).r()) != rt) continue;
+          chunks += cdiv(shape(i).len(), orth_chunk(rt));
+          if (g.count > 0 && chunks > ORTH_CHUNKS) break;
           s.len[g.count] = shape(i).len();
           g.index[g.count++] = i;
         }

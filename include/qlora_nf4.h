@@ -752,17 +752,19 @@ int qn_head_loss_bwd(const qn_head* h, const float* loss, const float* lse,
  * Matrices are dense row-major [rows][cols], min(rows, cols) <= QN_MAX_RANK
  * (an adapter's A and B), rows * cols < 2^31, aligned to their element.  The
  * X_k X_k^T and their products are formed in 64 bits, U times their product
- * in fp32.  A zero matrix gives zeros.  A NaN or infinity makes the results
- * of its own matrix NaN (a momentum and parameter also where U is finite).
+ * in fp32.  A zero matrix gives zeros.  A NaN or infinity in U makes all of
+ * its own matrix's result, or parameter, NaN; a momentum is so only where its
+ * own elements are.
  * Calls that run at the same time need workspaces of their own; they must be
  * 16-byte aligned.
  */
 #define QN_ORTH_MAX_STEPS 16
 #define QN_ORTH_BATCH_MAX 65536
+#define QN_ORTH_MIN_EPS 1e-20   /* a^steps / eps stays inside fp32 */
 
 typedef struct {
   double coef[3];
-  double eps;            /* > 0 */
+  double eps;            /* >= QN_ORTH_MIN_EPS */
   int32_t steps;         /* 1 .. QN_ORTH_MAX_STEPS */
 } qn_orth_hparams;
 

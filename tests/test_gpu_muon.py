@@ -114,12 +114,30 @@ def test_in_place_and_unaligned():
     assert buf[0] == 0 and (buf[1 + 33 * 70:] == 0).all()
 
 
+def test_one_row_of_the_longest():
+    # 2^31 - 1 columns: every element is the same, and so is every result
+    n = 2 ** 31 - 1
+    x = torch.ones((1, n), dtype=torch.bfloat16, device=DEV)
+    x[0, n // 3] = -1
+    capi.qn_orthogonalize(x, out=x)
+    want = float(om.orthogonalize(np.ones((1, 1)))[0, 0]) / n ** 0.5
+    x[0, n // 3] *= -1
+    assert bool((x == x[0, 0]).all())
+    assert abs(float(x[0, 0]) - want) <= (H + 8 * U) * want
+
+
 def test_zero_and_not_finite():
     zero, bad, good = torch.zeros(16, 100), matrix(16, 100, 1), matrix(16, 100, 2)
     bad[3, 50] = float("inf")
     ys = capi.qn_orthogonalize([t.to(DEV) for t in (zero, bad, good)])
     assert (ys[0] == 0).all() and torch.isnan(ys[1]).all()
     check_orth(good, ys[2])
+
+
+@pytest.mark.parametrize("r", [3, 20, 100])
+def test_zero_matrix_with_the_smallest_eps(r):
+    zero = torch.zeros(r, 200, device=DEV)
+    assert (capi.qn_orthogonalize(zero, steps=16, eps=1e-20) == 0).all()
 
 
 def muon_case(shapes, seed):

@@ -137,6 +137,15 @@ def test_muon_refusals():
                           None) == EINVAL
 
 
+def test_eps_too_small_for_fp32_is_refused():
+    # the factors of a zero matrix, a^steps / eps, have to be finite in fp32
+    assert capi.ORTH_COEF[0] ** 16 / 1e-20 < 3e38
+    job = (capi._OrthJob * 1)(capi._OrthJob(P, 0, P, 0, 16, 64))
+    for eps in (9.9e-21, 1e-40, 5e-324):
+        assert capi.lib().qn_orthogonalize(job, 1, ctypes.byref(_orth_hp(eps=eps)), P, BIG,
+                                           None) == EINVAL
+
+
 def test_binding_refuses_host_tensors_and_odd_arguments():
     x, w, lab = torch.zeros(4, 64).bfloat16(), torch.zeros(9, 64).bfloat16(), torch.zeros(4).long()
     f = capi.HeadLoss(torch.zeros(4), torch.zeros(4))
