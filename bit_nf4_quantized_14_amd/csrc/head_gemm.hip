@@ -168,7 +168,8 @@ __device__ __forceinline__ int64_t g_block(int m, int64_t v, int64_t vp) {
 // Where an operand's tile comes from; load() fetches one step after another.
 // N: `base` is the tile's first row, vo[i] the byte offset of slot i in step 0
 // (G_OOB for a row outside); the reduction's elements from `left` on read as
-// zeros.  T: `base` is the step's first reduction row at the operand's first
+// zeros, and steps behind the last one load at no offset (one past the
+// resource's range would leave the range check nothing to compare with).  T: `base` is the step's first reduction row at the operand's first
 // column, vo[i] the offset of slot i inside a step (G_OOB for columns
 // outside); rows from `left` on read as zeros by the resource's range.  TG: as T
 // for G, `vp_bytes` from one block of 256 rows to the next.
@@ -211,7 +212,7 @@ struct HeadLoader {
   __device__ __forceinline__ void slot(uint32_t lds, int i, int wave, int tid) {
     if constexpr (KIND == HK_TG) ok = O::red_t(tid, i) < left;
     load_lds16(r, lds + wave * 1024 + NT * 16 * i, KIND == HK_T || ok ? vo[i] : G_OOB,
-               KIND == HK_N ? so : 0);
+               KIND == HK_N && left > 0 ? so : 0);
   }
   __device__ __forceinline__ void end() {
     left -= HD_BK;
