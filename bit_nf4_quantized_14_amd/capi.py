@@ -9,6 +9,7 @@ exception is raised.
 
 from __future__ import annotations
 
+import bisect
 import ctypes
 import os
 from dataclasses import dataclass
@@ -1262,6 +1263,19 @@ def _matrix(fn: str, name: str, t, index: int | None):
     return index, t.shape
 
 
+def _apart(fn: str, what: str, written, read=()):
+    """Refuses written tensors that share memory with one another or with what is read."""
+    def span(t):
+        return t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
+    w = sorted(span(t) for t in written)
+    bad = any(a[1] > b[0] for a, b in zip(w, w[1:]))
+    for lo, hi in map(span, read):
+        i = bisect.bisect_left(w, (hi,))          # the last one that begins below hi
+        bad |= i > 0 and w[i - 1][1] > lo
+    if bad:
+        raise _bad(fn, f"{what} share memory")
+
+
 def qn_orthogonalize(x, out=None, dtype: int | None = None, steps: int = 5, coef=ORTH_COEF,
                      eps: float = 1e-7, ws=None, stream=None):
     """Newton-Schulz steps on a matrix [rows, cols] (fp32 or bf16, the fewer
@@ -1278,6 +1292,9 @@ def qn_orthogonalize(x, out=None, dtype: int | None = None, steps: int = 5, coef
     index = None
     for t in xs:
         index, _ = _matrix(fn, "x", t, index)
+    if out is not None:              # an x may lie only where its own result does
+        _apart(fn, "x and out", [y for y in outs if y is not None],
+               [t for t, y in zip(xs, outs) if y is None or y.data_ptr() != t.data_ptr()])
 
     def body(st):
         arr = (_OrthJob * len(xs))()
@@ -1328,6 +1345,7 @@ class MuonBatch:
                               _tensor(fn, "m", m, shape, f32, self.index), shape[0], shape[1])
             self.keep += [p, g]
             self.momenta.append(m)
+        _apart(fn, "p, g and m", self.keep[::2] + self.momenta, self.keep[1::2])
         self.arr, self.count = arr, len(jobs)
         self.ws_bytes = int(lib().qn_muon_workspace_bytes(arr, self.count))
         if self.ws_bytes == 0:

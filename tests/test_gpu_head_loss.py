@@ -360,3 +360,65 @@ def test_other_streams_and_two_calls_at_once():
     torch.cuda.synchronize()
     for g, b in got:
         assert torch.equal(g.loss, f.loss) and torch.equal(b[0], a[0]) and torch.equal(b[1], a[1])
+
+
+def test_batches_as_their_callers_hold_them():
+    # hidden states that are a view of a padded batch are taken once they are
+    # dense; strided ones, other types and hosts are refused
+    x, w, lab = make(40, 64, 300, 1)
+    xd, wd, ld = x.to(DEV), w.to(DEV), lab.to(DEV)
+    f = capi.qn_head_loss_fwd(xd, wd, ld)
+    padded = torch.zeros(4, 12, 64, dtype=torch.bfloat16, device=DEV)
+    padded[:, :10] = xd.view(4, 10, 64)
+    plab = torch.full((4, 12), -100, device=DEV)
+    plab[:, :10] = ld.view(4, 10)
+    g = capi.qn_head_loss_fwd(padded.view(48, 64), wd, plab.view(48))
+    assert torch.equal(g.loss.view(4, 12)[:, :10].reshape(40), f.loss)
+    dx, _ = capi.qn_head_loss_bwd(padded.view(48, 64), wd, plab.view(48), g)
+    assert (dx.view(4, 12, 64)[:, 10:] == 0).all()
+    for bad in ((xd[::2], wd, ld[::2]), (xd, wd[::2], ld), (xd.float(), wd, ld), (xd, wd, ld.int()),
+                (xd, wd, lab), (xd, w, ld), (xd, wd, ld[:39]), (xd[:, :60].contiguous(), wd, ld),
+                (xd.view(4, 10, 64), wd, ld)):
+        with pytest.raises(capi.QNError):
+            capi.qn_head_loss_fwd(*bad)
+        with pytest.raises(capi.QNError):
+            capi.qn_head_loss_bwd(*bad, f)
+    with pytest.raises(capi.QNError):
+        capi.qn_head_loss_bwd(xd, wd, ld, capi.HeadLoss(f.loss[:39], f.lse))
+    with pytest.raises(capi.QNError):
+        capi.qn_head_loss_bwd(xd, wd, ld, f, need_dx=False)
+
+
+def test_two_graphs_with_one_workspace():
+    # replayed in turn on one stream they may share it
+    from test_gpu_graphs import _capture, _eager_noise
+    cases = [make(60, 128, 700, 1), make(300, 128, 33000, 2)]
+    n = max(max(capi.qn_head_fwd_workspace_bytes(c[0].shape[0], 128, c[1].shape[0]),
+                capi.qn_head_bwd_workspace_bytes(c[0].shape[0], 128, c[1].shape[0], True, True))
+            for c in cases)
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    graphs, outs, want = [], [], []
+    for c in cases:
+        x, w, lab = (t.to(DEV) for t in c)
+        rows = x.shape[0]
+        out = capi.HeadLoss(*(torch.empty(k, device=DEV) for k in (rows, rows, 2, rows)))
+        dx, dw = torch.empty_like(x), torch.empty_like(w)
+
+        def step():
+            capi.qn_head_loss_fwd(x, w, lab, out=out, ws=ws)
+            capi.qn_head_loss_bwd(x, w, lab, out, dx=dx, dw=dw, ws=ws)
+        step()
+        torch.cuda.synchronize()
+        outs.append((out.loss, out.mean, dx, dw, out, x, w, lab))    # all that the graph uses
+        want.append([t.clone() for t in outs[-1][:4]])
+        graphs.append(_capture(step))
+    for rep in range(4):
+        for g, o in zip(graphs, outs):
+            for t in o[:4]:
+                t.fill_(rep)
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for o, r in zip(outs, want):
+            assert all(torch.equal(a, b) for a, b in zip(o, r)), rep
+        _eager_noise()

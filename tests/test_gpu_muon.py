@@ -278,3 +278,29 @@ def test_not_finite_gradient_keeps_to_its_matrix():
     assert torch.isnan(bad.keep[2]).all()
     for i in (0, 2):
         assert torch.equal(clean.keep[2 * i], bad.keep[2 * i])
+
+
+def test_shared_memory_is_refused():
+    a, b = torch.randn(16, 64, device=DEV), torch.randn(16, 64, device=DEV)
+    buf = torch.zeros(17 * 64, device=DEV)
+    for xs, outs in (([a, b], [a, a]), ([a, b], [b, torch.empty_like(a)]), ([a, a], [a, b]),
+                     ([buf[:1024].view(16, 64)], [buf[64:].view(16, 64)]),
+                     ([buf[64:].view(16, 64)], [buf[:1024].view(16, 64)])):
+        with pytest.raises(capi.QNError):
+            capi.qn_orthogonalize(xs, out=outs)
+    assert torch.equal(*capi.qn_orthogonalize([a, a], out=[torch.empty_like(a), b]))
+    p, q = torch.zeros(16, 64, device=DEV).bfloat16(), torch.zeros(16, 64, device=DEV).bfloat16()
+    for jobs in ([(p, a, None), (p, b, None)], [(p, a, b), (q, a, b)], [(p, a, a)]):
+        with pytest.raises(capi.QNError):
+            capi.MuonBatch(jobs)
+    capi.MuonBatch([(p, a, None), (q, a, None)])     # a gradient may serve two
+
+
+def test_host_tensors_among_them_are_refused():
+    a = torch.randn(16, 64, device=DEV)
+    with pytest.raises(capi.QNError):
+        capi.qn_orthogonalize([a, a.cpu()])
+    with pytest.raises(capi.QNError):
+        capi.qn_orthogonalize(a, out=torch.empty(16, 64))
+    with pytest.raises(capi.QNError):
+        capi.MuonBatch([(a.bfloat16(), a.cpu(), None)])
