@@ -293,7 +293,8 @@ __device__ __forceinline__ void orth_pair(int p, int& i, int& j) {
 // Up to 64 rows a wave takes every fourth group of four positions and all
 // pairs of tiles, above that all positions and every fourth (eighth) pair.
 template <int MODE, int RT>
-__global__ __launch_bounds__(orth_threads(RT)) void k_orth_gram(OrthBatch b) {
+__global__ __launch_bounds__(orth_threads(RT), orth_gram_wgs(RT) * orth_threads(RT) / 256) void
+k_orth_gram(OrthBatch b) {
   using C = OrthCfg<RT>;
   constexpr int WAVES = C::NT / 64;
   constexpr bool SPLIT = RT <= 4;                        // positions over the waves
@@ -312,8 +313,6 @@ __global__ __launch_bounds__(orth_threads(RT)) void k_orth_gram(OrthBatch b) {
   for (int p = 0; p < NP; ++p) acc[p] = f64x4{0, 0, 0, 0};
   orth_pad<RT, false>(s, J, tid);
   // the next chunk's elements are on their way while this one's are used
-  // (not where the pairs' sums take the registers)
-  constexpr bool AHEAD = RT < 16;
   const OrthMap<RT> map(J, tid);
   float u[C::G4][4] = {}, m[MODE == OM_MUON ? C::G4 : 1][4] = {};
   auto fetch = [&](int c) {
@@ -327,26 +326,14 @@ __global__ __launch_bounds__(orth_threads(RT)) void k_orth_gram(OrthBatch b) {
         orth_fetch<MODE, RT>(J, OrthGroup4<RT>(J, c, tid, k), u[k], m[MODE == OM_MUON ? k : 0]);
     }
   };
-  if (AHEAD) fetch(c0);
+  fetch(c0);
   for (int c = c0; c < c1; ++c) {
-    if constexpr (MODE == OM_MUON && AHEAD)
+    if constexpr (MODE == OM_MUON)
 #pragma unroll
       for (int k = 0; k < C::G4; ++k)
 #pragma unroll
         for (int e = 0; e < 4; ++e) u[k][e] = muon_u(u[k][e], m[k][e], b);
-    if (!AHEAD) {
-#pragma unroll 4
-      for (int k = 0; k < C::G4; ++k) {
-        const OrthGroup4<RT> at(J, c, tid, k);
-        if (!at.in(J, tid, k)) continue;
-        float x[4], y[4];
-        orth_fetch<MODE, RT>(J, at, x, y);
-        if constexpr (MODE == OM_MUON)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] = muon_u(x[e], y[e], b);
-        orth_put<RT>(s, J, at, x);
-      }
-    } else if (OrthMap<RT>::ok(J, c)) {
+    if (OrthMap<RT>::ok(J, c)) {
 #pragma unroll
       for (int k = 0; k < C::G4; ++k) orth_put<RT>(s, map, k, u[k]);
     } else {
@@ -356,7 +343,7 @@ __global__ __launch_bounds__(orth_threads(RT)) void k_orth_gram(OrthBatch b) {
         if (at.in(J, tid, k)) orth_put<RT>(s, J, at, u[k]);
       }
     }
-    if (AHEAD && c + 1 < c1) fetch(c + 1);
+    if (c + 1 < c1) fetch(c + 1);
     lds_barrier();
     const float* from = s + (lane & 15) * C::PITCH + (lane >> 4);
     if constexpr (SPLIT) {
@@ -410,25 +397,31 @@ __global__ __launch_bounds__(orth_threads(RT)) void k_orth_gram(OrthBatch b) {
   }
 }
 
-// Adds up a matrix's partial Gram matrices, a workgroup to a pair of tiles:
-// four threads take every fourth partial of an element each.
+// Adds up a matrix's partial Gram matrices: a workgroup takes a part of a pair of
+// tiles, PARTS threads every PARTS-th partial of an element each.
+template <int PARTS>
 __global__ __launch_bounds__(1024) void k_orth_sum(OrthBatch b, int pairs) {
-  __shared__ double s[4][256];
-  const int jx = blockIdx.y, x = threadIdx.x & 255, part = threadIdx.x >> 8;
+  constexpr int N = 1024 / PARTS;                       // elements
+  __shared__ double s[PARTS][N];
+  const int jx = blockIdx.y, x = threadIdx.x % N, part = threadIdx.x / N;
   const int slices = b.job[jx].slices;
   const int64_t stride = pairs * 256;
-  double* base = b.part + (int64_t)jx * b.max_slices * stride + blockIdx.x * 256 + x;
+  double* base = b.part + (int64_t)jx * b.max_slices * stride + blockIdx.x * N + x;
   double t = 0.0;
-  for (int i = part; i < slices; i += 32) {
+  for (int i = part; i < slices; i += 8 * PARTS) {
     double v[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = i + 4 * k < slices ? base[(i + 4 * k) * stride] : 0.0;
+    for (int k = 0; k < 8; ++k) v[k] = i + PARTS * k < slices ? base[(i + PARTS * k) * stride] : 0.0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) t += v[k];
   }
   s[part][x] = t;
   __syncthreads();
-  if (part == 0) *base = (s[0][x] + s[1][x]) + (s[2][x] + s[3][x]);
+  if (part != 0) return;
+  t = 0.0;
+#pragma unroll
+  for (int k = 0; k < PARTS; ++k) t += s[k][x];
+  *base = t;
 }
 
 // Products of symmetric matrices that commute, in tiles of 16 x 16 as
@@ -666,18 +659,23 @@ __global__ __launch_bounds__(256) void k_orth_mul(OrthBatch b, OrthMul m0, OrthM
   }
 }
 
+// Four elements of the parameter.
+__device__ __forceinline__ void orth_param(const OrthJob& J, int64_t e, int n, bool vec,
+                                           uint16_t (&p)[4]) {
+  load4<u32x2>(static_cast<const uint16_t*>(J.out) + e, n, vec, p);
+}
+
 // What becomes of four elements of O: the result, or the parameter's step and
 // the new momentum.
 template <int MODE, bool OUT_BF16>
 __device__ __forceinline__ void orth_finish(const OrthJob& J, const OrthBatch& b, int64_t e, int n,
-                                            bool vec, float (&o)[4], const float (&m)[4]) {
+                                            bool vec, float (&o)[4], const float (&m)[4],
+                                            const uint16_t (&p)[4]) {
   if constexpr (MODE == OM_MUON) {
-    uint16_t v[4];
-    load4<u32x2>(static_cast<const uint16_t*>(J.out) + e, n, vec, v);
     {
 #pragma clang fp contract(off)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) o[x] = bf16_to_f32(v[x]) * b.decay - J.step * o[x];
+      for (int x = 0; x < 4; ++x) o[x] = bf16_to_f32(p[x]) * b.decay - J.step * o[x];
     }
     store4<f32x4>(J.m + e, n, vec, m);
   }
@@ -705,6 +703,11 @@ __global__ __launch_bounds__(orth_threads(RT)) void k_orth_apply(OrthBatch b) {
   const int chunk = blockIdx.x - b.afirst[jx];
   __shared__ double sum[RT == 1 ? 1024 : 1];
   float m[C::G4][4];
+  // the parameter's elements are on their way as early as those of U, but where
+  // that takes a workgroup's registers (65 to 128 rows: 544 us for 14 pairs x
+  // 8192 x 128, 532 with the loads at the end; 7 pairs x 256: 890, 913)
+  constexpr bool EARLY = MODE == OM_MUON && RT != 8;
+  uint16_t p[EARLY ? C::G4 : 1][4];
   orth_pad<RT, RT == 1>(s, J, tid);
   const bool whole = OrthMap<RT>::ok(J, chunk);
   const OrthMap<RT> map(J, tid);
@@ -717,6 +720,16 @@ __global__ __launch_bounds__(orth_threads(RT)) void k_orth_apply(OrthBatch b) {
       else
         orth_fetch<MODE, RT>(J, OrthGroup4<RT>(J, chunk, tid, k), u[k], m[k]);
     }
+    if constexpr (EARLY)
+#pragma unroll
+      for (int k = 0; k < C::G4; ++k) {
+        if (whole) {
+          if (map.at[k] >= 0) orth_param(J, OrthMap<RT>::first(J, chunk) + map.off[k], 4, true, p[k]);
+        } else {
+          const OrthGroup4<RT> at(J, chunk, tid, k);
+          orth_param(J, at.e, at.n, J.vec != 0, p[k]);
+        }
+      }
     if constexpr (MODE == OM_MUON)
 #pragma unroll
       for (int k = 0; k < C::G4; ++k)
@@ -739,13 +752,14 @@ __global__ __launch_bounds__(orth_threads(RT)) void k_orth_apply(OrthBatch b) {
   f32x4 q1;
   if constexpr (RT == 1) q1 = orth_poly_tile(b, jx, J.slices, sum, wave, lane);
   __syncthreads();
-  // a wave's tile rows ti, ti + WAVES, ... and its four tiles of positions
+  // a wave's tile rows ti, ti + WAVES, ... and its PT tiles of positions
   const int ti = RT >= WAVES ? wave : wave % RT, tl = RT >= WAVES ? 0 : 4 * (wave / RT);
-  f32x4 acc[IT][4];
+  constexpr int PT = RT >= WAVES ? C::LC / 16 : 4;
+  f32x4 acc[IT][PT];
 #pragma unroll
   for (int i = 0; i < IT; ++i)
 #pragma unroll
-    for (int t = 0; t < 4; ++t) acc[i][t] = f32x4{0, 0, 0, 0};
+    for (int t = 0; t < PT; ++t) acc[i][t] = f32x4{0, 0, 0, 0};
   const float* q = b.q + (int64_t)jx * C::RP * C::RP;
 #pragma unroll 2
   for (int k = 0; k < RT; ++k) {
@@ -760,7 +774,7 @@ __global__ __launch_bounds__(orth_threads(RT)) void k_orth_apply(OrthBatch b) {
     for (int e = 0; e < 4; ++e) {
       const float* from = s + (16 * k + 4 * (lane >> 4) + e) * C::PITCH + 16 * tl + (lane & 15);
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+      for (int t = 0; t < PT; ++t) {
         const float x = from[16 * t];
 #pragma unroll
         for (int i = 0; i < IT; ++i)
@@ -772,7 +786,7 @@ __global__ __launch_bounds__(orth_threads(RT)) void k_orth_apply(OrthBatch b) {
 #pragma unroll
   for (int i = 0; i < IT; ++i)
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+    for (int t = 0; t < PT; ++t)
 #pragma unroll
       for (int v = 0; v < 4; ++v)
         s[(16 * (ti + WAVES * i) + 4 * (lane >> 4) + v) * C::PITCH + 16 * (tl + t) + (lane & 15)] =
@@ -792,13 +806,16 @@ __global__ __launch_bounds__(orth_threads(RT)) void k_orth_apply(OrthBatch b) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[e] = from[e * C::PITCH];
       }
-      orth_finish<MODE, OUT_BF16>(J, b, OrthMap<RT>::first(J, chunk) + map.off[k], 4, true, o, m[k]);
+      const int64_t e = OrthMap<RT>::first(J, chunk) + map.off[k];
+      if constexpr (MODE == OM_MUON && !EARLY) orth_param(J, e, 4, true, p[0]);
+      orth_finish<MODE, OUT_BF16>(J, b, e, 4, true, o, m[k], p[EARLY ? k : 0]);
     } else {
       const OrthGroup4<RT> at(J, chunk, tid, k);
       if (!at.in(J, tid, k) || at.n == 0) continue;
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[e] = at.l[e] < C::LC ? s[at.i[e] * C::PITCH + at.l[e]] : 0.0f;
-      orth_finish<MODE, OUT_BF16>(J, b, at.e, at.n, J.vec != 0, o, m[k]);
+      if constexpr (MODE == OM_MUON && !EARLY) orth_param(J, at.e, at.n, J.vec != 0, p[0]);
+      orth_finish<MODE, OUT_BF16>(J, b, at.e, at.n, J.vec != 0, o, m[k], p[EARLY ? k : 0]);
     }
   }
 }
@@ -807,8 +824,10 @@ template <int RT>
 void poly_launch(hipStream_t st, const OrthBatch& b) {
   if constexpr (RT == 1) return;       // k_orth_apply forms them itself
   constexpr int PAIRS = orth_pairs(RT);
-  if (b.max_slices > 1)
-    QN_LAUNCH("k_orth_sum", k_orth_sum, dim3(PAIRS, b.count), dim3(1024), st, b, PAIRS);
+  if (b.max_slices > 32)
+    QN_LAUNCH("k_orth_sum", k_orth_sum<16>, dim3(4 * PAIRS, b.count), dim3(1024), st, b, PAIRS);
+  else if (b.max_slices > 1)
+    QN_LAUNCH("k_orth_sum", k_orth_sum<4>, dim3(PAIRS, b.count), dim3(1024), st, b, PAIRS);
   if constexpr (RT > 1 && RT < ORTH_BIG) {
     QN_LAUNCH("k_orth_poly", (k_orth_poly<RT>), dim3(b.count), dim3(OrthPoly<RT>::NT), st, b);
   } else if constexpr (RT >= ORTH_BIG) {

@@ -13,16 +13,21 @@ constexpr int64_t ORTH_CHUNKS = int64_t(1) << 22;
 constexpr int64_t ORTH_MAX_NUMEL = int64_t(1) << 31;
 
 // Matrices whose short side takes rt tiles of 16 (1, 2, 4, 8 or 16), chunks of
-// orth_chunk(rt) positions of the long side.
-constexpr int orth_chunk(int rt) { return rt == 1 ? 256 : (rt == 2 ? 128 : 64); }
+// orth_chunk(rt) positions of the long side: what a workgroup holds in registers
+// ahead of its use (7 pairs x 8192 x 256: 913 us with chunks of 64 that are
+// loaded when they are needed, 862 with 32).
+constexpr int orth_chunk(int rt) { return rt == 1 ? 256 : (rt == 2 ? 128 : (rt == 16 ? 32 : 64)); }
 constexpr int orth_threads(int rt) { return rt == 16 ? 512 : 256; }
-// workgroups of k_orth_gram on a CU at a time (its registers)
-constexpr int orth_gram_wgs(int rt) { return rt <= 2 ? 4 : (rt == 4 ? 3 : (rt == 8 ? 2 : 1)); }
+// workgroups of k_orth_gram on a CU at a time: its registers' (with 64 rows
+// planned for three where two fit, 28 pairs x 8192 took 225 us, not 210; with 128
+// held to two, 14 pairs took 500, not 532)
+constexpr int orth_gram_wgs(int rt) { return rt <= 2 ? 4 : (rt <= 8 ? 2 : 1); }
 constexpr int orth_pairs(int rt) { return rt * (rt + 1) / 2; }
 // from here on a matrix's polynomials take launches of their own; with one
 // tile they are formed where they are used
 constexpr int ORTH_BIG = 8;
-constexpr int ORTH_MAX_SLICES = 128;        // partial Gram matrices of one matrix
+// partial Gram matrices of one matrix (28672 x 256: 353 us with 128, 293 with 256)
+constexpr int ORTH_MAX_SLICES = 256;
 constexpr int ORTH_MATS = 5;                // 64-bit matrices of one that does
 
 struct OrthShape {
