@@ -287,18 +287,55 @@ __device__ __forceinline__ void orth_pair(int p, int& i, int& j) {
   j = p - i * (i + 1) / 2;
 }
 
+// The pairs of tiles of a wave where all waves go over all positions: of the
+// blocks of 2 x 2 tiles below the diagonal FULL whole ones and half of another,
+// and one block on the diagonal.  A block's tiles share their operands' reads
+// and conversions (7 pairs x 8192 x 256: 723 us with a pair at a time, 578 so).
+template <int RT, int WAVES>
+struct OrthBlocks {
+  static constexpr int SIDE = RT / 2, OFF = SIDE * (SIDE - 1) / 2, FULL = OFF / WAVES;
+  // block p below the diagonal: (1,0) (2,0) (2,1) ...
+  static __device__ __forceinline__ void off(int p, int& i, int& j) {
+    orth_pair(p, i, j);
+    ++i;
+  }
+};
+// R x S tiles of a block over a chunk; DIAG: of a block on the diagonal, the
+// three tiles on and below it.
+template <int R, int S, bool DIAG>
+__device__ __forceinline__ void gram_block(const float* fi, const float* fj, int pitch, int lc,
+                                           f64x4* acc) {
+#pragma unroll 4
+  for (int k = 0; k < lc / 4; ++k) {
+    double x[R], y[S];
+#pragma unroll
+    for (int t = 0; t < R; ++t) x[t] = (double)fi[16 * t * pitch + 4 * k];
+#pragma unroll
+    for (int t = 0; t < S; ++t) y[t] = DIAG ? x[t] : (double)fj[16 * t * pitch + 4 * k];
+    int p = 0;
+#pragma unroll
+    for (int t = 0; t < R; ++t)
+#pragma unroll
+      for (int u = 0; u < (DIAG ? t + 1 : S); ++u, ++p)
+        acc[p] = __builtin_amdgcn_mfma_f64_16x16x4f64(x[t], y[u], acc[p], 0, 0, 0);
+  }
+}
+
 // Partial Gram matrices: workgroup (job, slice) sums u u^T over its chunks
 // with v_mfma_f64_16x16x4_f64 (lane l gives row l % 16, reduction l / 16 of
 // either operand; accumulator v holds row 4 v + l / 16, column l % 16).
 // Up to 64 rows a wave takes every fourth group of four positions and all
-// pairs of tiles, above that all positions and every fourth (eighth) pair.
+// pairs of tiles, above that all positions and its share of the pairs.
 template <int MODE, int RT>
 __global__ __launch_bounds__(orth_threads(RT), orth_gram_wgs(RT) * orth_threads(RT) / 256) void
 k_orth_gram(OrthBatch b) {
   using C = OrthCfg<RT>;
   constexpr int WAVES = C::NT / 64;
   constexpr bool SPLIT = RT <= 4;                        // positions over the waves
-  constexpr int NP = SPLIT ? C::PAIRS : (C::PAIRS + WAVES - 1) / WAVES;
+  constexpr int NP = SPLIT ? C::PAIRS : C::PAIRS / WAVES;
+  static_assert(SPLIT || (RT == 2 * WAVES && OrthBlocks<RT, WAVES>::OFF % WAVES == WAVES / 2 &&
+                          4 * OrthBlocks<RT, WAVES>::FULL + 5 == NP),
+                "pairs of a wave");
   __shared__ __attribute__((aligned(16))) float s[C::RP * C::PITCH];
   __shared__ double red[SPLIT ? C::PAIRS * 256 : 1];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -360,16 +397,19 @@ k_orth_gram(OrthBatch b) {
             acc[p] = __builtin_amdgcn_mfma_f64_16x16x4f64(x[i], x[j], acc[p], 0, 0, 0);
       }
     } else {
+      using B = OrthBlocks<RT, WAVES>;
+      int i, j;
 #pragma unroll
-      for (int p = 0; p < NP; ++p) {
-        int i, j;
-        orth_pair(min(wave + WAVES * p, C::PAIRS - 1), i, j);
-        const float *fi = from + 16 * i * C::PITCH, *fj = from + 16 * j * C::PITCH;
-#pragma unroll 4
-        for (int k = 0; k < C::LC / 4; ++k)
-          acc[p] = __builtin_amdgcn_mfma_f64_16x16x4f64((double)fi[4 * k], (double)fj[4 * k],
-                                                        acc[p], 0, 0, 0);
+      for (int f = 0; f < B::FULL; ++f) {
+        B::off(wave + WAVES * f, i, j);
+        gram_block<2, 2, false>(from + 32 * i * C::PITCH, from + 32 * j * C::PITCH, C::PITCH, C::LC,
+                                acc + 4 * f);
       }
+      B::off(WAVES * B::FULL + (wave >> 1), i, j);
+      gram_block<1, 2, false>(from + (32 * i + 16 * (wave & 1)) * C::PITCH, from + 32 * j * C::PITCH,
+                              C::PITCH, C::LC, acc + 4 * B::FULL);
+      gram_block<2, 2, true>(from + 32 * wave * C::PITCH, from + 32 * wave * C::PITCH, C::PITCH, C::LC,
+                             acc + 4 * B::FULL + 2);
     }
     lds_barrier();
   }
@@ -389,11 +429,24 @@ k_orth_gram(OrthBatch b) {
     }
     for (int x = tid; x < C::PAIRS * 256; x += C::NT) to[x] = red[x];
   } else {
+    using B = OrthBlocks<RT, WAVES>;
+    auto out = [&](int i, int j, const f64x4& x) {
 #pragma unroll
-    for (int p = 0; p < NP; ++p)
-      if (wave + WAVES * p < C::PAIRS)
+      for (int v = 0; v < 4; ++v) to[((i * (i + 1) / 2 + j) * 4 + v) * 64 + lane] = x[v];
+    };
+    int i, j;
 #pragma unroll
-        for (int v = 0; v < 4; ++v) to[((wave + WAVES * p) * 4 + v) * 64 + lane] = acc[p][v];
+    for (int f = 0; f < B::FULL; ++f) {
+      B::off(wave + WAVES * f, i, j);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) out(2 * i + (t >> 1), 2 * j + (t & 1), acc[4 * f + t]);
+    }
+    B::off(WAVES * B::FULL + (wave >> 1), i, j);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) out(2 * i + (wave & 1), 2 * j + t, acc[4 * B::FULL + t]);
+    out(2 * wave, 2 * wave, acc[NP - 3]);
+    out(2 * wave + 1, 2 * wave, acc[NP - 2]);
+    out(2 * wave + 1, 2 * wave + 1, acc[NP - 1]);
   }
 }
 
@@ -579,7 +632,17 @@ __device__ __forceinline__ f32x4 orth_poly_tile(const OrthBatch& b, int jx, int 
 
 // The polynomials for 65 to 256 rows, where a matrix fills more than a CU's
 // LDS: one launch for each set of products that do not wait for one another.
-// First: the Gram matrix over the squared norm, its rows in order.
+// They lie in tiles of 16 x 16, each in the order in which a wave loads it: lane l
+// takes row l % 16, columns 4 (l / 16) .. + 3, as two loads of 16 bytes that are
+// each contiguous over the wave.
+template <int RT>
+__device__ __forceinline__ int orth_at(int i, int j) {
+  const int l = (i & 15) + 16 * ((j & 15) >> 2);
+  return ((i >> 4) * RT + (j >> 4)) * 256 + 128 * ((j >> 1) & 1) + 2 * l + (j & 1);
+}
+typedef double f64x2 __attribute__((ext_vector_type(2)));
+
+// First: the Gram matrix over the squared norm.
 template <int RT>
 __global__ __launch_bounds__(1024) void k_orth_norm(OrthBatch b) {
   constexpr int RP = 16 * RT, PAIRS = orth_pairs(RT);
@@ -608,53 +671,85 @@ __global__ __launch_bounds__(1024) void k_orth_norm(OrthBatch b) {
   const int row = 16 * i + 4 * (x >> 6) + ((x & 63) >> 4), col = 16 * j + (x & 15);
   const double v = (part[p * 256 + x] * inv) * inv;
   double* A = b.mats + (int64_t)blockIdx.y * ORTH_MATS * RP * RP;
-  A[row * RP + col] = v;
-  if (i != j) A[col * RP + row] = v;
+  A[orth_at<RT>(row, col)] = v;
+  if (i != j) A[orth_at<RT>(col, row)] = v;
 }
 
-// dst = x y, for one or two products (blockIdx.z), 32 x 32 elements of the
-// lower half to a workgroup.  OB_P: a I + b x + c x y instead.  OB_Q: into q in
-// fp32, over the norm, instead of dst.
+// dst = x y, for one or two products, 32 x 32 elements of the lower half to a
+// workgroup.  OB_P: a I + b x + c x y instead.  OB_Q: into q in fp32, over the
+// norm, instead of dst.  Each wave takes a quarter of the reduction for all four
+// tiles, all its loads at once, so that nothing is loaded twice: what the L1 and
+// L2 deliver bounds it (256 x 4096 alone: 134 us; with a tile to a wave 198, of
+// which 14 of these launches 140).
 enum { OB_P = 1, OB_Q = 2 };
 struct OrthMul {
   int8_t dst, x, y, kind;       // matrices of a job
 };
+struct OrthMulBatch {
+  OrthMul m[2];
+  int32_t products, count;
+  int32_t pinned;               // a matrix's workgroups are all on one XCD
+  double a, b, c;
+  float* q;
+  double *inv, *mats;
+};
 template <int RT>
-__global__ __launch_bounds__(256) void k_orth_mul(OrthBatch b, OrthMul m0, OrthMul m1) {
-  constexpr int RP = 16 * RT;
-  const OrthMul m = blockIdx.z == 0 ? m0 : m1;
+__global__ __launch_bounds__(256) void k_orth_mul(OrthMulBatch b) {
+  constexpr int RP = 16 * RT, BLOCKS = orth_pairs(RT / 2);
+  // (workgroups are dealt round the 8 XCDs)
+  const int each = BLOCKS * b.products, ix = b.pinned ? blockIdx.x >> 3 : blockIdx.x;
+  const int job = b.pinned ? (blockIdx.x & 7) + 8 * (ix / each) : ix / each, in = ix % each;
+  if (job >= b.count) return;
+  const OrthMul m = b.m[in / BLOCKS];
+  __shared__ double red[4][4][256];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int bi, bj;
-  orth_pair(blockIdx.x, bi, bj);
-  const int i = 2 * bi + (wave >> 1), j = 2 * bj + (wave & 1);
-  double* base = b.mats + (int64_t)blockIdx.y * ORTH_MATS * RP * RP;
+  orth_pair(in % BLOCKS, bi, bj);
+  double* base = b.mats + (int64_t)job * ORTH_MATS * RP * RP;
   const double* X = base + m.x * RP * RP;
-  // lane l takes reduction elements 16 k + 4 (l / 16) .. + 3 of its row
-  const f64x4* fx = reinterpret_cast<const f64x4*>(X + (16 * i + (lane & 15)) * RP + 4 * (lane >> 4));
-  const f64x4* fy = reinterpret_cast<const f64x4*>(base + m.y * RP * RP +
-                                                   (16 * j + (lane & 15)) * RP + 4 * (lane >> 4));
-  f64x4 acc = {0, 0, 0, 0};
-#pragma unroll 8
-  for (int k = 0; k < RP / 16; ++k) {
-    const f64x4 u = fx[4 * k], v = fy[4 * k];
+  const f64x2* fx = reinterpret_cast<const f64x2*>(X + 2 * bi * RT * 256) + lane;
+  const f64x2* fy = reinterpret_cast<const f64x2*>(base + m.y * RP * RP + 2 * bj * RT * 256) + lane;
+  constexpr int KT = RT / 4;                            // tiles of a wave along the reduction
+  f64x2 u[KT][2][2], v[KT][2][2];                       // [..][row tile][half]
+#pragma unroll
+  for (int k = 0; k < KT; ++k)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int at = ((t >> 1) * RT + wave + 4 * k) * 128 + 64 * (t & 1);
+      u[k][t >> 1][t & 1] = fx[at];
+      v[k][t >> 1][t & 1] = fy[at];
+    }
+  f64x4 acc[2][2] = {};
+#pragma unroll
+  for (int k = 0; k < KT; ++k)
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      acc = __builtin_amdgcn_mfma_f64_16x16x4f64(u[e], v[e], acc, 0, 0, 0);
-  }
-  double* D = base + m.dst * RP * RP;
-  float* q = b.q + (int64_t)blockIdx.y * RP * RP;
-  const double inv = m.kind & OB_Q ? b.inv[blockIdx.y] : 0.0;
 #pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    const int row = 16 * i + 4 * v + (lane >> 4), col = 16 * j + (lane & 15);
-    double d = acc[v];
-    if (m.kind & OB_P) d = (row == col ? b.a : 0.0) + b.b * X[row * RP + col] + b.c * d;
+      for (int t = 0; t < 4; ++t)
+        acc[t >> 1][t & 1] = __builtin_amdgcn_mfma_f64_16x16x4f64(
+            u[k][t >> 1][e >> 1][e & 1], v[k][t & 1][e >> 1][e & 1], acc[t >> 1][t & 1], 0, 0, 0);
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) red[wave][t][64 * x + lane] = acc[t >> 1][t & 1][x];
+  __syncthreads();
+  // a wave ends one of the four tiles
+  const int i = 2 * bi + (wave >> 1), j = 2 * bj + (wave & 1);
+  double* D = base + m.dst * RP * RP;
+  float* q = b.q + (int64_t)job * RP * RP;
+  const double inv = m.kind & OB_Q ? b.inv[job] : 0.0;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const int row = 16 * i + 4 * x + (lane >> 4), col = 16 * j + (lane & 15), s = 64 * x + lane;
+    double d = (red[0][wave][s] + red[1][wave][s]) + (red[2][wave][s] + red[3][wave][s]);
+    const int at = orth_at<RT>(row, col);
+    if (m.kind & OB_P) d = (row == col ? b.a : 0.0) + b.b * X[at] + b.c * d;
     if (m.kind & OB_Q) {
       q[row * RP + col] = (float)(d * inv);
       if (bi != bj) q[col * RP + row] = (float)(d * inv);
     } else {
-      D[row * RP + col] = d;
-      if (bi != bj) D[col * RP + row] = d;
+      D[at] = d;
+      if (bi != bj) D[orth_at<RT>(col, row)] = d;
     }
   }
 }
@@ -832,9 +927,15 @@ void poly_launch(hipStream_t st, const OrthBatch& b) {
     QN_LAUNCH("k_orth_poly", (k_orth_poly<RT>), dim3(b.count), dim3(OrthPoly<RT>::NT), st, b);
   } else if constexpr (RT >= ORTH_BIG) {
     constexpr int BLOCKS = orth_pairs(RT / 2);
+    // on one XCD what a product writes is in the L2 that the next one reads: 7
+    // pairs x 256 717 us, 753 spread over all; but with few matrices the CUs
+    // of an XCD have to suffice (one of 256 rows: 169 us, 134 spread)
+    const bool pinned = b.count >= 8 || BLOCKS <= G_CUS / 8;
     QN_LAUNCH("k_orth_norm", (k_orth_norm<RT>), dim3((PAIRS + 3) / 4, b.count), dim3(1024), st, b);
     auto mul = [&](int n, OrthMul x, OrthMul y) {
-      QN_LAUNCH("k_orth_mul", (k_orth_mul<RT>), dim3(BLOCKS, b.count, n), dim3(256), st, b, x, y);
+      const OrthMulBatch mb{{x, y}, n, b.count, pinned, b.a, b.b, b.c, b.q, b.inv, b.mats};
+      const unsigned jobs = pinned ? 8 * (unsigned)cdiv(b.count, 8) : b.count;
+      QN_LAUNCH("k_orth_mul", (k_orth_mul<RT>), dim3(jobs * BLOCKS * n), dim3(256), st, mb);
     };
     // matrices: 0 is A; P, Q and two free ones take turns in 1 .. 4
     int8_t P = 1, Q = 2, F = 3, G = 4;
