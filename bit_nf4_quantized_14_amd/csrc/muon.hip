@@ -798,11 +798,9 @@ __global__ __launch_bounds__(orth_threads(RT)) void k_orth_apply(OrthBatch b) {
   const int chunk = blockIdx.x - b.afirst[jx];
   __shared__ double sum[RT == 1 ? 1024 : 1];
   float m[C::G4][4];
-  // the parameter's elements are on their way as early as those of U, but where
-  // that takes a workgroup's registers (65 to 128 rows: 544 us for 14 pairs x
-  // 8192 x 128, 532 with the loads at the end; 7 pairs x 256: 890, 913)
-  constexpr bool EARLY = MODE == OM_MUON && RT != 8;
-  uint16_t p[EARLY ? C::G4 : 1][4];
+  // the parameter's elements, on their way as early as those of U
+  constexpr bool PARAM = MODE == OM_MUON;
+  uint16_t p[PARAM ? C::G4 : 1][4];
   orth_pad<RT, RT == 1>(s, J, tid);
   const bool whole = OrthMap<RT>::ok(J, chunk);
   const OrthMap<RT> map(J, tid);
@@ -815,7 +813,7 @@ __global__ __launch_bounds__(orth_threads(RT)) void k_orth_apply(OrthBatch b) {
       else
         orth_fetch<MODE, RT>(J, OrthGroup4<RT>(J, chunk, tid, k), u[k], m[k]);
     }
-    if constexpr (EARLY)
+    if constexpr (PARAM)
 #pragma unroll
       for (int k = 0; k < C::G4; ++k) {
         if (whole) {
@@ -901,16 +899,14 @@ __global__ __launch_bounds__(orth_threads(RT)) void k_orth_apply(OrthBatch b) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[e] = from[e * C::PITCH];
       }
-      const int64_t e = OrthMap<RT>::first(J, chunk) + map.off[k];
-      if constexpr (MODE == OM_MUON && !EARLY) orth_param(J, e, 4, true, p[0]);
-      orth_finish<MODE, OUT_BF16>(J, b, e, 4, true, o, m[k], p[EARLY ? k : 0]);
+      orth_finish<MODE, OUT_BF16>(J, b, OrthMap<RT>::first(J, chunk) + map.off[k], 4, true, o, m[k],
+                                  p[PARAM ? k : 0]);
     } else {
       const OrthGroup4<RT> at(J, chunk, tid, k);
       if (!at.in(J, tid, k) || at.n == 0) continue;
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[e] = at.l[e] < C::LC ? s[at.i[e] * C::PITCH + at.l[e]] : 0.0f;
-      if constexpr (MODE == OM_MUON && !EARLY) orth_param(J, at.e, at.n, J.vec != 0, p[0]);
-      orth_finish<MODE, OUT_BF16>(J, b, at.e, at.n, J.vec != 0, o, m[k], p[EARLY ? k : 0]);
+      orth_finish<MODE, OUT_BF16>(J, b, at.e, at.n, J.vec != 0, o, m[k], p[PARAM ? k : 0]);
     }
   }
 }

@@ -15,12 +15,12 @@ constexpr int64_t ORTH_MAX_NUMEL = int64_t(1) << 31;
 // Matrices whose short side takes rt tiles of 16 (1, 2, 4, 8 or 16), chunks of
 // orth_chunk(rt) positions of the long side: what a workgroup holds in registers
 // ahead of its use (7 pairs x 8192 x 256: 913 us with chunks of 64 that are
-// loaded when they are needed, 862 with 32).
-constexpr int orth_chunk(int rt) { return rt == 1 ? 256 : (rt == 2 ? 128 : (rt == 16 ? 32 : 64)); }
+// loaded when they are needed, 862 with 32; 14 pairs x 128: 389 with 64, 349;
+// one 64 x 4096: 46.0, 44.4).
+constexpr int orth_chunk(int rt) { return rt == 1 ? 256 : (rt == 2 ? 128 : 32); }
 constexpr int orth_threads(int rt) { return rt == 16 ? 512 : 256; }
-// workgroups of k_orth_gram on a CU at a time: its registers' (with 64 rows
-// planned for three where two fit, 28 pairs x 8192 took 225 us, not 210; with 128
-// held to two, 14 pairs took 500, not 532)
+// workgroups of k_orth_gram that a CU is planned to hold, by its registers; with
+// 64 rows three fit and measure as two do (211 us, 28 pairs x 8192)
 constexpr int orth_gram_wgs(int rt) { return rt <= 2 ? 4 : (rt <= 8 ? 2 : 1); }
 constexpr int orth_pairs(int rt) { return rt * (rt + 1) / 2; }
 // from here on a matrix's polynomials take launches of their own; with one
