@@ -44,7 +44,7 @@ struct HeadLogits {
   uint16_t* g;                 // [mp / 256][vp / 64][256][64], zeros for words from v1
   int64_t vp;
 };
-// few: the rows' lists are not made yet (tile HT_SMALL)
+// few: the rows' lists are not made yet (tiles HT_SMALL, HT_TINY)
 void launch_head_logits(hipStream_t st, int tile, bool bwd, bool few, const HeadLogits& a,
                         const HeadRows& rows);
 

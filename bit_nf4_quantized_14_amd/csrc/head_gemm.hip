@@ -18,6 +18,8 @@
 // 3), and read transposed with ds_read_b64_tr_b16.  LDS holds two stages;
 // the next stage's loads are issued at the start of a step and written
 // behind the step's last MFMAs.
+#include <type_traits>
+
 #include "head_rows.h"
 
 namespace {
@@ -33,13 +35,15 @@ template <int TILE>
 struct HeadCfg {
   static constexpr int BP = head_bp(TILE), BQ = head_bq(TILE);
   static constexpr int WP = TILE == HT_SMALL ? 4 : 2;
-  static constexpr int WQ = TILE == HT_256 || TILE == HT_HALF ? 4 : (TILE == HT_128 ? 2 : 1);
+  static constexpr int WQ =
+      TILE == HT_256 || TILE == HT_HALF ? 4 : (TILE == HT_128 || TILE == HT_64 ? 2 : 1);
   static constexpr int NT = 64 * WP * WQ;
   static constexpr int WTP = BP / WP, WTQ = BQ / WQ;    // a wave's part
   static constexpr int TP = WTP / 32, TQ = WTQ / 32;    // its 32 x 32 tiles
   // stages in LDS of the operand that comes from far (the weight, or G for
   // dW) and of the other one
-  static constexpr int RFAR = TILE == HT_SMALL ? 4 : 3, RNEAR = TILE == HT_SMALL ? 4 : 2;
+  static constexpr int RFAR = TILE == HT_TINY ? 8 : (TILE == HT_64 ? 5 : (TILE == HT_SMALL ? 4 : 3));
+  static constexpr int RNEAR = TILE == HT_TINY ? 8 : (TILE == HT_64 ? 5 : (TILE == HT_SMALL ? 4 : 2));
 };
 
 // s_waitcnt vmcnt(n) expcnt(7) lgkmcnt(0) (gfx9 encoding)
@@ -309,6 +313,57 @@ __device__ __forceinline__ void head_mainloop(LP& lp, LQ& lq, char* lds, int ste
     HEAD_WAIT_VM(S::OUT + LD);
   }
   head_barrier();
+  if constexpr (MPK <= 2) {
+    // With one or two matrix instructions to a slice, each slice would wait for
+    // its reads: here a step's reads go out together, a step ahead (1 row of 8000
+    // words x 8192: 42 us a slice ahead, 36 so).
+    static_assert(RP == RQ && !FILLED, "stages of a small tile");
+    u32x4 a[2][4][TP], b[2][4][TQ];
+    auto read = [&](int to, int sp) {
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+        for (int i = 0; i < TP; ++i) a[to][kk][i] = rp.read(lds, sp * PB, i, kk);
+#pragma unroll
+        for (int j = 0; j < TQ; ++j) b[to][kk][j] = rq.read(lds, RP * PB + sp * QB, j, kk);
+      }
+    };
+    int s = 0;
+    auto step = [&](auto now) {
+      constexpr int N = decltype(now)::value;
+      const int next = s + 1 == RP ? 0 : s + 1;
+      HEAD_WAIT_VM(S::OUT);            // the next stages are there, this step's are read
+      head_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      lp.begin(tid);
+      lq.begin(tid);
+#pragma unroll
+      for (int n = 0; n < LD; ++n) {
+        if (n < OP::CH) lp.slot(lds0 + s * PB, n, wave, tid);
+        else lq.slot(lds0 + RP * PB + s * QB, n - OP::CH, wave, tid);
+      }
+      lp.end();
+      lq.end();
+      read(1 - N, next);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+        for (int i = 0; i < TP; ++i)
+#pragma unroll
+          for (int j = 0; j < TQ; ++j) acc[i][j] = mfma32(a[N][kk][i], b[N][kk][j], acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);
+      s = next;
+    };
+    read(0, 0);
+    int st = 0;
+    for (; st + 1 < steps; st += 2) {
+      step(std::integral_constant<int, 0>());
+      step(std::integral_constant<int, 1>());
+    }
+    if (st < steps) step(std::integral_constant<int, 0>());
+    HEAD_WAIT_VM(0);   // nothing of this workgroup's is on its way into LDS
+    return;
+  }
   u32x4 a[2][TP], b[2][TQ];
   // Fragment n of slice kk
   auto frag = [&](int n, int sp, int sq, int kk) {
@@ -521,7 +576,6 @@ __device__ __forceinline__ void logits_finish(
     }
   }
   if constexpr (!BWD && C::WTP != HEAD_SLICE) {
-    static_assert(C::BP == HEAD_SLICE, "an entry to a tile");
     __syncthreads();
     const int tid = threadIdx.x;
     if (tid < C::BQ && q0 + tid < cnt) {
@@ -533,7 +587,7 @@ __device__ __forceinline__ void logits_finish(
         t.y = t.y * __builtin_amdgcn_exp2f(t.x - at) + o.y * __builtin_amdgcn_exp2f(o.x - at);
         t.x = top;
       }
-      a.part[(p0 - a.v0) / HEAD_SLICE * a.mp + q0 + tid] = t;
+      a.part[(p0 - a.v0) / C::BP * a.mp + q0 + tid] = t;      // an entry to a tile
     }
   }
 }
@@ -568,7 +622,7 @@ struct LogitsTile {
   }
 };
 
-// A tile to a workgroup (HT_128, HT_SMALL).  FEW: every workgroup lists the
+// A tile to a workgroup (HT_128, HT_SMALL and their halves).  FEW: every workgroup lists the
 // counted rows itself, and the first leaves the list in memory.
 template <int TILE, bool BWD, bool FEW>
 __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_logits(HeadLogits a, HeadRows rows) {
@@ -972,8 +1026,12 @@ void launch_head_logits(hipStream_t st, int tile, bool bwd, bool few, const Head
       logits_t<HT_SMALL, true>(st, bwd, a, rows);
     else
       logits_t<HT_SMALL, false>(st, bwd, a, rows);
+  } else if (tile == HT_TINY) {
+    logits_t<HT_TINY, true>(st, bwd, a, rows);      // the vocabulary is one piece
   } else if (tile == HT_128) {
     logits_t<HT_128, false>(st, bwd, a, rows);
+  } else if (tile == HT_64) {
+    logits_t<HT_64, false>(st, bwd, a, rows);
   } else {
     const int64_t tiles = cdiv(a.v1 - a.v0, 256) * cdiv(a.rows, 256);
     const dim3 grid((unsigned)std::min<int64_t>(G_CUS, cdiv(tiles, 8) * 8)), wg(512);

@@ -16,13 +16,16 @@ constexpr int64_t HEAD_MAX_DIM = int64_t(1) << 20;
 
 // Output tiles: P positions (vocabulary, or columns of dX and dW) by Q
 // positions (tokens, or words of dW).
-// HT_HALF: of a tile HT_256 half its tokens.
-enum HeadTile { HT_256 = 0, HT_128 = 1, HT_SMALL = 2, HT_HALF = 3 };
-constexpr int head_bp(int t) { return t == HT_256 || t == HT_HALF ? 256 : 128; }
-constexpr int head_bq(int t) {
-  return t == HT_256 ? 256 : (t == HT_SMALL ? 32 : 128);
+// HT_HALF: of a tile HT_256 half its tokens.  HT_64, HT_TINY: of logits HT_128
+// and HT_SMALL with half the words, where these were less than half the CUs.
+enum HeadTile { HT_256 = 0, HT_128 = 1, HT_SMALL = 2, HT_HALF = 3, HT_64 = 4, HT_TINY = 5 };
+constexpr int head_bp(int t) {
+  return t == HT_256 || t == HT_HALF ? 256 : (t == HT_64 || t == HT_TINY ? 64 : 128);
 }
-// words of a row that one statistics entry covers
+constexpr int head_bq(int t) {
+  return t == HT_256 ? 256 : (t == HT_SMALL || t == HT_TINY ? 32 : 128);
+}
+// words of a row that one statistics entry covers at most
 constexpr int64_t HEAD_SLICE = 128;
 
 #if defined(__HIPCC__)

@@ -100,6 +100,12 @@ def test_large_tiles(rows, dim, vocab):
     check(*make(rows, dim, vocab, rows), need_dw=vocab < 20000)
 
 
+@pytest.mark.parametrize("rows,dim,vocab", [(16, 72, 17000), (64, 136, 17003), (127, 64, 16500),
+                                            (200, 64, 20001), (32, 512, 16384), (100, 512, 16385)])
+def test_few_rows_of_many_words(rows, dim, vocab):
+    check(*make(rows, dim, vocab, rows), need_dw=rows < 100)
+
+
 def test_weighted_rows_and_outputs_given():
     x, w, lab = make(150, 96, 2000, 1)
     on = oh.counted(lab.numpy(), 2000)
