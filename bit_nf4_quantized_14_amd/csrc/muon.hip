@@ -325,7 +325,10 @@ __device__ __forceinline__ void gram_block(const float* fi, const float* fj, int
 // with v_mfma_f64_16x16x4_f64 (lane l gives row l % 16, reduction l / 16 of
 // either operand; accumulator v holds row 4 v + l / 16, column l % 16).
 // Up to 64 rows a wave takes every fourth group of four positions and all
-// pairs of tiles, above that all positions and its share of the pairs.
+// pairs of tiles, above that all positions and its share of the pairs.  28 pairs
+// of 8192 x 64 (235 MB of gradients and momenta): 64 to 72 us, reading (44) and
+// the 64-bit instructions (57 ns each on a SIMD) side by side; 7 pairs x 256 205,
+// bound by the instructions.
 template <int MODE, int RT>
 __global__ __launch_bounds__(orth_threads(RT), orth_gram_wgs(RT) * orth_threads(RT) / 256) void
 k_orth_gram(OrthBatch b) {
@@ -451,7 +454,8 @@ k_orth_gram(OrthBatch b) {
 }
 
 // Adds up a matrix's partial Gram matrices: a workgroup takes a part of a pair of
-// tiles, PARTS threads every PARTS-th partial of an element each.
+// tiles, PARTS threads every PARTS-th partial of an element each.  4 to 5 us, a
+// launch and the latency of its loads (14 matrices x 256 rows x 18 slices, 69 MB: 13).
 template <int PARTS>
 __global__ __launch_bounds__(1024) void k_orth_sum(OrthBatch b, int pairs) {
   constexpr int N = 1024 / PARTS;                       // elements
@@ -518,6 +522,8 @@ struct OrthPoly {
 
 // The polynomials of a matrix with 17 to 64 rows: one workgroup, everything in
 // LDS, a barrier after each set of products that do not wait for one another.
+// 64 rows, five steps: 30 us for one matrix or 56 (a CU each), of which the 170
+// tile products keep one CU's four matrix cores busy for 20; 32 rows 12 us.
 template <int RT>
 __global__ __launch_bounds__(OrthPoly<RT>::NT) void k_orth_poly(OrthBatch b) {
   using C = OrthPoly<RT>;
@@ -786,6 +792,10 @@ __device__ __forceinline__ void orth_finish(const OrthJob& J, const OrthBatch& b
 // O = Q U of one chunk (v_mfma_f32_16x16x4_f32: lane l gives row or column l
 // % 16, reduction l / 16; accumulator v holds row 4 (l / 16) + v), and what
 // becomes of it: the result, or the parameter's step with the new momentum.
+// Reading g, m and p and writing m and p bounds it (28 pairs of 8192 x 64: 470 MB
+// in 99 us, 4.7 TB/s); from 65 rows on the fp32 instructions take about as long (14
+// pairs x 128 139 us, 7 pairs x 256 186), at small sizes latency (7 pairs of 4096 x
+// 16: 12 us, of which the polynomials in every workgroup are about 3).
 template <int MODE, int RT, bool OUT_BF16>
 __global__ __launch_bounds__(orth_threads(RT)) void k_orth_apply(OrthBatch b) {
   using C = OrthCfg<RT>;

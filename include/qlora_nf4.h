@@ -16,7 +16,9 @@
  * constants) for quantization-error comparisons, an 8-bit AdamW step on
  * the adapters with its state in device memory or paged through host memory,
  * 8-bit checkpoints of activations with the layer's backward from such a
- * checkpoint, and the paired log-ratio loss of preference tuning.
+ * checkpoint, the paired log-ratio loss of preference tuning, the cross entropy
+ * of a dense vocabulary head without its logits in memory, and a momentum step
+ * on the adapters with orthogonalised updates.
  *
  * Sources for what each call computes are the pages "Qlora Expert" (Core
  * Concept), "QLoRA: The 4-bit Revolution" (sections 1 and 2), "QLoRA Guide"
