@@ -200,6 +200,11 @@ __global__ __launch_bounds__(256) void k_head_fill(HeadRows a) {
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
+bool apart(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a == nullptr || b == nullptr || x + na <= y || y + nb <= x;
+}
+
 bool valid_head(const qn_head* h) {
   if (h == nullptr || !valid_head_sizes(h->rows, h->dim, h->vocab)) return false;
   if (h->w == nullptr || !aligned16(h->w)) return false;
@@ -289,6 +294,11 @@ extern "C" int qn_head_loss_bwd(const qn_head* h, const float* loss, const float
   const bool need_dx = dx != nullptr && h->rows > 0;
   const HeadBwdPlan P = head_bwd_plan(h->rows, h->dim, h->vocab, need_dx, dw != nullptr);
   if (ws == nullptr || ws_bytes < P.total || !aligned16(ws)) return QN_EWORKSPACE;
+  // the later pieces of the vocabulary read x and w again
+  const int64_t nx = h->rows * h->dim * 2, nw = h->vocab * h->dim * 2;
+  if (!apart(dx, nx, h->x, nx) || !apart(dx, nx, h->w, nw) || !apart(dw, nw, h->x, nx) ||
+      !apart(dw, nw, h->w, nw) || !apart(dx, nx, dw, nw))
+    return QN_EINVAL;
   if (!need_dx && dw == nullptr) return QN_OK;
   hipStream_t st = (hipStream_t)stream;
   HeadRows r{};

@@ -734,7 +734,8 @@ int qn_head_loss_fwd(const qn_head* h, float* loss, float* lse, float* lse_lo,
  * softmax_label) multiplies dX in fp32, and X in bf16 for dW.
  * ws    : ws_bytes >= qn_head_bwd_workspace_bytes(rows, dim, vocab, dx !=
  *         NULL, dw != NULL), 16-byte aligned, as above.
- * Overlap and errors as qn_head_loss_fwd.
+ * Overlap and errors as qn_head_loss_fwd; dx or dw over x, w or one another is
+ * QN_EINVAL.
  */
 int qn_head_loss_bwd(const qn_head* h, const float* loss, const float* lse,
                      const float* lse_lo, const float* dloss, uint16_t* dx,

@@ -62,6 +62,18 @@ def test_head_refusals():
         assert capi.qn_head_bwd_workspace_bytes(**s, need_dw=True) == 0
 
 
+def test_gradients_over_their_inputs_are_refused():
+    # x: 64 x 128 bf16 (16 KB), w: 1000 x 128 (256000 bytes), far apart
+    X, W, DX, DW = (k << 32 for k in range(1, 5))
+    head = _head(x=X, w=W)
+
+    def bwd(dx, dw):
+        return capi.lib().qn_head_loss_bwd(head, P, P, None, None, dx, dw, P, BIG, None)
+    for dx, dw in ((X, None), (X + 16368, DW), (X - 16368, None), (W, None), (W + 255984, DW),
+                   (None, W), (None, X), (DX, X + 16), (DX, DX + 16), (DX, DX - 255984)):
+        assert bwd(dx, dw) == EINVAL, (dx, dw)
+
+
 def test_head_workspaces_stay_bounded():
     # G is kept for a piece of the vocabulary: 256 MB, or 8192 words
     for rows, dim, vocab in ((4096, 4096, 128256), (65536, 4096, 128256), (1, 8192, 262144)):
