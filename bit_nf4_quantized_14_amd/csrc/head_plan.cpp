@@ -7,19 +7,21 @@ namespace qn {
 
 namespace {
 
-// Output tiles of np x nq positions: the tile whose rounds take less time.  A
-// round of tiles HT_256 is one to a CU (the last one halves its tiles where
-// that suffices).  Tiles HT_128 take 1.45 / 4 of the time each (they are bound
-// by what L2 delivers: 786 of them 136 us where 197 HT_256 took 122, 200 rows of
-// 50257 words x 4096) and are preferred only by a fifth, because rows that do
-// not count leave fewer tiles than are planned here.
+// Output tiles of np x nq positions: the tile whose rounds take less time.  Tiles
+// HT_128 run two to a CU; where they all run at once they are taken (200 rows of
+// 32000 words x 4096: 80 us, 96 with HT_256).  A round of tiles HT_256 is one to a
+// CU (the last one halves its tiles where that suffices).  Tiles HT_128 take 1.45
+// / 4 of the time each (they are bound by what L2 delivers: 786 of them 167 us
+// where 197 HT_256 took 140, 200 rows of 50257 words x 4096) and are preferred
+// only by a fifth, because rows that do not count leave fewer tiles than are
+// planned here.
 int pick_tile(int64_t np, int64_t nq) {
   if (nq <= 32) return HT_SMALL;
-  if (nq <= 128) return HT_128;
+  const int64_t tiles = cdiv(np, 128) * cdiv(nq, 128);
+  if (nq <= 128 || tiles <= 2 * G_CUS) return HT_128;
   const int64_t large = cdiv(np, 256) * cdiv(nq, 256), rest = large % G_CUS;
   const double rounds = double(large / G_CUS) + (rest == 0 ? 0.0 : (2 * rest <= G_CUS ? 0.6 : 1.0));
-  const double small = 1.45 / (4 * G_CUS) * double(cdiv(np, 128) * cdiv(nq, 128));
-  return 1.25 * small < rounds ? HT_128 : HT_256;
+  return 1.25 * 1.45 / (4 * G_CUS) * double(tiles) < rounds ? HT_128 : HT_256;
 }
 
 // The same for logits, whose tiles are halved where they would be for at most half

@@ -100,6 +100,10 @@ def test_large_tiles(rows, dim, vocab):
     check(*make(rows, dim, vocab, rows), need_dw=vocab < 20000)
 
 
+def test_whole_and_last_rounds_of_large_tiles():
+    check(*make(1500, 72, 17001, 1))
+
+
 @pytest.mark.parametrize("rows,dim,vocab", [(16, 72, 17000), (64, 136, 17003), (127, 64, 16500),
                                             (200, 64, 20001), (32, 512, 16384), (100, 512, 16385)])
 def test_few_rows_of_many_words(rows, dim, vocab):
@@ -334,7 +338,8 @@ def test_guard_bands_and_repeatability():
     assert torch.equal(v["loss"], f.loss) and torch.equal(v["mean"], f.mean)
 
 
-@pytest.mark.parametrize("rows,dim,vocab", [(3, 64, 500), (100, 64, 500), (300, 128, 33000)])
+@pytest.mark.parametrize("rows,dim,vocab", [(3, 64, 500), (100, 64, 500), (300, 128, 33000),
+                                            (1100, 64, 17000)])
 def test_graph_replays(rows, dim, vocab):
     from test_gpu_graphs import _check_replays
     x, w, lab = make(rows, dim, vocab, 2)
