@@ -151,9 +151,11 @@ __global__ __launch_bounds__(HF_THREADS) void k_head_finish(HeadFinish a) {
       all += (double)(s_part[w][lane].y * __builtin_amdgcn_exp2f(s_part[w][lane].x - from));
     const double at = (double)from / HEAD_LOG2E;
     const double other = at + log(all);
-    // log(1 + exp(d)) and max + log(1 + exp(-|d|)); two equal infinities
-    // have no difference, and the loss then none either
-    const double d = other - (double)hit;
+    // log(1 + exp(d)) and max + log(1 + exp(-|d|)).  Two equal infinities have
+    // no difference, and the loss then none either; nor has a row whose label is
+    // at +infinity, since the label is a word of its own sum (any other word there
+    // has made `other` NaN).
+    const double d = hit == __builtin_inff() ? __builtin_nan("") : other - (double)hit;
     const double tail = log1p(exp(-fabs(d)));
     loss = d > 0.0 ? d + tail : tail;
     const double lse = d > 0.0 ? other + tail : (double)hit + tail;

@@ -678,10 +678,10 @@ int qn_pref_loss_bwd(const qn_seq_batch* b, const float* lse,
  *            not counted.
  * 0 <= rows < 2^24 (x and labels may be NULL when it is 0), dim a multiple of
  * 8 up to 2^20, 1 <= vocab <= 2^28, rows * dim <= 2^30.
- * A row whose logits hold a NaN or +infinity has no loss: its loss, lse and
- * dX row are NaN, and so are the mean and every element of dW.  A label at
- * -infinity in a row that has others makes its loss +infinity and leaves its
- * gradient finite.
+ * A row whose logits hold a NaN or +infinity, the label's among them, has no
+ * loss: its loss, lse and dX row are NaN, and so are the mean and every element
+ * of dW.  A label at -infinity in a row that has others makes its loss
+ * +infinity and leaves its gradient finite where w is.
  */
 typedef struct {
   const uint16_t* x;

@@ -3,7 +3,8 @@ and a bf16 head, the loss and log-sum-exp of counted rows, and the gradients
 of sum_t d_t loss_t with respect to both operands.
 
 A row counts when 0 <= label < vocab.  Everything is formed row by row from
-the definition; rows that do not count contribute nothing anywhere.
+the definition; rows that do not count contribute nothing anywhere.  A row
+with a word at +infinity, its label or another, has no loss: NaN.
 """
 
 import numpy as np
@@ -23,7 +24,9 @@ def head_loss(x, w, labels):
         top = z.max()
         lse[t] = top + np.log(np.exp(z - top).sum())
         others = np.delete(z, labels[t])
-        if others.size:
+        if z[labels[t]] == np.inf:          # an infinity less an infinity
+            loss[t] = np.nan
+        elif others.size:
             o = others.max()
             d = o + np.log(np.exp(others - o).sum()) - z[labels[t]]
             loss[t] = np.log1p(np.exp(d)) if d < 30 else d + np.log1p(np.exp(-d))
@@ -43,7 +46,8 @@ def head_gradient(x, w, labels, dloss=None):
         p = np.exp(z - z.max())
         p /= p.sum()
         # the label's element without the cancellation of 1 - p
+        none = np.isnan(p).any()
         p[labels[t]] = 0.0
         p[labels[t]] = -p.sum() if vocab > 1 else 0.0
-        g[t] = dloss[t] * p
+        g[t] = dloss[t] * (np.full(vocab, np.nan) if none else p)
     return g @ w, g.T @ x.astype(np.float64), g
