@@ -28,6 +28,8 @@ def head_loss(x, w, labels):
             loss[t] = np.nan
         elif others.size:
             o = others.max()
+            if o == -np.inf and z[labels[t]] > o:      # no other word has a share
+                continue
             d = o + np.log(np.exp(others - o).sum()) - z[labels[t]]
             loss[t] = np.log1p(np.exp(d)) if d < 30 else d + np.log1p(np.exp(-d))
     return loss, lse

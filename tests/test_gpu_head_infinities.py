@@ -63,3 +63,22 @@ def test_one_word_at_infinity():
     assert f.loss[0] == 0 and f.lse[0] == 8 and (dx[0] == 0).all()
     for t in (f.loss[1], f.lse[1], f.mean[0], dx[1], dw):
         assert torch.isnan(t).all()
+
+
+@pytest.mark.parametrize("rows,dim,vocab", SHAPES)
+def test_a_label_without_rivals_is_certain(rows, dim, vocab):
+    # every other word of one row is at -infinity
+    x, w, lab, _ = case(rows, dim, vocab, "overflow")
+    w[:, 0] = 2.0 ** 70
+    w[lab[ROW], 0] = 0
+    d = torch.rand(rows, device=DEV) + 0.5
+    f, dx, dw = run(x, w, lab, d)
+    rest = torch.arange(rows, device=DEV) != ROW
+    x[ROW, 0] = -(2.0 ** 70)
+    g, db, dwb = run(x, w, lab, d)
+    z = (x[ROW, 1:].double() * w[lab[ROW], 1:].double()).sum()
+    slack = (dim + 1) * 2.0 ** -24 * float((x[ROW, 1:].float() * w[lab[ROW], 1:].float()).abs().sum())
+    assert g.loss[ROW] == 0 and abs(float(g.lse[ROW]) - float(z)) <= slack + 2.0 ** -24 * abs(float(z))
+    assert (db[ROW] == 0).all() and torch.isfinite(dwb).all()
+    for a, b in ((g.loss, f.loss), (g.lse, f.lse), (db, dx)):
+        assert torch.equal(a[rest], b[rest])

@@ -41,3 +41,10 @@ def test_a_word_at_infinity_leaves_no_loss(z, label):
     got, ref = both(z, label)
     assert np.isnan(ref[0]) and np.isnan(ref[2]).all()
     assert np.isnan(got[0]) and np.isnan(got[2]).all()
+
+
+@pytest.mark.parametrize("z,label", [([-INF, 2.0, -INF], 1), ([-INF, -INF, 700.0], 2)])
+def test_a_label_without_rivals_is_certain(z, label):
+    got, ref = both(z, label)
+    assert got[0] == ref[0] == 0 and got[1] == ref[1] == z[label]
+    assert (got[2] == 0).all() and (ref[2] == 0).all()
