@@ -1323,9 +1323,10 @@ class MuonBatch:
     """Descriptors of a qn_muon_step call, with its workspace, kept alive with
     the tensors they point to.  jobs: sequence of (p, g, m): a bf16 parameter
     [rows, cols], its fp32 gradient and its fp32 momentum (None: zeros of its
-    own), which the steps read and update where they lie.  Steps of one batch
-    that run at the same time (on different streams) share its workspace and
-    must not."""
+    own), which the steps read and update where they lie.  Making a batch waits
+    for the current stream, so that its first step may be on any.  Steps of one
+    batch that run at the same time (on different streams) share its workspace
+    and must not."""
 
     def __init__(self, jobs):
         import torch
@@ -1354,6 +1355,13 @@ class MuonBatch:
         # what is allocated here belongs to the stream that is current now
         self.own = [self.ws] + [m for (_, _, m0), m in zip(jobs, self.momenta) if m0 is None]
         self.stream = _raw_stream(self.index)
+        # and is ready for any other when that stream has filled it, and has ended what it
+        # did with this memory before: a captured step could wait for neither
+        now = torch.cuda.current_stream(self.index)
+        with torch.cuda.device(self.index):
+            capturing = torch.cuda.is_current_stream_capturing()
+        if not capturing:
+            now.synchronize()
 
 
 def qn_muon_workspace_bytes(batch: MuonBatch) -> int:
