@@ -723,6 +723,13 @@ def _raw_stream(index: int) -> int:
     return _raw(index)
 
 
+def _capturing(index: int) -> bool:
+    """Whether device `index`'s current stream is being captured."""
+    import torch
+    with torch.cuda.device(index):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _run_on(index: int, stream, body):
     """body(handle) on the stream given, or on device `index`'s current one;
     that stream and device are current inside."""
@@ -1323,10 +1330,10 @@ class MuonBatch:
     """Descriptors of a qn_muon_step call, with its workspace, kept alive with
     the tensors they point to.  jobs: sequence of (p, g, m): a bf16 parameter
     [rows, cols], its fp32 gradient and its fp32 momentum (None: zeros of its
-    own), which the steps read and update where they lie.  Making a batch waits
-    for the current stream, so that its first step may be on any.  Steps of one
-    batch that run at the same time (on different streams) share its workspace
-    and must not."""
+    own, not while a graph is captured), which the steps read and update where
+    they lie.  Making a batch waits for the current stream, so that its first
+    step may be on any.  Steps of one batch that run at the same time (on
+    different streams) share its workspace and must not."""
 
     def __init__(self, jobs):
         import torch
@@ -1340,6 +1347,8 @@ class MuonBatch:
         for i, (p, g, m) in enumerate(jobs):
             self.index, shape = _matrix(fn, "p", p, self.index)
             if m is None:
+                if _capturing(self.index):       # every replay would clear it again
+                    raise _bad(fn, "momenta have to be given while a graph is captured")
                 m = torch.zeros(shape, dtype=f32, device=p.device)
             arr[i] = _MuonJob(_tensor(fn, "p", p, shape, torch.bfloat16, self.index),
                               _tensor(fn, "g", g, shape, f32, self.index),
@@ -1357,11 +1366,8 @@ class MuonBatch:
         self.stream = _raw_stream(self.index)
         # and is ready for any other when that stream has filled it, and has ended what it
         # did with this memory before: a captured step could wait for neither
-        now = torch.cuda.current_stream(self.index)
-        with torch.cuda.device(self.index):
-            capturing = torch.cuda.is_current_stream_capturing()
-        if not capturing:
-            now.synchronize()
+        if not _capturing(self.index):
+            torch.cuda.current_stream(self.index).synchronize()
 
 
 def qn_muon_workspace_bytes(batch: MuonBatch) -> int:

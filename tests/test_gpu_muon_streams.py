@@ -66,3 +66,26 @@ def test_captured_first_step():
             assert torch.equal(ref.keep[2 * i], new.keep[2 * i]), (rep, i)
             assert torch.equal(ref.momenta[i], new.momenta[i]), (rep, i)
         (out.float() * 2 + 1).sum().item()
+
+
+def test_momenta_that_every_replay_would_clear_are_refused():
+    jobs = copies()
+    momenta = [torch.zeros(p.shape, device=DEV) for p, _ in jobs]
+    ref = batch(copies())
+    g, x = torch.cuda.CUDAGraph(), torch.zeros(4, device=DEV)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        with pytest.raises(capi.QNError):
+            batch(jobs)
+        # given ones may be stepped by a batch made inside
+        new = capi.MuonBatch([(p, q, m) for (p, q), m in zip(jobs, momenta)])
+        capi.qn_muon_step(new)
+        x += 1
+    for rep in range(4):
+        g.replay()
+        capi.qn_muon_step(ref)
+        torch.cuda.synchronize()
+        assert (x == rep + 1).all()
+        for i in range(len(SHAPES)):
+            assert torch.equal(ref.keep[2 * i], new.keep[2 * i]), (rep, i)
+            assert torch.equal(ref.momenta[i], momenta[i]), (rep, i)
