@@ -1017,7 +1017,9 @@ OrthJob job_of_shape(const OrthShape& s, int32_t slices) {
 bool valid_hparams(const qn_orth_hparams* h) {
   return h != nullptr && h->steps >= 1 && h->steps <= QN_ORTH_MAX_STEPS && std::isfinite(h->eps) &&
          h->eps >= QN_ORTH_MIN_EPS && std::isfinite(h->coef[0]) && std::isfinite(h->coef[1]) &&
-         std::isfinite(h->coef[2]);
+         std::isfinite(h->coef[2]) &&
+         // Q of a zero matrix, or of a direction that U lacks, in fp32
+         std::pow(std::fabs(h->coef[0]), h->steps) / h->eps <= QN_ORTH_MAX_GAIN;
 }
 
 template <class Job>

@@ -763,10 +763,11 @@ int qn_head_loss_bwd(const qn_head* h, const float* loss, const float* lse,
  */
 #define QN_ORTH_MAX_STEPS 16
 #define QN_ORTH_BATCH_MAX 65536
-#define QN_ORTH_MIN_EPS 1e-20   /* a^steps / eps stays inside fp32 */
+#define QN_ORTH_MIN_EPS 1e-20
+#define QN_ORTH_MAX_GAIN 3e38   /* the products' factor of a zero matrix, in fp32 */
 
 typedef struct {
-  double coef[3];
+  double coef[3];        /* finite; |coef[0]|^steps / eps <= QN_ORTH_MAX_GAIN */
   double eps;            /* >= QN_ORTH_MIN_EPS */
   int32_t steps;         /* 1 .. QN_ORTH_MAX_STEPS */
 } qn_orth_hparams;
