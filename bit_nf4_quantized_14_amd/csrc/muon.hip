@@ -14,7 +14,12 @@
 //   O = Q U                                                 k_orth_apply
 // The r x r matrices are held in 64 bits: a small singular value grows by a =
 // 3.44 with every step, so an error d in A_0 moves its direction's factor by
-// about 1.4 (11.9^0 + ... + 11.9^(s-1)) d, 3e4 d after five steps.
+// about 1.4 (11.9^0 + ... + 11.9^(s-1)) d, 3e4 d after five steps.  The matrices
+// are kept exactly symmetric: of a product that is symmetric up to rounding the
+// half below the diagonal is taken for both.  What is antisymmetric in A_k
+// would grow by 10 a step, also when all singular values have come near 1 (16 x 700,
+// 16 steps, relative error 8e-8; 5e-3 with the 16 x 16 tiles on the diagonal as
+// they are formed).
 //
 // A matrix is seen as r rows ("short" index i) of its long side l, wherever
 // they lie: element (i, l) at i L + l (wide) or l r + i (tall).
@@ -486,8 +491,9 @@ __global__ __launch_bounds__(1024) void k_orth_sum(OrthBatch b, int pairs) {
 // 16, 16 j + l % 16) in register v of lane l.  That is also the first operand's
 // layout for rows 16 j .. and reduction 16 i + 4 v .., and the second's for
 // columns 16 j .., so a stored tile is read by its lane as it was written.  A
-// product's tiles on and below the diagonal are formed, the others are their
-// mirror images.  Register v of lane l lies at 64 v + (l ^ 4 v): a mirrored
+// product's tiles on and below the diagonal are formed; elements above it are
+// the mirror images of those below, in other tiles and in the diagonal's own.
+// Register v of lane l lies at 64 v + (l ^ 4 v): a mirrored
 // store, where 16 lanes go to 16 lanes of one register or another, then
 // spreads over all banks (at 64 v + l it took 64 cycles, 45% of the kernel).
 template <int RT>
@@ -514,8 +520,9 @@ struct OrthPoly {
     const int mv = (lane & 15) >> 2, ml = 16 * (lane & 3) + (lane >> 4);
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
+      if (i == j && 4 * v + (lane >> 4) < (lane & 15)) continue;
       tile(m, i, j)[at(v, lane)] = x[v];
-      if (i != j) tile(m, j, i)[at(mv, ml + 4 * v)] = x[v];
+      tile(m, j, i)[at(mv, ml + 4 * v)] = x[v];
     }
   }
 };
@@ -591,7 +598,8 @@ __global__ __launch_bounds__(OrthPoly<RT>::NT) void k_orth_poly(OrthBatch b) {
 // The same for at most 16 rows, by one wave in registers, from the partial
 // Gram matrices: every operand is a register as the instruction left it.
 // `sum` holds 4 x 256 doubles; all four waves get the result, Q[l % 16][4 v + l /
-// 16] in element v.
+// 16] in element v.  A is made symmetric through LDS, from the fifth new one on: what
+// has grown until then is 1e-11, and five steps need none.
 __device__ __forceinline__ f32x4 orth_poly_tile(const OrthBatch& b, int jx, int slices, double* sum,
                                                 int wave, int lane) {
   const double* part = b.part + (int64_t)jx * b.max_slices * 256 + lane;
@@ -629,6 +637,16 @@ __device__ __forceinline__ f32x4 orth_poly_tile(const OrthBatch& b, int jx, int 
       P[v] = (4 * v + (lane >> 4) == (lane & 15) ? b.a : 0.0) + b.b * A[v] + b.c * P[v];
     Q = st == 0 ? P : mul(P, Q);
     if (st + 1 < b.steps) A = mul(mul(P, A), P);
+    if (st + 1 < b.steps && st >= 4) {
+      double* own = sum + 256 * wave;
+      __syncthreads();                 // everyone has read what was there
+#pragma unroll
+      for (int v = 0; v < 4; ++v) own[64 * v + lane] = A[v];
+      __syncthreads();
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        if (4 * v + (lane >> 4) < (lane & 15)) A[v] = own[16 * (lane & 15) + 4 * v + (lane >> 4)];
+    }
   }
   f32x4 q;
 #pragma unroll
@@ -747,15 +765,16 @@ __global__ __launch_bounds__(256) void k_orth_mul(OrthMulBatch b) {
 #pragma unroll
   for (int x = 0; x < 4; ++x) {
     const int row = 16 * i + 4 * x + (lane >> 4), col = 16 * j + (lane & 15), s = 64 * x + lane;
+    if (row < col) continue;            // the mirror image of another
     double d = (red[0][wave][s] + red[1][wave][s]) + (red[2][wave][s] + red[3][wave][s]);
     const int at = orth_at<RT>(row, col);
     if (m.kind & OB_P) d = (row == col ? b.a : 0.0) + b.b * X[at] + b.c * d;
     if (m.kind & OB_Q) {
       q[row * RP + col] = (float)(d * inv);
-      if (bi != bj) q[col * RP + row] = (float)(d * inv);
+      q[col * RP + row] = (float)(d * inv);
     } else {
       D[at] = d;
-      if (bi != bj) D[orth_at<RT>(col, row)] = d;
+      D[orth_at<RT>(col, row)] = d;
     }
   }
 }
