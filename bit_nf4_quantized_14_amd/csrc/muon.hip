@@ -14,12 +14,11 @@
 //   O = Q U                                                 k_orth_apply
 // The r x r matrices are held in 64 bits: a small singular value grows by a =
 // 3.44 with every step, so an error d in A_0 moves its direction's factor by
-// about 1.4 (11.9^0 + ... + 11.9^(s-1)) d, 3e4 d after five steps.  The matrices
-// are kept exactly symmetric: of a product that is symmetric up to rounding the
-// half below the diagonal is taken for both.  What is antisymmetric in A_k
-// would grow by 10 a step, also when all singular values have come near 1 (16 x 700,
-// 16 steps, relative error 8e-8; 5e-3 with the 16 x 16 tiles on the diagonal as
-// they are formed).
+// about 1.4 (11.9^0 + ... + 11.9^(s-1)) d, 3e4 d after five steps.  A_k is kept
+// exactly symmetric: of the product, which is so up to rounding, the half below the
+// diagonal is taken for both.  What is antisymmetric in it would grow by 10 a
+// step, also when all singular values have come near 1 (16 x 700, 16 steps,
+// relative error 8e-8; 5e-3 with the tiles on the diagonal as they are formed).
 //
 // A matrix is seen as r rows ("short" index i) of its long side l, wherever
 // they lie: element (i, l) at i L + l (wide) or l r + i (tall).
@@ -491,9 +490,9 @@ __global__ __launch_bounds__(1024) void k_orth_sum(OrthBatch b, int pairs) {
 // 16, 16 j + l % 16) in register v of lane l.  That is also the first operand's
 // layout for rows 16 j .. and reduction 16 i + 4 v .., and the second's for
 // columns 16 j .., so a stored tile is read by its lane as it was written.  A
-// product's tiles on and below the diagonal are formed; elements above it are
-// the mirror images of those below, in other tiles and in the diagonal's own.
-// Register v of lane l lies at 64 v + (l ^ 4 v): a mirrored
+// product's tiles on and below the diagonal are formed, the others are their
+// mirror images; for A, whose errors would grow (above), so are the elements above
+// the diagonal in the tiles on it (of all four matrices: 1 us more).  Register v of lane l lies at 64 v + (l ^ 4 v): a mirrored
 // store, where 16 lanes go to 16 lanes of one register or another, then
 // spreads over all banks (at 64 v + l it took 64 cycles, 45% of the kernel).
 template <int RT>
@@ -516,13 +515,14 @@ struct OrthPoly {
     }
     return acc;
   }
+  template <bool SYM = false>
   static __device__ __forceinline__ void put(double* m, int i, int j, int lane, const f64x4& x) {
     const int mv = (lane & 15) >> 2, ml = 16 * (lane & 3) + (lane >> 4);
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      if (i == j && 4 * v + (lane >> 4) < (lane & 15)) continue;
+      if (SYM && i == j && 4 * v + (lane >> 4) < (lane & 15)) continue;
       tile(m, i, j)[at(v, lane)] = x[v];
-      tile(m, j, i)[at(mv, ml + 4 * v)] = x[v];
+      if (SYM || i != j) tile(m, j, i)[at(mv, ml + 4 * v)] = x[v];
     }
   }
 };
@@ -583,7 +583,7 @@ __global__ __launch_bounds__(OrthPoly<RT>::NT) void k_orth_poly(OrthBatch b) {
     Q2 = s;
     __syncthreads();
     if (!last) {                    // A = (P A) P
-      if (wave < C::PAIRS) C::put(A, i, j, lane, C::mul(R, P, i, j, lane));
+      if (wave < C::PAIRS) C::template put<true>(A, i, j, lane, C::mul(R, P, i, j, lane));
       __syncthreads();
     }
   }
