@@ -71,8 +71,9 @@ __device__ __forceinline__ HeadRsrc head_rsrc(const char* base, uint32_t bytes) 
 // lds, r and so are the same in the whole wave.  Written as assembly because
 // the compiler, which cannot tell the stages apart, would wait for all of
 // these loads at the next read of any stage; the waits are HEAD_WAIT_VM and
-// the barriers of the main loop.  m0 is only ever set right before its use, in
-// compiled code too.
+// the barriers of the main loop.  m0 is a reserved register: the compiler keeps
+// nothing in it, sets it right before an instruction of its own that reads it
+// (these kernels have none) and warns where a clobber list names it.
 __device__ __forceinline__ void load_lds16(const HeadRsrc& r, uint32_t lds, uint32_t vo, int so) {
   asm volatile(
       "s_mov_b32 m0, %0\n\t"
@@ -498,7 +499,9 @@ __device__ __forceinline__ void pack_rows(const float (&x)[16], u32x4 (&out)[2])
   const int wp = wave / C::WQ, wq = wave % C::WQ
 
 // Logits p0 .. of counted rows q0 .. as they leave the main loop: statistics or
-// G.  lab and lseo are those of counted rows; `red` is LDS for the statistics of
+// G, which is rounded to bf16 once for the matrix cores: relative to the row's
+// label element, which is exact, so that dX keeps its output's rounding (1.7e-3 of
+// its norm, with G in fp32 too).  lab and lseo are those of counted rows; `red` is LDS for the statistics of
 // the waves that share an entry (null: none do).
 template <int TILE, bool BWD>
 __device__ __forceinline__ void logits_finish(
@@ -636,8 +639,10 @@ struct LogitsTile {
 
 // A tile to a workgroup (HT_128, HT_SMALL and their halves): with few rows
 // reading the weight bounds it (one row, 32000 words x 4096, 262 MB that no cache
-// holds: 59 us, 4.5 TB/s; 44 when the cache holds part of it).  FEW: every workgroup lists the
-// counted rows itself, and the first leaves the list in memory.
+// holds: 59 us, 4.5 TB/s; 44 when the cache holds part of it; 128256 words 194 us with the
+// join, 5.4 TB/s).  FEW: every workgroup lists the counted rows itself, and the first leaves
+// the list in memory.  The lists leave a CU's LDS to one workgroup of HT_SMALL, not two,
+// which that rate does not show.
 template <int TILE, bool BWD, bool FEW>
 __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_logits(HeadLogits a, HeadRows rows) {
   using C = HeadCfg<TILE>;

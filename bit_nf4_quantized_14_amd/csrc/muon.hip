@@ -703,8 +703,9 @@ __global__ __launch_bounds__(1024) void k_orth_norm(OrthBatch b) {
 // workgroup.  OB_P: a I + b x + c x y instead.  OB_Q: into q in fp32, over the
 // norm, instead of dst.  Each wave takes a quarter of the reduction for all four
 // tiles, all its loads at once, so that nothing is loaded twice: what the L1 and
-// L2 deliver bounds it (256 x 4096 alone: 134 us; with a tile to a wave 198, of
-// which 14 of these launches 140).
+// L2 deliver bounds it (256 x 4096 alone: 126 us; with a tile to a wave 198, of
+// which 14 of these launches 140).  The upper half is the lower one's mirror image,
+// in the blocks on the diagonal too.
 enum { OB_P = 1, OB_Q = 2 };
 struct OrthMul {
   int8_t dst, x, y, kind;       // matrices of a job
@@ -953,8 +954,8 @@ void poly_launch(hipStream_t st, const OrthBatch& b) {
   } else if constexpr (RT >= ORTH_BIG) {
     constexpr int BLOCKS = orth_pairs(RT / 2);
     // on one XCD what a product writes is in the L2 that the next one reads: 7
-    // pairs x 256 717 us, 753 spread over all; but with few matrices the CUs
-    // of an XCD have to suffice (one of 256 rows: 169 us, 134 spread)
+    // pairs x 256 576 us, 612 spread over all; but with few matrices the CUs
+    // of an XCD have to suffice (one of 256 rows: 163 us, 126 spread)
     const bool pinned = b.count >= 8 || BLOCKS <= G_CUS / 8;
     QN_LAUNCH("k_orth_norm", (k_orth_norm<RT>), dim3((PAIRS + 3) / 4, b.count), dim3(1024), st, b);
     auto mul = [&](int n, OrthMul x, OrthMul y) {

@@ -757,9 +757,9 @@ int qn_head_loss_bwd(const qn_head* h, const float* loss, const float* lse,
  * X_k X_k^T and their products are formed in 64 bits, U times their product
  * in fp32: a direction that U lacks comes back with an error of about
  * |a|^steps 2^-24, as steps in fp32 leave it (3e-5 at 5 steps, 2e-2 at 10, as
- * large as the others from 13 on).  A zero matrix gives zeros.  A NaN or infinity in U makes all of
- * its own matrix's result, or parameter, NaN; a momentum is so only where its
- * own elements are.
+ * large as the others from 13 on).  A zero matrix gives zeros.  A NaN or
+ * infinity in U makes all of its own matrix's result, or parameter, NaN; a
+ * momentum is so only where its own elements are.
  * Calls that run at the same time need workspaces of their own; they must be
  * 16-byte aligned.
  */

@@ -71,3 +71,13 @@ def check(x, w, lab, dloss, need_dw):
 def test_paths_of_large_tiles(rows, dim, vocab, skip, need_dw):
     x, w, lab = make(rows, dim, vocab, rows + vocab, skip=skip)
     check(x, w, lab, torch.rand(rows, device=DEV) + 0.5, need_dw)
+
+
+@pytest.mark.parametrize("rows,dim,vocab", [(520, 64, 22001), (4400, 264, 3001)])
+@pytest.mark.parametrize("counted", [0, 1, 30])
+def test_few_rows_of_many_count(rows, dim, vocab, counted):
+    # plans are made for all rows, the work is that of the counted ones
+    x, w, lab = make(rows, dim, vocab, rows + counted, skip=0.0)
+    keep = torch.randperm(rows, generator=torch.Generator().manual_seed(counted))[:counted]
+    lab = torch.full_like(lab, -100).index_copy(0, keep, lab[keep])
+    check(x, w, lab, torch.rand(rows, device=DEV) + 0.5, True)
