@@ -21,7 +21,8 @@ struct HeadRows {
   float *loss, *lse, *lse_lo;
   // backward
   const float *in_loss, *in_lse, *in_lo, *dloss;
-  float *lseo, *scale;
+  float2* lseo;
+  float* scale;
   const uint16_t* x;
   uint16_t *dx, *xs;                    // either may be null
 };
@@ -35,12 +36,13 @@ struct HeadLogits {
   // words [v0, v1) of the vocabulary
   int64_t v0, v1;
   // forward: statistics and label's logit
-  float2* part;                // [slices][mp]: maximum (to base 2) and sum
+  float2* part;                // [slices][mp]: maximum, and sum from it
                                // without the label, of 128 words
   float* hit;                  // [mp]
   int64_t mp;
   // backward: softmax over the other words, -1 at the label, in bf16
-  const float* lseo;           // [mp] log2 of the sum over the other words
+  const float2* lseo;          // [mp] log of the sum over the other words: a
+                               // float near it, and the rest to base 2
   uint16_t* g;                 // [mp / 256][vp / 64][256][64], zeros for words from v1
   int64_t vp;
 };

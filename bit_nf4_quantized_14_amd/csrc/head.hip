@@ -114,7 +114,7 @@ __global__ __launch_bounds__(HF_THREADS) void k_head_finish(HeadFinish a) {
   const int cnt = a.cnt[0], blocks = max(1, (cnt + HF_ROWS - 1) / HF_ROWS);
   if ((int)blockIdx.x >= blocks) return;
   const int m = blockIdx.x * HF_ROWS + lane;
-  // logarithms to base 2; as many entries in flight as 32000 words have
+  // as many entries in flight as 32000 words have
   float mx = -__builtin_inff(), sum = 0.0f, hit = 0.0f;
   int t = 0;
   if (m < cnt) {
@@ -131,9 +131,9 @@ __global__ __launch_bounds__(HF_THREADS) void k_head_finish(HeadFinish a) {
 #pragma unroll
       for (int i = 0; i < HF_AHEAD; ++i) top = fmaxf(top, p[i].x);
       const float at = top == -__builtin_inff() ? 0.0f : top;
-      sum *= __builtin_amdgcn_exp2f(mx - at);
+      sum *= head_exp(mx, at);
 #pragma unroll
-      for (int i = 0; i < HF_AHEAD; ++i) sum += p[i].y * __builtin_amdgcn_exp2f(p[i].x - at);
+      for (int i = 0; i < HF_AHEAD; ++i) sum += p[i].y * head_exp(p[i].x, at);
       mx = top;
     }
   }
@@ -148,21 +148,22 @@ __global__ __launch_bounds__(HF_THREADS) void k_head_finish(HeadFinish a) {
     double all = 0.0;
 #pragma unroll
     for (int w = 0; w < HF_WAVES; ++w)
-      all += (double)(s_part[w][lane].y * __builtin_amdgcn_exp2f(s_part[w][lane].x - from));
-    const double at = (double)from / HEAD_LOG2E;
-    const double other = at + log(all);
+      all += (double)(s_part[w][lane].y * head_exp(s_part[w][lane].x, from));
+    // d = o_t less the label's logit, large ones subtracted first;
     // log(1 + exp(d)) and max + log(1 + exp(-|d|)).  Two equal infinities have
     // no difference, and the loss then none either; nor has a row whose label is
     // at +infinity, since the label is a word of its own sum (any other word there
     // has made `other` NaN).
-    const double d = hit == __builtin_inff() ? __builtin_nan("") : other - (double)hit;
+    const double other = log(all);
+    const double d =
+        hit == __builtin_inff() ? __builtin_nan("") : ((double)from - (double)hit) + other;
     const double tail = log1p(exp(-fabs(d)));
     loss = d > 0.0 ? d + tail : tail;
-    const double lse = d > 0.0 ? other + tail : (double)hit + tail;
-    const float hi = (float)lse;
+    const double base = d > 0.0 ? (double)from : (double)hit, more = d > 0.0 ? other + tail : tail;
+    const float hi = (float)(base + more);
     a.loss[t] = (float)loss;
     a.lse[t] = hi;
-    if (a.lse_lo) a.lse_lo[t] = (float)(lse - (double)hi);
+    if (a.lse_lo) a.lse_lo[t] = (float)((base - (double)hi) + more);
   }
   if (a.mean == nullptr) return;
   if (wave == 0) {
@@ -316,7 +317,7 @@ extern "C" int qn_head_loss_bwd(const qn_head* h, const float* loss, const float
   r.in_lse = lse;
   r.in_lo = lse_lo;
   r.dloss = dloss;
-  r.lseo = ws_at<float>(ws, P.lseo);
+  r.lseo = ws_at<float2>(ws, P.lseo);
   r.scale = ws_at<float>(ws, P.scale);
   r.dx = need_dx ? dx : nullptr;
   r.xs = dw ? ws_at<uint16_t>(ws, P.xs) : nullptr;

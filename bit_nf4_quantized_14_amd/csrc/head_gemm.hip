@@ -25,7 +25,6 @@ namespace {
 
 using namespace qn;
 
-constexpr float HD_LOG2E = 1.4426950408889634f;
 constexpr float HD_NEG_INF = -__builtin_inff();
 constexpr int HD_BK = 64;
 
@@ -506,7 +505,7 @@ __device__ __forceinline__ void pack_rows(const float (&x)[16], u32x4 (&out)[2])
 template <int TILE, bool BWD>
 __device__ __forceinline__ void logits_finish(
     const HeadLogits& a, f32x16 (&acc)[HeadCfg<TILE>::TP][HeadCfg<TILE>::TQ], int64_t p0, int q0,
-    int cnt, const int32_t* labs, const float* lseos, float2* red, int wp, int wq, int lane) {
+    int cnt, const int32_t* labs, const float2* lseos, float2* red, int wp, int wq, int lane) {
   using C = HeadCfg<TILE>;
   // word of accumulator v of tile i: pw + 32 i + 8 (v / 4) + v % 4
   const int64_t pw = p0 + wp * C::WTP + 4 * (lane >> 5);
@@ -547,16 +546,12 @@ __device__ __forceinline__ void logits_finish(
 #pragma unroll
         for (int v = 0; v < 16; ++v) mx = fmaxf(mx, acc[i][j][v]);
       mx = fmaxf(mx, __shfl_xor(mx, 32));
-      // the maximum to base 2 is only where the sum is held from: its rounding
-      // is no error
-      mx *= HD_LOG2E;
       const float at = mx == HD_NEG_INF ? 0.0f : mx;
       float sum[2] = {0.0f, 0.0f};
 #pragma unroll
       for (int i = 0; i < C::TP; ++i)
 #pragma unroll
-        for (int v = 0; v < 16; ++v)
-          sum[v & 1] += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][v], HD_LOG2E, -at));
+        for (int v = 0; v < 16; ++v) sum[v & 1] += head_exp(acc[i][j][v], at);
       st[j] = make_float2(mx, sum[0] + sum[1]);
       st[j].y += __shfl_xor(st[j].y, 32);
       if constexpr (C::WTP == HEAD_SLICE) {
@@ -567,15 +562,14 @@ __device__ __forceinline__ void logits_finish(
       }
     } else {
       // rows behind the last counted one are read by nobody
-      const float lseo = row ? lseos[m] : 0.0f;
+      const float2 lseo = row ? lseos[m] : make_float2(0.0f, 0.0f);
       const bool any = __any(lab >= 0);
 #pragma unroll
       for (int i = 0; i < C::TP; ++i) {
         float x[16];
         u32x4 out[2];
 #pragma unroll
-        for (int v = 0; v < 16; ++v)
-          x[v] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][v], HD_LOG2E, -lseo));
+        for (int v = 0; v < 16; ++v) x[v] = head_exp(acc[i][j][v], lseo);
         if (any || ragged)
 #pragma unroll
           for (int v = 0; v < 16; ++v) {
@@ -599,7 +593,7 @@ __device__ __forceinline__ void logits_finish(
       for (int w = 1; w < C::WP; ++w) {
         const float2 o = red[w * C::BQ + tid];
         const float top = fmaxf(t.x, o.x), at = top == HD_NEG_INF ? 0.0f : top;
-        t.y = t.y * __builtin_amdgcn_exp2f(t.x - at) + o.y * __builtin_amdgcn_exp2f(o.x - at);
+        t.y = t.y * head_exp(t.x, at) + o.y * head_exp(o.x, at);
         t.x = top;
       }
       a.part[(p0 - a.v0) / C::BP * a.mp + q0 + tid] = t;      // an entry to a tile
@@ -648,9 +642,10 @@ __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_logits(HeadLogits a,
   using C = HeadCfg<TILE>;
   HEAD_LDS(C, C::RFAR, C::RNEAR);
   __shared__ int32_t s_idx[FEW ? HEAD_FEW : 1], s_lab[FEW ? HEAD_FEW : 1], s_cnt;
-  __shared__ float s_lseo[FEW ? HEAD_FEW : 1], s_scale[FEW ? HEAD_FEW : 1];
+  __shared__ float2 s_lseo[FEW ? HEAD_FEW : 1];
+  __shared__ float s_scale[FEW ? HEAD_FEW : 1];
   const int32_t *idx = a.idx, *labs = a.lab;
-  const float* lseos = a.lseo;
+  const float2* lseos = a.lseo;
   int cnt;
   if constexpr (FEW) {
     if (wave == 0) {
@@ -670,7 +665,8 @@ __global__ __launch_bounds__(HeadCfg<TILE>::NT) void k_head_logits(HeadLogits a,
           rows.lab[m] = (int32_t)lab;
         }
         if constexpr (BWD) {
-          float lseo, scale;
+          float2 lseo;
+          float scale;
           head_row_bwd(rows, lane, 1.0f / (float)n, lseo, scale);
           s_lseo[m] = lseo;
           s_scale[m] = scale;

@@ -86,7 +86,7 @@ HeadBwdPlan head_bwd_plan(int64_t rows, int64_t dim, int64_t vocab, bool need_dx
   P.cnt = take(&at, 256);
   P.idx = take(&at, size_t(P.mp) * 4);
   P.lab = take(&at, size_t(P.mp) * 4);
-  P.lseo = take(&at, size_t(P.mp) * 4);
+  P.lseo = take(&at, size_t(P.mp) * 8);
   P.scale = take(&at, size_t(P.mp) * 4);
   P.g = take(&at, size_t(P.mp) * P.vp * 2);
   P.xs = take(&at, need_dw ? size_t(P.mp) * dim * 2 : 0);

@@ -6,20 +6,34 @@
 
 namespace qn {
 
-// log2 e; logarithms in the kernels are to base 2
+// log2 e.  Logits are subtracted before they are multiplied by it: an exponent
+// then is as exact as the difference, however large the logits (2^20 and 1/8
+// apart: with exp2(l log2 e - o log2 e) a loss was 1e-2 off), and no finite
+// logit's overflows.  One operation more for a logit.
 constexpr double HEAD_LOG2E = 1.4426950408889634;
+constexpr float HEAD_LOG2EF = (float)HEAD_LOG2E;
 
-// The backward's numbers of counted row m, which is row t: o_t = log2 of the sum
-// over its other words, and c_t (1 - exp(-loss_t)).
-__device__ __forceinline__ void head_row_bwd(const HeadRows& a, int t, float each, float& lseo,
+// exp(l - o) for o = from.x + from.y / log2 e
+__device__ __forceinline__ float head_exp(float l, float2 from) {
+  return __builtin_amdgcn_exp2f(__builtin_fmaf(l - from.x, HEAD_LOG2EF, -from.y));
+}
+// exp(l - at)
+__device__ __forceinline__ float head_exp(float l, float at) {
+  return __builtin_amdgcn_exp2f((l - at) * HEAD_LOG2EF);
+}
+
+// The backward's numbers of counted row m, which is row t: o_t = log of the sum
+// over its other words, as lse_t and the rest, and c_t (1 - exp(-loss_t)).
+__device__ __forceinline__ void head_row_bwd(const HeadRows& a, int t, float each, float2& lseo,
                                              float& scale) {
   const float loss = a.in_loss[t];
   const double rest = -expm1(-(double)loss);            // 1 - p(label)
-  const double lse = (double)a.in_lse[t] + (a.in_lo ? (double)a.in_lo[t] : 0.0);
+  const double lo = a.in_lo ? (double)a.in_lo[t] : 0.0;
   // a label that is certain to the last bit, or the only word there is: no other
   // word has a share
   const bool sure = loss < 1.2e-38f;
-  lseo = sure ? __builtin_inff() : (float)((lse + log(rest)) * HEAD_LOG2E);
+  lseo.x = sure ? __builtin_inff() : a.in_lse[t];
+  lseo.y = sure ? 0.0f : (float)((lo + log(rest)) * HEAD_LOG2E);
   scale = sure ? 0.0f : (float)((a.dloss ? a.dloss[t] : each) * rest);
 }
 

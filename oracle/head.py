@@ -30,7 +30,7 @@ def head_loss(x, w, labels):
             o = others.max()
             if o == -np.inf and z[labels[t]] > o:      # no other word has a share
                 continue
-            d = o + np.log(np.exp(others - o).sum()) - z[labels[t]]
+            d = (o - z[labels[t]]) + np.log(np.exp(others - o).sum())
             loss[t] = np.log1p(np.exp(d)) if d < 30 else d + np.log1p(np.exp(-d))
     return loss, lse
 
